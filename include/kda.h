@@ -83,6 +83,16 @@ extern "C" {
                                      affected outputs and states are invalid (kda_chunk_prefill and
                                      kda_mixed_batch with K and V in {64, 128}) */
 
+#define KDA_ERRFLAG_PAGES 8u      /* bit 3: kda_batch_maps ran out of free pages or block-table columns, or
+                                     met a page id outside [0, num_pages); those tokens' slots are -1 */
+#define KDA_ERRFLAG_LENGTHS 16u   /* bit 4: kda_batch_maps met a negative or too large length (the request
+                                     counts as empty) or more tokens than num_tokens (cut off) */
+
+/* Element types of the calls that take more than one (kda_norm_quant, kda_fp8_matmul). */
+#define KDA_BF16 0
+#define KDA_FP16 1
+#define KDA_FP32 2
+
 /* Per-layer head parameters shared by every call. */
 typedef struct kda_heads {
     int32_t H, K, V;        /* heads, key dim, value dim */
@@ -350,6 +360,93 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
                                int64_t num_seqs, int32_t chunk_size, const kda_heads *heads,
                                const kda_state *state, uint16_t *out, int64_t ld_out,
                                uint32_t *err_flags, void *stream);
+
+/*
+ * The calls below are what a layer's step does around the recurrence: the batch's maps,
+ * the norm in front of the projections with its 8-bit output, and the 8-bit projections.
+ * They follow the conventions above (device pointers, host checks, no allocation, no
+ * synchronisation, enqueued on `stream`) and can all be captured in a CUDA graph.
+ * 8-bit values are e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest 448, no infinity)
+ * passed as uint8_t bit patterns.
+ */
+
+/*
+ * kda_norm_quant — the residual's addition, the RMS norm and the quantisation to 8 bits of
+ * N rows of D columns, each step optional but the last:
+ *   h[c] = x[c] + residual[c]                                  (residual NULL: h = x)
+ *   y[c] = h[c] / sqrt(mean_c h[c]^2 + eps) * weight[c]        (weight NULL: y = h)
+ *   s[g] = max(max_{c in g} |y[c]|, 448 * 2^-126) / 448        per group g of 128 columns
+ *   q[c] = e4m3(y[c] / s[g]), round to nearest even            (the last group may be short)
+ * x, residual, residual_out and y_out have the element type `dtype` (KDA_BF16, KDA_FP16 or
+ * KDA_FP32), weight is fp32 [D]. residual_out (NULL without a residual) receives h and
+ * y_out (may be NULL) y, each rounded once; the sum, the norm and y itself are held in
+ * fp32, and q is made from the unrounded y. scales: fp32, s of row r and group g at
+ * scales[r*scale_row_stride + g*scale_group_stride]. residual_out may be residual or x, and
+ * y_out may be x (each row is read before it is written); no other overlap is allowed.
+ * A NaN in a group makes the group's scale and all of its q NaN (with a weight: the whole
+ * row). Without a weight an infinity gives its group an infinite scale, q = 0 at the finite
+ * columns and NaN at the infinite ones; with a weight it makes its group NaN and the rest of
+ * its row zeros, as does a sum of squares that passes the range of fp32.
+ * 1 <= D <= 32768. Any strides >= D and alignments of the element type are accepted; rows
+ * on 16-byte boundaries (q: 8-byte) move in 16-byte vectors.
+ */
+int kda_norm_quant(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int32_t dtype,
+                   const float *weight, float eps, int64_t N, int64_t D, void *residual_out,
+                   int64_t ld_residual_out, void *y_out, int64_t ld_y, uint8_t *q, int64_t ld_q,
+                   float *scales, int64_t scale_row_stride, int64_t scale_group_stride, void *stream);
+
+/*
+ * kda_fp8_matmul — out = A W^T with e4m3 operands and a scale for each block of 128:
+ *   out[m, n] = sum_k a[m, k] * sa[m, k / 128] * w[n, k] * sw[n / 128, k / 128]
+ * a: e4m3 [M, ld_a], w: e4m3 [N, ld_w] (row n holds output n's weights), K columns used of
+ * each; sa at a_scales[m*sa_row_stride + g*sa_group_stride] and sw at
+ * w_scales[(n/128)*sw_row_stride + g*sw_group_stride], fp32, g < ceil(K / 128). out has the
+ * type out_dtype (KDA_BF16, KDA_FP16, KDA_FP32), row m at out + m*ld_out. Each group's products are
+ * summed on the tensor cores in fp32, scaled and added up in fp32, and rounded once.
+ * Operands whose base and row pitch are multiples of 16 bytes take the tensor cores; others
+ * are computed by a slower kernel with the same result up to fp32 rounding. Columns K .. ld
+ * of a and w are never read. M, N and K may be any size >= 1 (K = 0: zeros; M or N = 0:
+ * nothing to do), up to 2^31 - 1 each. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT
+ * in *err_flags (may be NULL) and leaves its tile unwritten.
+ */
+int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
+                   int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
+                   int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
+                   void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, void *stream);
+
+/*
+ * kda_batch_maps — the maps of one step, from the requests' lengths. Request r < R has
+ * query_lens[r] = q_r new tokens on top of context_lens[r] = c_r, the state slot
+ * state_slots[r * state_stride] and row r of a block table whose first ceil(c_r / P) entries
+ * are its cache pages of P = page_size tokens. Written:
+ *   order[R]          the requests in running order: q_r == 1 first, the others after them,
+ *                     each part in the given order (the order kda_mixed_batch wants)
+ *   cu_seqlens[R + 1] the rows of the requests in that order
+ *   state_indices[R]  their state slots in that order
+ *   num_decodes[1]    the number of requests with q_r == 1
+ *   block_table       in place: columns ceil(c_r / P) .. ceil((c_r + q_r) / P) - 1 of row r
+ *                     get pages from the free stack, the k-th page handed out (over all
+ *                     requests in the given order) being free_pages[free_count - 1 - k]
+ *   free_left[1]      what is left on the stack; free_pages itself is not changed
+ *   positions[num_tokens], slot_map[num_tokens]  for token row t of the order above, with p =
+ *                     c_r + (t - cu_seqlens[s]): p, and block_table[r][p / P] * P + p % P
+ *                     (64 bits); rows past the last token get 0 and -1 (padded graph replays)
+ * num_tokens is the capacity of the step: requests are cut off where it ends. When the stack
+ * is empty (entry -1), a page lies past table_width or a page id outside [0, num_pages), the
+ * token's slot is -1. Both cases, and lengths that are negative or pass 2^31 - 1, set their
+ * bit of *err_flags (may be NULL; KDA_ERRFLAG_PAGES, KDA_ERRFLAG_LENGTHS). num_free is the length of
+ * free_pages; *free_count is clamped to [0, num_free]. The inputs may not overlap the outputs:
+ * free_left must not be free_count.
+ * order, cu_seqlens, state_indices, num_decodes, positions, free_left and the lengths are int32; query_lens, context_lens,
+ * the outputs and free_pages are contiguous, block_table row r starts at block_table + r*table_stride.
+ */
+int kda_batch_maps(const int32_t *query_lens, const int32_t *context_lens, const int32_t *state_slots,
+                   int64_t state_stride, int64_t R, int32_t *block_table, int64_t table_stride,
+                   int64_t table_width, const int32_t *free_pages, int64_t num_free,
+                   const int32_t *free_count, int64_t num_pages, int32_t page_size, int64_t num_tokens,
+                   int32_t *order, int32_t *cu_seqlens, int32_t *state_indices, int32_t *num_decodes,
+                   int32_t *positions, int64_t *slot_map, int32_t *free_left, uint32_t *err_flags,
+                   void *stream);
 
 #ifdef __cplusplus
 }

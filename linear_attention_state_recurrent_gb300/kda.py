@@ -13,9 +13,12 @@ Tensor conventions:
   state_pool fp32 [num_slots, H, K, V] with contiguous inner [H, K, V]; any slot stride
   state_indices int32 1-D, any positive stride
   cu_seqlens int32 [num_seqs + 1] on the GPU (a host copy is taken for launch sizing)
+The calls around the recurrence (kda_norm_quant, kda_fp8_matmul, kda_batch_maps) take 8-bit values
+as float8_e4m3fn tensors; their docstrings give the rest.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -30,11 +33,14 @@ KDA_ERR_WORKSPACE = 3
 KDA_ERR_CUDA = 4
 KDA_ERRFLAG_SLOT_RANGE = 1
 KDA_ERRFLAG_TIMEOUT = 2
+KDA_ERRFLAG_PAGES = 8
+KDA_ERRFLAG_LENGTHS = 16
 
 EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decode",
             "kda_spec_verify", "kda_spec_verify_checkpoints", "kda_fused_decode",
             "kda_fused_spec_verify", "kda_selftest_bounded_wait", "kda_chunk_prefill_workspace_bytes",
-            "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc")
+            "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
+            "kda_norm_quant", "kda_fp8_matmul", "kda_batch_maps")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -105,6 +111,14 @@ def _load():
     lib.kda_chunk_prefill_no_alloc.restype = ctypes.c_int
     lib.kda_chunk_prefill_no_alloc.argtypes = [P, I64, P, I64, P, I64, P, P, I64, I32, HP, SP, P,
                                                I64, P, P]
+    lib.kda_norm_quant.restype = ctypes.c_int
+    lib.kda_norm_quant.argtypes = [P, I64, P, I64, I32, P, ctypes.c_float, I64, I64, P, I64, P, I64, P, I64,
+                                   P, I64, I64, P]
+    lib.kda_fp8_matmul.restype = ctypes.c_int
+    lib.kda_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, P, P]
+    lib.kda_batch_maps.restype = ctypes.c_int
+    lib.kda_batch_maps.argtypes = [P, P, P, I64, I64, P, I64, I64, P, I64, P, I64, I32, I64, P, P, P, P, P, P,
+                                   P, P, P]
     return lib
 
 
@@ -474,3 +488,188 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
                                _ptr(out), ld_out, _ptr(err_flags), _stream(stream)),
            "kda_mixed_batch")
     return out, initial_state
+
+
+# ---- the operators around the recurrence -------------------------------------------------
+# These run in a few microseconds, so their wrappers pass plain integers and keep the checks
+# to comparisons.
+
+_DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_E4M3 = torch.float8_e4m3fn
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _matrix(t, name, dtype, rows, cols):
+    """The row stride of a 2-D tensor of the given type and shape with unit inner stride."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}] (got {tuple(t.shape)})")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    return ld if rows > 1 else max(ld, cols)   # the stride of a single row says nothing
+
+
+def _scale_strides(t, name, rows, groups):
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != groups:
+        raise ValueError(f"{name} must be fp32 [{rows}, {groups}] (got {t.dtype} {tuple(t.shape)})")
+    a, b = t.stride()
+    return (a if rows > 1 else 1), (b if groups > 1 else 1)
+
+
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("every tensor must be on the GPU")
+
+
+def _vector(t, name, dtype, n):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] < n or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor of at least {n} entries")
+
+
+def _rows16(rows, cols, dtype, device):
+    """An uninitialised [rows, cols] view whose rows start on 16-byte boundaries."""
+    per = 16 // dtype.itemsize
+    return torch.empty(rows, -(-cols // per) * per, dtype=dtype, device=device)[:, :cols]
+
+
+def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None, y=None, q=None,
+                   scales=None, stream=None):
+    """h = x + residual, y = h / sqrt(mean h^2 + eps) * weight, and y in e4m3 with an fp32 scale per
+    row and group of 128 columns (y = q * scale). Without `residual` h = x; without `weight` y = h
+    (only the quantisation).
+
+    x, residual: [N, D] bf16, fp16 or fp32 (the same type); weight: fp32 [D]. residual_out receives h
+    (it may be residual itself) and y, if given, the unquantised y. q: float8_e4m3fn [N, D]; scales:
+    fp32 [N, ceil(D / 128)], any strides. What is not given is allocated: q with rows on 16-byte
+    boundaries and scales with the rows next to each other (the layouts kda_fp8_matmul reads fastest).
+    Returns (q, scales, residual_out), residual_out None without a residual."""
+    if x.dim() != 2 or x.dtype not in _DTYPE_CODE:
+        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
+    N, D = x.shape
+    groups = -(-D // 128)
+    dt = x.dtype
+    if q is None:
+        q = _rows16(N, D, _E4M3, x.device)
+    if scales is None:
+        scales = torch.empty(groups, N, dtype=torch.float32, device=x.device).t()
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        ld_res = ld_ro = 0
+    else:
+        if residual_out is None:
+            residual_out = torch.empty(N, D, dtype=dt, device=x.device)
+        ld_res = _matrix(residual, "residual", dt, N, D)
+        ld_ro = _matrix(residual_out, "residual_out", dt, N, D)
+    if weight is not None and (weight.dtype != torch.float32 or weight.dim() != 1 or weight.shape[0] != D
+                               or not weight.is_contiguous()):
+        raise ValueError(f"weight must be a contiguous fp32 tensor of {D} entries")
+    s_row, s_group = _scale_strides(scales, "scales", N, groups)
+    ld_x, ld_q = _matrix(x, "x", dt, N, D), _matrix(q, "q", _E4M3, N, D)
+    ld_y = 0 if y is None else _matrix(y, "y", dt, N, D)
+    _on_gpu(x, weight, residual, residual_out, y, q, scales)
+    status = lib.kda_norm_quant(x.data_ptr(), ld_x, _address(residual), ld_res, _DTYPE_CODE[dt], _address(weight),
+                                eps, N, D, _address(residual_out), ld_ro, _address(y), ld_y, q.data_ptr(), ld_q,
+                                scales.data_ptr(), s_row, s_group, _raw_stream(stream))
+    if status:
+        _check(status, "kda_norm_quant")
+    return q, scales, residual_out
+
+
+def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat16, err_flags=None, stream=None):
+    """out[m, n] = sum_k a[m, k] a_scales[m, k / 128] w[n, k] w_scales[n / 128, k / 128].
+
+    a: float8_e4m3fn [M, K]; w: float8_e4m3fn [N, K]; a_scales: fp32 [M, ceil(K / 128)]; w_scales:
+    fp32 [ceil(N / 128), ceil(K / 128)], any strides. out: bf16, fp16 or fp32 [M, N] (allocated as
+    out_dtype when not given). Operands with rows on 16-byte boundaries take the tensor cores.
+    Returns out."""
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a and w must be 2-D with the same number of columns")
+    M, K = a.shape
+    N = w.shape[0]
+    groups = -(-K // 128)
+    if out is None:
+        if out_dtype not in _DTYPE_CODE:
+            raise ValueError("out_dtype must be bf16, fp16 or fp32")
+        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
+    elif out.dtype not in _DTYPE_CODE:
+        raise ValueError("out must be bf16, fp16 or fp32")
+    ld_a, ld_w = _matrix(a, "a", _E4M3, M, K), _matrix(w, "w", _E4M3, N, K)
+    sa_row, sa_group = _scale_strides(a_scales, "a_scales", M, groups)
+    sw_row, sw_group = _scale_strides(w_scales, "w_scales", -(-N // 128), groups)
+    ld_out = _matrix(out, "out", out.dtype, M, N)
+    _on_gpu(a, a_scales, w, w_scales, out, err_flags)
+    status = lib.kda_fp8_matmul(a.data_ptr(), ld_a, a_scales.data_ptr(), sa_row, sa_group, w.data_ptr(), ld_w,
+                                w_scales.data_ptr(), sw_row, sw_group, M, N, K, out.data_ptr(), ld_out,
+                                _DTYPE_CODE[out.dtype], _address(err_flags), _raw_stream(stream))
+    if status:
+        _check(status, "kda_fp8_matmul")
+    return out
+
+
+BatchMaps = collections.namedtuple("BatchMaps", "order cu_seqlens state_indices num_decodes positions slot_map "
+                                                "free_left")
+
+
+def make_batch_maps(num_reqs, num_tokens, device):
+    """The output buffers of kda_batch_maps for a step of num_reqs requests and at most num_tokens tokens."""
+    def i32(n):
+        return torch.empty(n, dtype=torch.int32, device=device)
+    return BatchMaps(i32(num_reqs), i32(num_reqs + 1), i32(num_reqs), i32(1), i32(num_tokens),
+                     torch.empty(num_tokens, dtype=torch.int64, device=device), i32(1))
+
+
+def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_pages, free_count, page_size, *,
+                   num_pages, num_tokens=None, out=None, err_flags=None, stream=None):
+    """The maps of a step from its requests' lengths: running order (decodes first), cu_seqlens, state
+    indices, positions and cache slots of its tokens; new pages go into block_table in place.
+
+    query_lens, context_lens: int32 [R]; state_slots: int32 [R], any positive stride; block_table: int32
+    [R, width], unit inner stride; free_pages: int32 stack of free page ids of which the first
+    free_count (int32 [1]) are free, handed out from the top; page ids are below num_pages.
+    num_tokens: the rows of the step's buffers (or `out`, from make_batch_maps, whose positions give it).
+    Returns BatchMaps(order, cu_seqlens, state_indices, num_decodes, positions, slot_map, free_left);
+    free_pages and free_count are not changed, so a repeated call gives the same maps."""
+    R = query_lens.shape[0]
+    if out is None:
+        if num_tokens is None:
+            raise ValueError("kda_batch_maps needs num_tokens or out")
+        out = make_batch_maps(R, num_tokens, query_lens.device)
+    i32 = torch.int32
+    tokens = out.positions.shape[0]
+    if num_tokens is not None and num_tokens != tokens:
+        raise ValueError("num_tokens must be the length of out.positions")
+    for t, name, n in ((query_lens, "query_lens", R), (context_lens, "context_lens", R), (free_pages, "free_pages", 0),
+                       (free_count, "free_count", 1), (out.order, "out.order", R),
+                       (out.cu_seqlens, "out.cu_seqlens", R + 1), (out.state_indices, "out.state_indices", R),
+                       (out.num_decodes, "out.num_decodes", 1), (out.positions, "out.positions", tokens),
+                       (out.free_left, "out.free_left", 1)):
+        _vector(t, name, i32, n)
+    _vector(out.slot_map, "out.slot_map", torch.int64, tokens)
+    if state_slots.dtype != i32 or state_slots.dim() != 1 or state_slots.shape[0] < R:
+        raise ValueError("state_slots must be a 1-D int32 tensor with an entry per request")
+    if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] < R or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [num_reqs, width] with unit inner stride")
+    width = block_table.shape[1]
+    _on_gpu(query_lens, context_lens, state_slots, block_table, free_pages, free_count, err_flags, *out)
+    status = lib.kda_batch_maps(query_lens.data_ptr(), context_lens.data_ptr(), state_slots.data_ptr(),
+                                state_slots.stride(0) if R > 1 else 1, R, block_table.data_ptr(),
+                                block_table.stride(0) if R > 1 else max(width, 1), width, free_pages.data_ptr(),
+                                free_pages.shape[0], free_count.data_ptr(), num_pages, page_size, tokens,
+                                out.order.data_ptr(), out.cu_seqlens.data_ptr(), out.state_indices.data_ptr(),
+                                out.num_decodes.data_ptr(), out.positions.data_ptr(), out.slot_map.data_ptr(),
+                                out.free_left.data_ptr(), _address(err_flags), _raw_stream(stream))
+    if status:
+        _check(status, "kda_batch_maps")
+    return out
