@@ -1,15 +1,467 @@
 // kda_fp8_matmul: out = A W^T with e4m3 operands and a scale for each block of 128.
+//
+//   out[m, n] = sum_g sa[m, g] sw[n / 128, g] * (sum_{k in g} a[m, k] w[n, k])
+//
+// The inner sums of one group g (128 k: four tcgen05.mma steps of 32) go to a fresh
+// accumulator in tensor memory; as the tensor core forms the next group in another buffer,
+// the epilogue warps read the finished one, scale it and add it to sums they hold in fp32
+// registers. TMA brings 128-byte-wide tiles (one group) with the 128-byte swizzle that the
+// matrix descriptors name; columns past K and rows past the matrix read as zeros.
+//
+// Two arrangements:
+//  - wide_kernel: tiles of 256 rows of A x 256 of W by a pair of CTAs (cta_group::2), persistent.
+//    A thread of the epilogue holds one row of out, so its two scales are one factor per group.
+//  - thin_kernel: 128 rows of W (the MMA's M side) x up to 128 rows of A, for few rows of A: the
+//    weights stream through at HBM's rate; the inner axis is split over a cluster whose CTAs
+//    join their sums through distributed shared memory in a fixed order.
+// Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
 #include <climits>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include "kda_common.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_launch.h"
 #include "kda_layer.h"
 #include "kda_pdl.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace {
+
+// ---- pieces shared by the tensor-core kernels ---------------------------------------------
+
+// Matrix descriptor of a K-major tile of 128-byte rows with the 128-byte swizzle: groups of 8
+// rows follow each other at 1024 bytes; the tile starts on a 1024-byte boundary. One MMA step
+// of 32 k is 32 bytes further.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// D (+)= A B^T of one group of 128 k, e4m3 operands (format 0 of kind::f8f6f4), fp32 sums.
+template <int CG>
+__device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
+{
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+        const uint64_t da = desc_sw128(a) + s * 2, db = desc_sw128(b) + s * 2;
+        if (CG == 1)
+            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                         :: "r"(d), "l"(da), "l"(db), "r"(idesc), "r"(s > 0 ? 1u : 0u));
+        else
+            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                         " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                         :: "r"(d), "l"(da), "l"(db), "r"(idesc), "r"(s > 0 ? 1u : 0u));
+    }
+}
+
+// 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address in CTA `rank` of the cluster of a shared-memory address of this CTA
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void arrive_local(uint32_t mbar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void store_out(void *out, int64_t i, int dtype, float v)
+{
+    if (dtype == 0) static_cast<uint16_t *>(out)[i] = f32_to_bf16(v);
+    else if (dtype == 1) static_cast<__half *>(out)[i] = __float2half_rn(v);
+    else static_cast<float *>(out)[i] = v;
+}
+
+__device__ __forceinline__ void report(const Fp8Params &p)
+{
+    if (p.err) atomicOr(p.err, kErrTimeout);
+}
+
+constexpr int BK = 128;                       // bytes (= k) per group
+
+// ---- few rows of A ------------------------------------------------------------------------
+
+template <int NT>
+struct Thin {
+    static constexpr int EW = NT > 64 ? 8 : 4;              // epilogue warps
+    static constexpr int THREADS = 64 + EW * 32;
+    static constexpr int COLS = NT * 4 / EW;                // columns (rows of A) per epilogue thread
+    static constexpr int NBUF = NT > 64 ? 2 : 4;            // accumulators in tensor memory
+    static constexpr int STAGE = 128 * BK + NT * BK;
+    static constexpr int STAGES = NT > 64 ? 3 : NT > 32 ? 4 : 5;
+    static constexpr int SMEM = 1024 + STAGES * STAGE;      // two CTAs per SM
+};
+
+template <int NT>
+__global__ void __launch_bounds__(Thin<NT>::THREADS, 2)
+thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Fp8Params p,
+            const int split)
+{
+    using C = Thin<NT>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint64_t bars[2 * C::STAGES + 2 * C::NBUF];
+    __shared__ uint32_t tmem_base;
+    __shared__ alignas(16) float scales[4][NT];
+    const uint32_t ring = (tc::smem_addr(dyn) + 1023u) & ~1023u;
+    float *red = reinterpret_cast<float *>(dyn + (ring - tc::smem_addr(dyn)));   // the ring again, once it is drained
+    const uint32_t b0 = tc::smem_addr(bars);
+    auto full = [&](int s) { return b0 + s * 8; };
+    auto empty = [&](int s) { return b0 + (C::STAGES + s) * 8; };
+    auto tfull = [&](int b) { return b0 + (2 * C::STAGES + b) * 8; };
+    auto tempty = [&](int b) { return b0 + (2 * C::STAGES + C::NBUF + b) * 8; };
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
+        for (int b = 0; b < C::NBUF; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), C::EW); }
+        tc::prefetch_tensormap(&tm_w);
+        tc::prefetch_tensormap(&tm_a);
+    }
+    pdl_wait();
+    // tensor memory is taken before the next grid may start: it could hold what this one waits for
+    if (warp == 1) tc::tmem_alloc<C::NBUF * NT>(tc::smem_addr(&tmem_base));
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    pdl_release();
+
+    const uint32_t tmem = tmem_base;
+    const int rank = blockIdx.x % split;
+    const int n0 = blockIdx.x / split * 128, t0 = blockIdx.y * NT;
+    const int groups = (p.K + BK - 1) / BK;
+    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / split);
+    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / split);
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int g = g0, i = 0; g < g1; g++, i++) {
+                const int s = i % C::STAGES;
+                if (i >= C::STAGES && !tc::mbar_wait(empty(s), ((i / C::STAGES) - 1) & 1)) { report(p); break; }
+                const uint32_t at = ring + s * C::STAGE;
+                tc::mbar_expect_tx(full(s), C::STAGE);
+                tc::tma_load_2d(at, &tm_w, g * BK, n0, full(s));
+                tc::tma_load_2d(at + 128 * BK, &tm_a, g * BK, t0, full(s));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t ID = tc::instr_desc(0, 128, NT);
+            for (int g = g0, i = 0; g < g1; g++, i++) {
+                const int s = i % C::STAGES, b = i % C::NBUF;
+                if (i >= C::NBUF && !tc::mbar_wait(tempty(b), ((i / C::NBUF) - 1) & 1)) { report(p); break; }
+                if (!tc::mbar_wait(full(s), (i / C::STAGES) & 1)) { report(p); break; }
+                tc::fence_after_sync();
+                const uint32_t at = ring + s * C::STAGE;
+                mma_group<1>(tmem + b * NT, at, at + 128 * BK, ID);
+                tc::commit(empty(s));
+                tc::commit(tfull(b));
+            }
+        }
+        __syncwarp();
+    } else {
+        const int e = threadIdx.x - 64;                       // 0 .. EW * 32 - 1
+        const int quarter = warp % 4, c0 = (warp - 2) / 4 * C::COLS;
+        const int n = quarter * 32 + lane;                    // row of W within the tile
+        const float *sw = p.sw + static_cast<int64_t>(n0 / 128) * p.sw_row;
+        const bool owns = e < NT && t0 + e < p.M;
+        const float *sa = p.sa + static_cast<int64_t>(t0 + e) * p.sa_row;
+        auto factor = [&](int g) { return owns && g < g1 ? sa[g * p.sa_group] * sw[g * p.sw_group] : 0.f; };
+        float2 acc[C::COLS / 2];
+#pragma unroll
+        for (int c = 0; c < C::COLS / 2; c++) acc[c] = make_float2(0.f, 0.f);
+        if (e < NT) scales[0][e] = factor(g0);
+        float next = factor(g0 + 1);
+        for (int g = g0, i = 0; g < g1; g++, i++) {
+            const int b = i % C::NBUF;
+            // this group's factors are visible after the barrier, and the slot written now was last read three groups ago
+            asm volatile("bar.sync 1, %0;" :: "n"(C::EW * 32) : "memory");
+            if (e < NT) scales[(i + 1) % 4][e] = next;
+            next = factor(g + 2);
+            if (ok && !tc::mbar_wait(tfull(b), (i / C::NBUF) & 1)) ok = false;
+            tc::fence_after_sync();
+            const float4 *f4 = reinterpret_cast<const float4 *>(&scales[i % 4][c0]);
+            const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * NT + c0;
+#pragma unroll
+            for (int c = 0; c < C::COLS; c += 16) {
+                float v[16];
+                tc::tmem_ld16(at + c, v);
+                tc::tmem_ld_wait();
+                if (c + 16 >= C::COLS) {
+                    tc::fence_before_sync();
+                    if (lane == 0) arrive_local(tempty(b));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float4 f = f4[c / 4 + j];
+                    acc[c / 2 + 2 * j] = ffma2(make_float2(v[4 * j], v[4 * j + 1]), make_float2(f.x, f.y), acc[c / 2 + 2 * j]);
+                    acc[c / 2 + 2 * j + 1] = ffma2(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(f.z, f.w), acc[c / 2 + 2 * j + 1]);
+                }
+            }
+        }
+        if (!ok) report(p);
+        if (split == 1) {
+            if (ok && n0 + n < p.N)
+#pragma unroll
+                for (int c = 0; c < C::COLS; c++)
+                    if (t0 + c0 + c < p.M)
+                        store_out(p.out, static_cast<int64_t>(t0 + c0 + c) * p.ld_out + n0 + n, p.out_dtype,
+                                  c % 2 ? acc[c / 2].y : acc[c / 2].x);
+        } else {
+#pragma unroll
+            for (int c = 0; c < C::COLS; c++) red[(c0 + c) * 128 + n] = c % 2 ? acc[c / 2].y : acc[c / 2].x;
+        }
+    }
+    if (split > 1) {
+        cluster_sync();
+        if (warp >= 2) {
+            // CTA `rank` joins the rows rank, rank + split, ... of A, over the CTAs in order
+            const int e = threadIdx.x - 64, n = e % 128;
+            const uint32_t mine = tc::smem_addr(red);
+            const int rows = min(NT, p.M - t0);
+            for (int t = rank + (e / 128) * split; t < rows; t += split * (C::EW / 4)) {
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; q++) {
+                    v[q] = 0.f;
+                    if (q < split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(in_cta(mine + (t * 128 + n) * 4, q)));
+                }
+                float sum = v[0];
+#pragma unroll
+                for (int q = 1; q < 8; q++) sum += v[q];
+                if (n0 + n < p.N) store_out(p.out, static_cast<int64_t>(t0 + t) * p.ld_out + n0 + n, p.out_dtype, sum);
+            }
+        }
+        cluster_sync();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc<C::NBUF * NT>(tmem);
+}
+
+// ---- many rows of A -----------------------------------------------------------------------
+
+struct Wide {
+    static constexpr int EW = 8;
+    static constexpr int THREADS = 128 + EW * 32;    // four warps that copy, issue or idle, then the epilogue's
+    // registers per thread: 384 * 168 at launch = 128 * 72 + 256 * 216
+    static constexpr int REGS_CONTROL = 72, REGS_EPILOGUE = 216;
+    static constexpr int STAGE = 2 * 128 * BK;       // per CTA: its 128 rows of A and its 128 rows of W
+    static constexpr int STAGES = 6;
+    static constexpr int SMEM = 1024 + STAGES * STAGE;
+};
+
+struct Tiles {
+    int m, n;          // tiles of 256
+    int band;          // tiles of A that are walked together over all of W, so that W stays in L2
+};
+
+__device__ __forceinline__ void tile_at(const Tiles &t, int i, int *tm, int *tn)
+{
+    const int per = t.band * t.n, b = i / per, r = i % per;
+    const int h = min(t.band, t.m - b * t.band);
+    *tm = b * t.band + r % h;
+    *tn = r / h;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
+wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Fp8Params p,
+            const Tiles tiles)
+{
+    using C = Wide;
+    extern __shared__ unsigned char dyn[];
+    __shared__ uint64_t bars[2 * C::STAGES + 4];
+    __shared__ uint32_t tmem_base;
+    const uint32_t ring = (tc::smem_addr(dyn) + 1023u) & ~1023u;
+    const uint32_t b0 = tc::smem_addr(bars);
+    auto full = [&](int s) { return b0 + s * 8; };
+    auto empty = [&](int s) { return b0 + (C::STAGES + s) * 8; };
+    auto tfull = [&](int b) { return b0 + (2 * C::STAGES + b) * 8; };
+    auto tempty = [&](int b) { return b0 + (2 * C::STAGES + 2 + b) * 8; };
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
+        for (int b = 0; b < 2; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), 2 * C::EW); }
+        tc::prefetch_tensormap(&tm_w);
+        tc::prefetch_tensormap(&tm_a);
+    }
+    pdl_wait();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(tc::smem_addr(&tmem_base)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after_sync();
+    pdl_release();
+
+    const uint32_t tmem = tmem_base;
+    const int groups = (p.K + BK - 1) / BK;
+    const int total = tiles.m * tiles.n, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::REGS_CONTROL));
+        if (warp == 0) {
+            if (lane == 0) {
+                int s = 0;
+                uint32_t phase = 1;
+                bool ok = true;
+                for (int i = pair; i < total && ok; i += pairs) {
+                    int tm, tn;
+                    tile_at(tiles, i, &tm, &tn);
+                    const int m0 = tm * 256 + rank * 128, n0 = tn * 256 + rank * 128;
+                    for (int g = 0; g < groups; g++) {
+                        if (!tc::mbar_wait(empty(s), phase)) { report(p); ok = false; break; }
+                        // both CTAs' copies are counted on the barrier of the one that issues the MMAs
+                        if (rank == 0) tc::mbar_expect_tx(full(s), 2 * C::STAGE);
+                        const uint32_t at = ring + s * C::STAGE, bar = in_cta(full(s), 0);
+                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                                     " [%0], [%1, {%2, %3}], [%4];" :: "r"(at), "l"(&tm_a), "r"(g * BK), "r"(m0), "r"(bar) : "memory");
+                        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                                     " [%0], [%1, {%2, %3}], [%4];" :: "r"(at + 128 * BK), "l"(&tm_w), "r"(g * BK), "r"(n0), "r"(bar) : "memory");
+                        if (++s == C::STAGES) { s = 0; phase ^= 1; }
+                    }
+                }
+                // the last arrivals on this CTA's barriers come from the pair's other CTA: not before them does it end
+                for (int k = 0; k < C::STAGES && ok; k++) {
+                    if (!tc::mbar_wait(empty(s), phase)) { report(p); ok = false; }
+                    if (++s == C::STAGES) { s = 0; phase ^= 1; }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                constexpr uint32_t ID = tc::instr_desc(0, 256, 256);
+                int s = 0, b = 0;
+                uint32_t phase = 0, tphase = 1;
+                bool ok = true;
+                for (int i = pair; i < total && ok; i += pairs)
+                    for (int g = 0; g < groups; g++) {
+                        if (!tc::mbar_wait(tempty(b), tphase) || !tc::mbar_wait(full(s), phase)) { report(p); ok = false; break; }
+                        tc::fence_after_sync();
+                        const uint32_t at = ring + s * C::STAGE;
+                        mma_group<2>(tmem + b * 256, at, at + 128 * BK, ID);
+                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                                     :: "r"(empty(s)), "h"(static_cast<uint16_t>(3)) : "memory");
+                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                                     :: "r"(tfull(b)), "h"(static_cast<uint16_t>(3)) : "memory");
+                        if (++s == C::STAGES) { s = 0; phase ^= 1; }
+                        if (++b == 2) { b = 0; tphase ^= 1; }
+                    }
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::REGS_EPILOGUE));
+        const int quarter = warp % 4, half = (warp - 4) / 4;      // TMEM lanes, columns of the tile
+        int b = 0;
+        uint32_t tphase = 0;
+        bool ok = true;
+        for (int i = pair; i < total && ok; i += pairs) {
+            int tm, tn;
+            tile_at(tiles, i, &tm, &tn);
+            const int64_t m = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32 + lane;
+            const int64_t n0 = static_cast<int64_t>(tn) * 256 + half * 128;
+            const bool live = m < p.M && n0 < p.N;
+            const float *sa = p.sa + (live ? m : 0) * p.sa_row, *sw = p.sw + (live ? n0 / 128 : 0) * p.sw_row;
+            float2 acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; c++) acc[c] = make_float2(0.f, 0.f);
+            float next = *sa * *sw;
+            for (int g = 0; g < groups; g++) {
+                const float f = next;
+                if (g + 1 < groups) next = sa[(g + 1) * p.sa_group] * sw[(g + 1) * p.sw_group];
+                if (!tc::mbar_wait(tfull(b), tphase)) { ok = false; break; }
+                tc::fence_after_sync();
+                const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * 256 + half * 128;
+                const float2 f2 = make_float2(f, f);
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t v[32];
+                    tmem_ld32(at + c * 32, v);
+                    tc::tmem_ld_wait();
+                    if (c == 3) {
+                        tc::fence_before_sync();
+                        if (lane == 0) arrive_cluster(in_cta(tempty(b), 0));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        acc[c * 16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f2, acc[c * 16 + j]);
+                }
+                if (++b == 2) { b = 0; tphase ^= 1; }
+            }
+            if (!ok) { report(p); break; }
+            if (!live) continue;
+            const int es = p.out_dtype == 2 ? 4 : 2;
+            unsigned char *o = static_cast<unsigned char *>(p.out) + (m * p.ld_out + n0) * es;
+            if (n0 + 128 <= p.N && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+                if (p.out_dtype == 2) {
+#pragma unroll
+                    for (int c = 0; c < 32; c++)
+                        reinterpret_cast<float4 *>(o)[c] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; c++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float2 x = acc[4 * c + j];
+                            if (p.out_dtype == 0) w[j] = pack_bf16x2(x.x, x.y);
+                            else w[j] = tc::pack_f16x2(x.x, x.y);
+                        }
+                        reinterpret_cast<uint4 *>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; c++)
+                    if (n0 + c < p.N) store_out(p.out, m * p.ld_out + n0 + c, p.out_dtype, c % 2 ? acc[c / 2].y : acc[c / 2].x);
+            }
+        }
+    }
+    tc::fence_before_sync();
+    cluster_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+}
+
+// ---- any strides and alignments -----------------------------------------------------------
 
 // e4m3 -> fp32 (exact)
 __device__ __forceinline__ float e4m3_to_f32(uint8_t v)
@@ -19,16 +471,8 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t v)
     return __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
 }
 
-__device__ __forceinline__ void store_out(void *out, int64_t i, int dtype, float v)
-{
-    if (dtype == 0) static_cast<uint16_t *>(out)[i] = f32_to_bf16(v);
-    else if (dtype == 1) static_cast<__half *>(out)[i] = __float2half_rn(v);
-    else static_cast<float *>(out)[i] = v;
-}
-
-// Any strides and alignments: 64 x 64 tiles on the ordinary FMA units.
 constexpr int GT = 64, GK = 32;
-__global__ void __launch_bounds__(256) fp8_general_kernel(const Fp8Params p, int tiles_n)
+__global__ void __launch_bounds__(256) general_kernel(const Fp8Params p, int tiles_n)
 {
     __shared__ float sA[GK][GT + 1], sB[GK][GT + 1];
     pdl_wait_then_release();
@@ -75,13 +519,116 @@ __global__ void __launch_bounds__(256) fp8_general_kernel(const Fp8Params p, int
         }
 }
 
+// ---- host ---------------------------------------------------------------------------------
+
+// cuTensorMapEncodeTiled, fetched once through the runtime
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// A map over `rows` rows of `cols` bytes at a pitch of `ld` bytes, read in boxes of `box` rows x
+// 128 bytes with the 128-byte swizzle.
+cudaError_t encode(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int box)
+{
+    const auto enc = encoder();
+    if (!enc) return cudaErrorSymbolNotFound;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t boxes[2] = {BK, static_cast<cuuint32_t>(box)};
+    const cuuint32_t es[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// TMA's conditions; a single row has no pitch of its own.
+bool tma_rows(const void *base, int64_t *ld, int64_t rows, int64_t cols)
+{
+    if (rows == 1) *ld = (cols + 15) / 16 * 16;
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && *ld % 16 == 0 && *ld < (int64_t(1) << 40);
+}
+
+template <int NT>
+cudaError_t run_thin(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int split, cudaStream_t stream)
+{
+    using C = Thin<NT>;
+    CUtensorMap tw, ta;
+    cudaError_t e;
+    if ((e = encode(&tw, p.w, p.K, p.N, ld_w, 128)) != cudaSuccess) return e;
+    if ((e = encode(&ta, p.a, p.K, p.M, ld_a, NT)) != cudaSuccess) return e;
+    static const cudaError_t attr = cudaFuncSetAttribute(thin_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (attr != cudaSuccess) return attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.N) + 127) / 128 * split), static_cast<unsigned>((p.M + NT - 1) / NT));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, thin_kernel<NT>, tw, ta, p, split);
+}
+
+cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cudaStream_t stream)
+{
+    CUtensorMap tw, ta;
+    cudaError_t e;
+    if ((e = encode(&tw, p.w, p.K, p.N, ld_w, 128)) != cudaSuccess) return e;
+    if ((e = encode(&ta, p.a, p.K, p.M, ld_a, 128)) != cudaSuccess) return e;
+    static const cudaError_t attr = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::SMEM);
+    if (attr != cudaSuccess) return attr;
+    const Tiles t{(p.M + 255) / 256, (p.N + 255) / 256, 16};
+    const int64_t total = static_cast<int64_t>(t.m) * t.n;
+    if (total > INT32_MAX - 4096) return cudaErrorInvalidConfiguration;
+    const int pairs = static_cast<int>(total < sms / 2 ? total : sms / 2);
+    return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, p, t);
+}
+
+cudaError_t sm_count(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
 {
-    const int64_t tm = (static_cast<int64_t>(p.M) + GT - 1) / GT, tn = (static_cast<int64_t>(p.N) + GT - 1) / GT;
-    if (tm * tn > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_pdl(fp8_general_kernel, dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, p, static_cast<int>(tn));
+    int64_t ld_a = p.ld_a, ld_w = p.ld_w;
+    if (p.K == 0 || !tma_rows(p.a, &ld_a, p.M, p.K) || !tma_rows(p.w, &ld_w, p.N, p.K)) {
+        const int64_t tm = (static_cast<int64_t>(p.M) + GT - 1) / GT, tn = (static_cast<int64_t>(p.N) + GT - 1) / GT;
+        if (tm * tn > INT32_MAX) return cudaErrorInvalidConfiguration;
+        return launch_pdl(general_kernel, dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, p, static_cast<int>(tn));
+    }
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    if (p.M > 256) return run_wide(p, ld_a, ld_w, sms, stream);
+    // split the inner axis until two CTAs per SM are running
+    const int groups = (p.K + BK - 1) / BK;
+    const int64_t tiles = (static_cast<int64_t>(p.N) + 127) / 128 * ((p.M + 127) / 128);
+    int split = 1;
+    while (split < 8 && split < groups && tiles * (split + 1) <= 2 * sms) split++;
+    if (p.M <= 16) return run_thin<16>(p, ld_a, ld_w, split, stream);
+    if (p.M <= 32) return run_thin<32>(p, ld_a, ld_w, split, stream);
+    if (p.M <= 64) return run_thin<64>(p, ld_a, ld_w, split, stream);
+    return run_thin<128>(p, ld_a, ld_w, split, stream);
 }
 
 }  // namespace kda
