@@ -60,6 +60,24 @@ __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint32_t b, ui
     }
 }
 
+// Waits for the mbarrier phase with the given parity; gives up after 4e9 clocks (~2 s). The
+// clock is read only every 64 tries: a wait here is on the path from one group to the next.
+__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity)
+{
+    long long start = 0;
+    for (uint32_t it = 1;; it++) {
+        uint32_t ok;
+        asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                     " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity) : "memory");
+        if (ok) return true;
+        if (it % 64 == 0) {
+            const long long now = clock64();
+            if (it == 64) start = now;
+            else if (now - start > 4000000000ll) return false;
+        }
+    }
+}
+
 // 32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -89,13 +107,21 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
+// Arrival on a barrier of any CTA of the cluster. What it orders are the reads of tensor memory,
+// by the tcgen05 fence in front of it; a release at cluster scope would wait for every
+// access of the thread each time (a third of the kernel's time, measured).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void arrive_local(uint32_t mbar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(mbar) : "memory");
+}
+// 4-byte asynchronous global -> shared copy
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -170,7 +196,7 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
         if (lane == 0) {
             for (int g = g0, i = 0; g < g1; g++, i++) {
                 const int s = i % C::STAGES;
-                if (i >= C::STAGES && !tc::mbar_wait(empty(s), ((i / C::STAGES) - 1) & 1)) { report(p); break; }
+                if (i >= C::STAGES && !wait_phase(empty(s), ((i / C::STAGES) - 1) & 1)) { report(p); break; }
                 const uint32_t at = ring + s * C::STAGE;
                 tc::mbar_expect_tx(full(s), C::STAGE);
                 tc::tma_load_2d(at, &tm_w, g * BK, n0, full(s));
@@ -183,8 +209,8 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
             constexpr uint32_t ID = tc::instr_desc(0, 128, NT);
             for (int g = g0, i = 0; g < g1; g++, i++) {
                 const int s = i % C::STAGES, b = i % C::NBUF;
-                if (i >= C::NBUF && !tc::mbar_wait(tempty(b), ((i / C::NBUF) - 1) & 1)) { report(p); break; }
-                if (!tc::mbar_wait(full(s), (i / C::STAGES) & 1)) { report(p); break; }
+                if (i >= C::NBUF && !wait_phase(tempty(b), ((i / C::NBUF) - 1) & 1)) { report(p); break; }
+                if (!wait_phase(full(s), (i / C::STAGES) & 1)) { report(p); break; }
                 tc::fence_after_sync();
                 const uint32_t at = ring + s * C::STAGE;
                 mma_group<1>(tmem + b * NT, at, at + 128 * BK, ID);
@@ -212,7 +238,7 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
             asm volatile("bar.sync 1, %0;" :: "n"(C::EW * 32) : "memory");
             if (e < NT) scales[(i + 1) % 4][e] = next;
             next = factor(g + 2);
-            if (ok && !tc::mbar_wait(tfull(b), (i / C::NBUF) & 1)) ok = false;
+            if (ok && !wait_phase(tfull(b), (i / C::NBUF) & 1)) ok = false;
             tc::fence_after_sync();
             const float4 *f4 = reinterpret_cast<const float4 *>(&scales[i % 4][c0]);
             const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * NT + c0;
@@ -277,14 +303,20 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
 // ---- many rows of A -----------------------------------------------------------------------
 
 struct Wide {
-    static constexpr int EW = 8;
-    static constexpr int THREADS = 128 + EW * 32;    // four warps that copy, issue or idle, then the epilogue's
-    // registers per thread: 384 * 168 at launch = 128 * 72 + 256 * 216
-    static constexpr int REGS_CONTROL = 72, REGS_EPILOGUE = 216;
+    static constexpr int EW = 16;                    // epilogue warps: four for each quarter of the TMEM lanes
+    static constexpr int COLS = 256 * 4 / EW;        // columns of the tile per epilogue thread
+    static constexpr int THREADS = 128 + EW * 32;    // copies, MMAs, scales, one idle warp, then the epilogue's
+    // registers per thread: 640 * 96 at launch = 128 * 32 + 512 * 112
+    static constexpr int REGS_CONTROL = 32, REGS_EPILOGUE = 112;
     static constexpr int STAGE = 2 * 128 * BK;       // per CTA: its 128 rows of A and its 128 rows of W
-    static constexpr int STAGES = 6;
-    static constexpr int SMEM = 1024 + STAGES * STAGE;
+    static constexpr int STAGES = 5;
+    static constexpr int BOX = 32 * 128;             // an epilogue warp's outputs on their way to memory: 32 rows of 128 bytes
+    static constexpr int SR = 4;                     // groups of scales in flight: 128 rows' and the tile's two of W
+    static constexpr int SCALES = SR * 132 * 4;
+    static constexpr int BARS = (2 * STAGES + 4 + 2 * SR) * 8;
+    static constexpr int SMEM = STAGES * STAGE + EW * BOX + SCALES + BARS + 16;
 };
+static_assert(Wide::SMEM <= 227 * 1024, "shared memory of one CTA");
 
 struct Tiles {
     int m, n;          // tiles of 256
@@ -300,30 +332,34 @@ __device__ __forceinline__ void tile_at(const Tiles &t, int i, int *tm, int *tn)
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
-wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Fp8Params p,
-            const Tiles tiles)
+wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+            const __grid_constant__ CUtensorMap tm_out, const bool tma_out, const Fp8Params p, const Tiles tiles)
 {
     using C = Wide;
-    extern __shared__ unsigned char dyn[];
-    __shared__ uint64_t bars[2 * C::STAGES + 4];
-    __shared__ uint32_t tmem_base;
-    const uint32_t ring = (tc::smem_addr(dyn) + 1023u) & ~1023u;
-    const uint32_t b0 = tc::smem_addr(bars);
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    const uint32_t ring = tc::smem_addr(dyn);
+    float *scales = reinterpret_cast<float *>(dyn + C::STAGES * C::STAGE + C::EW * C::BOX);   // [SR][128 | 2]
+    const uint32_t b0 = tc::smem_addr(scales) + C::SCALES;
+    volatile uint32_t *tmem_base = reinterpret_cast<uint32_t *>(dyn + C::SMEM - 16);
     auto full = [&](int s) { return b0 + s * 8; };
     auto empty = [&](int s) { return b0 + (C::STAGES + s) * 8; };
     auto tfull = [&](int b) { return b0 + (2 * C::STAGES + b) * 8; };
     auto tempty = [&](int b) { return b0 + (2 * C::STAGES + 2 + b) * 8; };
+    auto sfull = [&](int r) { return b0 + (2 * C::STAGES + 4 + r) * 8; };
+    auto sempty = [&](int r) { return b0 + (2 * C::STAGES + 4 + C::SR + r) * 8; };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
         for (int b = 0; b < 2; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), 2 * C::EW); }
+        for (int r = 0; r < C::SR; r++) { tc::mbar_init(sfull(r), 32); tc::mbar_init(sempty(r), C::EW); }
         tc::prefetch_tensormap(&tm_w);
         tc::prefetch_tensormap(&tm_a);
+        if (tma_out) tc::prefetch_tensormap(&tm_out);
     }
     pdl_wait();
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(tc::smem_addr(&tmem_base)) : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(b0 + C::BARS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc::fence_before_sync();
@@ -332,7 +368,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     tc::fence_after_sync();
     pdl_release();
 
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = *tmem_base;
     const int groups = (p.K + BK - 1) / BK;
     const int total = tiles.m * tiles.n, pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     if (warp < 4) {
@@ -347,7 +383,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                     tile_at(tiles, i, &tm, &tn);
                     const int m0 = tm * 256 + rank * 128, n0 = tn * 256 + rank * 128;
                     for (int g = 0; g < groups; g++) {
-                        if (!tc::mbar_wait(empty(s), phase)) { report(p); ok = false; break; }
+                        if (!wait_phase(empty(s), phase)) { report(p); ok = false; break; }
                         // both CTAs' copies are counted on the barrier of the one that issues the MMAs
                         if (rank == 0) tc::mbar_expect_tx(full(s), 2 * C::STAGE);
                         const uint32_t at = ring + s * C::STAGE, bar = in_cta(full(s), 0);
@@ -360,7 +396,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 }
                 // the last arrivals on this CTA's barriers come from the pair's other CTA: not before them does it end
                 for (int k = 0; k < C::STAGES && ok; k++) {
-                    if (!tc::mbar_wait(empty(s), phase)) { report(p); ok = false; }
+                    if (!wait_phase(empty(s), phase)) { report(p); ok = false; }
                     if (++s == C::STAGES) { s = 0; phase ^= 1; }
                 }
             }
@@ -373,7 +409,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 bool ok = true;
                 for (int i = pair; i < total && ok; i += pairs)
                     for (int g = 0; g < groups; g++) {
-                        if (!tc::mbar_wait(tempty(b), tphase) || !tc::mbar_wait(full(s), phase)) { report(p); ok = false; break; }
+                        if (!wait_phase(tempty(b), tphase) || !wait_phase(full(s), phase)) { report(p); ok = false; break; }
                         tc::fence_after_sync();
                         const uint32_t at = ring + s * C::STAGE;
                         mma_group<2>(tmem + b * 256, at, at + 128 * BK, ID);
@@ -386,74 +422,120 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                     }
             }
             __syncwarp();
+        } else if (warp == 2) {
+            // the groups' scales, copied while the tensor core is groups behind
+            int r = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int i = pair; i < total && ok; i += pairs) {
+                int tm, tn;
+                tile_at(tiles, i, &tm, &tn);
+                const int m0 = tm * 256 + rank * 128 + lane, nb = tn * 2;
+                const float *sa = p.sa + m0 * p.sa_row, *sw = p.sw + (nb + (lane & 1)) * p.sw_row;
+                const bool w_in = lane < 2 && (nb + lane) * 128 < p.N;
+                for (int g = 0; g < groups; g++) {
+                    if (!wait_phase(sempty(r), phase)) { report(p); ok = false; break; }
+                    const uint32_t at = tc::smem_addr(scales + r * 132);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (m0 + 32 * j < p.M) cp_async4(at + (lane + 32 * j) * 4, sa + 32 * j * p.sa_row);
+                    if (w_in) cp_async4(at + (128 + lane) * 4, sw);
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(r)) : "memory");
+                    sa += p.sa_group;
+                    sw += p.sw_group;
+                    if (++r == C::SR) { r = 0; phase ^= 1; }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::REGS_EPILOGUE));
-        const int quarter = warp % 4, half = (warp - 4) / 4;      // TMEM lanes, columns of the tile
-        int b = 0;
-        uint32_t tphase = 0;
-        bool ok = true;
-        for (int i = pair; i < total && ok; i += pairs) {
-            int tm, tn;
-            tile_at(tiles, i, &tm, &tn);
-            const int64_t m = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32 + lane;
-            const int64_t n0 = static_cast<int64_t>(tn) * 256 + half * 128;
-            const bool live = m < p.M && n0 < p.N;
-            const float *sa = p.sa + (live ? m : 0) * p.sa_row, *sw = p.sw + (live ? n0 / 128 : 0) * p.sw_row;
-            float2 acc[64];
+        const int quarter = warp % 4, c0 = (warp - 4) / 4 * C::COLS;      // TMEM lanes, columns of the tile
+        const int row = quarter * 32 + lane;
+        unsigned char *box = dyn + C::STAGES * C::STAGE + (warp - 4) * C::BOX;
+        int b = 0, r = 0;
+        uint32_t tphase = 0, sphase = 0;
+        for (int i = pair; i < total; i += pairs) {
+            float2 acc[C::COLS / 2];
 #pragma unroll
-            for (int c = 0; c < 64; c++) acc[c] = make_float2(0.f, 0.f);
-            float next = *sa * *sw;
+            for (int c = 0; c < C::COLS / 2; c++) acc[c] = make_float2(0.f, 0.f);
+            bool ok = true;
             for (int g = 0; g < groups; g++) {
-                const float f = next;
-                if (g + 1 < groups) next = sa[(g + 1) * p.sa_group] * sw[(g + 1) * p.sw_group];
-                if (!tc::mbar_wait(tfull(b), tphase)) { ok = false; break; }
+                if (!wait_phase(sfull(r), sphase)) { ok = false; break; }
+                const float s = scales[r * 132 + row] * scales[r * 132 + 128 + c0 / 128];
+                const float2 f = make_float2(s, s);
+                if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
                 tc::fence_after_sync();
-                const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * 256 + half * 128;
-                const float2 f2 = make_float2(f, f);
+                const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * 256 + c0;
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
+                for (int c = 0; c < C::COLS / 32; c++) {
                     uint32_t v[32];
                     tmem_ld32(at + c * 32, v);
                     tc::tmem_ld_wait();
-                    if (c == 3) {
+                    if (c == C::COLS / 32 - 1) {
                         tc::fence_before_sync();
-                        if (lane == 0) arrive_cluster(in_cta(tempty(b), 0));
+                        if (lane == 0) {
+                            arrive_cluster(in_cta(tempty(b), 0));
+                            arrive_local(sempty(r));
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        acc[c * 16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f2, acc[c * 16 + j]);
+                        acc[c * 16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[c * 16 + j]);
                 }
                 if (++b == 2) { b = 0; tphase ^= 1; }
+                if (++r == C::SR) { r = 0; sphase ^= 1; }
             }
             if (!ok) { report(p); break; }
-            if (!live) continue;
-            const int es = p.out_dtype == 2 ? 4 : 2;
-            unsigned char *o = static_cast<unsigned char *>(p.out) + (m * p.ld_out + n0) * es;
-            if (n0 + 128 <= p.N && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+            int tm, tn;
+            tile_at(tiles, i, &tm, &tn);
+            const int m0 = tm * 256 + rank * 128 + quarter * 32, n0 = tn * 256 + c0;   // of this warp's box
+            if (m0 >= p.M || n0 >= p.N) continue;
+            if (tma_out) {
+                // 32 rows of 128 bytes with the map's swizzle (16-byte piece j of row l at j ^ (l % 8)),
+                // written by TMA, which leaves out what lies past the matrix
+                auto put = [&](const uint32_t (&w)[32], int x) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane % 8)) * 16)) =
+                            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                                     :: "l"(&tm_out), "r"(x), "r"(m0), "r"(tc::smem_addr(box)) : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                };
                 if (p.out_dtype == 2) {
 #pragma unroll
-                    for (int c = 0; c < 32; c++)
-                        reinterpret_cast<float4 *>(o)[c] = make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x, acc[2 * c + 1].y);
-                } else {
+                    for (int h = 0; h < C::COLS / 32; h++) {
+                        uint32_t w[32];
 #pragma unroll
-                    for (int c = 0; c < 16; c++) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const float2 x = acc[4 * c + j];
-                            if (p.out_dtype == 0) w[j] = pack_bf16x2(x.x, x.y);
-                            else w[j] = tc::pack_f16x2(x.x, x.y);
+                        for (int j = 0; j < 16; j++) {
+                            w[2 * j] = __float_as_uint(acc[16 * h + j].x);
+                            w[2 * j + 1] = __float_as_uint(acc[16 * h + j].y);
                         }
-                        reinterpret_cast<uint4 *>(o)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (n0 + 32 * h < p.N) put(w, n0 + 32 * h);
                     }
-                }
-            } else {
+                } else {
+                    uint32_t w[32];
 #pragma unroll
-                for (int c = 0; c < 128; c++)
-                    if (n0 + c < p.N) store_out(p.out, m * p.ld_out + n0 + c, p.out_dtype, c % 2 ? acc[c / 2].y : acc[c / 2].x);
+                    for (int j = 0; j < 32; j++)
+                        w[j] = p.out_dtype == 0 ? pack_bf16x2(acc[j].x, acc[j].y) : tc::pack_f16x2(acc[j].x, acc[j].y);
+                    put(w, n0);
+                }
+            } else if (m0 + lane < p.M) {
+#pragma unroll
+                for (int c = 0; c < C::COLS; c++)
+                    if (n0 + c < p.N)
+                        store_out(p.out, static_cast<int64_t>(m0 + lane) * p.ld_out + n0 + c, p.out_dtype, c % 2 ? acc[c / 2].y : acc[c / 2].x);
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc::fence_before_sync();
     cluster_sync();
@@ -535,17 +617,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return fn;
 }
 
-// A map over `rows` rows of `cols` bytes at a pitch of `ld` bytes, read in boxes of `box` rows x
-// 128 bytes with the 128-byte swizzle.
-cudaError_t encode(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int box)
+// A map over `rows` rows of `cols` elements of `es` bytes at a pitch of `ld` elements, moved in
+// boxes of `box` rows x 128 bytes with the 128-byte swizzle.
+cudaError_t encode(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t ld, int box,
+                   CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8, int es = 1)
 {
     const auto enc = encoder();
     if (!enc) return cudaErrorSymbolNotFound;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-    const cuuint32_t boxes[2] = {BK, static_cast<cuuint32_t>(box)};
-    const cuuint32_t es[2] = {1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes, es,
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box)};
+    const cuuint32_t steps[2] = {1, 1};
+    const CUresult r = enc(m, type, 2, const_cast<void *>(base), dims, strides, boxes, steps,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -555,7 +638,7 @@ cudaError_t encode(CUtensorMap *m, const void *base, int64_t cols, int64_t rows,
 bool tma_rows(const void *base, int64_t *ld, int64_t rows, int64_t cols)
 {
     if (rows == 1) *ld = (cols + 15) / 16 * 16;
-    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && *ld % 16 == 0 && *ld < (int64_t(1) << 40);
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && *ld % 16 == 0 && *ld < (int64_t(1) << 39);
 }
 
 template <int NT>
@@ -585,17 +668,22 @@ cudaError_t run_thin(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int split, 
 
 cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cudaStream_t stream)
 {
-    CUtensorMap tw, ta;
+    CUtensorMap tw, ta, to = {};
     cudaError_t e;
     if ((e = encode(&tw, p.w, p.K, p.N, ld_w, 128)) != cudaSuccess) return e;
     if ((e = encode(&ta, p.a, p.K, p.M, ld_a, 128)) != cudaSuccess) return e;
+    const int es = p.out_dtype == 2 ? 4 : 2;
+    const bool tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld_out * es % 16 == 0 && p.ld_out < (int64_t(1) << 38);
+    const CUtensorMapDataType type = p.out_dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : p.out_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    if (tma_out && (e = encode(&to, p.out, p.N, p.M, p.ld_out, 32, type, es)) != cudaSuccess) return e;
     static const cudaError_t attr = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::SMEM);
     if (attr != cudaSuccess) return attr;
     const Tiles t{(p.M + 255) / 256, (p.N + 255) / 256, 16};
     const int64_t total = static_cast<int64_t>(t.m) * t.n;
     if (total > INT32_MAX - 4096) return cudaErrorInvalidConfiguration;
     const int pairs = static_cast<int>(total < sms / 2 ? total : sms / 2);
-    return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, p, t);
+    return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, to, tma_out, p, t);
 }
 
 cudaError_t sm_count(int *sms)
