@@ -78,6 +78,21 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity)
     }
 }
 
+// An arrival on the barrier at this place in both CTAs of the pair once its MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t mbar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(mbar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // 32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -402,21 +417,23 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             }
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 constexpr uint32_t ID = tc::instr_desc(0, 256, 256);
                 int s = 0, b = 0;
                 uint32_t phase = 0, tphase = 1;
                 bool ok = true;
                 for (int i = pair; i < total && ok; i += pairs)
                     for (int g = 0; g < groups; g++) {
-                        if (!wait_phase(tempty(b), tphase) || !wait_phase(full(s), phase)) { report(p); ok = false; break; }
+                        if (!wait_phase(tempty(b), tphase) || !wait_phase(full(s), phase)) ok = false;
+                        if (!__all_sync(0xffffffffu, ok)) { report(p); ok = false; break; }
                         tc::fence_after_sync();
                         const uint32_t at = ring + s * C::STAGE;
-                        mma_group<2>(tmem + b * 256, at, at + 128 * BK, ID);
-                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                                     :: "r"(empty(s)), "h"(static_cast<uint16_t>(3)) : "memory");
-                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                                     :: "r"(tfull(b)), "h"(static_cast<uint16_t>(3)) : "memory");
+                        if (elect_one()) {
+                            mma_group<2>(tmem + b * 256, at, at + 128 * BK, ID);
+                            commit_pair(empty(s));
+                            commit_pair(tfull(b));
+                        }
+                        __syncwarp();
                         if (++s == C::STAGES) { s = 0; phase ^= 1; }
                         if (++b == 2) { b = 0; tphase ^= 1; }
                     }
