@@ -35,29 +35,35 @@ namespace {
 
 // Matrix descriptor of a K-major tile of 128-byte rows with the 128-byte swizzle: groups of 8
 // rows follow each other at 1024 bytes; the tile starts on a 1024-byte boundary. One MMA step
-// of 32 k is 32 bytes further.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr)
+// of 32 k is 32 bytes further. `at16`: shared-memory address / 16.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t at16)
 {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+    constexpr uint32_t HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return static_cast<uint64_t>(HIGH) << 32 | (1u << 16) | at16;
 }
 
-// D (+)= A B^T of one group of 128 k, e4m3 operands (format 0 of kind::f8f6f4), fp32 sums.
+// D (+)= A B^T of 32 k, e4m3 operands (format 0 of kind::f8f6f4), fp32 sums.
+template <int CG, bool ADD>
+__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
+{
+    if (CG == 1)
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                     " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0));
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                     " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                     :: "r"(d), "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0));
+}
+
+// D = A B^T of one group of 128 k.
 template <int CG>
 __device__ __forceinline__ void mma_group(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
 {
+    const uint32_t a16 = a >> 4, b16 = b >> 4;
+    mma_step<CG, false>(d, desc_sw128(a16), desc_sw128(b16), idesc);
 #pragma unroll
-    for (int s = 0; s < 4; s++) {
-        const uint64_t da = desc_sw128(a) + s * 2, db = desc_sw128(b) + s * 2;
-        if (CG == 1)
-            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                         :: "r"(d), "l"(da), "l"(db), "r"(idesc), "r"(s > 0 ? 1u : 0u));
-        else
-            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                         " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                         :: "r"(d), "l"(da), "l"(db), "r"(idesc), "r"(s > 0 ? 1u : 0u));
-    }
+    for (int s = 1; s < 4; s++) mma_step<CG, true>(d, desc_sw128(a16 + 2 * s), desc_sw128(b16 + 2 * s), idesc);
 }
 
 // Waits for the mbarrier phase with the given parity; gives up after 4e9 clocks (~2 s). The
@@ -424,7 +430,8 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 bool ok = true;
                 for (int i = pair; i < total && ok; i += pairs)
                     for (int g = 0; g < groups; g++) {
-                        if (!wait_phase(tempty(b), tphase) || !wait_phase(full(s), phase)) ok = false;
+                        // the accumulator last: what follows it is on the way from one group to the next
+                        if (!wait_phase(full(s), phase) || !wait_phase(tempty(b), tphase)) ok = false;
                         if (!__all_sync(0xffffffffu, ok)) { report(p); ok = false; break; }
                         tc::fence_after_sync();
                         const uint32_t at = ring + s * C::STAGE;
