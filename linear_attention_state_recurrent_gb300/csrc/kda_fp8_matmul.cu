@@ -11,9 +11,9 @@
 // Two arrangements:
 //  - wide_kernel: tiles of 256 rows of A x 256 of W by a pair of CTAs (cta_group::2), persistent.
 //    A thread of the epilogue holds one row of out, so its two scales are one factor per group.
-//  - thin_kernel: 128 rows of W (the MMA's M side) x up to 128 rows of A, for few rows of A: the
-//    weights stream through at HBM's rate; the inner axis is split over a cluster whose CTAs
-//    join their sums through distributed shared memory in a fixed order.
+//  - slim_kernel: up to 128 rows of A x a tile of W that makes the CTAs fill the GPU once: the
+//    weights stream through at HBM's rate. The inner axis may be split over a cluster whose CTAs join
+//    their sums through distributed shared memory in a fixed order.
 // Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
 #include <climits>
 #include <cstdint>
@@ -99,6 +99,15 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Whether the phase with the given parity is over, without waiting.
+__device__ __forceinline__ bool test_phase(uint32_t mbar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity) : "memory");
+    return ok;
+}
+
 // 32 columns of this thread's TMEM lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -161,29 +170,33 @@ __device__ __forceinline__ void report(const Fp8Params &p)
 
 constexpr int BK = 128;                       // bytes (= k) per group
 
-// ---- few rows of A ------------------------------------------------------------------------
+// ---- a handful of rows of A ---------------------------------------------------------------
 
+// 128 rows of W are the MMA's M side and NT rows of A its N side, so that all four quarters of
+// the TMEM lanes have work and an epilogue thread holds only NT (or NT / 2) sums: its time per
+// group is what the stream of weights would otherwise wait for.
 template <int NT>
 struct Thin {
-    static constexpr int EW = NT > 64 ? 8 : 4;              // epilogue warps
-    static constexpr int THREADS = 64 + EW * 32;
+    static constexpr int EW = NT > 32 ? 8 : 4;              // epilogue warps
+    static constexpr int THREADS = 128 + EW * 32;           // copies, MMAs, scales, one idle warp, then the epilogue's
     static constexpr int COLS = NT * 4 / EW;                // columns (rows of A) per epilogue thread
-    static constexpr int NBUF = NT > 64 ? 2 : 4;            // accumulators in tensor memory
+    static constexpr int NBUF = 4;                          // accumulators in tensor memory
     static constexpr int STAGE = 128 * BK + NT * BK;
-    static constexpr int STAGES = NT > 64 ? 3 : NT > 32 ? 4 : 5;
+    static constexpr int STAGES = NT > 32 ? 4 : 5;
+    static constexpr int SR = 8, SLOT = NT + 4;             // groups of scales in flight: NT rows' and the tile's of W
     static constexpr int SMEM = 1024 + STAGES * STAGE;      // two CTAs per SM
 };
 
 template <int NT>
 __global__ void __launch_bounds__(Thin<NT>::THREADS, 2)
-thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Fp8Params p,
+thin_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Fp8Params p,
             const int split)
 {
     using C = Thin<NT>;
-    extern __shared__ unsigned char dyn[];
-    __shared__ uint64_t bars[2 * C::STAGES + 2 * C::NBUF];
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    __shared__ uint64_t bars[2 * C::STAGES + 2 * C::NBUF + 2 * C::SR];
     __shared__ uint32_t tmem_base;
-    __shared__ alignas(16) float scales[4][NT];
+    __shared__ alignas(16) float scales[C::SR][C::SLOT];
     const uint32_t ring = (tc::smem_addr(dyn) + 1023u) & ~1023u;
     float *red = reinterpret_cast<float *>(dyn + (ring - tc::smem_addr(dyn)));   // the ring again, once it is drained
     const uint32_t b0 = tc::smem_addr(bars);
@@ -191,10 +204,13 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
     auto empty = [&](int s) { return b0 + (C::STAGES + s) * 8; };
     auto tfull = [&](int b) { return b0 + (2 * C::STAGES + b) * 8; };
     auto tempty = [&](int b) { return b0 + (2 * C::STAGES + C::NBUF + b) * 8; };
+    auto sfull = [&](int r) { return b0 + (2 * C::STAGES + 2 * C::NBUF + r) * 8; };
+    auto sempty = [&](int r) { return b0 + (2 * C::STAGES + 2 * C::NBUF + C::SR + r) * 8; };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
         for (int b = 0; b < C::NBUF; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), C::EW); }
+        for (int r = 0; r < C::SR; r++) { tc::mbar_init(sfull(r), 32); tc::mbar_init(sempty(r), C::EW); }
         tc::prefetch_tensormap(&tm_w);
         tc::prefetch_tensormap(&tm_a);
     }
@@ -212,105 +228,124 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
     const int groups = (p.K + BK - 1) / BK;
     const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / split);
     const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / split);
-    bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
-            for (int g = g0, i = 0; g < g1; g++, i++) {
-                const int s = i % C::STAGES;
-                if (i >= C::STAGES && !wait_phase(empty(s), ((i / C::STAGES) - 1) & 1)) { report(p); break; }
+            int s = 0;
+            uint32_t phase = 1;
+            for (int g = g0; g < g1; g++) {
+                if (!wait_phase(empty(s), phase)) { report(p); break; }
                 const uint32_t at = ring + s * C::STAGE;
                 tc::mbar_expect_tx(full(s), C::STAGE);
                 tc::tma_load_2d(at, &tm_w, g * BK, n0, full(s));
                 tc::tma_load_2d(at + 128 * BK, &tm_a, g * BK, t0, full(s));
+                if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t ID = tc::instr_desc(0, 128, NT);
-            for (int g = g0, i = 0; g < g1; g++, i++) {
-                const int s = i % C::STAGES, b = i % C::NBUF;
-                if (i >= C::NBUF && !wait_phase(tempty(b), ((i / C::NBUF) - 1) & 1)) { report(p); break; }
-                if (!wait_phase(full(s), (i / C::STAGES) & 1)) { report(p); break; }
-                tc::fence_after_sync();
-                const uint32_t at = ring + s * C::STAGE;
+        constexpr uint32_t ID = tc::instr_desc(0, 128, NT);
+        int s = 0, b = 0, r = 0;
+        uint32_t phase = 0, tphase = 1, sphase = 0;
+        bool ok = true;
+        for (int g = g0; g < g1; g++) {
+            // the scales too, for the epilogue, which then waits for the products alone
+            if (!wait_phase(full(s), phase) || !wait_phase(sfull(r), sphase) || !wait_phase(tempty(b), tphase)) ok = false;
+            if (!__all_sync(0xffffffffu, ok)) { report(p); break; }
+            tc::fence_after_sync();
+            const uint32_t at = ring + s * C::STAGE;
+            if (elect_one()) {
                 mma_group<1>(tmem + b * NT, at, at + 128 * BK, ID);
                 tc::commit(empty(s));
                 tc::commit(tfull(b));
             }
+            __syncwarp();
+            if (++s == C::STAGES) { s = 0; phase ^= 1; }
+            if (++b == C::NBUF) { b = 0; tphase ^= 1; }
+            if (++r == C::SR) { r = 0; sphase ^= 1; }
         }
-        __syncwarp();
-    } else {
-        const int e = threadIdx.x - 64;                       // 0 .. EW * 32 - 1
-        const int quarter = warp % 4, c0 = (warp - 2) / 4 * C::COLS;
+    } else if (warp == 2) {
+        int r = 0;
+        uint32_t phase = 1;
+        const float *sa = p.sa + (t0 + lane) * p.sa_row + g0 * p.sa_group;
+        const float *sw = p.sw + static_cast<int64_t>(n0 / 128) * p.sw_row + g0 * p.sw_group;
+        for (int g = g0; g < g1; g++) {
+            if (!wait_phase(sempty(r), phase)) { report(p); break; }
+            const uint32_t at = tc::smem_addr(&scales[r][0]);
+#pragma unroll
+            for (int j = 0; j < NT; j += 32)
+                if (lane + j < NT && t0 + lane + j < p.M) cp_async4(at + (lane + j) * 4, sa + j * p.sa_row);
+            if (lane == 0) cp_async4(at + NT * 4, sw);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(r)) : "memory");
+            sa += p.sa_group;
+            sw += p.sw_group;
+            if (++r == C::SR) { r = 0; phase ^= 1; }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= 4) {
+        const int quarter = warp % 4, c0 = (warp - 4) / 4 * C::COLS;
         const int n = quarter * 32 + lane;                    // row of W within the tile
-        const float *sw = p.sw + static_cast<int64_t>(n0 / 128) * p.sw_row;
-        const bool owns = e < NT && t0 + e < p.M;
-        const float *sa = p.sa + static_cast<int64_t>(t0 + e) * p.sa_row;
-        auto factor = [&](int g) { return owns && g < g1 ? sa[g * p.sa_group] * sw[g * p.sw_group] : 0.f; };
-        float2 acc[C::COLS / 2];
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+        float acc[C::COLS];
 #pragma unroll
-        for (int c = 0; c < C::COLS / 2; c++) acc[c] = make_float2(0.f, 0.f);
-        if (e < NT) scales[0][e] = factor(g0);
-        float next = factor(g0 + 1);
-        for (int g = g0, i = 0; g < g1; g++, i++) {
-            const int b = i % C::NBUF;
-            // this group's factors are visible after the barrier, and the slot written now was last read three groups ago
-            asm volatile("bar.sync 1, %0;" :: "n"(C::EW * 32) : "memory");
-            if (e < NT) scales[(i + 1) % 4][e] = next;
-            next = factor(g + 2);
-            if (ok && !wait_phase(tfull(b), (i / C::NBUF) & 1)) ok = false;
+        for (int c = 0; c < C::COLS; c++) acc[c] = 0.f;
+        int b = 0, r = 0;
+        uint32_t tphase = 0;
+        bool ok = true;
+        for (int g = g0; g < g1; g++) {
+            if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
             tc::fence_after_sync();
-            const float4 *f4 = reinterpret_cast<const float4 *>(&scales[i % 4][c0]);
-            const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * NT + c0;
+            float v[C::COLS / 16][16];
 #pragma unroll
-            for (int c = 0; c < C::COLS; c += 16) {
-                float v[16];
-                tc::tmem_ld16(at + c, v);
-                tc::tmem_ld_wait();
-                if (c + 16 >= C::COLS) {
-                    tc::fence_before_sync();
-                    if (lane == 0) arrive_local(tempty(b));
-                }
+            for (int c = 0; c < C::COLS / 16; c++) tc::tmem_ld16(lanes + b * NT + c * 16, v[c]);
+            const float4 *f4 = reinterpret_cast<const float4 *>(&scales[r][c0]);
+            const float sw = scales[r][NT];
+            tc::tmem_ld_wait();
+            tc::fence_before_sync();
+            if (lane == 0) arrive_local(tempty(b));
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float4 f = f4[c / 4 + j];
-                    acc[c / 2 + 2 * j] = ffma2(make_float2(v[4 * j], v[4 * j + 1]), make_float2(f.x, f.y), acc[c / 2 + 2 * j]);
-                    acc[c / 2 + 2 * j + 1] = ffma2(make_float2(v[4 * j + 2], v[4 * j + 3]), make_float2(f.z, f.w), acc[c / 2 + 2 * j + 1]);
-                }
+            for (int c = 0; c < C::COLS / 4; c++) {
+                const float4 f = f4[c];
+                acc[4 * c] = fmaf(v[c / 4][4 * (c % 4)], f.x * sw, acc[4 * c]);
+                acc[4 * c + 1] = fmaf(v[c / 4][4 * (c % 4) + 1], f.y * sw, acc[4 * c + 1]);
+                acc[4 * c + 2] = fmaf(v[c / 4][4 * (c % 4) + 2], f.z * sw, acc[4 * c + 2]);
+                acc[4 * c + 3] = fmaf(v[c / 4][4 * (c % 4) + 3], f.w * sw, acc[4 * c + 3]);
             }
+            __syncwarp();
+            if (lane == 0) arrive_local(sempty(r));
+            if (++b == C::NBUF) { b = 0; tphase ^= 1; }
+            if (++r == C::SR) r = 0;
         }
         if (!ok) report(p);
-        if (split == 1) {
-            if (ok && n0 + n < p.N)
+        if (split > 1) {
 #pragma unroll
-                for (int c = 0; c < C::COLS; c++)
-                    if (t0 + c0 + c < p.M)
-                        store_out(p.out, static_cast<int64_t>(t0 + c0 + c) * p.ld_out + n0 + n, p.out_dtype,
-                                  c % 2 ? acc[c / 2].y : acc[c / 2].x);
-        } else {
+            for (int c = 0; c < C::COLS; c++) red[(c0 + c) * 128 + n] = acc[c];
+        } else if (ok && n0 + n < p.N) {
 #pragma unroll
-            for (int c = 0; c < C::COLS; c++) red[(c0 + c) * 128 + n] = c % 2 ? acc[c / 2].y : acc[c / 2].x;
+            for (int c = 0; c < C::COLS; c++)
+                if (t0 + c0 + c < p.M)
+                    store_out(p.out, static_cast<int64_t>(t0 + c0 + c) * p.ld_out + n0 + n, p.out_dtype, acc[c]);
         }
     }
     if (split > 1) {
         cluster_sync();
-        if (warp >= 2) {
+        if (warp >= 4) {
             // CTA `rank` joins the rows rank, rank + split, ... of A, over the CTAs in order
-            const int e = threadIdx.x - 64, n = e % 128;
-            const uint32_t mine = tc::smem_addr(red);
+            const int e = threadIdx.x - 128, n = e % 128;
             const int rows = min(NT, p.M - t0);
+            uint32_t part[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) part[k] = in_cta(ring, k < split ? k : 0);
+#pragma unroll 4
             for (int t = rank + (e / 128) * split; t < rows; t += split * (C::EW / 4)) {
                 float v[8];
 #pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    v[q] = 0.f;
-                    if (q < split)
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[q]) : "r"(in_cta(mine + (t * 128 + n) * 4, q)));
+                for (int k = 0; k < 8; k++) {
+                    v[k] = 0.f;
+                    if (k < split) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[k]) : "r"(part[k] + (t * 128 + n) * 4));
                 }
                 float sum = v[0];
 #pragma unroll
-                for (int q = 1; q < 8; q++) sum += v[q];
+                for (int k = 1; k < 8; k++) sum += v[k];
                 if (n0 + n < p.N) store_out(p.out, static_cast<int64_t>(t0 + t) * p.ld_out + n0 + n, p.out_dtype, sum);
             }
         }
@@ -319,6 +354,247 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CU
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc<C::NBUF * NT>(tmem);
+}
+
+// ---- few rows of A ------------------------------------------------------------------------
+
+// How a call is cut up: tiles of `bn` rows of W (a multiple of 16, chosen so that the CTAs fill the
+// GPU once), the inner axis over a cluster of `split` CTAs, 128 rows of A per blockIdx.y of which
+// `rows` (a multiple of 8) are copied.
+struct SlimPlan {
+    int bn, split, rows, stages, nbuf;   // nbuf accumulators of bn TMEM columns
+};
+
+struct Slim {
+    static constexpr int EW = 16;                       // epilogue warps: four strips of columns x four quarters of TMEM lanes
+    static constexpr int THREADS = 128 + EW * 32;       // copies, MMAs, scales, one idle warp, then the epilogue's
+    static constexpr int REGS_CONTROL = 32, REGS_EPILOGUE = 112;   // 640 * 96 at launch
+    static constexpr int MAX_STAGES = 12, MAX_BUF = 4;
+    static constexpr int SR = 4, SLOT = 132;            // groups of scales in flight: 128 rows' and up to three blocks' of W
+    static constexpr int TAIL = SR * SLOT * 4 + (2 * MAX_STAGES + 2 * MAX_BUF + 2 * SR) * 8 + 16;
+    static constexpr int RING = 227 * 1024 - TAIL;
+};
+
+__device__ __forceinline__ void store16(const Fp8Params &p, int64_t m, int n, const float (&v)[16])
+{
+    const int es = p.out_dtype == 2 ? 4 : 2;
+    unsigned char *o = static_cast<unsigned char *>(p.out) + (m * p.ld_out + n) * es;
+    if (n + 16 <= p.N && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+        if (p.out_dtype == 2) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                reinterpret_cast<float4 *>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                w[j] = p.out_dtype == 0 ? pack_bf16x2(v[2 * j], v[2 * j + 1]) : tc::pack_f16x2(v[2 * j], v[2 * j + 1]);
+            reinterpret_cast<uint4 *>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+        if (n + j < p.N) store_out(p.out, m * p.ld_out + n + j, p.out_dtype, v[j]);
+}
+
+// MAXC: chunks of 16 columns that an epilogue warp holds at most
+template <int MAXC>
+__global__ void __launch_bounds__(Slim::THREADS, 1)
+slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const Fp8Params p,
+            const SlimPlan q)
+{
+    using C = Slim;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    const uint32_t ring = tc::smem_addr(dyn), wring = ring + q.stages * q.rows * BK;
+    float *scales = reinterpret_cast<float *>(dyn + C::RING);
+    const uint32_t b0 = tc::smem_addr(scales) + C::SR * C::SLOT * 4;
+    volatile uint32_t *tmem_base = reinterpret_cast<uint32_t *>(dyn + C::RING + C::TAIL - 16);
+    auto full = [&](int s) { return b0 + s * 8; };
+    auto empty = [&](int s) { return b0 + (C::MAX_STAGES + s) * 8; };
+    auto tfull = [&](int b) { return b0 + (2 * C::MAX_STAGES + b) * 8; };
+    auto tempty = [&](int b) { return b0 + (2 * C::MAX_STAGES + C::MAX_BUF + b) * 8; };
+    auto sfull = [&](int r) { return b0 + (2 * C::MAX_STAGES + 2 * C::MAX_BUF + r) * 8; };
+    auto sempty = [&](int r) { return b0 + (2 * C::MAX_STAGES + 2 * C::MAX_BUF + C::SR + r) * 8; };
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = blockIdx.x % q.split;
+    const int n0 = blockIdx.x / q.split * q.bn, m0 = blockIdx.y * 128;
+    const int rows = min(128, p.M - m0);                       // live rows of A
+    const int chunks = q.bn / 16, per = (chunks + 3) / 4;      // of 16 columns, per strip
+    const int working = (rows + 31) / 32 * ((chunks + per - 1) / per);   // epilogue warps with something to do
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
+        for (int b = 0; b < q.nbuf; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), working); }
+        for (int r = 0; r < C::SR; r++) { tc::mbar_init(sfull(r), 32); tc::mbar_init(sempty(r), working); }
+        tc::prefetch_tensormap(&tm_w);
+        tc::prefetch_tensormap(&tm_a);
+    }
+    pdl_wait();
+    // tensor memory is taken before the next grid may start: it could hold what this one waits for
+    if (warp == 1) tc::tmem_alloc<512>(b0 + (2 * C::MAX_STAGES + 2 * C::MAX_BUF + 2 * C::SR) * 8);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    pdl_release();
+
+    const uint32_t tmem = *tmem_base;
+    const int groups = (p.K + BK - 1) / BK;
+    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / q.split);
+    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / q.split);
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::REGS_CONTROL));
+        if (warp == 0) {
+            if (lane == 0) {
+                int s = 0;
+                uint32_t phase = 1;
+                for (int g = g0; g < g1; g++) {
+                    if (!wait_phase(empty(s), phase)) { report(p); break; }
+                    tc::mbar_expect_tx(full(s), (q.rows + q.bn) * BK);
+                    tc::tma_load_2d(wring + s * q.bn * BK, &tm_w, g * BK, n0, full(s));
+                    tc::tma_load_2d(ring + s * q.rows * BK, &tm_a, g * BK, m0, full(s));
+                    if (++s == q.stages) { s = 0; phase ^= 1; }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // The MMA takes 128 rows of A whatever is there: those past the `rows` copied are other
+            // tiles' bytes, and their products are never read.
+            const uint32_t id = tc::instr_desc(0, 128, 0) | static_cast<uint32_t>(q.bn >> 3) << 17;
+            int s = 0, b = 0, r = 0;
+            uint32_t phase = 0, tphase = 1, sphase = 0;
+            bool ok = true;
+            for (int g = g0; g < g1; g++) {
+                // the scales too, for the epilogue, which then waits for the products alone
+                if (!wait_phase(full(s), phase) || !wait_phase(sfull(r), sphase) || !wait_phase(tempty(b), tphase)) ok = false;
+                if (!__all_sync(0xffffffffu, ok)) { report(p); break; }
+                tc::fence_after_sync();
+                if (elect_one()) {
+                    mma_group<1>(tmem + b * q.bn, ring + s * q.rows * BK, wring + s * q.bn * BK, id);
+                    tc::commit(empty(s));
+                    tc::commit(tfull(b));
+                }
+                __syncwarp();
+                if (++s == q.stages) { s = 0; phase ^= 1; }
+                if (++b == q.nbuf) { b = 0; tphase ^= 1; }
+                if (++r == C::SR) { r = 0; sphase ^= 1; }
+            }
+        } else if (warp == 2) {
+            int r = 0;
+            uint32_t phase = 1;
+            const float *sa = p.sa + (m0 + lane) * p.sa_row + g0 * p.sa_group;
+            const float *sw = p.sw + (n0 / 128 + (lane < 3 ? lane : 0)) * p.sw_row + g0 * p.sw_group;
+            const bool w_in = lane < 3 && (n0 / 128 + lane) * 128 < min(p.N, n0 + q.bn);
+            for (int g = g0; g < g1; g++) {
+                if (!wait_phase(sempty(r), phase)) { report(p); break; }
+                const uint32_t at = tc::smem_addr(scales + r * C::SLOT);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (lane + 32 * j < rows) cp_async4(at + (lane + 32 * j) * 4, sa + 32 * j * p.sa_row);
+                if (w_in) cp_async4(at + (128 + lane) * 4, sw);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(r)) : "memory");
+                sa += p.sa_group;
+                sw += p.sw_group;
+                if (++r == C::SR) { r = 0; phase ^= 1; }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(C::REGS_EPILOGUE));
+        const int quarter = warp % 4, first = (warp - 4) / 4 * per;
+        const int mine = max(0, min(per, chunks - first));
+        const int row = quarter * 32 + lane;
+        float acc[MAXC][16];
+#pragma unroll
+        for (int c = 0; c < MAXC; c++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) acc[c][j] = 0.f;
+        bool ok = true;
+        if (mine > 0 && quarter * 32 < rows) {
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + first * 16;
+            int b = 0, r = 0;
+            uint32_t tphase = 0;
+            // which block of W's scales a chunk has
+            int block[MAXC];
+#pragma unroll
+            for (int c = 0; c < MAXC; c++) block[c] = (n0 + (first + c) * 16) / 128 - n0 / 128;
+            for (int g = g0; g < g1; g++) {
+                if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
+                tc::fence_after_sync();
+                const float *slot = scales + r * C::SLOT;
+                const float s = slot[row];
+                constexpr int AT_ONCE = MAXC < 2 ? MAXC : 2;   // chunks in flight: registers
+#pragma unroll
+                for (int c = 0; c < MAXC; c += AT_ONCE) {
+                    float v[AT_ONCE][16], f[AT_ONCE];
+#pragma unroll
+                    for (int k = 0; k < AT_ONCE; k++)
+                        if (c + k < mine) {
+                            tc::tmem_ld16(lanes + b * q.bn + (c + k) * 16, v[k]);
+                            f[k] = s * slot[128 + block[c + k]];
+                        }
+                    tc::tmem_ld_wait();
+                    if (c + AT_ONCE >= MAXC) {
+                        tc::fence_before_sync();
+                        if (lane == 0) {
+                            arrive_local(tempty(b));
+                            arrive_local(sempty(r));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < AT_ONCE; k++)
+                        if (c + k < mine)
+#pragma unroll
+                            for (int j = 0; j < 16; j++) acc[c + k][j] = fmaf(v[k][j], f[k], acc[c + k][j]);
+                }
+                if (++b == q.nbuf) { b = 0; tphase ^= 1; }
+                if (++r == C::SR) r = 0;
+            }
+            if (!ok) report(p);
+            if (ok && row < rows)
+#pragma unroll
+                for (int c = 0; c < MAXC; c++)
+                    if (c < mine) {
+                        if (q.split == 1) {
+                            store16(p, m0 + row, n0 + (first + c) * 16, acc[c]);
+                        } else {
+                            // the ring again, now that this CTA's last MMA is done; an odd pitch spreads the banks
+                            float *red = reinterpret_cast<float *>(dyn) + row * (q.bn + 1) + (first + c) * 16;
+#pragma unroll
+                            for (int j = 0; j < 16; j++) red[j] = acc[c][j];
+                        }
+                    }
+        }
+    }
+    if (q.split > 1) {
+        cluster_sync();
+        if (warp >= 4) {
+            // CTA `rank` joins the rows rank, rank + split, ... of the tile, over the CTAs in order
+            const int cols = min(q.bn, p.N - n0), total = (rows - rank + q.split - 1) / q.split * cols;
+            uint32_t part[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) part[k] = in_cta(ring, k < q.split ? k : 0);
+#pragma unroll 4
+            for (int i = threadIdx.x - 128; i < total; i += C::EW * 32) {
+                const int row = i / cols * q.split + rank, n = i % cols;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    v[k] = 0.f;
+                    if (k < q.split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[k]) : "r"(part[k] + (row * (q.bn + 1) + n) * 4));
+                }
+                float sum = v[0];
+#pragma unroll
+                for (int k = 1; k < 8; k++) sum += v[k];
+                store_out(p.out, static_cast<int64_t>(m0 + row) * p.ld_out + n0 + n, p.out_dtype, sum);
+            }
+        }
+        cluster_sync();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc<512>(tmem);
 }
 
 // ---- many rows of A -----------------------------------------------------------------------
@@ -332,8 +608,9 @@ struct Wide {
     static constexpr int STAGE = 2 * 128 * BK;       // per CTA: its 128 rows of A and its 128 rows of W
     static constexpr int STAGES = 5;
     static constexpr int BOX = 32 * 128;             // an epilogue warp's outputs on their way to memory: 32 rows of 128 bytes
-    static constexpr int SR = 4;                     // groups of scales in flight: 128 rows' and the tile's two of W
-    static constexpr int SCALES = SR * 132 * 4;
+    static constexpr int SR = 2;                     // slots of scales, two groups each: 128 rows' and the tile's two of W
+    static constexpr int SLOT = 132 * 2;             // floats: [128 rows, 2 blocks of W][2 groups]
+    static constexpr int SCALES = SR * SLOT * 4;
     static constexpr int BARS = (2 * STAGES + 4 + 2 * SR) * 8;
     static constexpr int SMEM = STAGES * STAGE + EW * BOX + SCALES + BARS + 16;
 };
@@ -457,16 +734,21 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 const int m0 = tm * 256 + rank * 128 + lane, nb = tn * 2;
                 const float *sa = p.sa + m0 * p.sa_row, *sw = p.sw + (nb + (lane & 1)) * p.sw_row;
                 const bool w_in = lane < 2 && (nb + lane) * 128 < p.N;
-                for (int g = 0; g < groups; g++) {
+                for (int g = 0; g < groups; g += 2) {
                     if (!wait_phase(sempty(r), phase)) { report(p); ok = false; break; }
-                    const uint32_t at = tc::smem_addr(scales + r * 132);
+                    const uint32_t at = tc::smem_addr(scales + r * C::SLOT);
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        if (m0 + 32 * j < p.M) cp_async4(at + (lane + 32 * j) * 4, sa + 32 * j * p.sa_row);
-                    if (w_in) cp_async4(at + (128 + lane) * 4, sw);
+                    for (int h = 0; h < 2; h++) {
+                        if (g + h < groups) {
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                if (m0 + 32 * j < p.M) cp_async4(at + ((lane + 32 * j) * 2 + h) * 4, sa + 32 * j * p.sa_row);
+                            if (w_in) cp_async4(at + ((128 + lane) * 2 + h) * 4, sw);
+                        }
+                        sa += p.sa_group;
+                        sw += p.sw_group;
+                    }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(sfull(r)) : "memory");
-                    sa += p.sa_group;
-                    sw += p.sw_group;
                     if (++r == C::SR) { r = 0; phase ^= 1; }
                 }
             }
@@ -479,36 +761,44 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         unsigned char *box = dyn + C::STAGES * C::STAGE + (warp - 4) * C::BOX;
         int b = 0, r = 0;
         uint32_t tphase = 0, sphase = 0;
+        bool ready = false;
         for (int i = pair; i < total; i += pairs) {
             float2 acc[C::COLS / 2];
 #pragma unroll
             for (int c = 0; c < C::COLS / 2; c++) acc[c] = make_float2(0.f, 0.f);
             bool ok = true;
+            float2 s2;
             for (int g = 0; g < groups; g++) {
-                if (!wait_phase(sfull(r), sphase)) { ok = false; break; }
-                const float s = scales[r * 132 + row] * scales[r * 132 + 128 + c0 / 128];
-                const float2 f = make_float2(s, s);
-                if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
+                if (g % 2 == 0) {
+                    // two groups' scales at a time
+                    if (!wait_phase(sfull(r), sphase)) { ok = false; break; }
+                    const float2 *slot = reinterpret_cast<const float2 *>(scales + r * C::SLOT);
+                    const float2 x = slot[row], y = slot[128 + c0 / 128];
+                    s2 = make_float2(x.x * y.x, x.y * y.y);
+                    __syncwarp();
+                    if (lane == 0) arrive_local(sempty(r));
+                    if (++r == C::SR) { r = 0; sphase ^= 1; }
+                }
+                const float2 f = g % 2 == 0 ? make_float2(s2.x, s2.x) : make_float2(s2.y, s2.y);
+                if (!ready && !wait_phase(tfull(b), tphase)) { ok = false; break; }
                 tc::fence_after_sync();
                 const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * 256 + c0;
+                uint32_t v[32];
+                tmem_ld32(at, v);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < C::COLS / 32; c++) {
-                    uint32_t v[32];
-                    tmem_ld32(at + c * 32, v);
-                    tc::tmem_ld_wait();
-                    if (c == C::COLS / 32 - 1) {
-                        tc::fence_before_sync();
-                        if (lane == 0) {
-                            arrive_cluster(in_cta(tempty(b), 0));
-                            arrive_local(sempty(r));
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        acc[c * 16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[c * 16 + j]);
-                }
+                for (int j = 0; j < 16; j++)
+                    acc[j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[j]);
+                tmem_ld32(at + 32, v);
+                tc::tmem_ld_wait();
+                tc::fence_before_sync();
+                if (lane == 0) arrive_cluster(in_cta(tempty(b), 0));
                 if (++b == 2) { b = 0; tphase ^= 1; }
-                if (++r == C::SR) { r = 0; sphase ^= 1; }
+                // asked here, answered by the time the sums below are done
+                ready = test_phase(tfull(b), tphase);
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    acc[16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[16 + j]);
             }
             if (!ok) { report(p); break; }
             int tm, tn;
@@ -665,29 +955,123 @@ bool tma_rows(const void *base, int64_t *ld, int64_t rows, int64_t cols)
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && *ld % 16 == 0 && *ld < (int64_t(1) << 39);
 }
 
+// A launch with programmatic stream serialization over clusters of `split` CTAs.
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    Launch(dim3 grid, int threads, int smem, int split, cudaStream_t stream)
+    {
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+        cfg.attrs = at;
+        cfg.numAttrs = split > 1 ? 2 : 1;
+    }
+};
+
+// How many CTAs of a kernel run at once in clusters of 1 .. 8 (clusters leave SMs unused that do not
+// fit their GPC), asked once.
+struct Fit {
+    int ctas[9] = {};
+    cudaError_t status = cudaSuccess;
+    template <typename K>
+    Fit(K kernel, int threads, int smem, int sms, int per_sm)
+    {
+        status = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        ctas[1] = sms * per_sm;
+        for (int split = 2; split <= 8 && status == cudaSuccess; split++) {
+            Launch l(dim3(split), threads, smem, split, nullptr);
+            l.at[0] = l.at[1];   // the cluster alone
+            l.cfg.numAttrs = 1;
+            int n = 0;
+            status = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
+            ctas[split] = n * split;
+        }
+    }
+};
+
+// Time of a plan in nanoseconds: start and end, then for every wave of CTAs and group of 128 k the largest
+// of what HBM (6.6 kB/ns over all SMs), L2 (110 B/ns into one SM) and the epilogue need; a split adds its
+// join. Measured rates and latencies, to compare plans with.
+double plan_time(int64_t ctas, int fit, int groups, int split, double hbm_bytes, double l2_bytes, double epilogue)
+{
+    const double waves = static_cast<double>((ctas + fit - 1) / fit), at_once = ctas < fit ? ctas : fit;
+    double step = at_once * hbm_bytes / 6600.;
+    if (step < l2_bytes / 110.) step = l2_bytes / 110.;
+    if (step < epilogue) step = epilogue;
+    return waves * (3000. + step * ((groups + split - 1) / split) + (split > 1 ? 1500. : 0.));
+}
+
 template <int NT>
-cudaError_t run_thin(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int split, cudaStream_t stream)
+cudaError_t run_thin(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cudaStream_t stream)
 {
     using C = Thin<NT>;
+    static const Fit fit(thin_kernel<NT>, C::THREADS, C::SMEM, sms, 2);
+    if (fit.status != cudaSuccess) return fit.status;
+    const int groups = (p.K + BK - 1) / BK, tiles_n = (p.N - 1) / 128 + 1, tiles_t = (p.M + NT - 1) / NT;
+    int split = 1;
+    double least = 1e30;
+    for (int k = 1; k <= 8 && k <= groups; k++) {
+        if (fit.ctas[k] == 0) continue;
+        const double t = plan_time(static_cast<int64_t>(tiles_n) * tiles_t * k, fit.ctas[k], groups, k, 128. * BK / tiles_t, 2. * C::STAGE,
+                                   300. + NT);
+        if (t < least) { least = t; split = k; }
+    }
     CUtensorMap tw, ta;
     cudaError_t e;
     if ((e = encode(&tw, p.w, p.K, p.N, ld_w, 128)) != cudaSuccess) return e;
     if ((e = encode(&ta, p.a, p.K, p.M, ld_a, NT)) != cudaSuccess) return e;
-    static const cudaError_t attr = cudaFuncSetAttribute(thin_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    Launch l(dim3(static_cast<unsigned>(tiles_n) * split, static_cast<unsigned>(tiles_t)), C::THREADS, C::SMEM, split, stream);
+    return cudaLaunchKernelEx(&l.cfg, thin_kernel<NT>, ta, tw, p, split);
+}
+
+constexpr int SLIM_SMEM = Slim::RING + Slim::TAIL;
+
+// The plan of least time among the splits, each with the tile of W that fills the GPU once.
+double plan_slim(const Fp8Params &p, const Fit &fit, SlimPlan *best)
+{
+    const int groups = (p.K + BK - 1) / BK, mt = (p.M + 127) / 128;
+    const int rows = p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
+    double least = 1e30;
+    for (int split = 1; split <= 8 && split <= groups; split++) {
+        if (fit.ctas[split] == 0) continue;
+        const int tiles = fit.ctas[split] / (split * mt);           // of W in one wave
+        int bn = tiles < 1 ? 256 : (p.N - 1) / tiles + 1;
+        bn = bn > 256 ? 256 : (bn + 15) / 16 * 16;
+        if (split > 1 && (bn + 1) * rows * 4 > Slim::RING) continue;
+        const int64_t ctas = static_cast<int64_t>((p.N - 1) / bn + 1) * split * mt;
+        const double t = plan_time(ctas, fit.ctas[split], groups, split, static_cast<double>(bn) * BK / mt,
+                                   static_cast<double>(rows + bn) * BK, 250. + 40. * ((bn / 16 + 3) / 4));
+        if (t < least) {
+            least = t;
+            best->bn = bn;
+            best->split = split;
+        }
+    }
+    best->rows = rows;
+    const int s = Slim::RING / ((rows + best->bn) * BK), n = 512 / best->bn;
+    best->stages = s < Slim::MAX_STAGES ? s : Slim::MAX_STAGES;
+    best->nbuf = n < Slim::MAX_BUF ? n : Slim::MAX_BUF;
+    return least;
+}
+
+template <int MAXC>
+cudaError_t run_slim(const Fp8Params &p, const SlimPlan &q, int64_t ld_a, int64_t ld_w, cudaStream_t stream)
+{
+    static const cudaError_t attr = cudaFuncSetAttribute(slim_kernel<MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize, SLIM_SMEM);
     if (attr != cudaSuccess) return attr;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.N) + 127) / 128 * split), static_cast<unsigned>((p.M + NT - 1) / NT));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, thin_kernel<NT>, tw, ta, p, split);
+    CUtensorMap tw, ta;
+    cudaError_t e;
+    if ((e = encode(&tw, p.w, p.K, p.N, ld_w, q.bn)) != cudaSuccess) return e;
+    if ((e = encode(&ta, p.a, p.K, p.M, ld_a, q.rows)) != cudaSuccess) return e;
+    Launch l(dim3(static_cast<unsigned>((p.N - 1) / q.bn + 1) * q.split, static_cast<unsigned>((p.M + 127) / 128)), Slim::THREADS,
+             SLIM_SMEM, q.split, stream);
+    return cudaLaunchKernelEx(&l.cfg, slim_kernel<MAXC>, ta, tw, p, q);
 }
 
 cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cudaStream_t stream)
@@ -731,16 +1115,21 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    if (p.M > 256) return run_wide(p, ld_a, ld_w, sms, stream);
-    // split the inner axis until two CTAs per SM are running
+    if (p.M <= 16) return run_thin<16>(p, ld_a, ld_w, sms, stream);
+    if (p.M <= 32) return run_thin<32>(p, ld_a, ld_w, sms, stream);
+    if (p.M <= 64) return run_thin<64>(p, ld_a, ld_w, sms, stream);
+    // the wide kernel's time by the same measure: 500 ns per group and wave of tiles
+    static const Fit fit(slim_kernel<4>, Slim::THREADS, SLIM_SMEM, sms, 1);
+    if (fit.status != cudaSuccess) return fit.status;
     const int groups = (p.K + BK - 1) / BK;
-    const int64_t tiles = (static_cast<int64_t>(p.N) + 127) / 128 * ((p.M + 127) / 128);
-    int split = 1;
-    while (split < 8 && split < groups && tiles * (split + 1) <= 2 * sms) split++;
-    if (p.M <= 16) return run_thin<16>(p, ld_a, ld_w, split, stream);
-    if (p.M <= 32) return run_thin<32>(p, ld_a, ld_w, split, stream);
-    if (p.M <= 64) return run_thin<64>(p, ld_a, ld_w, split, stream);
-    return run_thin<128>(p, ld_a, ld_w, split, stream);
+    const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * ((static_cast<int64_t>(p.N) + 255) / 256);
+    const double wide = 4000. + 500. * groups * static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
+    SlimPlan q;
+    if (p.M > 1024 || plan_slim(p, fit, &q) > wide) return run_wide(p, ld_a, ld_w, sms, stream);
+    const int per = (q.bn / 16 + 3) / 4;
+    if (per <= 1) return run_slim<1>(p, q, ld_a, ld_w, stream);
+    if (per <= 2) return run_slim<2>(p, q, ld_a, ld_w, stream);
+    return run_slim<4>(p, q, ld_a, ld_w, stream);
 }
 
 }  // namespace kda
