@@ -19,6 +19,9 @@ struct NormQuantParams {
 };
 constexpr int kNormMaxCols = 32768;
 cudaError_t launch_norm_quant(const NormQuantParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_norm_quant_bf16(const NormQuantParams &p, cudaStream_t stream);
+cudaError_t launch_norm_quant_fp16(const NormQuantParams &p, cudaStream_t stream);
+cudaError_t launch_norm_quant_fp32(const NormQuantParams &p, cudaStream_t stream);
 
 struct Fp8Params {
     const uint8_t *a;   int64_t ld_a;

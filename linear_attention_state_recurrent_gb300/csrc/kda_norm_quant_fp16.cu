@@ -1,0 +1,8 @@
+// kda_norm_quant of fp16 rows: a translation unit per type, compiled in parallel.
+#include "kda_norm_quant.cuh"
+
+namespace kda {
+
+cudaError_t launch_norm_quant_fp16(const NormQuantParams &p, cudaStream_t stream) { return by_alignment<Fp16>(p, stream); }
+
+}  // namespace kda

@@ -491,49 +491,61 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
 
 
 # ---- the operators around the recurrence -------------------------------------------------
-# These run in a few microseconds, so their wrappers pass plain integers and keep the checks
-# to comparisons.
+# These run in a few microseconds, less than a careless wrapper costs: the checks below touch
+# each property of a tensor once, and say what is wrong only after something is.
 
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _F32, _I32, _I64 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index or 0)
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _refuse(t, name, dtype, shape, layout):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    raise ValueError(f"{name} must have {layout}")
 
 
 def _matrix(t, name, dtype, rows, cols):
-    """The row stride of a 2-D tensor of the given type and shape with unit inner stride."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be [{rows}, {cols}] (got {tuple(t.shape)})")
-    ld, inner = t.stride()
-    if inner != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit inner stride")
-    return ld if rows > 1 else max(ld, cols)   # the stride of a single row says nothing
+    """The row stride of a 2-D GPU tensor of the given type and shape with unit inner stride."""
+    if t.dtype is dtype and t.shape == (rows, cols) and t.is_cuda:
+        ld, inner = t.stride()
+        if inner == 1 or cols <= 1:
+            return ld if rows > 1 or ld > cols else cols   # the stride of a single row says nothing
+    _refuse(t, name, dtype, (rows, cols), "unit inner stride")
 
 
 def _scale_strides(t, name, rows, groups):
-    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != groups:
-        raise ValueError(f"{name} must be fp32 [{rows}, {groups}] (got {t.dtype} {tuple(t.shape)})")
-    a, b = t.stride()
-    return (a if rows > 1 else 1), (b if groups > 1 else 1)
-
-
-def _on_gpu(*tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor must be on the GPU")
+    if t.dtype is _F32 and t.shape == (rows, groups) and t.is_cuda:
+        a, b = t.stride()
+        return (a if rows > 1 else 1), (b if groups > 1 else 1)
+    _refuse(t, name, _F32, (rows, groups), "two strides")
 
 
 def _vector(t, name, dtype, n):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] < n or (t.shape[0] > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor of at least {n} entries")
+    """The address of a contiguous 1-D GPU tensor of at least n entries."""
+    if t.dtype is dtype and t.dim() == 1 and t.shape[0] >= n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous 1-D {dtype} GPU tensor of at least {n} entries")
+
+
+def _error_word(t):
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.numel() < 1 or not t.is_cuda:
+        raise ValueError("err_flags must be a 32-bit integer GPU tensor")
+    return t.data_ptr()
 
 
 def _rows16(rows, cols, dtype, device):
@@ -553,34 +565,36 @@ def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None
     fp32 [N, ceil(D / 128)], any strides. What is not given is allocated: q with rows on 16-byte
     boundaries and scales with the rows next to each other (the layouts kda_fp8_matmul reads fastest).
     Returns (q, scales, residual_out), residual_out None without a residual."""
-    if x.dim() != 2 or x.dtype not in _DTYPE_CODE:
+    dt = x.dtype
+    code = _DTYPE_CODE.get(dt)
+    if code is None or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
     N, D = x.shape
     groups = -(-D // 128)
-    dt = x.dtype
+    ld_x = _matrix(x, "x", dt, N, D)
     if q is None:
         q = _rows16(N, D, _E4M3, x.device)
     if scales is None:
-        scales = torch.empty(groups, N, dtype=torch.float32, device=x.device).t()
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-        ld_res = ld_ro = 0
-    else:
+        scales = torch.empty(groups, N, dtype=_F32, device=x.device).t()
+    res_p = ro_p = y_p = w_p = None
+    ld_res = ld_ro = ld_y = 0
+    if residual is not None:
         if residual_out is None:
             residual_out = torch.empty(N, D, dtype=dt, device=x.device)
-        ld_res = _matrix(residual, "residual", dt, N, D)
-        ld_ro = _matrix(residual_out, "residual_out", dt, N, D)
-    if weight is not None and (weight.dtype != torch.float32 or weight.dim() != 1 or weight.shape[0] != D
-                               or not weight.is_contiguous()):
-        raise ValueError(f"weight must be a contiguous fp32 tensor of {D} entries")
+        ld_res, res_p = _matrix(residual, "residual", dt, N, D), residual.data_ptr()
+        ld_ro, ro_p = _matrix(residual_out, "residual_out", dt, N, D), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if weight is not None:
+        if weight.dim() != 1 or weight.shape[0] != D:
+            raise ValueError(f"weight must have {D} entries")
+        w_p = _vector(weight, "weight", _F32, D)
+    if y is not None:
+        ld_y, y_p = _matrix(y, "y", dt, N, D), y.data_ptr()
     s_row, s_group = _scale_strides(scales, "scales", N, groups)
-    ld_x, ld_q = _matrix(x, "x", dt, N, D), _matrix(q, "q", _E4M3, N, D)
-    ld_y = 0 if y is None else _matrix(y, "y", dt, N, D)
-    _on_gpu(x, weight, residual, residual_out, y, q, scales)
-    status = lib.kda_norm_quant(x.data_ptr(), ld_x, _address(residual), ld_res, _DTYPE_CODE[dt], _address(weight),
-                                eps, N, D, _address(residual_out), ld_ro, _address(y), ld_y, q.data_ptr(), ld_q,
-                                scales.data_ptr(), s_row, s_group, _raw_stream(stream))
+    ld_q = _matrix(q, "q", _E4M3, N, D)
+    status = lib.kda_norm_quant(x.data_ptr(), ld_x, res_p, ld_res, code, w_p, eps, N, D, ro_p, ld_ro, y_p, ld_y,
+                                q.data_ptr(), ld_q, scales.data_ptr(), s_row, s_group, _raw_stream(stream, x.device))
     if status:
         _check(status, "kda_norm_quant")
     return q, scales, residual_out
@@ -593,7 +607,7 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
     fp32 [ceil(N / 128), ceil(K / 128)], any strides. out: bf16, fp16 or fp32 [M, N] (allocated as
     out_dtype when not given). Operands with rows on 16-byte boundaries take the tensor cores.
     Returns out."""
-    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+    if a.dim() != 2 or w.dim() != 2:
         raise ValueError("a and w must be 2-D with the same number of columns")
     M, K = a.shape
     N = w.shape[0]
@@ -602,16 +616,17 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
         if out_dtype not in _DTYPE_CODE:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
         out = torch.empty(M, N, dtype=out_dtype, device=a.device)
-    elif out.dtype not in _DTYPE_CODE:
+    dt = out.dtype
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
         raise ValueError("out must be bf16, fp16 or fp32")
     ld_a, ld_w = _matrix(a, "a", _E4M3, M, K), _matrix(w, "w", _E4M3, N, K)
     sa_row, sa_group = _scale_strides(a_scales, "a_scales", M, groups)
     sw_row, sw_group = _scale_strides(w_scales, "w_scales", -(-N // 128), groups)
-    ld_out = _matrix(out, "out", out.dtype, M, N)
-    _on_gpu(a, a_scales, w, w_scales, out, err_flags)
+    ld_out = _matrix(out, "out", dt, M, N)
     status = lib.kda_fp8_matmul(a.data_ptr(), ld_a, a_scales.data_ptr(), sa_row, sa_group, w.data_ptr(), ld_w,
-                                w_scales.data_ptr(), sw_row, sw_group, M, N, K, out.data_ptr(), ld_out,
-                                _DTYPE_CODE[out.dtype], _address(err_flags), _raw_stream(stream))
+                                w_scales.data_ptr(), sw_row, sw_group, M, N, K, out.data_ptr(), ld_out, code,
+                                _error_word(err_flags), _raw_stream(stream, a.device))
     if status:
         _check(status, "kda_fp8_matmul")
     return out
@@ -645,31 +660,26 @@ def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_page
         if num_tokens is None:
             raise ValueError("kda_batch_maps needs num_tokens or out")
         out = make_batch_maps(R, num_tokens, query_lens.device)
-    i32 = torch.int32
-    tokens = out.positions.shape[0]
+    order, cu, state_indices, num_decodes, positions, slot_map, free_left = out
+    tokens = positions.shape[0]
     if num_tokens is not None and num_tokens != tokens:
         raise ValueError("num_tokens must be the length of out.positions")
-    for t, name, n in ((query_lens, "query_lens", R), (context_lens, "context_lens", R), (free_pages, "free_pages", 0),
-                       (free_count, "free_count", 1), (out.order, "out.order", R),
-                       (out.cu_seqlens, "out.cu_seqlens", R + 1), (out.state_indices, "out.state_indices", R),
-                       (out.num_decodes, "out.num_decodes", 1), (out.positions, "out.positions", tokens),
-                       (out.free_left, "out.free_left", 1)):
-        _vector(t, name, i32, n)
-    _vector(out.slot_map, "out.slot_map", torch.int64, tokens)
-    if state_slots.dtype != i32 or state_slots.dim() != 1 or state_slots.shape[0] < R:
-        raise ValueError("state_slots must be a 1-D int32 tensor with an entry per request")
-    if block_table.dtype != i32 or block_table.dim() != 2 or block_table.shape[0] < R or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if state_slots.dtype is not _I32 or state_slots.dim() != 1 or state_slots.shape[0] < R or not state_slots.is_cuda:
+        raise ValueError("state_slots must be a 1-D int32 GPU tensor with an entry per request")
+    if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_cuda:
+        raise ValueError("block_table must be int32 [num_reqs, width] on the GPU")
+    rows, width = block_table.shape
+    table_stride, inner = block_table.stride()
+    if rows < R or (inner != 1 and width > 1):
         raise ValueError("block_table must be int32 [num_reqs, width] with unit inner stride")
-    width = block_table.shape[1]
-    _on_gpu(query_lens, context_lens, state_slots, block_table, free_pages, free_count, err_flags, *out)
-    status = lib.kda_batch_maps(query_lens.data_ptr(), context_lens.data_ptr(), state_slots.data_ptr(),
-                                state_slots.stride(0) if R > 1 else 1, R, block_table.data_ptr(),
-                                block_table.stride(0) if R > 1 else max(width, 1), width, free_pages.data_ptr(),
-                                free_pages.shape[0], free_count.data_ptr(), num_pages, page_size, tokens,
-                                out.order.data_ptr(), out.cu_seqlens.data_ptr(), out.state_indices.data_ptr(),
-                                out.num_decodes.data_ptr(), out.positions.data_ptr(), out.slot_map.data_ptr(),
-                                out.free_left.data_ptr(), _address(err_flags), _raw_stream(stream))
+    status = lib.kda_batch_maps(
+        _vector(query_lens, "query_lens", _I32, R), _vector(context_lens, "context_lens", _I32, R), state_slots.data_ptr(),
+        state_slots.stride(0) if R > 1 else 1, R, block_table.data_ptr(), table_stride if R > 1 else max(width, 1), width,
+        _vector(free_pages, "free_pages", _I32, 0), free_pages.shape[0], _vector(free_count, "free_count", _I32, 1), num_pages,
+        page_size, tokens, _vector(order, "out.order", _I32, R), _vector(cu, "out.cu_seqlens", _I32, R + 1),
+        _vector(state_indices, "out.state_indices", _I32, R), _vector(num_decodes, "out.num_decodes", _I32, 1),
+        _vector(positions, "out.positions", _I32, 0), _vector(slot_map, "out.slot_map", _I64, tokens),
+        _vector(free_left, "out.free_left", _I32, 1), _error_word(err_flags), _raw_stream(stream, query_lens.device))
     if status:
         _check(status, "kda_batch_maps")
     return out
