@@ -64,6 +64,12 @@ __device__ __forceinline__ Lens load_lens(const BatchMapsParams &p, int r)
     return l;
 }
 
+// ceil(n / d), both below 2^31
+__device__ __forceinline__ int32_t ceil_div(int32_t n, int32_t d)
+{
+    return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(d) - 1u) / static_cast<uint32_t>(d));
+}
+
 __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMapsParams p)
 {
     extern __shared__ int32_t own[];   // per token row of this CTA: request (-1: not its first row here)
@@ -78,12 +84,19 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
     for (int i = threadIdx.x; i < rows; i += blockDim.x) own[i] = -1;
     const int step = kItems * blockDim.x;
     // the decodes, all of them, before anything can be placed
-    int64_t nd = 0;
-    for (int r0 = 0; r0 < p.R; r0 += step)
+    Lens first[kItems];   // the first step's lengths stay for the scan
+    int32_t nd = 0;
+#pragma unroll
+    for (int i = 0; i < kItems; i++) {
+        first[i] = load_lens(p, threadIdx.x * kItems + i);
+        nd += first[i].q == 1;
+    }
+    for (int r0 = step; r0 < p.R; r0 += step)
 #pragma unroll
         for (int i = 0; i < kItems; i++) nd += load_lens(p, r0 + threadIdx.x * kItems + i).q == 1;
-    int64_t D;
-    block_exclusive(nd, part, &D);
+    int32_t D32;
+    block_exclusive(nd, reinterpret_cast<int32_t *>(part), &D32);
+    const int64_t D = D32;
 
     int64_t d_done = 0, t_done = 0, p_done = 0;
     for (int r0 = 0; r0 < p.R; r0 += step) {
@@ -93,7 +106,7 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
         int64_t mine = 0, pages = 0, pages_of[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; i++) {
-            l[i] = load_lens(p, r0 + threadIdx.x * kItems + i);
+            l[i] = r0 == 0 ? first[i] : load_lens(p, r0 + threadIdx.x * kItems + i);
             mine += l[i].q == 1 ? (int64_t(1) << 44) : l[i].q;
         }
         int64_t total;
@@ -120,8 +133,7 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
                 p.state_indices[s] = p.slots[r * p.slot_stride];
             }
             l[i].q = static_cast<int32_t>(ce - cs);
-            const int64_t last = static_cast<int64_t>(l[i].c) + l[i].q;
-            int64_t old = (static_cast<int64_t>(l[i].c) + p.page - 1) / p.page, now = (last + p.page - 1) / p.page;
+            int64_t old = ceil_div(l[i].c, p.page), now = ceil_div(l[i].c + l[i].q, p.page);
             if (now > p.width) { if (l[i].q > 0) err |= kErrPages; now = p.width; }
             pages_of[i] = now > old ? now - old : 0;
             pages += pages_of[i];
@@ -173,7 +185,12 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
     __syncthreads();
     int before = __shfl_up_sync(0xffffffffu, inc, 1);
     if (lane == 0) before = -1;
-    for (int w = 0; w < warp; w++) before = max(before, wpart[w]);
+    if (warp > 0) {   // the warps before this one, of 32 at most
+        int w = lane < warp ? wpart[lane] : -1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+        before = max(before, w);
+    }
     const int64_t live = D + t_done < N ? D + t_done : N;
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
@@ -186,8 +203,7 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
             const int r = own[o];
             const int32_t c = p.clen[r];
             pos = c + static_cast<int32_t>(t - own_start[o]);
-            const int64_t j = pos / p.page, old = (static_cast<int64_t>(c) + p.page - 1) / p.page;
-            const int off = pos % p.page;
+            const int32_t j = pos / p.page, old = ceil_div(c, p.page), off = pos - j * p.page;
             int32_t page = -1;
             if (j < p.width) {
                 int32_t *entry = p.table + r * p.table_stride + j;
