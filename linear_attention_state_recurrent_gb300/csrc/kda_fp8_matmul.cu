@@ -182,7 +182,7 @@ struct Thin {
     static constexpr int COLS = NT * 4 / EW;                // columns (rows of A) per epilogue thread
     static constexpr int NBUF = 4;                          // accumulators in tensor memory
     static constexpr int STAGE = 128 * BK + NT * BK;
-    static constexpr int STAGES = NT > 32 ? 4 : 5;
+    static constexpr int STAGES = NT > 32 ? 4 : NT > 16 ? 5 : 6;
     static constexpr int SR = 8, SLOT = NT + 4;             // groups of scales in flight: NT rows' and the tile's of W
     static constexpr int SMEM = 1024 + STAGES * STAGE;      // two CTAs per SM
 };
@@ -207,6 +207,17 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     auto sfull = [&](int r) { return b0 + (2 * C::STAGES + 2 * C::NBUF + r) * 8; };
     auto sempty = [&](int r) { return b0 + (2 * C::STAGES + 2 * C::NBUF + C::SR + r) * 8; };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = blockIdx.x % split;
+    const int n0 = blockIdx.x / split * 128, t0 = blockIdx.y * NT;
+    const int groups = (p.K + BK - 1) / BK;
+    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / split);
+    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / split);
+    auto load = [&](int g, int s) {
+        const uint32_t at = ring + s * C::STAGE;
+        tc::mbar_expect_tx(full(s), C::STAGE);
+        tc::tma_load_2d(at, &tm_w, g * BK, n0, full(s));
+        tc::tma_load_2d(at + 128 * BK, &tm_a, g * BK, t0, full(s));
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
         for (int b = 0; b < C::NBUF; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), C::EW); }
@@ -215,6 +226,10 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         tc::prefetch_tensormap(&tm_a);
     }
     pdl_wait();
+    // the ring's first turn needs nothing but its barriers, which this thread has made
+    const int ahead = min(C::STAGES, g1 - g0);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < ahead; i++) load(g0 + i, i);
     // tensor memory is taken before the next grid may start: it could hold what this one waits for
     if (warp == 1) tc::tmem_alloc<C::NBUF * NT>(tc::smem_addr(&tmem_base));
     tc::fence_before_sync();
@@ -223,21 +238,13 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     pdl_release();
 
     const uint32_t tmem = tmem_base;
-    const int rank = blockIdx.x % split;
-    const int n0 = blockIdx.x / split * 128, t0 = blockIdx.y * NT;
-    const int groups = (p.K + BK - 1) / BK;
-    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / split);
-    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / split);
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
-            uint32_t phase = 1;
-            for (int g = g0; g < g1; g++) {
+            uint32_t phase = 0;
+            for (int g = g0 + ahead; g < g1; g++) {
                 if (!wait_phase(empty(s), phase)) { report(p); break; }
-                const uint32_t at = ring + s * C::STAGE;
-                tc::mbar_expect_tx(full(s), C::STAGE);
-                tc::tma_load_2d(at, &tm_w, g * BK, n0, full(s));
-                tc::tma_load_2d(at + 128 * BK, &tm_a, g * BK, t0, full(s));
+                load(g, s);
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
         }
@@ -419,10 +426,18 @@ slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     auto sempty = [&](int r) { return b0 + (2 * C::MAX_STAGES + 2 * C::MAX_BUF + C::SR + r) * 8; };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = blockIdx.x % q.split;
+    const int groups = (p.K + BK - 1) / BK;
+    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / q.split);
+    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / q.split);
     const int n0 = blockIdx.x / q.split * q.bn, m0 = blockIdx.y * 128;
     const int rows = min(128, p.M - m0);                       // live rows of A
     const int chunks = q.bn / 16, per = (chunks + 3) / 4;      // of 16 columns, per strip
     const int working = (rows + 31) / 32 * ((chunks + per - 1) / per);   // epilogue warps with something to do
+    auto load = [&](int g, int s) {
+        tc::mbar_expect_tx(full(s), (q.rows + q.bn) * BK);
+        tc::tma_load_2d(wring + s * q.bn * BK, &tm_w, g * BK, n0, full(s));
+        tc::tma_load_2d(ring + s * q.rows * BK, &tm_a, g * BK, m0, full(s));
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < q.stages; s++) { tc::mbar_init(full(s), 1); tc::mbar_init(empty(s), 1); }
         for (int b = 0; b < q.nbuf; b++) { tc::mbar_init(tfull(b), 1); tc::mbar_init(tempty(b), working); }
@@ -431,6 +446,10 @@ slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         tc::prefetch_tensormap(&tm_a);
     }
     pdl_wait();
+    // the ring's first turn needs nothing but its barriers, which this thread has made
+    const int ahead = min(q.stages, g1 - g0);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < ahead; i++) load(g0 + i, i);
     // tensor memory is taken before the next grid may start: it could hold what this one waits for
     if (warp == 1) tc::tmem_alloc<512>(b0 + (2 * C::MAX_STAGES + 2 * C::MAX_BUF + 2 * C::SR) * 8);
     tc::fence_before_sync();
@@ -439,20 +458,15 @@ slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     pdl_release();
 
     const uint32_t tmem = *tmem_base;
-    const int groups = (p.K + BK - 1) / BK;
-    const int g0 = static_cast<int>(static_cast<int64_t>(groups) * rank / q.split);
-    const int g1 = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / q.split);
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(C::REGS_CONTROL));
         if (warp == 0) {
             if (lane == 0) {
                 int s = 0;
-                uint32_t phase = 1;
-                for (int g = g0; g < g1; g++) {
+                uint32_t phase = 0;
+                for (int g = g0 + ahead; g < g1; g++) {
                     if (!wait_phase(empty(s), phase)) { report(p); break; }
-                    tc::mbar_expect_tx(full(s), (q.rows + q.bn) * BK);
-                    tc::tma_load_2d(wring + s * q.bn * BK, &tm_w, g * BK, n0, full(s));
-                    tc::tma_load_2d(ring + s * q.rows * BK, &tm_a, g * BK, m0, full(s));
+                    load(g, s);
                     if (++s == q.stages) { s = 0; phase ^= 1; }
                 }
             }
@@ -1007,26 +1021,39 @@ double plan_time(int64_t ctas, int fit, int groups, int split, double hbm_bytes,
     return waves * (3000. + step * ((groups + split - 1) / split) + (split > 1 ? 1500. : 0.));
 }
 
+// The split of least time.
 template <int NT>
-cudaError_t run_thin(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cudaStream_t stream)
+double plan_thin(const Fp8Params &p, const Fit &fit, int *split)
 {
     using C = Thin<NT>;
-    static const Fit fit(thin_kernel<NT>, C::THREADS, C::SMEM, sms, 2);
-    if (fit.status != cudaSuccess) return fit.status;
     const int groups = (p.K + BK - 1) / BK, tiles_n = (p.N - 1) / 128 + 1, tiles_t = (p.M + NT - 1) / NT;
-    int split = 1;
     double least = 1e30;
     for (int k = 1; k <= 8 && k <= groups; k++) {
         if (fit.ctas[k] == 0) continue;
         const double t = plan_time(static_cast<int64_t>(tiles_n) * tiles_t * k, fit.ctas[k], groups, k, 128. * BK / tiles_t, 2. * C::STAGE,
-                                   300. + NT);
-        if (t < least) { least = t; split = k; }
+                                   NT > 32 ? 590. : NT > 16 ? 400. : 320.);
+        if (t < least) { least = t; *split = k; }
     }
+    return least;
+}
+
+template <int NT>
+const Fit &fit_thin(int sms)
+{
+    static const Fit fit(thin_kernel<NT>, Thin<NT>::THREADS, Thin<NT>::SMEM, sms, 2);
+    return fit;
+}
+
+template <int NT>
+cudaError_t run_thin(const Fp8Params &p, int split, int64_t ld_a, int64_t ld_w, cudaStream_t stream)
+{
+    using C = Thin<NT>;
     CUtensorMap tw, ta;
     cudaError_t e;
     if ((e = encode(&tw, p.w, p.K, p.N, ld_w, 128)) != cudaSuccess) return e;
     if ((e = encode(&ta, p.a, p.K, p.M, ld_a, NT)) != cudaSuccess) return e;
-    Launch l(dim3(static_cast<unsigned>(tiles_n) * split, static_cast<unsigned>(tiles_t)), C::THREADS, C::SMEM, split, stream);
+    Launch l(dim3(static_cast<unsigned>((p.N - 1) / 128 + 1) * split, static_cast<unsigned>((p.M + NT - 1) / NT)), C::THREADS, C::SMEM, split,
+             stream);
     return cudaLaunchKernelEx(&l.cfg, thin_kernel<NT>, ta, tw, p, split);
 }
 
@@ -1046,7 +1073,7 @@ double plan_slim(const Fp8Params &p, const Fit &fit, SlimPlan *best)
         if (split > 1 && (bn + 1) * rows * 4 > Slim::RING) continue;
         const int64_t ctas = static_cast<int64_t>((p.N - 1) / bn + 1) * split * mt;
         const double t = plan_time(ctas, fit.ctas[split], groups, split, static_cast<double>(bn) * BK / mt,
-                                   static_cast<double>(rows + bn) * BK, 250. + 40. * ((bn / 16 + 3) / 4));
+                                   static_cast<double>(rows + bn) * BK, 380. + 65. * ((bn / 16 + 3) / 4));
         if (t < least) {
             least = t;
             best->bn = bn;
@@ -1115,17 +1142,33 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    if (p.M <= 16) return run_thin<16>(p, ld_a, ld_w, sms, stream);
-    if (p.M <= 32) return run_thin<32>(p, ld_a, ld_w, sms, stream);
-    if (p.M <= 64) return run_thin<64>(p, ld_a, ld_w, sms, stream);
-    // the wide kernel's time by the same measure: 500 ns per group and wave of tiles
+    int split = 1;
+    if (p.M <= 16) {
+        const Fit &f = fit_thin<16>(sms);
+        if (f.status != cudaSuccess) return f.status;
+        plan_thin<16>(p, f, &split);
+        return run_thin<16>(p, split, ld_a, ld_w, stream);
+    }
+    if (p.M <= 32) {
+        const Fit &f = fit_thin<32>(sms);
+        if (f.status != cudaSuccess) return f.status;
+        plan_thin<32>(p, f, &split);
+        return run_thin<32>(p, split, ld_a, ld_w, stream);
+    }
+    // More rows: the arrangement of least time; the wide kernel's is 485 ns per group and wave of tiles.
+    if (p.M > 1024) return run_wide(p, ld_a, ld_w, sms, stream);
     static const Fit fit(slim_kernel<4>, Slim::THREADS, SLIM_SMEM, sms, 1);
     if (fit.status != cudaSuccess) return fit.status;
+    SlimPlan q;
+    const double slim = plan_slim(p, fit, &q);
+    if (p.M <= 64) {
+        const Fit &f = fit_thin<64>(sms);
+        if (f.status != cudaSuccess) return f.status;
+        if (plan_thin<64>(p, f, &split) <= slim) return run_thin<64>(p, split, ld_a, ld_w, stream);
+    }
     const int groups = (p.K + BK - 1) / BK;
     const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * ((static_cast<int64_t>(p.N) + 255) / 256);
-    const double wide = 4000. + 500. * groups * static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
-    SlimPlan q;
-    if (p.M > 1024 || plan_slim(p, fit, &q) > wide) return run_wide(p, ld_a, ld_w, sms, stream);
+    if (3000. + 485. * groups * static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) < slim) return run_wide(p, ld_a, ld_w, sms, stream);
     const int per = (q.bn / 16 + 3) / 4;
     if (per <= 1) return run_slim<1>(p, q, ld_a, ld_w, stream);
     if (per <= 2) return run_slim<2>(p, q, ld_a, ld_w, stream);
