@@ -1009,16 +1009,14 @@ struct Fit {
     }
 };
 
-// Time of a plan in nanoseconds: start and end, then for every wave of CTAs and group of 128 k the largest
-// of what HBM (6.6 kB/ns over all SMs), L2 (110 B/ns into one SM) and the epilogue need; a split adds its
-// join. Measured rates and latencies, to compare plans with.
-double plan_time(int64_t ctas, int fit, int groups, int split, double hbm_bytes, double l2_bytes, double epilogue)
+// The plans are compared by their time in nanoseconds, from what was measured for N of 1024 to 20512,
+// K of 1024 to 8192 and M of 16 to 512 with every split (the choice is within 10% of the best of
+// them): start and end of a wave of CTAs, then its groups of 128 k, each by the slower of the epilogue and the
+// streams (5.7 kB/ns from HBM over all SMs), then the join of a split.
+double plan_time(int64_t ctas, int fit, int groups, int split, double start, double step, double join)
 {
-    const double waves = static_cast<double>((ctas + fit - 1) / fit), at_once = ctas < fit ? ctas : fit;
-    double step = at_once * hbm_bytes / 6600.;
-    if (step < l2_bytes / 110.) step = l2_bytes / 110.;
-    if (step < epilogue) step = epilogue;
-    return waves * (3000. + step * ((groups + split - 1) / split) + (split > 1 ? 1500. : 0.));
+    const double waves = static_cast<double>((ctas + fit - 1) / fit);
+    return waves * (start + step * ((groups + split - 1) / split)) + (split > 1 ? join : 0.);
 }
 
 // The split of least time.
@@ -1030,8 +1028,13 @@ double plan_thin(const Fp8Params &p, const Fit &fit, int *split)
     double least = 1e30;
     for (int k = 1; k <= 8 && k <= groups; k++) {
         if (fit.ctas[k] == 0) continue;
-        const double t = plan_time(static_cast<int64_t>(tiles_n) * tiles_t * k, fit.ctas[k], groups, k, 128. * BK / tiles_t, 2. * C::STAGE,
-                                   NT > 32 ? 590. : NT > 16 ? 400. : 320.);
+        const int64_t ctas = static_cast<int64_t>(tiles_n) * tiles_t * k;
+        const double at_once = ctas < fit.ctas[k] ? ctas : fit.ctas[k], hbm = at_once * 128 * BK / tiles_t / 5700.;
+        const double l2 = (at_once > fit.ctas[1] / 2 ? 2 : 1) * C::STAGE / 85.;      // into one SM, of one CTA or two
+        double step = NT > 32 ? 322. : NT > 16 ? 288. : 281.;
+        if (step < hbm) step = hbm;
+        if (step < l2) step = l2;
+        const double t = plan_time(ctas, fit.ctas[k], groups, k, NT > 32 ? 4000. : NT > 16 ? 3200. : 2700., step, 1100.);
         if (t < least) { least = t; *split = k; }
     }
     return least;
@@ -1072,8 +1075,7 @@ double plan_slim(const Fp8Params &p, const Fit &fit, SlimPlan *best)
         bn = bn > 256 ? 256 : (bn + 15) / 16 * 16;
         if (split > 1 && (bn + 1) * rows * 4 > Slim::RING) continue;
         const int64_t ctas = static_cast<int64_t>((p.N - 1) / bn + 1) * split * mt;
-        const double t = plan_time(ctas, fit.ctas[split], groups, split, static_cast<double>(bn) * BK / mt,
-                                   static_cast<double>(rows + bn) * BK, 380. + 65. * ((bn / 16 + 3) / 4));
+        const double t = plan_time(ctas, fit.ctas[split], groups, split, 3400., 250. + 2.05 * bn, 1300. + 0.125 * rows * bn);
         if (t < least) {
             least = t;
             best->bn = bn;
@@ -1155,7 +1157,7 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
         plan_thin<32>(p, f, &split);
         return run_thin<32>(p, split, ld_a, ld_w, stream);
     }
-    // More rows: the arrangement of least time; the wide kernel's is 485 ns per group and wave of tiles.
+    // More rows: the arrangement of least time.
     if (p.M > 1024) return run_wide(p, ld_a, ld_w, sms, stream);
     static const Fit fit(slim_kernel<4>, Slim::THREADS, SLIM_SMEM, sms, 1);
     if (fit.status != cudaSuccess) return fit.status;
@@ -1168,7 +1170,10 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
     }
     const int groups = (p.K + BK - 1) / BK;
     const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * ((static_cast<int64_t>(p.N) + 255) / 256);
-    if (3000. + 485. * groups * static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) < slim) return run_wide(p, ld_a, ld_w, sms, stream);
+    const int pairs = sms / 2;
+    const double busy = tiles < pairs ? static_cast<double>(tiles) / pairs : 1.;
+    if (6000. + (340. + 100. * busy) * groups * static_cast<double>((tiles + pairs - 1) / pairs) < slim)
+        return run_wide(p, ld_a, ld_w, sms, stream);
     const int per = (q.bn / 16 + 3) / 4;
     if (per <= 1) return run_slim<1>(p, q, ld_a, ld_w, stream);
     if (per <= 2) return run_slim<2>(p, q, ld_a, ld_w, stream);
