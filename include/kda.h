@@ -406,7 +406,7 @@ int kda_norm_quant(const void *x, int64_t ld_x, const void *residual, int64_t ld
  * Operands whose base and row pitch are multiples of 16 bytes take the tensor cores; others
  * are computed by a slower kernel with the same result up to fp32 rounding. Columns K .. ld
  * of a and w are never read. M, N and K may be any size >= 1 (K = 0: zeros; M or N = 0:
- * nothing to do), up to 2^31 - 1 each. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT
+ * nothing to do), up to 2^30 each. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT
  * in *err_flags (may be NULL) and leaves its tile unwritten.
  */
 int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,

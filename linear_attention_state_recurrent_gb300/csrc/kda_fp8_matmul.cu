@@ -17,6 +17,7 @@
 // Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
 #include <climits>
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -992,20 +993,20 @@ struct Launch {
 // fit their GPC), asked once.
 struct Fit {
     int ctas[9] = {};
-    cudaError_t status = cudaSuccess;
     template <typename K>
-    Fit(K kernel, int threads, int smem, int sms, int per_sm)
+    cudaError_t ask(K kernel, int threads, int smem, int sms, int per_sm)
     {
-        status = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         ctas[1] = sms * per_sm;
-        for (int split = 2; split <= 8 && status == cudaSuccess; split++) {
+        for (int split = 2; split <= 8 && e == cudaSuccess; split++) {
             Launch l(dim3(split), threads, smem, split, nullptr);
             l.at[0] = l.at[1];   // the cluster alone
             l.cfg.numAttrs = 1;
             int n = 0;
-            status = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg);
             ctas[split] = n * split;
         }
+        return e;
     }
 };
 
@@ -1038,13 +1039,6 @@ double plan_thin(const Fp8Params &p, const Fit &fit, int *split)
         if (t < least) { least = t; *split = k; }
     }
     return least;
-}
-
-template <int NT>
-const Fit &fit_thin(int sms)
-{
-    static const Fit fit(thin_kernel<NT>, Thin<NT>::THREADS, Thin<NT>::SMEM, sms, 2);
-    return fit;
 }
 
 template <int NT>
@@ -1092,8 +1086,6 @@ double plan_slim(const Fp8Params &p, const Fit &fit, SlimPlan *best)
 template <int MAXC>
 cudaError_t run_slim(const Fp8Params &p, const SlimPlan &q, int64_t ld_a, int64_t ld_w, cudaStream_t stream)
 {
-    static const cudaError_t attr = cudaFuncSetAttribute(slim_kernel<MAXC>, cudaFuncAttributeMaxDynamicSharedMemorySize, SLIM_SMEM);
-    if (attr != cudaSuccess) return attr;
     CUtensorMap tw, ta;
     cudaError_t e;
     if ((e = encode(&tw, p.w, p.K, p.N, ld_w, q.bn)) != cudaSuccess) return e;
@@ -1114,21 +1106,47 @@ cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cu
     const CUtensorMapDataType type = p.out_dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                      : p.out_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     if (tma_out && (e = encode(&to, p.out, p.N, p.M, p.ld_out, 32, type, es)) != cudaSuccess) return e;
-    static const cudaError_t attr = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide::SMEM);
-    if (attr != cudaSuccess) return attr;
-    const Tiles t{(p.M + 255) / 256, (p.N + 255) / 256, 16};
+    const Tiles t{(p.M - 1) / 256 + 1, (p.N - 1) / 256 + 1, 16};
     const int64_t total = static_cast<int64_t>(t.m) * t.n;
     if (total > INT32_MAX - 4096) return cudaErrorInvalidConfiguration;
     const int pairs = static_cast<int>(total < sms / 2 ? total : sms / 2);
     return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, to, tma_out, p, t);
 }
 
-cudaError_t sm_count(int *sms)
+// What the launches need to know of a device, and the kernels' shared-memory limits set there, once.
+struct Device {
+    int sms = 0;
+    Fit thin16, thin32, thin64, slim;
+    cudaError_t status = cudaSuccess;
+    void ask(int dev)
+    {
+        cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        const auto limit = [](auto kernel, int smem) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        };
+        if (e == cudaSuccess) e = thin16.ask(thin_kernel<16>, Thin<16>::THREADS, Thin<16>::SMEM, sms, 2);
+        if (e == cudaSuccess) e = thin32.ask(thin_kernel<32>, Thin<32>::THREADS, Thin<32>::SMEM, sms, 2);
+        if (e == cudaSuccess) e = thin64.ask(thin_kernel<64>, Thin<64>::THREADS, Thin<64>::SMEM, sms, 2);
+        if (e == cudaSuccess) e = slim.ask(slim_kernel<4>, Slim::THREADS, SLIM_SMEM, sms, 1);
+        if (e == cudaSuccess) e = limit(slim_kernel<1>, SLIM_SMEM);
+        if (e == cudaSuccess) e = limit(slim_kernel<2>, SLIM_SMEM);
+        if (e == cudaSuccess) e = limit(wide_kernel, Wide::SMEM);
+        status = e;
+    }
+};
+
+cudaError_t this_device(const Device **out)
 {
+    constexpr int MOST = 64;
+    static Device devices[MOST];
+    static std::once_flag asked[MOST];
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev < 0 || dev >= MOST) return cudaErrorInvalidDevice;
+    std::call_once(asked[dev], [&] { devices[dev].ask(dev); });
+    *out = &devices[dev];
+    return devices[dev].status;
 }
 
 }  // namespace
@@ -1141,39 +1159,29 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
         if (tm * tn > INT32_MAX) return cudaErrorInvalidConfiguration;
         return launch_pdl(general_kernel, dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, p, static_cast<int>(tn));
     }
-    int sms = 0;
-    cudaError_t e = sm_count(&sms);
+    const Device *d = nullptr;
+    const cudaError_t e = this_device(&d);
     if (e != cudaSuccess) return e;
     int split = 1;
     if (p.M <= 16) {
-        const Fit &f = fit_thin<16>(sms);
-        if (f.status != cudaSuccess) return f.status;
-        plan_thin<16>(p, f, &split);
+        plan_thin<16>(p, d->thin16, &split);
         return run_thin<16>(p, split, ld_a, ld_w, stream);
     }
     if (p.M <= 32) {
-        const Fit &f = fit_thin<32>(sms);
-        if (f.status != cudaSuccess) return f.status;
-        plan_thin<32>(p, f, &split);
+        plan_thin<32>(p, d->thin32, &split);
         return run_thin<32>(p, split, ld_a, ld_w, stream);
     }
     // More rows: the arrangement of least time.
-    if (p.M > 1024) return run_wide(p, ld_a, ld_w, sms, stream);
-    static const Fit fit(slim_kernel<4>, Slim::THREADS, SLIM_SMEM, sms, 1);
-    if (fit.status != cudaSuccess) return fit.status;
+    if (p.M > 1024) return run_wide(p, ld_a, ld_w, d->sms, stream);
     SlimPlan q;
-    const double slim = plan_slim(p, fit, &q);
-    if (p.M <= 64) {
-        const Fit &f = fit_thin<64>(sms);
-        if (f.status != cudaSuccess) return f.status;
-        if (plan_thin<64>(p, f, &split) <= slim) return run_thin<64>(p, split, ld_a, ld_w, stream);
-    }
+    const double slim = plan_slim(p, d->slim, &q);
+    if (p.M <= 64 && plan_thin<64>(p, d->thin64, &split) <= slim) return run_thin<64>(p, split, ld_a, ld_w, stream);
     const int groups = (p.K + BK - 1) / BK;
     const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * ((static_cast<int64_t>(p.N) + 255) / 256);
-    const int pairs = sms / 2;
+    const int pairs = d->sms / 2;
     const double busy = tiles < pairs ? static_cast<double>(tiles) / pairs : 1.;
     if (6000. + (340. + 100. * busy) * groups * static_cast<double>((tiles + pairs - 1) / pairs) < slim)
-        return run_wide(p, ld_a, ld_w, sms, stream);
+        return run_wide(p, ld_a, ld_w, d->sms, stream);
     const int per = (q.bn / 16 + 3) / 4;
     if (per <= 1) return run_slim<1>(p, q, ld_a, ld_w, stream);
     if (per <= 2) return run_slim<2>(p, q, ld_a, ld_w, stream);

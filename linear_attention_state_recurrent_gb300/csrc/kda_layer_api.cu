@@ -65,8 +65,10 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
 {
     int s;
     if ((s = check_dtype(out_dtype, "out_dtype"))) return s;
-    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
-        return invalid("M, N and K must be in [0, 2^31)");
+    constexpr int64_t most = int64_t(1) << 30;   // tile ends past a side stay below 2^31
+    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most) return invalid("M, N and K must be in [0, 2^30]");
+    if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX)
+        return set_error(KDA_ERR_UNSUPPORTED, "%lld x %lld outputs exceed one launch: split the call", (long long)M, (long long)N);
     if (M == 0 || N == 0) return set_error(KDA_OK, "%s", "");
     if (!out) return invalid("out must be non-NULL");
     if (K > 0 && (!a || !a_scales || !w || !w_scales)) return invalid("a, w and their scales must be non-NULL");

@@ -179,3 +179,9 @@ def test_batch_maps_binding_refuses(kda):
 def test_status_of_a_refusal_reaches_the_caller(kda):
     assert _maps(kda, page=0) == 1
     assert "page_size" in ctypes.cast(kda.lib.kda_last_error(), ctypes.c_char_p).value.decode()
+
+
+def test_fp8_matmul_refuses_what_one_launch_cannot_cover(kda):
+    side = 1 << 30
+    assert _matmul(kda, M=side, N=side, ld_out=side) == 2 and "split" in kda.last_error()
+    assert _matmul(kda, M=side + 1) == 1

@@ -237,6 +237,31 @@ def test_fp8_matmul_unaligned_bases_and_views(kda, M):
     assert torch.all(buf[:, :3] == 9) and torch.all(buf[:, 304:] == 9)
 
 
+ARRANGEMENTS = [(24, 300, 640), (60, 500, 300), (60, 9000, 140), (100, 300, 640), (300, 1500, 300), (700, 4200, 140), (1500, 600, 260)]
+
+
+@pytest.mark.parametrize("M,N,K", ARRANGEMENTS)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_fp8_matmul_every_arrangement(kda, M, N, K, dtype, aligned):
+    """Each way a call may be cut up, with outputs on and off 16-byte boundaries and scales in either order."""
+    a, sa, w, sw = operands(M, N, K, M, (up16(K), up16(K)), group_major=aligned)
+    edge = 16 if aligned else 5
+    buf = torch.full((M, N + 2 * edge + up16(N) * aligned), 9.0, dtype=dtype, device="cuda")
+    check_matmul(kda, a, sa, w, sw, out=buf[:, edge:edge + N])
+    assert torch.all(buf[:, :edge] == 9) and torch.all(buf[:, edge + N:] == 9)
+
+
+@pytest.mark.parametrize("M,N,K", ARRANGEMENTS)
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_fp8_matmul_rounds_the_fp32_result_once(kda, M, N, K, dtype):
+    """How a call is cut up does not depend on the output's type, so a 16-bit output is the fp32 one, rounded."""
+    a, sa, w, sw = operands(M, N, K, M, (up16(K), up16(K)))
+    sa, sw = sa * 1e-4, sw * 1e-2
+    full = kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=FP32)
+    assert torch.equal(kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=dtype), full.to(dtype))
+
+
 def test_fp8_matmul_split_of_a_long_inner_axis(kda):
     for M in (1, 20, 130):
         a, sa, w, sw = operands(M, 40, 16384 + 48, 8)
