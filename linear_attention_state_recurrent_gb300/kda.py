@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -491,67 +492,28 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
 
 
 # ---- the operators around the recurrence -------------------------------------------------
-# These run in a few microseconds, less than a careless wrapper costs: the checks below touch
-# each property of a tensor once, and say what is wrong only after something is.
+# Their wrappers' checks are in the compiled module _kda_torch: these kernels run in a few
+# microseconds, less than such checks cost in Python.
 
-_DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_E4M3, _F32, _I32, _I64 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.int64
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 
 
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _current_raw_stream(device.index or 0)
+def _load_torch_binding():
+    path = os.path.join(os.path.dirname(_LIB_PATH), "_kda_torch.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_kda_torch.so is not built ({path}); run "
+                           "`python -c 'import __graft_entry__ as g; g.build()'` first")
+    spec = importlib.util.spec_from_file_location("_kda_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
-def _refuse(t, name, dtype, shape, layout):
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
-    raise ValueError(f"{name} must have {layout}")
+_torch_binding = _load_torch_binding()
 
 
-def _matrix(t, name, dtype, rows, cols):
-    """The row stride of a 2-D GPU tensor of the given type and shape with unit inner stride."""
-    if t.dtype is dtype and t.shape == (rows, cols) and t.is_cuda:
-        ld, inner = t.stride()
-        if inner == 1 or cols <= 1:
-            return ld if rows > 1 or ld > cols else cols   # the stride of a single row says nothing
-    _refuse(t, name, dtype, (rows, cols), "unit inner stride")
-
-
-def _scale_strides(t, name, rows, groups):
-    if t.dtype is _F32 and t.shape == (rows, groups) and t.is_cuda:
-        a, b = t.stride()
-        return (a if rows > 1 else 1), (b if groups > 1 else 1)
-    _refuse(t, name, _F32, (rows, groups), "two strides")
-
-
-def _vector(t, name, dtype, n):
-    """The address of a contiguous 1-D GPU tensor of at least n entries."""
-    if t.dtype is dtype and t.dim() == 1 and t.shape[0] >= n and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous 1-D {dtype} GPU tensor of at least {n} entries")
-
-
-def _error_word(t):
-    if t is None:
-        return None
-    if t.element_size() != 4 or t.numel() < 1 or not t.is_cuda:
-        raise ValueError("err_flags must be a 32-bit integer GPU tensor")
-    return t.data_ptr()
-
-
-def _rows16(rows, cols, dtype, device):
-    """An uninitialised [rows, cols] view whose rows start on 16-byte boundaries."""
-    per = 16 // dtype.itemsize
-    return torch.empty(rows, -(-cols // per) * per, dtype=dtype, device=device)[:, :cols]
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None, y=None, q=None,
@@ -565,39 +527,10 @@ def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None
     fp32 [N, ceil(D / 128)], any strides. What is not given is allocated: q with rows on 16-byte
     boundaries and scales with the rows next to each other (the layouts kda_fp8_matmul reads fastest).
     Returns (q, scales, residual_out), residual_out None without a residual."""
-    dt = x.dtype
-    code = _DTYPE_CODE.get(dt)
-    if code is None or x.dim() != 2:
-        raise ValueError("x must be a 2-D bf16, fp16 or fp32 tensor")
-    N, D = x.shape
-    groups = -(-D // 128)
-    ld_x = _matrix(x, "x", dt, N, D)
-    if q is None:
-        q = _rows16(N, D, _E4M3, x.device)
-    if scales is None:
-        scales = torch.empty(groups, N, dtype=_F32, device=x.device).t()
-    res_p = ro_p = y_p = w_p = None
-    ld_res = ld_ro = ld_y = 0
-    if residual is not None:
-        if residual_out is None:
-            residual_out = torch.empty(N, D, dtype=dt, device=x.device)
-        ld_res, res_p = _matrix(residual, "residual", dt, N, D), residual.data_ptr()
-        ld_ro, ro_p = _matrix(residual_out, "residual_out", dt, N, D), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    if weight is not None:
-        if weight.dim() != 1 or weight.shape[0] != D:
-            raise ValueError(f"weight must have {D} entries")
-        w_p = _vector(weight, "weight", _F32, D)
-    if y is not None:
-        ld_y, y_p = _matrix(y, "y", dt, N, D), y.data_ptr()
-    s_row, s_group = _scale_strides(scales, "scales", N, groups)
-    ld_q = _matrix(q, "q", _E4M3, N, D)
-    status = lib.kda_norm_quant(x.data_ptr(), ld_x, res_p, ld_res, code, w_p, eps, N, D, ro_p, ld_ro, y_p, ld_y,
-                                q.data_ptr(), ld_q, scales.data_ptr(), s_row, s_group, _raw_stream(stream, x.device))
-    if status:
-        _check(status, "kda_norm_quant")
-    return q, scales, residual_out
+    r = _torch_binding.norm_quant(x, weight, eps, residual, residual_out, y, q, scales, _handle(stream))
+    if type(r) is int:
+        _check(r, "kda_norm_quant")
+    return r
 
 
 def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat16, err_flags=None, stream=None):
@@ -607,29 +540,14 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
     fp32 [ceil(N / 128), ceil(K / 128)], any strides. out: bf16, fp16 or fp32 [M, N] (allocated as
     out_dtype when not given). Operands with rows on 16-byte boundaries take the tensor cores.
     Returns out."""
-    if a.dim() != 2 or w.dim() != 2:
-        raise ValueError("a and w must be 2-D with the same number of columns")
-    M, K = a.shape
-    N = w.shape[0]
-    groups = -(-K // 128)
     if out is None:
-        if out_dtype not in _DTYPE_CODE:
+        if out_dtype not in _FLOATS:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
-        out = torch.empty(M, N, dtype=out_dtype, device=a.device)
-    dt = out.dtype
-    code = _DTYPE_CODE.get(dt)
-    if code is None:
-        raise ValueError("out must be bf16, fp16 or fp32")
-    ld_a, ld_w = _matrix(a, "a", _E4M3, M, K), _matrix(w, "w", _E4M3, N, K)
-    sa_row, sa_group = _scale_strides(a_scales, "a_scales", M, groups)
-    sw_row, sw_group = _scale_strides(w_scales, "w_scales", -(-N // 128), groups)
-    ld_out = _matrix(out, "out", dt, M, N)
-    status = lib.kda_fp8_matmul(a.data_ptr(), ld_a, a_scales.data_ptr(), sa_row, sa_group, w.data_ptr(), ld_w,
-                                w_scales.data_ptr(), sw_row, sw_group, M, N, K, out.data_ptr(), ld_out, code,
-                                _error_word(err_flags), _raw_stream(stream, a.device))
-    if status:
-        _check(status, "kda_fp8_matmul")
-    return out
+        out = torch.empty(a.shape[0], w.shape[0], dtype=out_dtype, device=a.device)
+    r = _torch_binding.fp8_matmul(a, a_scales, w, w_scales, out, err_flags, _handle(stream))
+    if type(r) is int:
+        _check(r, "kda_fp8_matmul")
+    return r
 
 
 BatchMaps = collections.namedtuple("BatchMaps", "order cu_seqlens state_indices num_decodes positions slot_map "
@@ -655,31 +573,14 @@ def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_page
     num_tokens: the rows of the step's buffers (or `out`, from make_batch_maps, whose positions give it).
     Returns BatchMaps(order, cu_seqlens, state_indices, num_decodes, positions, slot_map, free_left);
     free_pages and free_count are not changed, so a repeated call gives the same maps."""
-    R = query_lens.shape[0]
     if out is None:
         if num_tokens is None:
             raise ValueError("kda_batch_maps needs num_tokens or out")
-        out = make_batch_maps(R, num_tokens, query_lens.device)
-    order, cu, state_indices, num_decodes, positions, slot_map, free_left = out
-    tokens = positions.shape[0]
-    if num_tokens is not None and num_tokens != tokens:
+        out = make_batch_maps(query_lens.shape[0], num_tokens, query_lens.device)
+    elif num_tokens is not None and num_tokens != out.positions.shape[0]:
         raise ValueError("num_tokens must be the length of out.positions")
-    if state_slots.dtype is not _I32 or state_slots.dim() != 1 or state_slots.shape[0] < R or not state_slots.is_cuda:
-        raise ValueError("state_slots must be a 1-D int32 GPU tensor with an entry per request")
-    if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_cuda:
-        raise ValueError("block_table must be int32 [num_reqs, width] on the GPU")
-    rows, width = block_table.shape
-    table_stride, inner = block_table.stride()
-    if rows < R or (inner != 1 and width > 1):
-        raise ValueError("block_table must be int32 [num_reqs, width] with unit inner stride")
-    status = lib.kda_batch_maps(
-        _vector(query_lens, "query_lens", _I32, R), _vector(context_lens, "context_lens", _I32, R), state_slots.data_ptr(),
-        state_slots.stride(0) if R > 1 else 1, R, block_table.data_ptr(), table_stride if R > 1 else max(width, 1), width,
-        _vector(free_pages, "free_pages", _I32, 0), free_pages.shape[0], _vector(free_count, "free_count", _I32, 1), num_pages,
-        page_size, tokens, _vector(order, "out.order", _I32, R), _vector(cu, "out.cu_seqlens", _I32, R + 1),
-        _vector(state_indices, "out.state_indices", _I32, R), _vector(num_decodes, "out.num_decodes", _I32, 1),
-        _vector(positions, "out.positions", _I32, 0), _vector(slot_map, "out.slot_map", _I64, tokens),
-        _vector(free_left, "out.free_left", _I32, 1), _error_word(err_flags), _raw_stream(stream, query_lens.device))
-    if status:
-        _check(status, "kda_batch_maps")
-    return out
+    r = _torch_binding.batch_maps(query_lens, context_lens, state_slots, block_table, free_pages, free_count, page_size, num_pages, out,
+                                  err_flags, _handle(stream))
+    if type(r) is int:
+        _check(r, "kda_batch_maps")
+    return r
