@@ -58,59 +58,75 @@ __device__ __forceinline__ Lens load_lens(const BatchMapsParams &p, int r)
 {
     Lens l{0, 0, false};
     if (r >= p.R) return l;
-    l.q = p.qlen[r];
-    l.c = p.clen[r];
+    l.q = __ldg(p.qlen + r);
+    l.c = __ldg(p.clen + r);
     if (l.q < 0 || l.c < 0 || static_cast<int64_t>(l.q) + l.c > INT32_MAX) l = Lens{0, 0, true};
     return l;
 }
 
-// ceil(n / d), both below 2^31
-__device__ __forceinline__ int32_t ceil_div(int32_t n, int32_t d)
-{
-    return static_cast<int32_t>((static_cast<uint32_t>(n) + static_cast<uint32_t>(d) - 1u) / static_cast<uint32_t>(d));
-}
+// Division by the page size, a shift where it is a power of two (shift >= 0).
+struct PageSize {
+    uint32_t size;
+    int shift;
+    __device__ __forceinline__ uint32_t floor(uint32_t n) const { return shift >= 0 ? n >> shift : n / size; }
+    __device__ __forceinline__ uint32_t ceil(uint32_t n) const { return floor(n + size - 1u); }   // n below 2^31, as the size
+};
 
-__global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMapsParams p)
+__global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMapsParams p, const PageSize page_of, const int share)
 {
     extern __shared__ int32_t own[];   // per token row of this CTA: request (-1: not its first row here)
     const int rows = kRows * blockDim.x;
-    int32_t *own_start = own + rows, *own_base = own + 2 * rows;   // its first row, its first new page's number
+    int32_t *own_start = own + rows, *own_base = own + 2 * rows;   // its first row, its first new page's number,
+    int32_t *own_context = own + 3 * rows;                         // and its context
     __shared__ int64_t part[32];
     const int64_t T0 = static_cast<int64_t>(blockIdx.x) * rows;
     const int64_t N = p.num_tokens;
     uint32_t err = 0;
     pdl_wait_then_release();
 
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) own[i] = -1;
-    const int step = kItems * blockDim.x;
-    // the decodes, all of them, before anything can be placed
-    Lens first[kItems];   // the first step's lengths stay for the scan
-    int32_t nd = 0;
+    // everything the first step reads is asked for at once; of the outputs per request a CTA writes a share
+    const int32_t free_count = __ldg(p.free_count);
+    const int step = kItems * blockDim.x, mine0 = blockIdx.x * share, mine1 = mine0 + share;
+    auto slot_of = [&](int r) { return r >= mine0 && r < mine1 && r < p.R ? __ldg(p.slots + r * p.slot_stride) : 0; };
+    Lens first[kItems];
+    int32_t first_slot[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; i++) {
         first[i] = load_lens(p, threadIdx.x * kItems + i);
-        nd += first[i].q == 1;
+        first_slot[i] = slot_of(threadIdx.x * kItems + i);
     }
-    for (int r0 = step; r0 < p.R; r0 += step)
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) own[i] = -1;
+    int64_t D = 0;
+    if (p.R > step) {
+        // the decodes, all of them, before anything can be placed (one step knows them from its scan)
+        int32_t nd = 0, all;
 #pragma unroll
-        for (int i = 0; i < kItems; i++) nd += load_lens(p, r0 + threadIdx.x * kItems + i).q == 1;
-    int32_t D32;
-    block_exclusive(nd, reinterpret_cast<int32_t *>(part), &D32);
-    const int64_t D = D32;
+        for (int i = 0; i < kItems; i++) nd += first[i].q == 1;
+        for (int r0 = step; r0 < p.R; r0 += step)
+#pragma unroll
+            for (int i = 0; i < kItems; i++) nd += load_lens(p, r0 + threadIdx.x * kItems + i).q == 1;
+        block_exclusive(nd, reinterpret_cast<int32_t *>(part), &all);
+        D = all;
+    }
 
-    int64_t d_done = 0, t_done = 0, p_done = 0;
+    int64_t d_done = 0, t_done = 0;
+    uint32_t p_done = 0;   // pages: at most one per token and request
     for (int r0 = 0; r0 < p.R; r0 += step) {
         Lens l[kItems];
+        int32_t slot[kItems];
         // decodes above bit 44, the others' tokens below it: 4096 requests of less than 2^31
         // tokens at most in one step
-        int64_t mine = 0, pages = 0, pages_of[kItems];
+        int64_t mine = 0;
+        uint32_t pages = 0, pages_of[kItems];
 #pragma unroll
         for (int i = 0; i < kItems; i++) {
             l[i] = r0 == 0 ? first[i] : load_lens(p, r0 + threadIdx.x * kItems + i);
+            slot[i] = r0 == 0 ? first_slot[i] : slot_of(r0 + threadIdx.x * kItems + i);
             mine += l[i].q == 1 ? (int64_t(1) << 44) : l[i].q;
         }
         int64_t total;
         int64_t before = block_exclusive(mine, part, &total);
+        if (p.R <= step) D = total >> 44;
         int64_t d = d_done + (before >> 44), t = t_done + (before & ((int64_t(1) << 44) - 1));
         int64_t start_of[kItems];
 #pragma unroll
@@ -127,19 +143,19 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
             if (l[i].bad || end > N) err |= kErrLengths;
             // cut off at the capacity
             const int64_t cs = start < N ? start : N, ce = end < N ? end : N;
-            if (blockIdx.x == 0) {
+            if (r >= mine0 && r < mine1) {
                 p.order[s] = r;
                 p.cu[s + 1] = static_cast<int32_t>(ce);
-                p.state_indices[s] = p.slots[r * p.slot_stride];
+                p.state_indices[s] = slot[i];
             }
             l[i].q = static_cast<int32_t>(ce - cs);
-            int64_t old = ceil_div(l[i].c, p.page), now = ceil_div(l[i].c + l[i].q, p.page);
+            int64_t old = page_of.ceil(l[i].c), now = page_of.ceil(l[i].c + l[i].q);
             if (now > p.width) { if (l[i].q > 0) err |= kErrPages; now = p.width; }
-            pages_of[i] = now > old ? now - old : 0;
+            pages_of[i] = now > old ? static_cast<uint32_t>(now - old) : 0;
             pages += pages_of[i];
         }
-        int64_t ptotal;
-        int64_t base = p_done + block_exclusive(pages, part, &ptotal);
+        uint32_t ptotal;
+        uint32_t base = p_done + block_exclusive(pages, reinterpret_cast<uint32_t *>(part), &ptotal);
 #pragma unroll
         for (int i = 0; i < kItems; i++) {
             const int r = r0 + threadIdx.x * kItems + i;
@@ -147,7 +163,8 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
                 const int o = static_cast<int>(start_of[i] > T0 ? start_of[i] - T0 : 0);
                 own[o] = r;
                 own_start[o] = static_cast<int32_t>(start_of[i]);
-                own_base[o] = static_cast<int32_t>(base < INT32_MAX ? base : INT32_MAX);
+                own_base[o] = static_cast<int32_t>(base);
+                own_context[o] = l[i].c;
             }
             base += pages_of[i];
         }
@@ -155,8 +172,7 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
         t_done += total & ((int64_t(1) << 44) - 1);
         p_done += ptotal;
     }
-    int64_t fc = *p.free_count;
-    fc = fc < 0 ? 0 : fc > p.num_free ? p.num_free : fc;
+    const int64_t fc = max(int64_t(0), min(static_cast<int64_t>(free_count), p.num_free));
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.cu[0] = 0;
         *p.num_decodes = static_cast<int32_t>(D);
@@ -201,17 +217,17 @@ __global__ void __launch_bounds__(kMaxThreads) batch_maps_kernel(const BatchMaps
         if (t < live) {
             const int o = head[i] >= 0 ? head[i] : before;
             const int r = own[o];
-            const int32_t c = p.clen[r];
+            const int32_t c = own_context[o];
             pos = c + static_cast<int32_t>(t - own_start[o]);
-            const int32_t j = pos / p.page, old = ceil_div(c, p.page), off = pos - j * p.page;
+            const int32_t j = page_of.floor(pos), old = page_of.ceil(c), off = pos - j * p.page;
             int32_t page = -1;
             if (j < p.width) {
                 int32_t *entry = p.table + r * p.table_stride + j;
                 if (j < old) {
                     page = *entry;
                 } else {
-                    const int64_t k = own_base[o] + (j - old);
-                    if (k < fc) page = p.free_pages[fc - 1 - k];
+                    const int64_t k = static_cast<int64_t>(static_cast<uint32_t>(own_base[o])) + (j - old);
+                    if (k < fc) page = __ldg(p.free_pages + (fc - 1 - k));
                     if (off == 0) *entry = page;   // a new page's first position is one of the query's
                 }
             }
@@ -235,8 +251,12 @@ cudaError_t launch_batch_maps(const BatchMapsParams &p, cudaStream_t stream)
     const int threads = static_cast<int>(want >= kMaxThreads ? kMaxThreads : want <= 32 ? 32 : (want + 31) / 32 * 32);
     const int64_t per = static_cast<int64_t>(kRows) * threads;
     const int64_t grid = p.num_tokens > 0 ? (p.num_tokens + per - 1) / per : 1;
+    PageSize page{static_cast<uint32_t>(p.page), -1};
+    for (int i = 0; i < 31; i++)
+        if (p.page == 1 << i) page.shift = i;
+    const int share = static_cast<int>((p.R + grid - 1) / grid);
     return launch_pdl(batch_maps_kernel, dim3(static_cast<unsigned>(grid)), dim3(threads),
-                      static_cast<size_t>(3 * per * sizeof(int32_t)), stream, p);
+                      static_cast<size_t>(4 * per * sizeof(int32_t)), stream, p, page, share);
 }
 
 }  // namespace kda
