@@ -55,6 +55,14 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// 1 / x to within one step, for 2^-126 <= x (infinity gives 0, a NaN itself)
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // two fp32 -> two e4m3 (lo in the low byte), round to nearest even, saturating at 448; NaN stays NaN
 __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi)
 {
@@ -134,7 +142,7 @@ constexpr float kE4m3Max = 448.f;
 // takes. RES and NORM leave out the registers (and so the warps) that steps which are
 // not asked for would cost.
 template <typename T, bool VEC, int TPR, int CH, bool RES, bool NORM>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, sizeof(typename T::raw) == 2 && CH <= 2 ? 1024 / (TPR < 128 ? 128 : TPR) : 1)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, sizeof(typename T::raw) == 2 && CH <= 2 ? (RES ? 1024 : 1536) / (TPR < 128 ? 128 : TPR) : 1)
 norm_quant_kernel(const NormQuantParams p)
 {
     constexpr int E = VEC ? 8 : 4;           // columns per chunk
@@ -220,10 +228,11 @@ norm_quant_kernel(const NormQuantParams p)
             for (int j = 0; j < E; j++) m = max_nan(m, fabsf(h[i][j]));
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float s = __fdiv_rn(max_nan(m, kE4m3Max * 1.17549435e-38f), kE4m3Max);
-            // y * (1 / s) in place of y / s: off by at most 2^-23 of the value, which moves a
-            // quotient across a rounding border of e4m3 (steps of 2^-3) about once in 10^6
-            const float inv = __fdiv_rn(1.f, s);
+            // A product with 1 / 448 and a reciprocal to one step in place of two divisions (28.7 -> 26.0 us at
+            // 2049 x 5003 fp32): the scale is off by at most 2^-23 and a quotient by 2^-22 of its value,
+            // which moves it across a rounding border of e4m3 (steps of 2^-3) about once in 10^6.
+            const float s = max_nan(m, kE4m3Max * 1.17549435e-38f) * (1.f / kE4m3Max);
+            const float inv = reciprocal(s);
             const int c0 = col0(i);
             if (c0 < D) {
                 if (t % LANES == 0) p.s[r * p.s_row + static_cast<int64_t>(c0 / 128) * p.s_group] = s;
