@@ -142,7 +142,7 @@ constexpr float kE4m3Max = 448.f;
 // takes. RES and NORM leave out the registers (and so the warps) that steps which are
 // not asked for would cost.
 template <typename T, bool VEC, int TPR, int CH, bool RES, bool NORM>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, sizeof(typename T::raw) == 2 && CH <= 2 ? (RES ? 1024 : 1536) / (TPR < 128 ? 128 : TPR) : 1)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, VEC && sizeof(typename T::raw) == 2 && CH <= 2 ? (RES ? 1024 : 1536) / (TPR < 128 ? 128 : TPR) : 1)
 norm_quant_kernel(const NormQuantParams p)
 {
     constexpr int E = VEC ? 8 : 4;           // columns per chunk
@@ -281,25 +281,47 @@ cudaError_t run(const NormQuantParams &p, cudaStream_t stream)
 // The smallest team that holds a row with two chunks per thread where there are rows enough to
 // fill the GPU (more chunks cost the warps that hide the loads), one per thread (more threads, a
 // shorter chain) where there are not.
-template <typename T, bool VEC>
-cudaError_t pick(const NormQuantParams &p, cudaStream_t stream)
+template <typename T>
+cudaError_t pick_vectors(const NormQuantParams &p, cudaStream_t stream)
 {
-    const int chunks = VEC ? (p.D + 7) / 8 : (p.D + 127) / 128 * 32;
+    const int chunks = (p.D + 7) / 8;
     const bool many = p.N >= 512;
-    if (chunks <= 32) return run<T, VEC, 32, 1>(p, stream);
-    if (many && chunks <= 64) return run<T, VEC, 32, 2>(p, stream);
-    if (chunks <= 128) return run<T, VEC, 128, 1>(p, stream);
-    if (many && chunks <= 256) return run<T, VEC, 128, 2>(p, stream);
-    if (many && chunks <= 512) return run<T, VEC, 256, 2>(p, stream);
-    if (chunks <= 512) return run<T, VEC, 512, 1>(p, stream);
-    if (chunks <= 1024) return run<T, VEC, 512, 2>(p, stream);
-    if (chunks <= 1536) return run<T, VEC, 512, 3>(p, stream);
-    if constexpr (VEC && sizeof(typename T::raw) == 2)
-        if (chunks <= 2048) return run<T, VEC, 1024, 2>(p, stream);
-    if (chunks <= 2048) return run<T, VEC, 512, 4>(p, stream);
-    if constexpr (!VEC)   // four columns per chunk: 32768 columns are 8192 chunks
-        if (chunks > 4096) return run<T, VEC, 512, 16>(p, stream);
-    return run<T, VEC, 512, 8>(p, stream);
+    if (chunks <= 32) return run<T, true, 32, 1>(p, stream);
+    if (many && chunks <= 64) return run<T, true, 32, 2>(p, stream);
+    if (chunks <= 128) return run<T, true, 128, 1>(p, stream);
+    if (many && chunks <= 256) return run<T, true, 128, 2>(p, stream);
+    if (many && chunks <= 512) return run<T, true, 256, 2>(p, stream);
+    if (chunks <= 512) return run<T, true, 512, 1>(p, stream);
+    if (chunks <= 1024) return run<T, true, 512, 2>(p, stream);
+    if (chunks <= 1536) return run<T, true, 512, 3>(p, stream);
+    if constexpr (sizeof(typename T::raw) == 2)
+        if (chunks <= 2048) return run<T, true, 1024, 2>(p, stream);
+    if (chunks <= 2048) return run<T, true, 512, 4>(p, stream);
+    return run<T, true, 512, 8>(p, stream);
+}
+
+// Single elements: four columns per chunk and little in flight per register, so more chunks per
+// thread, in teams that leave few threads without a column (20000 x 2051 bf16: 120 us in 256 threads
+// of three chunks, 151 in 512 of two).
+template <typename T>
+cudaError_t pick_elements(const NormQuantParams &p, cudaStream_t stream)
+{
+    const int chunks = (p.D + 127) / 128 * 32;
+    const bool many = p.N >= 512;
+    if (chunks <= 32) return run<T, false, 32, 1>(p, stream);
+    if (many && chunks <= 128) return run<T, false, 32, 4>(p, stream);
+    if (chunks <= 128) return run<T, false, 128, 1>(p, stream);
+    if (many && chunks <= 256) return run<T, false, 128, 2>(p, stream);
+    if (many && chunks <= 384) return run<T, false, 128, 3>(p, stream);
+    if (many && chunks <= 512) return run<T, false, 128, 4>(p, stream);
+    if (chunks <= 512) return run<T, false, 512, 1>(p, stream);
+    if (chunks <= 768) return run<T, false, 256, 3>(p, stream);
+    if (chunks <= 1024) return run<T, false, 256, 4>(p, stream);
+    if (chunks <= 1536) return run<T, false, 512, 3>(p, stream);
+    if (chunks <= 2048) return run<T, false, 512, 4>(p, stream);
+    if (chunks <= 2560) return run<T, false, 512, 5>(p, stream);
+    if (chunks <= 4096) return run<T, false, 512, 8>(p, stream);
+    return run<T, false, 512, 16>(p, stream);
 }
 
 template <typename T>
@@ -311,7 +333,7 @@ cudaError_t by_alignment(const NormQuantParams &p, cudaStream_t stream)
     };
     const bool vec = ok(p.x, p.ld_x) && ok(p.res, p.ld_res) && ok(p.res_out, p.ld_ro) && ok(p.y, p.ld_y) &&
                      reinterpret_cast<uintptr_t>(p.w) % 16 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && p.ld_q % 8 == 0;
-    return vec ? pick<T, true>(p, stream) : pick<T, false>(p, stream);
+    return vec ? pick_vectors<T>(p, stream) : pick_elements<T>(p, stream);
 }
 
 }  // namespace
