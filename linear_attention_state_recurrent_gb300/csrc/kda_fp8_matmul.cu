@@ -8,12 +8,21 @@
 // registers. TMA brings 128-byte-wide tiles (one group) with the 128-byte swizzle that the
 // matrix descriptors name; columns past K and rows past the matrix read as zeros.
 //
-// Two arrangements:
-//  - wide_kernel: tiles of 256 rows of A x 256 of W by a pair of CTAs (cta_group::2), persistent.
-//    A thread of the epilogue holds one row of out, so its two scales are one factor per group.
-//  - slim_kernel: up to 128 rows of A x a tile of W that makes the CTAs fill the GPU once: the
-//    weights stream through at HBM's rate. The inner axis may be split over a cluster whose CTAs join
-//    their sums through distributed shared memory in a fixed order.
+// Three arrangements (times on a GB300 for K = 4096; `wide` writes bf16):
+//  - thin_kernel, up to 64 rows of A: 128 rows of W are the MMA's M side, the rows of A its N side.
+//    Bound by the stream of weights: M = 1, N = 20512 16.9 us = 4.98 TB/s, of which the stream alone
+//    (no MMA, no epilogue) is 15.6 us; N = 4096 5.2 us.
+//  - slim_kernel, up to 128 rows of A per CTA and a tile of W that makes the CTAs fill the GPU once:
+//    M = 128, N = 20512 20.8 us (the stream alone 18.5 us).
+//    In both the inner axis may be split over a cluster whose CTAs join their sums through distributed
+//    shared memory in a fixed order.
+//  - wide_kernel: tiles of 256 x 256 by a pair of CTAs (cta_group::2), persistent: M = 33494,
+//    N = 20512 2.18 ms = 2.58 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
+//    (128 x 256 per group and SM) take 270 of the 950 clocks a group takes, the MMAs 553; two
+//    accumulators are all that tensor memory holds, and what is left is the way from one to
+//    the other and back. Measured and not kept: four accumulators of 128 columns (2.46 ms against 2.22),
+//    tiles of 192 with one load per group (2.36), loads of tensor memory overlapped across groups
+//    (2.49), the MMA loop unrolled over the ring (2.42, registers), one polling warp of four (2.35).
 // Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
 #include <climits>
 #include <cstdint>

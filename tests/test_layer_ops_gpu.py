@@ -12,6 +12,9 @@ Tolerances, from the arithmetic (e = torch.finfo(t).eps / 2 is half a step of th
   batch_maps  integers: equal.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -454,3 +457,29 @@ def test_in_a_graph(kda):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(-want[0], got[0]) and all(torch.equal(a, b) for a, b in zip(want[1], got[1]))
+
+
+def test_first_calls_inside_a_capture():
+    """What a first call on a device looks up and sets is allowed while a stream is captured."""
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch
+from linear_attention_state_recurrent_gb300 import kda
+x = torch.randn(300, 512, device="cuda").to(torch.bfloat16)
+w = torch.ones(256, 512, device="cuda").to(torch.float8_e4m3fn)
+sw = torch.ones(2, 4, device="cuda")
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+args = (i32(1, 2), i32(0, 3), i32(4, 5), torch.zeros(2, 4, dtype=torch.int32, device="cuda"), i32(7, 8), i32(2), 16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q, s, _ = kda.kda_norm_quant(x)
+    y = [kda.kda_fp8_matmul(q[:m], s[:m], w, sw) for m in (1, 20, 50, 100, 300)]
+    m = kda.kda_batch_maps(*args, num_pages=16, num_tokens=4)
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.isfinite(t.float()).all() for t in y) and m.cu_seqlens.tolist() == [0, 1, 3]
+print("captured")
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
