@@ -1115,7 +1115,8 @@ cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cu
     const CUtensorMapDataType type = p.out_dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                      : p.out_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     if (tma_out && (e = encode(&to, p.out, p.N, p.M, p.ld_out, 32, type, es)) != cudaSuccess) return e;
-    const Tiles t{(p.M - 1) / 256 + 1, (p.N - 1) / 256 + 1, 16};
+    // the pairs at work share two tiles of W: 2.15 ms at the widest product, 2.25 in bands of 8, 2.31 in bands of 64
+    const Tiles t{(p.M - 1) / 256 + 1, (p.N - 1) / 256 + 1, sms / 4};
     const int64_t total = static_cast<int64_t>(t.m) * t.n;
     if (total > INT32_MAX - 4096) return cudaErrorInvalidConfiguration;
     const int pairs = static_cast<int>(total < sms / 2 ? total : sms / 2);
