@@ -655,7 +655,7 @@ __device__ __forceinline__ void tile_at(const Tiles &t, int i, int *tm, int *tn)
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Wide::THREADS, 1)
 wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-            const __grid_constant__ CUtensorMap tm_out, const bool tma_out, const Fp8Params p, const Tiles tiles)
+            const __grid_constant__ CUtensorMap tm_out, const int tma_n, const Fp8Params p, const Tiles tiles)
 {
     using C = Wide;
     extern __shared__ __align__(1024) unsigned char dyn[];
@@ -677,7 +677,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         for (int r = 0; r < C::SR; r++) { tc::mbar_init(sfull(r), 32); tc::mbar_init(sempty(r), C::EW); }
         tc::prefetch_tensormap(&tm_w);
         tc::prefetch_tensormap(&tm_a);
-        if (tma_out) tc::prefetch_tensormap(&tm_out);
+        if (tma_n > 0) tc::prefetch_tensormap(&tm_out);
     }
     pdl_wait();
     if (warp == 1) {
@@ -829,9 +829,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             tile_at(tiles, i, &tm, &tn);
             const int m0 = tm * 256 + rank * 128 + quarter * 32, n0 = tn * 256 + c0;   // of this warp's box
             if (m0 >= p.M || n0 >= p.N) continue;
-            if (tma_out) {
+            if (n0 < tma_n) {
                 // 32 rows of 128 bytes with the map's swizzle (16-byte piece j of row l at j ^ (l % 8)),
-                // written by TMA, which leaves out what lies past the matrix
+                // written by TMA, which leaves out what lies past the map
                 auto put = [&](const uint32_t (&w)[32], int x) {
                     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
@@ -856,7 +856,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                             w[2 * j] = __float_as_uint(acc[16 * h + j].x);
                             w[2 * j + 1] = __float_as_uint(acc[16 * h + j].y);
                         }
-                        if (n0 + 32 * h < p.N) put(w, n0 + 32 * h);
+                        if (n0 + 32 * h < tma_n) put(w, n0 + 32 * h);
                     }
                 } else {
                     uint32_t w[32];
@@ -865,10 +865,11 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                         w[j] = p.out_dtype == 0 ? pack_bf16x2(acc[j].x, acc[j].y) : tc::pack_f16x2(acc[j].x, acc[j].y);
                     put(w, n0);
                 }
-            } else if (m0 + lane < p.M) {
+            }
+            if (n0 + C::COLS > tma_n && m0 + lane < p.M) {
 #pragma unroll
                 for (int c = 0; c < C::COLS; c++)
-                    if (n0 + c < p.N)
+                    if (n0 + c >= tma_n && n0 + c < p.N)
                         store_out(p.out, static_cast<int64_t>(m0 + lane) * p.ld_out + n0 + c, p.out_dtype, c % 2 ? acc[c / 2].y : acc[c / 2].x);
             }
         }
@@ -1114,13 +1115,15 @@ cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cu
     const bool tma_out = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld_out * es % 16 == 0 && p.ld_out < (int64_t(1) << 38);
     const CUtensorMapDataType type = p.out_dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                      : p.out_dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    if (tma_out && (e = encode(&to, p.out, p.N, p.M, p.ld_out, 32, type, es)) != cudaSuccess) return e;
+    // TMA writes whole 16-byte pieces, past the map's edge inside one too: the map ends at the last whole piece of a row
+    const int tma_n = tma_out ? p.N / (16 / es) * (16 / es) : 0;
+    if (tma_n > 0 && (e = encode(&to, p.out, tma_n, p.M, p.ld_out, 32, type, es)) != cudaSuccess) return e;
     // the pairs at work share two tiles of W: 2.15 ms at the widest product, 2.25 in bands of 8, 2.31 in bands of 64
     const Tiles t{(p.M - 1) / 256 + 1, (p.N - 1) / 256 + 1, sms / 4};
     const int64_t total = static_cast<int64_t>(t.m) * t.n;
     if (total > INT32_MAX - 4096) return cudaErrorInvalidConfiguration;
     const int pairs = static_cast<int>(total < sms / 2 ? total : sms / 2);
-    return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, to, tma_out, p, t);
+    return launch_pdl(wide_kernel, dim3(2 * pairs), dim3(Wide::THREADS), Wide::SMEM, stream, ta, tw, to, tma_n, p, t);
 }
 
 // What the launches need to know of a device, and the kernels' shared-memory limits set there, once.

@@ -265,6 +265,21 @@ def test_fp8_matmul_rounds_the_fp32_result_once(kda, M, N, K, dtype):
     assert torch.equal(kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=dtype), full.to(dtype))
 
 
+@pytest.mark.parametrize("M,N,K", [(2500, 1500, 1040), (1300, 1, 40), (1300, 3, 128), (1300, 7, 16), (1500, 263, 300), (1100, 4097, 140)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_fp8_matmul_leaves_the_columns_beside_it(kda, M, N, K, dtype):
+    """A view into wider rows, on 16-byte boundaries, that ends inside 16 bytes."""
+    a, sa, w, sw = operands(M, N, K, M, (up16(K), up16(K)))
+    buf = torch.full((M, N + 32 + up16(N)), 9.0, dtype=dtype, device="cuda")
+    if dtype == FP16:                                             # the range of its normal numbers, near enough
+        sa, sw = sa * 1e-3, sw * 1e-3
+        out = kda.kda_fp8_matmul(a, sa, w, sw, out=buf[:, 16:16 + N])
+        assert torch.equal(out, kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=FP32).to(FP16))
+    else:
+        check_matmul(kda, a, sa, w, sw, out=buf[:, 16:16 + N])
+    assert torch.all(buf[:, :16] == 9) and torch.all(buf[:, 16 + N:] == 9)
+
+
 def test_fp8_matmul_split_of_a_long_inner_axis(kda):
     for M in (1, 20, 130):
         a, sa, w, sw = operands(M, 40, 16384 + 48, 8)
