@@ -11,13 +11,13 @@
 // Three arrangements (times on a GB300 for K = 4096; `wide` writes bf16):
 //  - thin_kernel, up to 64 rows of A: 128 rows of W are the MMA's M side, the rows of A its N side.
 //    Bound by the stream of weights: M = 1, N = 20512 16.9 us = 4.98 TB/s, of which the stream alone
-//    (no MMA, no epilogue) is 15.6 us; N = 4096 5.2 us.
+//    (no MMA, no epilogue) is 15.6 us, and a plain kernel that reads as many bytes 16.9 us; N = 4096 5.2 us.
 //  - slim_kernel, up to 128 rows of A per CTA and a tile of W that makes the CTAs fill the GPU once:
 //    M = 128, N = 20512 20.8 us (the stream alone 18.5 us).
 //    In both the inner axis may be split over a cluster whose CTAs join their sums through distributed
 //    shared memory in a fixed order.
 //  - wide_kernel: tiles of 256 x 256 by a pair of CTAs (cta_group::2), persistent: M = 33494,
-//    N = 20512 2.18 ms = 2.58 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
+//    N = 20512 2.15 ms = 2.62 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
 //    (128 x 256 per group and SM) take 270 of the 950 clocks a group takes, the MMAs 553; two
 //    accumulators are all that tensor memory holds, and what is left is the way from one to
 //    the other and back. Measured and not kept: four accumulators of 128 columns (2.46 ms against 2.22),
@@ -1071,10 +1071,11 @@ double plan_slim(const Fp8Params &p, const Fit &fit, SlimPlan *best)
     const int groups = (p.K + BK - 1) / BK, mt = (p.M + 127) / 128;
     const int rows = p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
     double least = 1e30;
+    if (mt > 65535) return least;                   // the grid's y axis ends there
     for (int split = 1; split <= 8 && split <= groups; split++) {
         if (fit.ctas[split] == 0) continue;
         const int tiles = fit.ctas[split] / (split * mt);           // of W in one wave
-        int bn = tiles < 1 ? 256 : (p.N - 1) / tiles + 1;
+        int bn = tiles < 1 ? p.N : (p.N - 1) / tiles + 1;
         bn = bn > 256 ? 256 : (bn + 15) / 16 * 16;
         if (split > 1 && (bn + 1) * rows * 4 > Slim::RING) continue;
         const int64_t ctas = static_cast<int64_t>((p.N - 1) / bn + 1) * split * mt;
@@ -1184,8 +1185,9 @@ cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
         plan_thin<32>(p, d->thin32, &split);
         return run_thin<32>(p, split, ld_a, ld_w, stream);
     }
-    // More rows: the arrangement of least time.
-    if (p.M > 1024) return run_wide(p, ld_a, ld_w, d->sms, stream);
+    // More rows: the arrangement of least time. Beyond a thousand rows that is slim_kernel where few columns
+    // or a short inner axis leave the pairs of wide_kernel idle or starting: 1311 x 167 x 365 4.0 us against 6.7,
+    // 1968 x 600 x 684 7.0 against 9.1, 1500 x 4096 x 4096 33.4 against 35.4.
     SlimPlan q;
     const double slim = plan_slim(p, d->slim, &q);
     if (p.M <= 64 && plan_thin<64>(p, d->thin64, &split) <= slim) return run_thin<64>(p, split, ld_a, ld_w, stream);

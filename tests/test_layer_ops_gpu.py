@@ -265,6 +265,30 @@ def test_fp8_matmul_rounds_the_fp32_result_once(kda, M, N, K, dtype):
     assert torch.equal(kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=dtype), full.to(dtype))
 
 
+@pytest.mark.parametrize("M,N,K", [(1025, 16, 16), (1311, 167, 365), (1101, 207, 725), (1968, 600, 684), (1100, 40, 4000),
+                                   (9038, 243, 168), (16809, 37, 479), (2500, 1500, 1040)])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_fp8_matmul_many_rows_of_few_columns(kda, M, N, K, aligned):
+    """More rows than one wave of narrow tiles, where both the narrow and the wide arrangement are open."""
+    a, sa, w, sw = operands(M, N, K, M, (up16(K), up16(K)), group_major=aligned)
+    edge = 16 if aligned else 5
+    buf = torch.full((M, N + 2 * edge + up16(N) * aligned), 9.0, dtype=BF16, device="cuda")
+    check_matmul(kda, a, sa, w, sw, out=buf[:, edge:edge + N])
+    assert torch.all(buf[:, :edge] == 9) and torch.all(buf[:, edge + N:] == 9)
+
+
+@pytest.mark.parametrize("M", [65535 * 128, 65535 * 128 + 1])
+def test_fp8_matmul_rows_past_a_grid_axis(kda, M):
+    """Rows of ones count their columns: exact, whichever side of the grid's limit the rows end on."""
+    a = torch.ones(M, 16, device="cuda").to(E4M3)
+    w = torch.ones(3, 16, device="cuda").to(E4M3)
+    w.view(torch.uint8)[1] = 0
+    sa = torch.arange(M, device="cuda").remainder(5).add(1).to(FP32)[:, None]
+    sw = torch.full((1, 1), 0.5, device="cuda")
+    out = kda.kda_fp8_matmul(a, sa, w, sw)
+    assert torch.equal(out, torch.tensor([8.0, 0.0, 8.0], device="cuda") * sa)
+
+
 @pytest.mark.parametrize("M,N,K", [(2500, 1500, 1040), (1300, 1, 40), (1300, 3, 128), (1300, 7, 16), (1500, 263, 300), (1100, 4097, 140)])
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 def test_fp8_matmul_leaves_the_columns_beside_it(kda, M, N, K, dtype):
