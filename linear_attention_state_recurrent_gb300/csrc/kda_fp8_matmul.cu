@@ -17,7 +17,7 @@
 //    In both the inner axis may be split over a cluster whose CTAs join their sums through distributed
 //    shared memory in a fixed order.
 //  - wide_kernel: tiles of 256 x 256 by a pair of CTAs (cta_group::2), persistent: M = 33494,
-//    N = 20512 2.15 ms = 2.62 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
+//    N = 20512 2.12-2.22 ms = 2.53-2.65 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
 //    (128 x 256 per group and SM) take 270 of the 950 clocks a group takes, the MMAs 553; two
 //    accumulators are all that tensor memory holds, and what is left is the way from one to
 //    the other and back. Measured and not kept: four accumulators of 128 columns (2.46 ms against 2.22),
