@@ -380,7 +380,8 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
  * x, residual, residual_out and y_out have the element type `dtype` (KDA_BF16, KDA_FP16 or
  * KDA_FP32), weight is fp32 [D]. residual_out (NULL without a residual) receives h and
  * y_out (may be NULL) y, each rounded once; the sum, the norm and y itself are held in
- * fp32, and q is made from the unrounded y. scales: fp32, s of row r and group g at
+ * fp32, and q is made from the unrounded y: s is off by 2^-23 of itself at most, and q is the e4m3 value nearest
+ * to y / s in fp32, for the s that is stored. scales: fp32, s of row r and group g at
  * scales[r*scale_row_stride + g*scale_group_stride]. residual_out may be residual or x, and
  * y_out may be x (each row is read before it is written); no other overlap is allowed.
  * A NaN in a group makes the group's scale and all of its q NaN (with a weight: the whole

@@ -1,0 +1,71 @@
+"""Edges of the operators around the recurrence where a result could be right nearly everywhere: values between
+two of a type's, streams other than the current one, waits that give up, and every way a product is cut up."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kda():
+    assert torch.cuda.is_available()
+    from linear_attention_state_recurrent_gb300 import build
+    build.build()
+    from linear_attention_state_recurrent_gb300 import kda as k
+    return k
+
+
+# ---- kda_norm_quant: values between two of e4m3 -------------------------------------------
+
+
+def midpoints():
+    """Every value half way between two neighbours of e4m3, as fp64."""
+    subnormal = [(m + 0.5) * 2.0 ** -9 for m in range(8)]
+    normal = [(8 + m + 0.5) * 2.0 ** (e - 3) for e in range(-6, 9) for m in range(8)]
+    return np.array([v for v in subnormal + normal if v < 448])
+
+
+def tie_rows(dtype):
+    """Rows of one group whose largest value gives a scale of j / 64 exactly, the others midpoints of e4m3 times
+    that scale where the type holds them (else 0): y / s is the midpoint, with nothing to round."""
+    reciprocal = np.float32(1) / np.float32(448)
+    rows, want = [], []
+    for j in range(1, 2000, 2):
+        if np.float32(7 * j) * reciprocal != np.float32(j / 64) or torch.tensor(7.0 * j).to(dtype).double() != 7 * j:
+            continue
+        for sign in (1, -1):
+            for half in np.array_split(midpoints(), 2):
+                v = torch.zeros(128, dtype=torch.float64)
+                v[1:1 + len(half)] = torch.from_numpy(sign * half)
+                x = v * (j / 64)
+                held = x.to(dtype).double() == x
+                x, v = torch.where(held, x, 0), torch.where(held, v, 0)
+                x[0], v[0] = 7 * j, 448
+                rows.append(x.to(dtype))
+                want.append(v.float())
+    return torch.stack(rows), torch.stack(want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("pad", [0, 1])   # rows on 16-byte boundaries and off them
+def test_norm_quant_rounds_midpoints_to_even(kda, dtype, pad):
+    x, v = tie_rows(dtype)
+    assert (v != 0).sum() > 200
+    buf = torch.zeros(x.shape[0], 128 + pad, dtype=dtype, device="cuda")
+    buf[:, :128] = x.cuda()
+    q, s, _ = kda.kda_norm_quant(buf[:, :128])
+    assert torch.equal(s[:, 0].cpu(), (x[:, 0].float() / 448))
+    assert torch.equal(q.float().cpu(), v.to(E4M3).float())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_norm_quant_rounds_the_quotient_by_its_scale(kda, dtype):
+    """q is the nearest e4m3 of y / s in fp32, for the scale that is returned: exactly, whatever the values."""
+    g = torch.Generator().manual_seed(31)
+    x = (torch.randn(2000, 1024, generator=g) * torch.exp(2 * torch.randn(2000, 1, generator=g))).to(dtype).cuda()
+    q, s, _ = kda.kda_norm_quant(x)
+    quotient = (x.double() / s.double().repeat_interleave(128, 1)).float().clamp(-448, 448)
+    assert torch.equal(q.float(), quotient.to(E4M3).float())
