@@ -94,6 +94,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity)
     }
 }
 
+// The same by a converged warp, with one answer for all its lanes: what follows is instructions of the whole warp.
+__device__ __forceinline__ bool wait_warp(uint32_t mbar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, wait_phase(mbar, parity));
+}
+
 // An arrival on the barrier at this place in both CTAs of the pair once its MMAs so far are done.
 __device__ __forceinline__ void commit_pair(uint32_t mbar)
 {
@@ -138,6 +144,7 @@ __device__ __forceinline__ uint32_t cluster_rank()
 }
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();   // warps come here from loops that each lane left for itself
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // the address in CTA `rank` of the cluster of a shared-memory address of this CTA
@@ -309,7 +316,7 @@ thin_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         uint32_t tphase = 0;
         bool ok = true;
         for (int g = g0; g < g1; g++) {
-            if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
+            if (!wait_warp(tfull(b), tphase)) { ok = false; break; }
             tc::fence_after_sync();
             float v[C::COLS / 16][16];
 #pragma unroll
@@ -543,7 +550,7 @@ slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 #pragma unroll
             for (int c = 0; c < MAXC; c++) block[c] = (n0 + (first + c) * 16) / 128 - n0 / 128;
             for (int g = g0; g < g1; g++) {
-                if (!wait_phase(tfull(b), tphase)) { ok = false; break; }
+                if (!wait_warp(tfull(b), tphase)) { ok = false; break; }
                 tc::fence_after_sync();
                 const float *slot = scales + r * C::SLOT;
                 const float s = slot[row];
@@ -560,6 +567,7 @@ slim_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                     tc::tmem_ld_wait();
                     if (c + AT_ONCE >= MAXC) {
                         tc::fence_before_sync();
+                        __syncwarp();   // every lane has read the slot
                         if (lane == 0) {
                             arrive_local(tempty(b));
                             arrive_local(sempty(r));
@@ -795,7 +803,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             for (int g = 0; g < groups; g++) {
                 if (g % 2 == 0) {
                     // two groups' scales at a time
-                    if (!wait_phase(sfull(r), sphase)) { ok = false; break; }
+                    if (!wait_warp(sfull(r), sphase)) { ok = false; break; }
                     const float2 *slot = reinterpret_cast<const float2 *>(scales + r * C::SLOT);
                     const float2 x = slot[row], y = slot[128 + c0 / 128];
                     s2 = make_float2(x.x * y.x, x.y * y.y);
@@ -804,7 +812,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                     if (++r == C::SR) { r = 0; sphase ^= 1; }
                 }
                 const float2 f = g % 2 == 0 ? make_float2(s2.x, s2.x) : make_float2(s2.y, s2.y);
-                if (!ready && !wait_phase(tfull(b), tphase)) { ok = false; break; }
+                if (!ready && !wait_warp(tfull(b), tphase)) { ok = false; break; }
                 tc::fence_after_sync();
                 const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * 256 + c0;
                 uint32_t v[32];
@@ -819,7 +827,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 if (lane == 0) arrive_cluster(in_cta(tempty(b), 0));
                 if (++b == 2) { b = 0; tphase ^= 1; }
                 // asked here, answered by the time the sums below are done
-                ready = test_phase(tfull(b), tphase);
+                ready = __all_sync(0xffffffffu, test_phase(tfull(b), tphase));
 #pragma unroll
                 for (int j = 0; j < 16; j++)
                     acc[16 + j] = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f, acc[16 + j]);
