@@ -408,12 +408,24 @@ int kda_norm_quant(const void *x, int64_t ld_x, const void *residual, int64_t ld
  * are computed by a slower kernel with the same result up to fp32 rounding. Columns K .. ld
  * of a and w are never read. M, N and K may be any size >= 1 (K = 0: zeros; M or N = 0:
  * nothing to do), up to 2^30 each. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT
- * in *err_flags (may be NULL) and leaves its tile unwritten.
+ * in *err_flags (may be NULL), and what its sums were to give stays as it was in out.
  */
 int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
                    int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
                    int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
                    void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, void *stream);
+
+/*
+ * kda_selftest_fp8_matmul — exercises that error path without a fault: kda_fp8_matmul in which the
+ * scales of CTA `stalled` (0 .. 7) of each thread-block cluster never come, so that what waits
+ * for them gives up after ~2 s. err_flags is required. Operands that take the slower kernel, and
+ * clusters of `stalled` CTAs or fewer, are computed as ever. The CUDA context stays usable.
+ */
+int kda_selftest_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
+                            int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
+                            int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
+                            void *out, int64_t ld_out, int32_t out_dtype, int32_t stalled, uint32_t *err_flags,
+                            void *stream);
 
 /*
  * kda_batch_maps — the maps of one step, from the requests' lengths. Request r < R has

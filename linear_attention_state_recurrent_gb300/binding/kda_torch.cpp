@@ -212,12 +212,12 @@ PyObject *norm_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// (a, a_scales, w, w_scales, out, err_flags, stream) -> out
+// (a, a_scales, w, w_scales, out, err_flags, stalled, stream) -> out; stalled: None, or the self-test's
 PyObject *fp8_matmul(PyObject *, PyObject *const *v, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     const Tensor *a, *sa, *w, *sw, *out;
-    if (!count(n, 7) || !tensor(v[0], "a", false, &a) || !tensor(v[1], "a_scales", false, &sa) || !tensor(v[2], "w", false, &w) ||
+    if (!count(n, 8) || !tensor(v[0], "a", false, &a) || !tensor(v[1], "a_scales", false, &sa) || !tensor(v[2], "w", false, &w) ||
         !tensor(v[3], "w_scales", false, &sw) || !tensor(v[4], "out", false, &out))
         return nullptr;
     if (a->dim() != 2 || w->dim() != 2) return refuse("a and w must be 2-D with the same number of columns");
@@ -225,18 +225,23 @@ PyObject *fp8_matmul(PyObject *, PyObject *const *v, Py_ssize_t n)
     const int code = code_of(out->scalar_type());
     if (code < 0) return refuse("out must be bf16, fp16 or fp32");
     int64_t ld_a, ld_w, ld_out, sa_row, sa_group, sw_row, sw_group;
+    int64_t stalled = 0;
     uint32_t *err;
     void *stream;
     if (!matrix(*a, "a", E4M3, M, K, nullptr, &ld_a) || !matrix(*w, "w", E4M3, N, K, a, &ld_w) ||
         !scales_of(*sa, "a_scales", M, groups, a, &sa_row, &sa_group) ||
         !scales_of(*sw, "w_scales", (N + 127) / 128, groups, a, &sw_row, &sw_group) ||
-        !matrix(*out, "out", out->scalar_type(), M, N, a, &ld_out) || !error_word(v[5], a, &err) || !stream_of(v[6], *a, &stream))
+        !matrix(*out, "out", out->scalar_type(), M, N, a, &ld_out) || !error_word(v[5], a, &err) ||
+        (v[6] != Py_None && !integer(v[6], &stalled)) || !stream_of(v[7], *a, &stream))
         return nullptr;
+    if (stalled < 0 || stalled > 7) return refuse("stalled must be in [0, 7]");
     const c10::cuda::CUDAGuard guard(a->device());
-    const int status = kda_fp8_matmul(static_cast<const uint8_t *>(a->data_ptr()), ld_a, static_cast<const float *>(sa->data_ptr()), sa_row,
-                                      sa_group, static_cast<const uint8_t *>(w->data_ptr()), ld_w,
-                                      static_cast<const float *>(sw->data_ptr()), sw_row, sw_group, M, N, K, out->data_ptr(), ld_out, code,
-                                      err, stream);
+    const auto pa = static_cast<const uint8_t *>(a->data_ptr()), pw = static_cast<const uint8_t *>(w->data_ptr());
+    const auto psa = static_cast<const float *>(sa->data_ptr()), psw = static_cast<const float *>(sw->data_ptr());
+    const int status = v[6] == Py_None ? kda_fp8_matmul(pa, ld_a, psa, sa_row, sa_group, pw, ld_w, psw, sw_row, sw_group, M, N, K,
+                                                        out->data_ptr(), ld_out, code, err, stream)
+                                       : kda_selftest_fp8_matmul(pa, ld_a, psa, sa_row, sa_group, pw, ld_w, psw, sw_row, sw_group, M, N,
+                                                                 K, out->data_ptr(), ld_out, code, static_cast<int32_t>(stalled), err, stream);
     if (status != KDA_OK) return PyLong_FromLong(status);
     return Py_NewRef(v[4]);
     END_HANDLE_TH_ERRORS

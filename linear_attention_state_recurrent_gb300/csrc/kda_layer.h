@@ -31,6 +31,7 @@ struct Fp8Params {
     int M, N, K;
     void *out;          int64_t ld_out;   int out_dtype;
     uint32_t *err;
+    int stalled;                         // self-test: the CTA of each cluster whose scales never come (-1: none)
 };
 cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream);
 

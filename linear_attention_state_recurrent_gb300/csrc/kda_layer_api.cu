@@ -27,6 +27,31 @@ int check_dtype(int32_t dtype, const char *name)
     return KDA_OK;
 }
 
+int fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
+               int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
+               int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
+               void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, int stalled, void *stream)
+{
+    int s;
+    if ((s = check_dtype(out_dtype, "out_dtype"))) return s;
+    constexpr int64_t most = int64_t(1) << 30;   // tile ends past a side stay below 2^31
+    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most) return invalid("M, N and K must be in [0, 2^30]");
+    if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX)
+        return set_error(KDA_ERR_UNSUPPORTED, "%lld x %lld outputs exceed one launch: split the call", (long long)M, (long long)N);
+    if (M == 0 || N == 0) return set_error(KDA_OK, "%s", "");
+    if (!out) return invalid("out must be non-NULL");
+    if (K > 0 && (!a || !a_scales || !w || !w_scales)) return invalid("a, w and their scales must be non-NULL");
+    if (ld_a < K || ld_w < K || ld_out < N) return invalid("row strides must be >= K (a, w) and >= N (out)");
+    if (sa_row_stride < 1 || sa_group_stride < 1 || sw_row_stride < 1 || sw_group_stride < 1)
+        return invalid("scale strides must be >= 1");
+    if (!aligned(out, out_dtype == KDA_FP32 ? 4 : 2) || !aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(err_flags, 4))
+        return invalid("a pointer is not aligned to its element type");
+    kda::Fp8Params p{a, ld_a, a_scales, sa_row_stride, sa_group_stride, w, ld_w, w_scales, sw_row_stride,
+                 sw_group_stride, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), out, ld_out,
+                 out_dtype, err_flags, stalled};
+    return done(kda::launch_fp8_matmul(p, static_cast<cudaStream_t>(stream)), "kda_fp8_matmul launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -63,24 +88,20 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
                    int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
                    void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, void *stream)
 {
-    int s;
-    if ((s = check_dtype(out_dtype, "out_dtype"))) return s;
-    constexpr int64_t most = int64_t(1) << 30;   // tile ends past a side stay below 2^31
-    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most) return invalid("M, N and K must be in [0, 2^30]");
-    if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX)
-        return set_error(KDA_ERR_UNSUPPORTED, "%lld x %lld outputs exceed one launch: split the call", (long long)M, (long long)N);
-    if (M == 0 || N == 0) return set_error(KDA_OK, "%s", "");
-    if (!out) return invalid("out must be non-NULL");
-    if (K > 0 && (!a || !a_scales || !w || !w_scales)) return invalid("a, w and their scales must be non-NULL");
-    if (ld_a < K || ld_w < K || ld_out < N) return invalid("row strides must be >= K (a, w) and >= N (out)");
-    if (sa_row_stride < 1 || sa_group_stride < 1 || sw_row_stride < 1 || sw_group_stride < 1)
-        return invalid("scale strides must be >= 1");
-    if (!aligned(out, out_dtype == KDA_FP32 ? 4 : 2) || !aligned(a_scales, 4) || !aligned(w_scales, 4) || !aligned(err_flags, 4))
-        return invalid("a pointer is not aligned to its element type");
-    kda::Fp8Params p{a, ld_a, a_scales, sa_row_stride, sa_group_stride, w, ld_w, w_scales, sw_row_stride,
-                     sw_group_stride, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), out, ld_out,
-                     out_dtype, err_flags};
-    return done(kda::launch_fp8_matmul(p, static_cast<cudaStream_t>(stream)), "kda_fp8_matmul launch");
+    return fp8_matmul(a, ld_a, a_scales, sa_row_stride, sa_group_stride, w, ld_w, w_scales, sw_row_stride, sw_group_stride, M, N, K, out,
+                      ld_out, out_dtype, err_flags, -1, stream);
+}
+
+int kda_selftest_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
+                            int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
+                            int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
+                            void *out, int64_t ld_out, int32_t out_dtype, int32_t stalled, uint32_t *err_flags,
+                            void *stream)
+{
+    if (!err_flags) return invalid("err_flags must be non-NULL");
+    if (stalled < 0 || stalled > 7) return invalid("stalled must be in [0, 7]");
+    return fp8_matmul(a, ld_a, a_scales, sa_row_stride, sa_group_stride, w, ld_w, w_scales, sw_row_stride, sw_group_stride, M, N, K, out,
+                      ld_out, out_dtype, err_flags, stalled, stream);
 }
 
 int kda_batch_maps(const int32_t *query_lens, const int32_t *context_lens, const int32_t *state_slots,

@@ -41,7 +41,7 @@ EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decod
             "kda_spec_verify", "kda_spec_verify_checkpoints", "kda_fused_decode",
             "kda_fused_spec_verify", "kda_selftest_bounded_wait", "kda_chunk_prefill_workspace_bytes",
             "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
-            "kda_norm_quant", "kda_fp8_matmul", "kda_batch_maps")
+            "kda_norm_quant", "kda_fp8_matmul", "kda_selftest_fp8_matmul", "kda_batch_maps")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -117,6 +117,8 @@ def _load():
                                    P, I64, I64, P]
     lib.kda_fp8_matmul.restype = ctypes.c_int
     lib.kda_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, P, P]
+    lib.kda_selftest_fp8_matmul.restype = ctypes.c_int
+    lib.kda_selftest_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, I32, P, P]
     lib.kda_batch_maps.restype = ctypes.c_int
     lib.kda_batch_maps.argtypes = [P, P, P, I64, I64, P, I64, I64, P, I64, P, I64, I32, I64, P, P, P, P, P, P,
                                    P, P, P]
@@ -544,9 +546,18 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
         if out_dtype not in _FLOATS:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
         out = torch.empty(a.shape[0], w.shape[0], dtype=out_dtype, device=a.device)
-    r = _torch_binding.fp8_matmul(a, a_scales, w, w_scales, out, err_flags, _handle(stream))
+    r = _torch_binding.fp8_matmul(a, a_scales, w, w_scales, out, err_flags, None, _handle(stream))
     if type(r) is int:
         _check(r, "kda_fp8_matmul")
+    return r
+
+
+def kda_selftest_fp8_matmul(a, a_scales, w, w_scales, out, err_flags, stalled=0, stream=None):
+    """kda_fp8_matmul in which the scales of CTA `stalled` of each cluster never come: what waits for them gives up
+    (~2 s) and sets KDA_ERRFLAG_TIMEOUT in err_flags, and what it was to write to `out` stays as it was."""
+    r = _torch_binding.fp8_matmul(a, a_scales, w, w_scales, out, err_flags, stalled, _handle(stream))
+    if type(r) is int:
+        _check(r, "kda_selftest_fp8_matmul")
     return r
 
 

@@ -1,0 +1,41 @@
+"""Host side of the operators around the recurrence beyond their own refusals: the self-test's. No GPU: every call here
+fails its checks before anything is launched."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def kda():
+    from linear_attention_state_recurrent_gb300 import build
+    build.build()
+    from linear_attention_state_recurrent_gb300 import kda as k
+    return k
+
+
+F = 1 << 20   # never dereferenced: validation fails before any launch
+
+
+def _selftest(kda, **kw):
+    a = dict(a=F, ld_a=128, sa=F, sar=1, sag=8, w=F, ld_w=128, sw=F, swr=1, swg=1, M=8, N=8, K=128, out=F, ld_out=8,
+             dtype=0, stalled=0, err=F, stream=None)
+    a.update(kw)
+    return kda.lib.kda_selftest_fp8_matmul(*a.values())
+
+
+@pytest.mark.parametrize("bad,word", [(dict(err=None), "err_flags"), (dict(stalled=-1), "stalled"), (dict(stalled=8), "stalled"),
+                                      (dict(out=None), "out"), (dict(ld_a=127), "strides"), (dict(dtype=3), "out_dtype")])
+def test_fp8_matmul_selftest_refuses(kda, bad, word):
+    assert _selftest(kda, **bad) == 1
+    assert word in kda.last_error()
+
+
+def test_fp8_matmul_selftest_of_nothing_is_nothing(kda):
+    assert _selftest(kda, M=0) == 0 and kda.last_error() == ""
+
+
+def test_fp8_matmul_selftest_binding_refuses(kda):
+    a, w, out = (torch.zeros(n, 128).to(torch.float8_e4m3fn) for n in (4, 8, 4))
+    args = dict(a=a, a_scales=torch.ones(4, 1), w=w, w_scales=torch.ones(1, 1), out=torch.zeros(4, 8), err_flags=None)
+    for bad in (dict(a=a[0]), dict(w=w.float()), dict(out=out), dict(stalled=8), dict()):   # the last: not on the GPU
+        with pytest.raises(ValueError):
+            kda.kda_selftest_fp8_matmul(**(args | bad))

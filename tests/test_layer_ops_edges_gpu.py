@@ -18,6 +18,16 @@ def kda():
     return k
 
 
+def i32(*values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def weights(n, k, seed):
+    """e4m3 [n, k] with scales."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(n, k, generator=g).to(E4M3).cuda(), torch.exp(torch.randn(-(-n // 128), -(-k // 128), generator=g)).cuda()
+
+
 # ---- kda_norm_quant: values between two of e4m3 -------------------------------------------
 
 
@@ -69,3 +79,35 @@ def test_norm_quant_rounds_the_quotient_by_its_scale(kda, dtype):
     q, s, _ = kda.kda_norm_quant(x)
     quotient = (x.double() / s.double().repeat_interleave(128, 1)).float().clamp(-448, 448)
     assert torch.equal(q.float(), quotient.to(E4M3).float())
+
+
+# ---- waits that give up -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 16432), (20, 40, 16432), (50, 40, 16432), (130, 40, 16432),   # the inner axis split
+                                   (9, 20512, 256), (100, 20512, 256), (4000, 1500, 1040)])              # and not
+def test_fp8_matmul_whose_waits_give_up_leaves_out_alone(kda, M, N, K):
+    """Sums that wait for scales which never come are not stored, neither a CTA's own nor those of a split that
+    it is part of; the error word says so, and the next call on the context is right."""
+    a, sa = weights(M, K, 51)
+    sa = sa.repeat_interleave(128, 0)[:M].contiguous()
+    w, sw = weights(N, K, 52)
+    err = i32(0)
+    want = kda.kda_fp8_matmul(a, sa, w, sw, err_flags=err)
+    assert err.item() == 0
+    out = torch.full((M, N), 9.0, dtype=BF16, device="cuda")
+    kda.kda_selftest_fp8_matmul(a, sa, w, sw, out, err)
+    torch.cuda.synchronize()
+    assert err.item() == kda.KDA_ERRFLAG_TIMEOUT
+    assert torch.all(out == 9)
+    err.zero_()
+    assert torch.equal(kda.kda_fp8_matmul(a, sa, w, sw, out=out, err_flags=err), want) and err.item() == 0
+
+
+def test_fp8_matmul_selftest_stalls_nothing_that_is_not_there(kda):
+    a, sa = weights(128, 256, 53)
+    w, sw = weights(200, 256, 54)
+    err, out = i32(0), torch.empty(128, 200, dtype=BF16, device="cuda")
+    sa = sa.repeat_interleave(128, 0)
+    kda.kda_selftest_fp8_matmul(a, sa, w, sw, out, err, stalled=7)   # two groups: clusters of two at most
+    assert torch.equal(out, kda.kda_fp8_matmul(a, sa, w, sw)) and err.item() == 0
