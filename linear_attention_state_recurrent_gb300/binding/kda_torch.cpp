@@ -172,6 +172,11 @@ PyObject *norm_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (q && !matrix(*q, "q", E4M3, N, D, x, &ld_q)) return nullptr;
     if (scales && !scales_of(*scales, "scales", N, groups, x, &s_row, &s_group)) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
+    void *stream;
+    if (!stream_of(a[8], *x, &stream)) return nullptr;
+    // what is allocated below belongs to the stream that the kernel runs on
+    c10::cuda::OptionalCUDAStreamGuard on;
+    if (a[8] != Py_None) on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), x->device().index()));
     Tensor made_q, made_s, made_r;
     if (!q) {   // rows on 16-byte boundaries
         ld_q = (D + 15) / 16 * 16;
@@ -189,8 +194,6 @@ PyObject *norm_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
         res_out = &made_r;
         ld_ro = D;
     }
-    void *stream;
-    if (!stream_of(a[8], *x, &stream)) return nullptr;
     const int status = kda_norm_quant(
         x->data_ptr(), ld_x, res ? res->data_ptr() : nullptr, ld_res, code,
         weight ? static_cast<const float *>(weight->data_ptr()) : nullptr, static_cast<float>(eps), N, D,

@@ -14,11 +14,13 @@ Tensor conventions:
   state_indices int32 1-D, any positive stride
   cu_seqlens int32 [num_seqs + 1] on the GPU (a host copy is taken for launch sizing)
 The calls around the recurrence (kda_norm_quant, kda_fp8_matmul, kda_batch_maps) take 8-bit values
-as float8_e4m3fn tensors; their docstrings give the rest.
+as float8_e4m3fn tensors; their docstrings give the rest. With `stream` they run there, the arguments have to
+be ready there, and the tensors they allocate belong to it, as those made under torch.cuda.stream(stream) do.
 """
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -518,6 +520,14 @@ def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
 
+def _on(stream):
+    """The context for what a call allocates itself: torch's allocator takes a block to be in use on the stream
+    that was current when it was made, so that has to be the stream the call's kernel runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
 def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None, y=None, q=None,
                    scales=None, stream=None):
     """h = x + residual, y = h / sqrt(mean h^2 + eps) * weight, and y in e4m3 with an fp32 scale per
@@ -545,7 +555,8 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
     if out is None:
         if out_dtype not in _FLOATS:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
-        out = torch.empty(a.shape[0], w.shape[0], dtype=out_dtype, device=a.device)
+        with _on(stream):
+            out = torch.empty(a.shape[0], w.shape[0], dtype=out_dtype, device=a.device)
     r = _torch_binding.fp8_matmul(a, a_scales, w, w_scales, out, err_flags, None, _handle(stream))
     if type(r) is int:
         _check(r, "kda_fp8_matmul")
@@ -587,7 +598,8 @@ def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_page
     if out is None:
         if num_tokens is None:
             raise ValueError("kda_batch_maps needs num_tokens or out")
-        out = make_batch_maps(query_lens.shape[0], num_tokens, query_lens.device)
+        with _on(stream):
+            out = make_batch_maps(query_lens.shape[0], num_tokens, query_lens.device)
     elif num_tokens is not None and num_tokens != out.positions.shape[0]:
         raise ValueError("num_tokens must be the length of out.positions")
     r = _torch_binding.batch_maps(query_lens, context_lens, state_slots, block_table, free_pages, free_count, page_size, num_pages, out,

@@ -111,3 +111,70 @@ def test_fp8_matmul_selftest_stalls_nothing_that_is_not_there(kda):
     sa = sa.repeat_interleave(128, 0)
     kda.kda_selftest_fp8_matmul(a, sa, w, sw, out, err, stalled=7)   # two groups: clusters of two at most
     assert torch.equal(out, kda.kda_fp8_matmul(a, sa, w, sw)) and err.item() == 0
+
+
+# ---- streams other than the current one ---------------------------------------------------
+
+
+def calls(kda):
+    """The calls that allocate, each with outputs of a megabyte or more."""
+    g = torch.Generator().manual_seed(41)
+    x, r = torch.randn(2, 1500, 2048, generator=g).to(BF16).cuda()
+    q, s, _ = kda.kda_norm_quant(x)
+    (w, sw), ones = weights(1100, 2048, 42), torch.ones(2048, device="cuda")
+    maps = (i32(300000, 1, 200000), i32(0, 7, 3), i32(4, 5, 6), torch.zeros(3, 6000, dtype=torch.int32, device="cuda"),
+            torch.arange(9000, dtype=torch.int32, device="cuda"), i32(9000), 100)
+    return {"norm_quant": lambda stream: kda.kda_norm_quant(x, ones, residual=r, stream=stream),
+            "fp8_matmul": lambda stream: (kda.kda_fp8_matmul(q, s, w, sw, stream=stream),),
+            "batch_maps": lambda stream: kda.kda_batch_maps(*maps, num_pages=9000, num_tokens=500001, stream=stream)}
+
+
+@pytest.mark.parametrize("name", ["norm_quant", "fp8_matmul", "batch_maps"])
+@pytest.mark.parametrize("default", [False, True])   # from the default stream to another, and from another to the default one
+def test_what_a_call_allocates_belongs_to_its_stream(kda, name, default):
+    """Once dropped it is not handed out on the stream that was current, where its kernel may still be running, but
+    on the call's own."""
+    call = calls(kda)[name]
+    other = torch.cuda.Stream()
+    current, stream = (other, torch.cuda.default_stream()) if default else (torch.cuda.default_stream(), other)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(current):
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        out = call(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.double(), b.double()) for a, b in zip(want, out))
+        blocks = {t.data_ptr(): t.untyped_storage().nbytes() for t in out if t.untyped_storage().nbytes() >= 1 << 20}
+        assert blocks
+        del out
+        here = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in blocks.values()]
+        with torch.cuda.stream(stream):
+            there = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in blocks.values()]
+    assert not {t.data_ptr() for t in here} & set(blocks)
+    assert {t.data_ptr() for t in there} == set(blocks)
+
+
+def test_results_dropped_before_their_readers_have_run(kda):
+    """q and the scales pass between two calls on a busy stream and are dropped at once; what is allocated and
+    written on the current stream meanwhile must not be their memory."""
+    g = torch.Generator().manual_seed(43)
+    x = torch.randn(4000, 2048, generator=g).to(BF16).cuda()
+    w, sw = weights(640, 2048, 44)
+    q, s, _ = kda.kda_norm_quant(x)
+    want = kda.kda_fp8_matmul(q, s, w, sw)
+    del q, s
+    side = torch.cuda.Stream()
+    busy = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(40):
+            busy.fill_(i)
+    q, s, _ = kda.kda_norm_quant(x, stream=side)
+    got = kda.kda_fp8_matmul(q, s, w, sw, stream=side)
+    sizes = [t.untyped_storage().nbytes() for t in (q, s)]
+    del q, s
+    junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert len(junk) == 2 and torch.equal(got, want)
