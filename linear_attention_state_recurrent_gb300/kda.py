@@ -14,8 +14,9 @@ Tensor conventions:
   state_indices int32 1-D, any positive stride
   cu_seqlens int32 [num_seqs + 1] on the GPU (a host copy is taken for launch sizing)
 The calls around the recurrence (kda_norm_quant, kda_fp8_matmul, kda_batch_maps) take 8-bit values
-as float8_e4m3fn tensors; their docstrings give the rest. With `stream` they run there, the arguments have to
-be ready there, and the tensors they allocate belong to it, as those made under torch.cuda.stream(stream) do.
+as float8_e4m3fn tensors; their docstrings give the rest.
+With `stream` a call runs there, its arguments have to be ready there, and the tensors it allocates
+belong to that stream, as those made under torch.cuda.stream(stream) do.
 """
 from __future__ import annotations
 
@@ -153,6 +154,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(stream):
+    """The context for what a call allocates itself: torch's allocator takes a block to be in use on the stream
+    that was current when it was made, so that has to be the stream the call's kernel runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
 def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16):
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
@@ -191,9 +200,10 @@ def make_state(state_pool, state_indices, null_slot=-1):
                     index_stride=state_indices.stride(0), null_slot=int(null_slot))
 
 
-def _out(out, N, H, V, device):
+def _out(out, N, H, V, device, stream):
     if out is None:
-        out = torch.empty(N, H * V, dtype=torch.bfloat16, device=device)
+        with _on(stream):
+            out = torch.empty(N, H * V, dtype=torch.bfloat16, device=device)
     elif out.dim() != 2 or out.shape[0] < N:
         raise ValueError(f"out must have at least {N} rows")
     return out, _rows(out, "out")
@@ -215,10 +225,11 @@ def kda_gate(raw_g, raw_beta, A_log, dt_bias=None, lower_bound=None, *, K=None, 
     K = raw_g.shape[1] // H if K is None else K
     ld_g, ld_b = _rows(raw_g, "raw_g"), _rows(raw_beta, "raw_beta")
     hd = make_heads(A_log, dt_bias, lower_bound, K, K)
-    if g_out is None:
-        g_out = torch.empty(N, H * K, dtype=torch.float32, device=raw_g.device)
-    if beta_out is None:
-        beta_out = torch.empty(N, H, dtype=torch.float32, device=raw_g.device)
+    with _on(stream):
+        if g_out is None:
+            g_out = torch.empty(N, H * K, dtype=torch.float32, device=raw_g.device)
+        if beta_out is None:
+            beta_out = torch.empty(N, H, dtype=torch.float32, device=raw_g.device)
     _check(lib.kda_gate(_ptr(raw_g), ld_g, _ptr(raw_beta), ld_b, N, ctypes.byref(hd),
                         _ptr(g_out), _ptr(beta_out), _stream(stream)), "kda_gate")
     return g_out, beta_out
@@ -235,7 +246,7 @@ def kda_packed_decode(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, i
     if state_indices.shape[0] < N:
         raise ValueError("state_indices has fewer entries than sequences")
     _need_rows(N, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     _check(lib.kda_packed_decode(_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g),
                                  _rows(raw_g, "raw_g"), _ptr(raw_beta), _rows(raw_beta, "raw_beta"),
                                  N, ctypes.byref(hd), ctypes.byref(st), _ptr(out), ld_out,
@@ -257,7 +268,7 @@ def kda_spec_verify(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
     if state_indices.shape[0] < R:
         raise ValueError("state_indices has fewer entries than requests")
     _need_rows(N, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     _check(lib.kda_spec_verify(_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g),
                                _rows(raw_g, "raw_g"), _ptr(raw_beta), _rows(raw_beta, "raw_beta"),
                                R, int(tokens_per_req), ctypes.byref(hd), ctypes.byref(st),
@@ -290,7 +301,7 @@ def kda_spec_verify_checkpoints(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lowe
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(state_pool, block_table[:, 0], null_slot)
     _need_rows(N, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     _check(lib.kda_spec_verify_checkpoints(
         _ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g), _rows(raw_g, "raw_g"),
         _ptr(raw_beta), _rows(raw_beta, "raw_beta"), R, T, _ptr(num_accepted),
@@ -337,7 +348,7 @@ def _fused(name, mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, initia
         raise ValueError("conv_state must have a slot for every state slot")
     cv = None if conv is None else make_conv(*conv)
     nm = None if norm is None else make_norm(*norm)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     head = (_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g), _rows(raw_g, "raw_g"),
             _ptr(raw_beta), _rows(raw_beta, "raw_beta"), E)
     tail = (ctypes.byref(hd), ctypes.byref(st), None if cv is None else ctypes.byref(cv),
@@ -409,11 +420,12 @@ def kda_chunk_prefill_workspace_bytes(cu_seqlens_host, H, K, V, chunk_size=64, n
                                                      ctypes.byref(hd), chunk_size))
 
 
-def _workspace(nbytes, device, workspace):
+def _workspace(nbytes, device, workspace, stream):
     if nbytes == 0:
         return None, 0
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -429,9 +441,9 @@ def kda_chunk_prefill(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, i
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(initial_state, state_indices, null_slot)
     _check_varlen(cu_h, N, S, state_indices, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     nb = kda_chunk_prefill_workspace_bytes(cu_h, H, K, V, chunk_size)
-    ws, ws_bytes = _workspace(nb, mixed_qkv.device, workspace)
+    ws, ws_bytes = _workspace(nb, mixed_qkv.device, workspace, stream)
     _check(lib.kda_chunk_prefill(_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g),
                                  _rows(raw_g, "raw_g"), _ptr(raw_beta), _rows(raw_beta, "raw_beta"),
                                  _ptr(cu_seqlens), ctypes.c_void_p(cu_h.data_ptr()), S,
@@ -459,7 +471,7 @@ def kda_chunk_prefill_no_alloc(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(initial_state, state_indices, null_slot)
     _check_varlen(cu_h, N, S, state_indices, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     _check(lib.kda_chunk_prefill_no_alloc(_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g),
                                           _rows(raw_g, "raw_g"), _ptr(raw_beta), _rows(raw_beta, "raw_beta"),
                                           _ptr(cu_seqlens), ctypes.c_void_p(cu_h.data_ptr()), S,
@@ -483,9 +495,9 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(initial_state, state_indices, null_slot)
     _check_varlen(cu_h, N, S, state_indices, raw_g=raw_g, raw_beta=raw_beta)
-    out, ld_out = _out(out, N, H, V, mixed_qkv.device)
+    out, ld_out = _out(out, N, H, V, mixed_qkv.device, stream)
     nb = kda_chunk_prefill_workspace_bytes(cu_h[num_decodes:], H, K, V, 64, num_seqs=P)
-    ws, ws_bytes = _workspace(nb, mixed_qkv.device, workspace)
+    ws, ws_bytes = _workspace(nb, mixed_qkv.device, workspace, stream)
     _check(lib.kda_mixed_batch(_ptr(mixed_qkv), _rows(mixed_qkv, "mixed_qkv"), _ptr(raw_g),
                                _rows(raw_g, "raw_g"), _ptr(raw_beta), _rows(raw_beta, "raw_beta"),
                                _ptr(cu_seqlens), ctypes.c_void_p(cu_h.data_ptr()), int(num_decodes),
@@ -518,14 +530,6 @@ _torch_binding = _load_torch_binding()
 
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
-
-
-def _on(stream):
-    """The context for what a call allocates itself: torch's allocator takes a block to be in use on the stream
-    that was current when it was made, so that has to be the stream the call's kernel runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream))
 
 
 def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None, y=None, q=None,
