@@ -388,13 +388,14 @@ def kda_selftest_bounded_wait(err_flags, stream=None):
     _check(lib.kda_selftest_bounded_wait(_ptr(err_flags), _stream(stream)), "kda_selftest_bounded_wait")
 
 
-def _host_cu(cu_seqlens, cu_seqlens_host):
-    """The host copy of cu_seqlens (read from the device when not given; a given copy must
-    hold the same values as the device tensor, which the library sizes its launch from)."""
+def _host_cu(cu_seqlens, cu_seqlens_host, stream):
+    """The host copy of cu_seqlens (read from the device when not given, on the call's stream; a given
+    copy must hold the same values as the device tensor, which the library sizes its launch from)."""
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor")
     if cu_seqlens_host is None:
-        cu_seqlens_host = cu_seqlens.cpu()
+        with _on(stream):
+            cu_seqlens_host = cu_seqlens.cpu()
     cu = cu_seqlens_host.to(torch.int32).contiguous()
     if cu.numel() != cu_seqlens.numel():
         raise ValueError("cu_seqlens_host and cu_seqlens must have the same length")
@@ -436,7 +437,7 @@ def kda_chunk_prefill(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, i
     """Chunked varlen prefill; returns (out, initial_state)."""
     _, H, K, V = initial_state.shape
     N = mixed_qkv.shape[0]
-    cu_h = _host_cu(cu_seqlens, cu_seqlens_host)
+    cu_h = _host_cu(cu_seqlens, cu_seqlens_host, stream)
     S = cu_h.numel() - 1
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(initial_state, state_indices, null_slot)
@@ -466,7 +467,7 @@ def kda_chunk_prefill_no_alloc(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower
     N = mixed_qkv.shape[0]
     if out is None or cu_seqlens_host is None:
         raise ValueError("kda_chunk_prefill_no_alloc needs `out` and `cu_seqlens_host`")
-    cu_h = _host_cu(cu_seqlens, cu_seqlens_host)
+    cu_h = _host_cu(cu_seqlens, cu_seqlens_host, stream)
     S = cu_h.numel() - 1
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)
     st = make_state(initial_state, state_indices, null_slot)
@@ -489,7 +490,7 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
     path, the rest the chunked prefill path; returns (out, initial_state)."""
     _, H, K, V = initial_state.shape
     N = mixed_qkv.shape[0]
-    cu_h = _host_cu(cu_seqlens, cu_seqlens_host)
+    cu_h = _host_cu(cu_seqlens, cu_seqlens_host, stream)
     S = cu_h.numel() - 1
     P = S - num_decodes
     hd = make_heads(A_log, dt_bias, lower_bound, K, V, scale, l2_eps)

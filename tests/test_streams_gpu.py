@@ -1,4 +1,5 @@
-"""The recurrence's calls with stream=: the outputs and workspaces they allocate belong to that stream."""
+"""The recurrence's calls with stream=: the outputs and workspaces they allocate belong to that stream, and the
+lengths they fetch are read there."""
 import pytest
 import torch
 
@@ -97,3 +98,21 @@ def test_a_workspace_is_not_handed_out_while_it_is_used(kda, name):
     junk = [torch.full((n << 20,), 0x7F, dtype=torch.uint8, device="cuda") for n in (1, 2, 4, 8, 16, 32, 64)]
     torch.cuda.synchronize()
     assert len(junk) == 7 and all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_lengths_are_read_on_the_stream(kda):
+    """cu_seqlens written on a busy stream and fetched by a call on it, with no host copy given."""
+    x = inputs(256, 4, 3)
+    state = x["state"].clone()
+    values = torch.tensor([0, 100, 200, 256], dtype=torch.int32).cuda()
+    args = (x["qkv"], x["g"], x["b"], x["A"], x["dt"], None)
+    want, _ = kda.kda_chunk_prefill(*args, x["state"], x["index"], values)
+    cu, busy, side = torch.zeros_like(values), torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for i in range(40):
+            busy.fill_(i)
+        cu.copy_(values)
+    got, _ = kda.kda_chunk_prefill(*args, state, x["index"], cu, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(state, x["state"])
