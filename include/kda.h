@@ -416,6 +416,15 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
                    void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, void *stream);
 
 /*
+ * kda_fp8_matmul_plan — how kda_fp8_matmul would compute a product on the current device: plan (host int32
+ * [3]) receives the rows of a per tile (16, 32, 64: thin; 128: slim; 256: wide; 0: the slower kernel for
+ * operands off 16-byte boundaries), the CTAs that split the inner axis, and the rows of w per tile. Of a
+ * and w only the alignment counts; nothing is launched.
+ */
+int kda_fp8_matmul_plan(const uint8_t *a, int64_t ld_a, const uint8_t *w, int64_t ld_w, int64_t M, int64_t N,
+                        int64_t K, int32_t *plan);
+
+/*
  * kda_selftest_fp8_matmul — exercises that error path without a fault: kda_fp8_matmul in which the
  * scales of CTA `stalled` (0 .. 7) of each thread-block cluster never come, so that what waits
  * for them gives up after ~2 s. err_flags is required. Operands that take the slower kernel, and

@@ -1223,44 +1223,79 @@ cudaError_t this_device(const Device **out)
     return devices[dev].status;
 }
 
-}  // namespace
-
-cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
-{
-    int64_t ld_a = p.ld_a, ld_w = p.ld_w;
-    if (p.K == 0 || !tma_rows(p.a, &ld_a, p.M, p.K) || !tma_rows(p.w, &ld_w, p.N, p.K)) {
-        const int64_t tm = (static_cast<int64_t>(p.M) + GT - 1) / GT, tn = (static_cast<int64_t>(p.N) + GT - 1) / GT;
-        if (tm * tn > INT32_MAX) return cudaErrorInvalidConfiguration;
-        return launch_pdl(general_kernel, dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, p, static_cast<int>(tn));
-    }
-    const Device *d = nullptr;
-    const cudaError_t e = this_device(&d);
-    if (e != cudaSuccess) return e;
+// Which kernel a call takes, in what tiles.
+struct Choice {
+    int rows = 0;              // of A per tile: 0 (general_kernel), 16, 32, 64 (thin_kernel), 128 (slim_kernel), 256 (wide_kernel)
     int split = 1;
-    if (p.M <= 16) {
-        plan_thin<16>(p, d->thin16, &split);
-        return run_thin<16>(p, split, ld_a, ld_w, stream);
-    }
+    SlimPlan slim;
+    int64_t ld_a, ld_w;
+    const Device *device = nullptr;
+};
+
+cudaError_t choose(const Fp8Params &p, Choice *c)
+{
+    c->ld_a = p.ld_a;
+    c->ld_w = p.ld_w;
+    if (p.K == 0 || !tma_rows(p.a, &c->ld_a, p.M, p.K) || !tma_rows(p.w, &c->ld_w, p.N, p.K)) return cudaSuccess;
+    const cudaError_t e = this_device(&c->device);
+    if (e != cudaSuccess) return e;
+    const Device *d = c->device;
     if (p.M <= 32) {
-        plan_thin<32>(p, d->thin32, &split);
-        return run_thin<32>(p, split, ld_a, ld_w, stream);
+        c->rows = p.M <= 16 ? 16 : 32;
+        p.M <= 16 ? plan_thin<16>(p, d->thin16, &c->split) : plan_thin<32>(p, d->thin32, &c->split);
+        return cudaSuccess;
     }
     // More rows: the arrangement of least time. Beyond a thousand rows that is slim_kernel where few columns
     // or a short inner axis leave the pairs of wide_kernel idle or starting: 1311 x 167 x 365 4.0 us against 6.7,
     // 1968 x 600 x 684 7.0 against 9.1, 1500 x 4096 x 4096 33.4 against 35.4.
-    SlimPlan q;
-    const double slim = plan_slim(p, d->slim, &q);
-    if (p.M <= 64 && plan_thin<64>(p, d->thin64, &split) <= slim) return run_thin<64>(p, split, ld_a, ld_w, stream);
+    const double slim = plan_slim(p, d->slim, &c->slim);
+    if (p.M <= 64 && plan_thin<64>(p, d->thin64, &c->split) <= slim) {
+        c->rows = 64;
+        return cudaSuccess;
+    }
     const int groups = (p.K + BK - 1) / BK;
     const int64_t tiles = (static_cast<int64_t>(p.M) + 255) / 256 * ((static_cast<int64_t>(p.N) + 255) / 256);
     const int pairs = d->sms / 2;
     const double busy = tiles < pairs ? static_cast<double>(tiles) / pairs : 1.;
-    if (6000. + (340. + 100. * busy) * groups * static_cast<double>((tiles + pairs - 1) / pairs) < slim)
-        return run_wide(p, ld_a, ld_w, d->sms, stream);
-    const int per = (q.bn / 16 + 3) / 4;
-    if (per <= 1) return run_slim<1>(p, q, ld_a, ld_w, stream);
-    if (per <= 2) return run_slim<2>(p, q, ld_a, ld_w, stream);
-    return run_slim<4>(p, q, ld_a, ld_w, stream);
+    const bool wide = 6000. + (340. + 100. * busy) * groups * static_cast<double>((tiles + pairs - 1) / pairs) < slim;
+    c->rows = wide ? 256 : 128;
+    c->split = wide ? 1 : c->slim.split;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t plan_fp8_matmul(const Fp8Params &p, int32_t (&plan)[3])
+{
+    Choice c;
+    const cudaError_t e = choose(p, &c);
+    if (e != cudaSuccess) return e;
+    plan[0] = c.rows;
+    plan[1] = c.split;
+    plan[2] = c.rows == 0 ? GT : c.rows <= 64 ? 128 : c.rows == 128 ? c.slim.bn : 256;
+    return cudaSuccess;
+}
+
+cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream)
+{
+    Choice c;
+    const cudaError_t e = choose(p, &c);
+    if (e != cudaSuccess) return e;
+    switch (c.rows) {
+    case 16: return run_thin<16>(p, c.split, c.ld_a, c.ld_w, stream);
+    case 32: return run_thin<32>(p, c.split, c.ld_a, c.ld_w, stream);
+    case 64: return run_thin<64>(p, c.split, c.ld_a, c.ld_w, stream);
+    case 128: {
+        const int per = (c.slim.bn / 16 + 3) / 4;
+        if (per <= 1) return run_slim<1>(p, c.slim, c.ld_a, c.ld_w, stream);
+        if (per <= 2) return run_slim<2>(p, c.slim, c.ld_a, c.ld_w, stream);
+        return run_slim<4>(p, c.slim, c.ld_a, c.ld_w, stream);
+    }
+    case 256: return run_wide(p, c.ld_a, c.ld_w, c.device->sms, stream);
+    }
+    const int64_t tm = (static_cast<int64_t>(p.M) + GT - 1) / GT, tn = (static_cast<int64_t>(p.N) + GT - 1) / GT;
+    if (tm * tn > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(general_kernel, dim3(static_cast<unsigned>(tm * tn)), dim3(256), 0, stream, p, static_cast<int>(tn));
 }
 
 }  // namespace kda

@@ -34,6 +34,8 @@ struct Fp8Params {
     int stalled;                         // self-test: the CTA of each cluster whose scales never come (-1: none)
 };
 cudaError_t launch_fp8_matmul(const Fp8Params &p, cudaStream_t stream);
+// Rows of A per tile (0: the general kernel), CTAs that split the inner axis, rows of W per tile.
+cudaError_t plan_fp8_matmul(const Fp8Params &p, int32_t (&plan)[3]);
 
 struct BatchMapsParams {
     const int32_t *qlen, *clen;

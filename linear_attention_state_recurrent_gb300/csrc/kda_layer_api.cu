@@ -27,6 +27,8 @@ int check_dtype(int32_t dtype, const char *name)
     return KDA_OK;
 }
 
+constexpr int64_t kMostSide = int64_t(1) << 30;   // of a product: tile ends past a side stay below 2^31
+
 int fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,
                int64_t sa_group_stride, const uint8_t *w, int64_t ld_w, const float *w_scales,
                int64_t sw_row_stride, int64_t sw_group_stride, int64_t M, int64_t N, int64_t K,
@@ -34,8 +36,7 @@ int fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa
 {
     int s;
     if ((s = check_dtype(out_dtype, "out_dtype"))) return s;
-    constexpr int64_t most = int64_t(1) << 30;   // tile ends past a side stay below 2^31
-    if (M < 0 || N < 0 || K < 0 || M > most || N > most || K > most) return invalid("M, N and K must be in [0, 2^30]");
+    if (M < 0 || N < 0 || K < 0 || M > kMostSide || N > kMostSide || K > kMostSide) return invalid("M, N and K must be in [0, 2^30]");
     if ((M + 63) / 64 * ((N + 63) / 64) > INT32_MAX)
         return set_error(KDA_ERR_UNSUPPORTED, "%lld x %lld outputs exceed one launch: split the call", (long long)M, (long long)N);
     if (M == 0 || N == 0) return set_error(KDA_OK, "%s", "");
@@ -90,6 +91,26 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
 {
     return fp8_matmul(a, ld_a, a_scales, sa_row_stride, sa_group_stride, w, ld_w, w_scales, sw_row_stride, sw_group_stride, M, N, K, out,
                       ld_out, out_dtype, err_flags, -1, stream);
+}
+
+int kda_fp8_matmul_plan(const uint8_t *a, int64_t ld_a, const uint8_t *w, int64_t ld_w, int64_t M, int64_t N,
+                        int64_t K, int32_t *plan)
+{
+    if (!plan) return invalid("plan must be non-NULL");
+    if (M < 1 || N < 1 || K < 0 || M > kMostSide || N > kMostSide || K > kMostSide) return invalid("M and N must be in [1, 2^30], K in [0, 2^30]");
+    if (ld_a < K || ld_w < K) return invalid("row strides must be >= K");
+    kda::Fp8Params p{};
+    p.a = a;
+    p.ld_a = ld_a;
+    p.w = w;
+    p.ld_w = ld_w;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    int32_t got[3];
+    const cudaError_t e = kda::plan_fp8_matmul(p, got);
+    for (int i = 0; i < 3 && e == cudaSuccess; i++) plan[i] = got[i];
+    return done(e, "kda_fp8_matmul_plan");
 }
 
 int kda_selftest_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_t sa_row_stride,

@@ -44,7 +44,8 @@ EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decod
             "kda_spec_verify", "kda_spec_verify_checkpoints", "kda_fused_decode",
             "kda_fused_spec_verify", "kda_selftest_bounded_wait", "kda_chunk_prefill_workspace_bytes",
             "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
-            "kda_norm_quant", "kda_fp8_matmul", "kda_selftest_fp8_matmul", "kda_batch_maps")
+            "kda_norm_quant", "kda_fp8_matmul", "kda_fp8_matmul_plan",
+            "kda_selftest_fp8_matmul", "kda_batch_maps")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -120,6 +121,8 @@ def _load():
                                    P, I64, I64, P]
     lib.kda_fp8_matmul.restype = ctypes.c_int
     lib.kda_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, P, P]
+    lib.kda_fp8_matmul_plan.restype = ctypes.c_int
+    lib.kda_fp8_matmul_plan.argtypes = [P, I64, P, I64, I64, I64, I64, P]
     lib.kda_selftest_fp8_matmul.restype = ctypes.c_int
     lib.kda_selftest_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, I32, P, P]
     lib.kda_batch_maps.restype = ctypes.c_int
@@ -566,6 +569,19 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
     if type(r) is int:
         _check(r, "kda_fp8_matmul")
     return r
+
+
+def kda_fp8_matmul_plan(a, w):
+    """How kda_fp8_matmul would compute a product of these operands on the current device: (rows of a per tile, CTAs that
+    split the inner axis, rows of w per tile). 16, 32, 64, 128 and 256 rows are the tensor cores' arrangements, 0 the
+    slower kernel that operands off 16-byte boundaries take."""
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a and w must be 2-D with the same number of columns")
+    plan = (ctypes.c_int32 * 3)()
+    # the stride of a single row says nothing
+    ld = [max(t.stride(0), t.shape[1]) if t.shape[0] == 1 else t.stride(0) for t in (a, w)]
+    _check(lib.kda_fp8_matmul_plan(_ptr(a), ld[0], _ptr(w), ld[1], a.shape[0], w.shape[0], a.shape[1], plan), "kda_fp8_matmul_plan")
+    return tuple(plan)
 
 
 def kda_selftest_fp8_matmul(a, a_scales, w, w_scales, out, err_flags, stalled=0, stream=None):

@@ -1,5 +1,7 @@
-"""Host side of the operators around the recurrence beyond their own refusals: the self-test's. No GPU: every call here
+"""Host side of the operators around the recurrence beyond their own refusals: the plan's and the self-test's. No GPU: every call here
 fails its checks before anything is launched."""
+import ctypes
+
 import pytest
 import torch
 
@@ -39,3 +41,29 @@ def test_fp8_matmul_selftest_binding_refuses(kda):
     for bad in (dict(a=a[0]), dict(w=w.float()), dict(out=out), dict(stalled=8), dict()):   # the last: not on the GPU
         with pytest.raises(ValueError):
             kda.kda_selftest_fp8_matmul(**(args | bad))
+
+
+def _plan(kda, **kw):
+    a = dict(a=F, ld_a=128, w=F, ld_w=128, M=8, N=8, K=128, plan=(ctypes.c_int32 * 3)())
+    a.update(kw)
+    return kda.lib.kda_fp8_matmul_plan(*a.values())
+
+
+@pytest.mark.parametrize("bad", [dict(plan=None), dict(M=0), dict(N=0), dict(K=-1), dict(M=(1 << 30) + 1), dict(ld_a=127), dict(ld_w=0)])
+def test_fp8_matmul_plan_refuses(kda, bad):
+    assert _plan(kda, **bad) == 1 and kda.last_error()
+
+
+@pytest.mark.parametrize("off", [dict(a=F + 1), dict(w=F + 8), dict(ld_a=129), dict(ld_w=136), dict(K=0)])
+def test_fp8_matmul_plan_of_what_the_tensor_cores_cannot_load(kda, off):
+    plan = (ctypes.c_int32 * 3)()
+    assert _plan(kda, plan=plan, **off) == 0 and list(plan) == [0, 1, 64]
+
+
+def test_fp8_matmul_plan_binding(kda):
+    e = torch.float8_e4m3fn
+    a, w = torch.zeros(4, 129).to(e), torch.zeros(8, 129).to(e)
+    assert kda.kda_fp8_matmul_plan(a, w) == (0, 1, 64)
+    for bad in ((a[0], w), (a, w[:, :128])):
+        with pytest.raises(ValueError):
+            kda.kda_fp8_matmul_plan(*bad)

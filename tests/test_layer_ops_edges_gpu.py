@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests.test_layer_ops_gpu import check_matmul, operands, up16
+
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
@@ -79,6 +81,65 @@ def test_norm_quant_rounds_the_quotient_by_its_scale(kda, dtype):
     q, s, _ = kda.kda_norm_quant(x)
     quotient = (x.double() / s.double().repeat_interleave(128, 1)).float().clamp(-448, 448)
     assert torch.equal(q.float(), quotient.to(E4M3).float())
+
+
+# ---- every way a product is cut up ---------------------------------------------------------
+
+# rows of a per tile, whether the inner axis is split, the least and the most rows of w per tile, and a size that gets there
+WAYS = {"thin 16": (16, False, 128, 128, (9, 300, 300)), "thin 16 split": (16, True, 128, 128, (9, 300, 1040)),
+        "thin 32": (32, False, 128, 128, (24, 300, 300)), "thin 32 split": (32, True, 128, 128, (24, 500, 2100)),
+        "thin 64": (64, False, 128, 128, (37, 12374, 529)), "thin 64 split": (64, True, 128, 128, (60, 1500, 1040)),
+        "slim, one chunk": (128, False, 16, 64, (100, 300, 300)), "slim, one chunk, split": (128, True, 16, 64, (130, 300, 1040)),
+        "slim, two chunks": (128, False, 80, 128, (130, 9000, 140)), "slim, two chunks, split": (128, True, 80, 128, (100, 1500, 2100)),
+        "slim, four chunks": (128, False, 144, 256, (700, 4200, 140)), "slim, four chunks, split": (128, True, 144, 256, (300, 1500, 8200)),
+        "wide": (256, False, 256, 256, (2500, 1500, 1040)), "wide, few columns": (256, False, 256, 256, (19859, 2, 17)),
+        "wide, a warp's columns": (256, False, 256, 256, (21674, 64, 17)), "wide, an edge": (256, False, 256, 256, (9961, 260, 28)),
+        "general": (0, False, 64, 64, (70, 130, 261))}
+
+
+def product(way):
+    """The operands of one way, with scales in either order."""
+    rows, _, _, _, (M, N, K) = WAYS[way]
+    pad = (1, 0) if rows == 0 else (up16(K), up16(K))
+    return operands(M, N, K, M + N, pad, group_major=N % 8 == 0)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_fp8_matmul_plan(kda, way):
+    """The sizes below reach what they are there for: a change of the plans that empties a test fails here."""
+    rows, split, least, most, _ = WAYS[way]
+    a, _, w, _ = product(way)
+    got = kda.kda_fp8_matmul_plan(a, w)
+    assert got[0] == rows and (got[1] > 1) == split and least <= got[2] <= most
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_fp8_matmul_every_way(kda, way, dtype, aligned):
+    """Each kernel, split and not, with outputs of each type on and off 16-byte boundaries, in wider rows whose other columns
+    stay as they were. A 16-bit output is the fp32 one, rounded once: fp16 is compared with that (its subnormals have
+    no relative bound), the others with 64 bits."""
+    a, sa, w, sw = product(way)
+    M, N = a.shape[0], w.shape[0]
+    edge = 16 if aligned else 5
+    buf = torch.full((M, N + 2 * edge + up16(N) * aligned), 9.0, dtype=dtype, device="cuda")
+    out = buf[:, edge:edge + N]
+    if dtype == FP16:
+        sa, sw = sa * 1e-4, sw * 1e-2
+        kda.kda_fp8_matmul(a, sa, w, sw, out=out)
+        assert torch.equal(out, kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=FP32).to(FP16))
+    else:
+        check_matmul(kda, a, sa, w, sw, out=out)
+    assert torch.all(buf[:, :edge] == 9) and torch.all(buf[:, edge + N:] == 9)
+
+
+@pytest.mark.parametrize("way", [w for w in WAYS if "split" in w] + ["thin 64", "wide", "wide, an edge"])
+def test_fp8_matmul_every_way_repeats_bit_for_bit(kda, way):
+    a, sa, w, sw = product(way)
+    first = kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=FP32)
+    for _ in range(20):
+        assert torch.equal(first, kda.kda_fp8_matmul(a, sa, w, sw, out_dtype=FP32))
 
 
 # ---- waits that give up -------------------------------------------------------------------
