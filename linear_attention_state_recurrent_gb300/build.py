@@ -98,14 +98,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    _link_binding(binding.result())   # libkda.so is there without it
     return LIB
 
 

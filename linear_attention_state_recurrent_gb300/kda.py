@@ -518,18 +518,24 @@ def kda_mixed_batch(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, lower_bound, ini
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 
 
-def _load_torch_binding():
-    path = os.path.join(os.path.dirname(_LIB_PATH), "_kda_torch.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"_kda_torch.so is not built ({path}); run "
-                           "`python -c 'import __graft_entry__ as g; g.build()'` first")
-    spec = importlib.util.spec_from_file_location("_kda_torch", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    return module
+class _TorchBinding:
+    """The compiled module's functions, loaded with the first call: without it (it needs the torch it was built
+    against) the recurrence's calls are all there."""
+
+    def __getattr__(self, name):
+        path = os.path.join(os.path.dirname(_LIB_PATH), "_kda_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_kda_torch.so is not built ({path}); run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        spec = importlib.util.spec_from_file_location("_kda_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        for f in ("norm_quant", "fp8_matmul", "batch_maps"):
+            setattr(self, f, getattr(module, f))
+        return getattr(module, name)
 
 
-_torch_binding = _load_torch_binding()
+_torch_binding = _TorchBinding()
 
 
 def _handle(stream):
