@@ -1,10 +1,11 @@
 """Builds libkda.so in-tree from csrc/*.cu for sm_103a (nvcc, one translation unit per
 process, compiled in parallel, then linked into one shared library), and beside it
-_kda_torch.so from binding/kda_torch.cpp (the host compiler against the installed torch)."""
+_kda_torch-<torch>-<python>.so from binding/kda_torch.cpp (the host compiler against the installed torch)."""
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -17,7 +18,6 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 BINDING = os.path.join(PKG, "binding", "kda_torch.cpp")
-BINDING_LIB = os.path.join(PKG, "_kda_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -31,6 +31,12 @@ def nvcc() -> str:
     return path
 
 
+def binding_lib() -> str:
+    """The torch binding's file, named after the torch and the Python it is built against: one of another
+    torch is not taken for it."""
+    return os.path.join(PKG, f"_kda_torch-{importlib.metadata.version('torch')}-{sysconfig.get_config_var('SOABI')}.so")
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -42,9 +48,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
+    binding = binding_lib()
+    if not os.path.exists(LIB) or not os.path.exists(binding):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(binding))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -70,10 +77,10 @@ def _compile_binding():
 
 def _link_binding(obj):
     lib = os.path.join(_torch_dir(), "lib")
-    tmp = BINDING_LIB + ".tmp"
+    tmp = binding_lib() + ".tmp"
     _run(["g++", "-shared", obj, "-o", tmp, "-L" + PKG, "-l:libkda.so", "-Wl,-rpath,$ORIGIN", "-L" + lib, "-ltorch_python", "-ltorch_cpu",
           "-lc10", "-lc10_cuda"], "linking the torch binding")
-    os.replace(tmp, BINDING_LIB)
+    os.replace(tmp, binding_lib())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:

@@ -28,6 +28,8 @@ import os
 
 import torch
 
+from . import build
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
 KDA_OK = 0
@@ -523,9 +525,9 @@ class _TorchBinding:
     against) the recurrence's calls are all there."""
 
     def __getattr__(self, name):
-        path = os.path.join(os.path.dirname(_LIB_PATH), "_kda_torch.so")
+        path = build.binding_lib()
         if not os.path.exists(path):
-            raise RuntimeError(f"_kda_torch.so is not built ({path}); run "
+            raise RuntimeError(f"the torch binding is not built for this torch and Python ({path}); run "
                                "`python -c 'import __graft_entry__ as g; g.build()'` first")
         spec = importlib.util.spec_from_file_location("_kda_torch", path)
         module = importlib.util.module_from_spec(spec)

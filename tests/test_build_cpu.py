@@ -58,8 +58,7 @@ except RuntimeError as e:
 def test_a_binding_that_does_not_compile_leaves_the_library(build, monkeypatch, tmp_path):
     def fails():
         raise RuntimeError("no headers")
-    for name in ("LIB", "BINDING_LIB"):
-        monkeypatch.setattr(build, name, str(tmp_path / os.path.basename(getattr(build, name))))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libkda.so"))
     monkeypatch.setattr(build, "_compile_binding", fails)
     monkeypatch.setattr(build, "OBJ", str(tmp_path / "obj"))
     small = tmp_path / "one.cu"
@@ -68,3 +67,16 @@ def test_a_binding_that_does_not_compile_leaves_the_library(build, monkeypatch, 
     with pytest.raises(RuntimeError, match="no headers"):
         build.build(force=True)
     assert os.path.exists(build.LIB)
+
+
+def test_a_binding_of_another_torch_is_not_taken_for_built(build, monkeypatch):
+    from linear_attention_state_recurrent_gb300 import kda
+    assert build.up_to_date()
+    here = build.binding_lib()
+    real = build.importlib.metadata.version
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "1.0" if name == "torch" else real(name))
+    assert build.binding_lib() != here and not build.up_to_date()
+    with pytest.raises(RuntimeError, match="not built for this torch"):
+        kda._TorchBinding().norm_quant
+    monkeypatch.undo()
+    assert build.up_to_date()
