@@ -24,6 +24,7 @@
 //    tiles of 192 with one load per group (2.36), loads of tensor memory overlapped across groups
 //    (2.49), the MMA loop unrolled over the ring (2.42, registers), one polling warp of four (2.35).
 // Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <mutex>
@@ -1191,8 +1192,7 @@ cudaError_t run_wide(const Fp8Params &p, int64_t ld_a, int64_t ld_w, int sms, cu
 struct Device {
     int sms = 0;
     Fit thin16, thin32, thin64, slim;
-    cudaError_t status = cudaSuccess;
-    void ask(int dev)
+    cudaError_t ask(int dev)
     {
         cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         const auto limit = [](auto kernel, int smem) {
@@ -1205,22 +1205,31 @@ struct Device {
         if (e == cudaSuccess) e = limit(slim_kernel<1>, SLIM_SMEM);
         if (e == cudaSuccess) e = limit(slim_kernel<2>, SLIM_SMEM);
         if (e == cudaSuccess) e = limit(wide_kernel, Wide::SMEM);
-        status = e;
+        return e;
     }
 };
 
+// Kept once it has been asked with success: a failure is the call's, not the process's.
 cudaError_t this_device(const Device **out)
 {
     constexpr int MOST = 64;
     static Device devices[MOST];
-    static std::once_flag asked[MOST];
+    static std::atomic<bool> known[MOST];
+    static std::mutex asking;
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= MOST) return cudaErrorInvalidDevice;
-    std::call_once(asked[dev], [&] { devices[dev].ask(dev); });
+    if (!known[dev].load(std::memory_order_acquire)) {
+        const std::lock_guard<std::mutex> one(asking);
+        if (!known[dev].load(std::memory_order_relaxed)) {
+            const cudaError_t asked = devices[dev].ask(dev);
+            if (asked != cudaSuccess) return asked;
+            known[dev].store(true, std::memory_order_release);
+        }
+    }
     *out = &devices[dev];
-    return devices[dev].status;
+    return cudaSuccess;
 }
 
 // Which kernel a call takes, in what tiles.

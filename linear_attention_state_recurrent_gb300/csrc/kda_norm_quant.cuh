@@ -8,6 +8,7 @@
 // lanes one group of 128, whose maximum is four shuffles.
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -270,14 +271,20 @@ cudaError_t go(const NormQuantParams &p, cudaStream_t stream)
 {
     constexpr int rows = TPR < 128 ? 128 / TPR : 1, threads = TPR < 128 ? 128 : TPR;
     const auto kernel = norm_quant_kernel<T, VEC, TPR, CH, RES, NORM>;
-    static const int resident = [&] {
-        int dev = 0, sms = 0, n = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess)
-            return 0;
-        return n * sms;
-    }();
-    if (resident < 1) return cudaErrorInvalidConfiguration;
+    static std::atomic<int> known[64];   // per device, once a query has answered
+    int dev = 0, resident = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev < 64;
+    if (kept) resident = known[dev].load(std::memory_order_relaxed);
+    if (resident == 0) {
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess ||
+            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, 0)) != cudaSuccess)
+            return e;
+        resident *= sms;
+        if (resident < 1) return cudaErrorInvalidConfiguration;
+        if (kept) known[dev].store(resident, std::memory_order_relaxed);
+    }
     const int64_t want = (p.N + rows - 1) / rows;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(want < resident ? want : resident)), dim3(threads), 0, stream, p);
 }

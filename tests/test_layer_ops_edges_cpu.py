@@ -1,6 +1,9 @@
 """Host side of the operators around the recurrence beyond their own refusals: the plan's and the self-test's. No GPU: every call here
 fails its checks before anything is launched."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -67,3 +70,22 @@ def test_fp8_matmul_plan_binding(kda):
     for bad in ((a[0], w), (a, w[:, :128])):
         with pytest.raises(ValueError):
             kda.kda_fp8_matmul_plan(*bad)
+
+
+def test_what_a_device_answers_is_asked_again_after_a_failure(kda):
+    """With no device to ask, each call gives CUDA's own reason, the second as the first: no failure is kept in place of an
+    answer. In a process that sees no GPU, so nothing can be launched."""
+    code = f"""
+import sys; sys.path.insert(0, {os.path.dirname(os.path.dirname(os.path.abspath(__file__)))!r})
+from linear_attention_state_recurrent_gb300 import kda
+F = 1 << 20
+for i in range(2):
+    assert kda.lib.kda_norm_quant(F, 256, None, 0, 0, F, 1e-5, 4, 256, None, 0, None, 0, F, 256, F, 1, 4, None) == 4
+    print(kda.last_error())
+    assert kda.lib.kda_fp8_matmul(F, 128, F, 1, 8, F, 128, F, 1, 1, 8, 8, 128, F, 8, 0, None, None) == 4
+    print(kda.last_error())
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, env=dict(os.environ, CUDA_VISIBLE_DEVICES=""))
+    assert r.returncode == 0, r.stderr[-2000:]
+    said = [line.split(": ", 1)[1] for line in r.stdout.splitlines()]
+    assert len(said) == 4 and len(set(said)) == 1 and "configuration" not in said[0]
