@@ -387,7 +387,8 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
  * A NaN in a group makes the group's scale and all of its q NaN (with a weight: the whole
  * row). Without a weight an infinity gives its group an infinite scale, q = 0 at the finite
  * columns and NaN at the infinite ones; with a weight it makes its group NaN and the rest of
- * its row zeros, as does a sum of squares that passes the range of fp32.
+ * its row zeros, as does a sum of squares that passes the range of fp32; one that falls below that range
+ * counts as 0 (eps = 0 then gives what a row of zeros gives: NaN and infinities).
  * 1 <= D <= 32768. Any strides >= D and alignments of the element type are accepted; rows
  * on 16-byte boundaries (q: 8-byte) move in 16-byte vectors.
  */
@@ -401,11 +402,13 @@ int kda_norm_quant(const void *x, int64_t ld_x, const void *residual, int64_t ld
  *   out[m, n] = sum_k a[m, k] * sa[m, k / 128] * w[n, k] * sw[n / 128, k / 128]
  * a: e4m3 [M, ld_a], w: e4m3 [N, ld_w] (row n holds output n's weights), K columns used of
  * each; sa at a_scales[m*sa_row_stride + g*sa_group_stride] and sw at
- * w_scales[(n/128)*sw_row_stride + g*sw_group_stride], fp32, g < ceil(K / 128). out has the
+ * w_scales[(n/128)*sw_row_stride + g*sw_group_stride], fp32, g < ceil(K / 128), the strides >= 1. out has the
  * type out_dtype (KDA_BF16, KDA_FP16, KDA_FP32), row m at out + m*ld_out. Each group's products are
  * summed on the tensor cores in fp32, scaled and added up in fp32, and rounded once.
- * Operands whose base and row pitch are multiples of 16 bytes take the tensor cores; others
- * are computed by a slower kernel with the same result up to fp32 rounding. Columns K .. ld
+ * (A block's two scales are multiplied first, so their product has to stay within the normal numbers of
+ * fp32.) Operands whose base and row pitch are multiples of 16 bytes take the tensor cores; others are
+ * computed on the FMA units with the same result up to fp32 rounding, up to a hundred times slower (1000 x
+ * 4096 x 4095: 1.97 ms, in padded rows 20 us): pad rows, or ask kda_fp8_matmul_plan. Columns K .. ld
  * of a and w are never read. M, N and K may be any size >= 1 (K = 0: zeros; M or N = 0:
  * nothing to do), up to 2^30 each. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT
  * in *err_flags (may be NULL), and what its sums were to give stays as it was in out.

@@ -10,20 +10,23 @@
 //
 // Three arrangements (times on a GB300 for K = 4096; `wide` writes bf16):
 //  - thin_kernel, up to 64 rows of A: 128 rows of W are the MMA's M side, the rows of A its N side.
-//    Bound by the stream of weights: M = 1, N = 20512 16.9 us = 4.98 TB/s, of which the stream alone
+//    Bound by the stream of weights: M = 1, N = 20512 17.1-17.4 us = 4.9 TB/s, of which the stream alone
 //    (no MMA, no epilogue) is 15.6 us, and a plain kernel that reads as many bytes 16.9 us; N = 4096 5.2 us.
 //  - slim_kernel, up to 128 rows of A per CTA and a tile of W that makes the CTAs fill the GPU once:
-//    M = 128, N = 20512 20.8 us (the stream alone 18.5 us).
+//    M = 128, N = 20512 21.0-21.4 us. The stream alone is 15.1 us, with the MMAs 18.6, the rest the sums; that each CTA
+//    copies all rows of A again costs nothing (kept in shared memory from the first turn on: the same times).
 //    In both the inner axis may be split over a cluster whose CTAs join their sums through distributed
 //    shared memory in a fixed order.
 //  - wide_kernel: tiles of 256 x 256 by a pair of CTAs (cta_group::2), persistent: M = 33494,
-//    N = 20512 2.12-2.22 ms = 2.53-2.65 PFLOP/s, 61% of the tensor pipe's cycles. The epilogue's additions
-//    (128 x 256 per group and SM) take 270 of the 950 clocks a group takes, the MMAs 553; two
-//    accumulators are all that tensor memory holds, and what is left is the way from one to
-//    the other and back. Measured and not kept: four accumulators of 128 columns (2.46 ms against 2.22),
+//    N = 20512 2.19-2.28 ms = 2.47-2.57 PFLOP/s (the card's clock falls under it), 59% of the tensor pipe's cycles.
+//    Of the 490 ns a group takes, the copies alone need 225 and the MMAs alone 287; MMAs and copies with every
+//    accumulator handed back unread take 359, read but not added up 427, and all of it without copies 447. So it
+//    is the way of an accumulator through the epilogue and back that bounds it, with the two that tensor memory holds.
+//    Measured and not kept: four accumulators of 128 columns (2.46 ms against 2.22),
 //    tiles of 192 with one load per group (2.36), loads of tensor memory overlapped across groups
 //    (2.49), the MMA loop unrolled over the ring (2.42, registers), one polling warp of four (2.35).
-// Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel.
+// Operands that TMA cannot address (rows off 16-byte boundaries) take general_kernel, on the FMA units: 1000 x 4096 x
+// 4095 1.97 ms, where rows padded to 16 bytes take 20 us.
 #include <atomic>
 #include <climits>
 #include <cstdint>
@@ -1101,7 +1104,7 @@ double plan_thin(const Fp8Params &p, const Fit &fit, int *split)
         if (fit.ctas[k] == 0) continue;
         const int64_t ctas = static_cast<int64_t>(tiles_n) * tiles_t * k;
         const double at_once = ctas < fit.ctas[k] ? ctas : fit.ctas[k], hbm = at_once * 128 * BK / tiles_t / 5700.;
-        const double l2 = (at_once > fit.ctas[1] / 2 ? 2 : 1) * C::STAGE / 85.;      // into one SM, of one CTA or two
+        const double l2 = (at_once > fit.ctas[1] / 2 ? 2 : 1) * C::STAGE / 85.;      // a group's copies of one SM's CTAs, fitted
         double step = NT > 32 ? 322. : NT > 16 ? 288. : 281.;
         if (step < hbm) step = hbm;
         if (step < l2) step = l2;

@@ -3,7 +3,7 @@
 //
 // A row stays in the registers of its threads between the sum of squares and the
 // quantisation, so each input is read once and each output written once; the kernel is bound
-// by HBM (33494 x 4096 bf16 with a residual: 142-145 us, the measured copy's rate; quantisation of
+// by HBM (33494 x 4096 bf16 with a residual: 142-143 us, the measured copy's rate; quantisation of
 // 16480 x 4096 alone 32.5 us, 94% of it). Eight consecutive columns per thread and chunk (16 bytes of a 16-bit type) make 16
 // lanes one group of 128, whose maximum is four shuffles.
 #pragma once

@@ -552,7 +552,7 @@ def kda_norm_quant(x, weight=None, eps=1e-5, *, residual=None, residual_out=None
 
     x, residual: [N, D] bf16, fp16 or fp32 (the same type); weight: fp32 [D]. residual_out receives h
     (it may be residual itself) and y, if given, the unquantised y. q: float8_e4m3fn [N, D]; scales:
-    fp32 [N, ceil(D / 128)], any strides. What is not given is allocated: q with rows on 16-byte
+    fp32 [N, ceil(D / 128)], any positive strides. What is not given is allocated: q with rows on 16-byte
     boundaries and scales with the rows next to each other (the layouts kda_fp8_matmul reads fastest).
     Returns (q, scales, residual_out), residual_out None without a residual."""
     r = _torch_binding.norm_quant(x, weight, eps, residual, residual_out, y, q, scales, _handle(stream))
@@ -565,9 +565,10 @@ def kda_fp8_matmul(a, a_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat
     """out[m, n] = sum_k a[m, k] a_scales[m, k / 128] w[n, k] w_scales[n / 128, k / 128].
 
     a: float8_e4m3fn [M, K]; w: float8_e4m3fn [N, K]; a_scales: fp32 [M, ceil(K / 128)]; w_scales:
-    fp32 [ceil(N / 128), ceil(K / 128)], any strides. out: bf16, fp16 or fp32 [M, N] (allocated as
-    out_dtype when not given). Operands with rows on 16-byte boundaries take the tensor cores.
-    Returns out."""
+    fp32 [ceil(N / 128), ceil(K / 128)], any positive strides (a scale expanded over rows or groups is
+    refused). out: bf16, fp16 or fp32 [M, N] (allocated as
+    out_dtype when not given). Operands with rows on 16-byte boundaries take the tensor cores,
+    others a kernel that is up to a hundred times slower (kda_fp8_matmul_plan tells). Returns out."""
     if out is None:
         if out_dtype not in _FLOATS:
             raise ValueError("out_dtype must be bf16, fp16 or fp32")
