@@ -239,3 +239,48 @@ def test_results_dropped_before_their_readers_have_run(kda):
     junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in sizes]
     torch.cuda.synchronize()
     assert len(junk) == 2 and torch.equal(got, want)
+
+
+# ---- offsets past 32 bits -----------------------------------------------------------------
+
+FAR = (1 << 30) + 16   # elements from a row to the next: the third starts past 2^31
+
+
+@pytest.fixture(scope="module")
+def far():
+    """Four buffers of 5 GB, from which rows are taken FAR elements apart."""
+    bufs = [torch.zeros(5 * FAR, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    yield bufs
+    del bufs
+    torch.cuda.empty_cache()
+
+
+def rows_apart(buf, t, stride):
+    """The values of `t` in rows of `buf` that lie `stride` elements apart."""
+    v = buf.view(t.dtype).as_strided(t.shape, (stride, 1))
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("cols", [384, 391])
+def test_norm_quant_rows_far_apart(kda, far, cols):
+    x = torch.randn(2, cols, generator=torch.Generator().manual_seed(61)).to(BF16).cuda()
+    w = torch.ones(cols, device="cuda")
+    q, s, ro = kda.kda_norm_quant(x, w, residual=x)
+    got = {"residual_out": rows_apart(far[1], torch.zeros_like(x), 2 * FAR), "q": rows_apart(far[2], torch.zeros_like(q), 4 * FAR),
+           "scales": rows_apart(far[3], torch.zeros_like(s), FAR)}
+    kda.kda_norm_quant(rows_apart(far[0], x, 2 * FAR), w, residual=x, **got)
+    assert torch.equal(got["residual_out"], ro) and torch.equal(got["q"].float(), q.float()) and torch.equal(got["scales"], s)
+
+
+@pytest.mark.parametrize("M", [5, 40, 3000])
+@pytest.mark.parametrize("step", [FAR, FAR - 3])   # rows on 16-byte boundaries and off them
+def test_fp8_matmul_rows_far_apart(kda, far, M, step):
+    """w's rows, and with five of them a's and the output's too."""
+    a, sa, w, sw = operands(M, 5, 272, 62)
+    w = rows_apart(far[1], w, step)
+    out = None
+    if M == 5:
+        a, out = rows_apart(far[0], a, step), rows_apart(far[2], torch.zeros(5, 5, dtype=BF16, device="cuda"), FAR // 2)
+    assert (kda.kda_fp8_matmul_plan(a, w)[0] == 0) == (step != FAR)
+    check_matmul(kda, a, sa, w, sw, out=out)
