@@ -86,7 +86,8 @@ extern "C" {
 #define KDA_ERRFLAG_PAGES 8u      /* bit 3: kda_batch_maps ran out of free pages or block-table columns, or
                                      met a page id outside [0, num_pages); those tokens' slots are -1 */
 #define KDA_ERRFLAG_LENGTHS 16u   /* bit 4: kda_batch_maps met a negative or too large length (the request
-                                     counts as empty) or more tokens than num_tokens (cut off) */
+                                     counts as empty) or more tokens than num_tokens (cut off), or
+                                     kda_gdn_chunk_prefill a sequence that is no range of the rows */
 
 /* Element types of the calls that take more than one (kda_norm_quant, kda_fp8_matmul). */
 #define KDA_BF16 0
@@ -360,6 +361,53 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
                                int64_t num_seqs, int32_t chunk_size, const kda_heads *heads,
                                const kda_state *state, uint16_t *out, int64_t ld_out,
                                uint32_t *err_flags, void *stream);
+
+/*
+ * The gated delta rule with ONE decay per token and head, and value heads that may share key heads: the KDA recurrence
+ * with a scalar gate. Per token t and value head h < Hv, with hk = h / (Hv / Hk) its key head:
+ *   g     = -exp(A_log[h]) * softplus(raw_g[t, h] + dt_bias[h]),   alpha = exp(g),   beta = sigmoid(raw_beta[t, h])
+ *   q^    = scale * q_hk / sqrt(|q_hk|^2 + l2_eps),   k^ = k_hk / sqrt(|k_hk|^2 + l2_eps)
+ *   S_t   = (I - beta k^ k^T) alpha S_{t-1} + beta k^ v_h^T        (K x V, fp32)
+ *   o_t   = S_t^T q^                                                (V, bf16 out)
+ * mixed_qkv: bf16 [N, ld_qkv], row t = [ q (Hk*K) | k (Hk*K) | v (Hv*V) ]; raw_g and raw_beta: bf16 [N, ld], Hv used;
+ * out: bf16 [N, ld_out], Hv*V written; the state pool holds [Hv][K][V] per slot. Alignment, slots, the null slot, error
+ * bits and sizes are those of the calls above with H = Hv. All three calls can be captured in a CUDA graph, and none
+ * uses a workspace. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
+ * several tokens); values of any magnitude that fp32 holds are accepted.
+ */
+typedef struct kda_gdn_heads {
+    int32_t Hk, Hv, K, V;   /* key heads, value heads (a multiple of Hk), key dim, value dim */
+    const float *A_log;     /* device fp32 [Hv] */
+    const float *dt_bias;   /* device fp32 [Hv]; NULL = zeros */
+    float scale;            /* multiplies q^ (commonly K^-1/2); finite */
+    float l2_eps;           /* inside the q/k L2 norms; >= 0 */
+} kda_gdn_heads;
+
+/* kda_gdn_decode - one token per sequence, as kda_packed_decode. */
+int kda_gdn_decode(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
+                   const uint16_t *raw_beta, int64_t ld_beta, int64_t num_seqs, const kda_gdn_heads *heads,
+                   const kda_state *state, uint16_t *out, int64_t ld_out, uint32_t *err_flags, void *stream);
+
+/*
+ * kda_gdn_spec_verify - requests of tokens_per_req rows (1..64), as kda_spec_verify: request r owns rows
+ * [r*T, (r+1)*T); its state is read once, advanced over them and written back once.
+ */
+int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
+                        const uint16_t *raw_beta, int64_t ld_beta, int64_t num_reqs, int32_t tokens_per_req,
+                        const kda_gdn_heads *heads, const kda_state *state, uint16_t *out, int64_t ld_out,
+                        uint32_t *err_flags, void *stream);
+
+/*
+ * kda_gdn_chunk_prefill - packed sequences: sequence s < num_seqs owns rows [cu_seqlens[s], cu_seqlens[s+1]) of the
+ * num_rows rows and slot indices[s*index_stride]. cu_seqlens is read on the device alone (int32 [num_seqs + 1], e.g.
+ * kda_batch_maps'): lengths may differ from one graph replay to the next. A pair that is no range of the rows
+ * (negative, decreasing, past num_rows) counts as an empty sequence and sets KDA_ERRFLAG_LENGTHS. Rows of no sequence
+ * are left as they were; the slot of an empty sequence is left untouched (one >= num_slots is still flagged).
+ */
+int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
+                          const uint16_t *raw_beta, int64_t ld_beta, const int32_t *cu_seqlens, int64_t num_seqs,
+                          int64_t num_rows, const kda_gdn_heads *heads, const kda_state *state, uint16_t *out,
+                          int64_t ld_out, uint32_t *err_flags, void *stream);
 
 /*
  * The calls below are what a layer's step does around the recurrence: the batch's maps,

@@ -7,6 +7,8 @@
 // ValueError.
 #include <Python.h>
 
+#include <cmath>
+
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -298,10 +300,111 @@ PyObject *batch_maps(PyObject *, PyObject *const *v, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A float argument.
+bool number(PyObject *o, double *v)
+{
+    *v = PyFloat_AsDouble(o);
+    return !(*v == -1.0 && PyErr_Occurred());
+}
+
+// The row stride of a [>= rows, >= cols] tensor with unit inner stride.
+bool rows_of(const Tensor &t, const char *name, ScalarType type, int64_t rows, int64_t cols, const Tensor *first, int64_t *ld)
+{
+    if (!of_type(t, name, type)) return false;
+    if (t.dim() != 2 || t.size(0) < rows || t.size(1) < cols) {
+        refuse("%s must have at least %lld rows of %lld entries", name, (long long)rows, (long long)cols);
+        return false;
+    }
+    if (t.size(1) > 1 && t.stride(1) != 1) {
+        refuse("%s must have unit inner stride", name);
+        return false;
+    }
+    *ld = t.size(0) > 1 || t.stride(0) > t.size(1) ? t.stride(0) : t.size(1);
+    return on_device(t, name, first);
+}
+
+// (mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads, scale, l2_eps,
+//  null_slot, out, err_flags, stream) -> out. tokens: rows per request, 0 for decode; cu_seqlens: the prefill's, else None;
+// num_k_heads, scale: None for one key head per value head and K^-1/2
+PyObject *gdn(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *x, *g, *b, *A, *dt, *pool, *idx, *cu, *out;
+    int64_t tokens, null_slot;
+    double scale = 0, eps;
+    if (!count(n, 16) || !tensor(a[0], "mixed_qkv", false, &x) || !tensor(a[1], "raw_g", false, &g) || !tensor(a[2], "raw_beta", false, &b) ||
+        !tensor(a[3], "A_log", false, &A) || !tensor(a[4], "dt_bias", true, &dt) || !tensor(a[5], "initial_state", false, &pool) ||
+        !tensor(a[6], "state_indices", false, &idx) || !integer(a[7], &tokens) || !tensor(a[8], "cu_seqlens", true, &cu) ||
+        (a[10] != Py_None && !number(a[10], &scale)) || !number(a[11], &eps) || !integer(a[12], &null_slot) ||
+        !tensor(a[13], "out", true, &out))
+        return nullptr;
+    const ScalarType H = ScalarType::BFloat16, F = ScalarType::Float;
+    if (pool->scalar_type() != F || pool->dim() != 4) return refuse("initial_state must be fp32 [num_slots, H, K, V]");
+    const int64_t Hv = pool->size(1), K = pool->size(2), V = pool->size(3);
+    if (Hv < 1 || Hv > INT32_MAX || K > INT32_MAX || V > INT32_MAX || pool->size(0) < 1) return refuse("initial_state has no slot or no head");
+    if (pool->stride(3) != 1 || pool->stride(2) != V || (Hv > 1 && pool->stride(1) != K * V))
+        return refuse("initial_state's [H, K, V] part must be contiguous");
+    int64_t Hk = Hv;
+    if (a[9] != Py_None && !integer(a[9], &Hk)) return nullptr;
+    if (Hk < 1 || Hk > Hv || Hv % Hk != 0) return refuse("num_k_heads must divide the %lld value heads (got %lld)", (long long)Hv, (long long)Hk);
+    if (a[10] == Py_None) scale = 1.0 / std::sqrt(static_cast<double>(K));
+    if (x->dim() != 2) return refuse("mixed_qkv must be 2-D");
+    const int64_t N = x->size(0);
+    int64_t per = tokens == 0 ? 1 : tokens, ld_x, ld_g, ld_b, ld_out = Hv * V;
+    if (per < 1 || (!cu && N % per != 0)) return refuse("the row count must be a multiple of tokens_per_req");
+    if (cu && (cu->scalar_type() != ScalarType::Int || cu->dim() != 1 || cu->size(0) < 1 || !cu->is_contiguous()))
+        return refuse("cu_seqlens must be a contiguous 1-D int32 tensor");
+    if (cu && !on_device(*cu, "cu_seqlens", x)) return nullptr;
+    const int64_t entries = cu ? cu->size(0) - 1 : N / per;
+    if (!rows_of(*x, "mixed_qkv", H, N, 2 * Hk * K + Hv * V, nullptr, &ld_x) || !rows_of(*g, "raw_g", H, N, Hv, x, &ld_g) ||
+        !rows_of(*b, "raw_beta", H, N, Hv, x, &ld_b) || !vector(*A, "A_log", F, Hv, x) || (dt && !vector(*dt, "dt_bias", F, Hv, x)) ||
+        !on_device(*pool, "initial_state", x) || !of_type(*idx, "state_indices", ScalarType::Int) || !on_device(*idx, "state_indices", x))
+        return nullptr;
+    if (A->size(0) != Hv || (dt && dt->size(0) != Hv)) return refuse("A_log and dt_bias must have an entry per value head (%lld)", (long long)Hv);
+    if (idx->dim() != 1) return refuse("`state_indices` must be one-dimensional.");
+    if (idx->size(0) < entries) return refuse("state_indices has fewer entries (%lld) than sequences (%lld)", (long long)idx->size(0), (long long)entries);
+    if (out && !rows_of(*out, "out", H, N, Hv * V, x, &ld_out)) return nullptr;
+    if (null_slot < INT32_MIN || null_slot > INT32_MAX || per > INT32_MAX) return refuse("null_slot or tokens_per_req is out of range");
+    uint32_t *err;
+    void *stream;
+    if (!error_word(a[14], x, &err) || !stream_of(a[15], *x, &stream)) return nullptr;
+    const c10::cuda::CUDAGuard guard(x->device());
+    Tensor made;
+    if (!out) {   // it belongs to the stream that the kernel runs on
+        c10::cuda::OptionalCUDAStreamGuard on;
+        if (a[15] != Py_None) on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), x->device().index()));
+        made = at::empty({N, Hv * V}, x->options());
+        out = &made;
+    }
+    const kda_gdn_heads heads = {static_cast<int32_t>(Hk), static_cast<int32_t>(Hv), static_cast<int32_t>(K), static_cast<int32_t>(V),
+                                 static_cast<const float *>(A->data_ptr()), dt ? static_cast<const float *>(dt->data_ptr()) : nullptr,
+                                 static_cast<float>(scale), static_cast<float>(eps)};
+    const int64_t slot_stride = pool->size(0) > 1 ? pool->stride(0) : Hv * K * V;
+    const kda_state state = {static_cast<float *>(pool->data_ptr()), pool->size(0), slot_stride, static_cast<const int32_t *>(idx->data_ptr()),
+                             entries > 1 ? idx->stride(0) : 1, static_cast<int32_t>(null_slot)};
+    auto u16 = [](const Tensor *t) { return static_cast<uint16_t *>(t->data_ptr()); };
+    int status = KDA_OK;
+    if (N == 0 && !cu) {   // nothing to do, and no rows to point to
+    } else if (cu) {
+        if (N > 0)
+            status = kda_gdn_chunk_prefill(u16(x), ld_x, u16(g), ld_g, u16(b), ld_b, static_cast<const int32_t *>(cu->data_ptr()), entries, N,
+                                           &heads, &state, u16(out), ld_out, err, stream);
+    } else if (tokens == 0) {
+        status = kda_gdn_decode(u16(x), ld_x, u16(g), ld_g, u16(b), ld_b, N, &heads, &state, u16(out), ld_out, err, stream);
+    } else {
+        status = kda_gdn_spec_verify(u16(x), ld_x, u16(g), ld_g, u16(b), ld_b, entries, static_cast<int32_t>(per), &heads, &state, u16(out),
+                                     ld_out, err, stream);
+    }
+    if (status != KDA_OK) return PyLong_FromLong(status);
+    return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[13]);
+    END_HANDLE_TH_ERRORS
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL
 PyMethodDef methods[] = {{"norm_quant", FAST(norm_quant), nullptr},
                          {"fp8_matmul", FAST(fp8_matmul), nullptr},
                          {"batch_maps", FAST(batch_maps), nullptr},
+                         {"gdn", FAST(gdn), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

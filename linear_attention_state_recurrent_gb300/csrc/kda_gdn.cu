@@ -1,0 +1,503 @@
+// The gated delta rule with one decay per token and head, token by token or in blocks of a few tokens.
+//
+//   S <- alpha S,  u = beta (v - S^T k^),  S <- S + k^ u^T,  o = S^T q^       (S fp32 [K][V] per value head)
+//
+// with alpha = exp(-e^{A_log} softplus(raw_g + dt_bias)) and value head h on key head h / (Hv / Hk).
+//
+// decode_kernel: one token. A CTA owns a slice of 32 value columns of one state (they are independent: column j of
+// the new S depends on column j of the old one alone). Bound by the state's bytes.
+//
+// rows_kernel: n tokens per step, n <= 8 or 16, on mma.sync, for the requests of a few rows and for what the chunked
+// kernel does not take (K = 32, rows off 16-byte boundaries). With b the running log-decay inside the block, D[r, i] = e^{b_r - b_i},
+// A[r, i] = beta_r (k^_r . k^_i) D[r, i] (i < r) and T = (I + A)^-1, the block's tokens need S only twice:
+//   U = T diag(beta) (v - e^b (k^ S)),  o = e^b (q^ S) + (q^ k^^T * D) U,  S <- e^{b_n} S + (k^ e^{b_n - b})^T U
+// so a state is read from memory once, kept in registers as the MMAs' accumulators, and written once. It is held
+// transposed (rows of an MMA = value columns, columns = key channels): the accumulator layout is then the layout of the
+// first operand of the next product. fp32 values enter the MMAs as two bf16 terms (2^-18 of the value); q and k are bf16 already.
+#include "kda_gdn_common.cuh"
+#include "kda_pdl.cuh"
+
+namespace kda {
+namespace gdn {
+
+template <int K, int V>
+__global__ void __launch_bounds__(128, K == 128 ? 12 : 8) decode_kernel(GdnParams p)
+{
+    constexpr int VT = 32, VS = V / VT, RPT = K / 16, CPL = K / 32;
+    // Thread (rg, cg) copies, reads and stores rows rg, rg + 16, .. of four columns: no register holds the slice, and
+    // shared memory (17.9 KB at K = 128) lets twelve CTAs have their loads in flight on an SM.
+    __shared__ __align__(16) float4 s_tile[RPT][128];
+    __shared__ uint32_t s_kq[K];                           // bf16 k | q << 16
+    __shared__ __align__(16) float4 s_red[4][2][VT / 4];   // [warp][k^T S, q^T S][column group]
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cg = tid & 7, rg = tid >> 3;
+    pdl_wait_then_release();   // no global read before this
+
+    const int64_t b = blockIdx.x;
+    const int vs = static_cast<int>(b % VS);
+    const int h = static_cast<int>((b / VS) % p.Hv), hk = h / (p.Hv / p.Hk);
+    const int64_t e = b / (static_cast<int64_t>(VS) * p.Hv);
+    const int j0 = vs * VT + cg * 4;
+    const int64_t slot = load_slot(p, e);
+    uint16_t *orow = p.out + e * p.ld_out + static_cast<int64_t>(h) * V + j0;
+    if (slot >= p.num_slots) {                             // out of range: flag, zero outputs
+        if (tid == 0 && p.err) atomicOr(p.err, kErrSlotRange);
+        if (rg == 0) *reinterpret_cast<uint2 *>(orow) = make_uint2(0u, 0u);
+        return;
+    }
+    const bool has_state = slot >= 0, writable = has_state && slot != p.null_slot;
+    float *tile = has_state ? p.pool + slot * p.slot_stride + static_cast<int64_t>(h) * K * V + j0 : nullptr;
+    if (has_state) {
+#pragma unroll
+        for (int i = 0; i < RPT; i++)
+            cp_async16(static_cast<uint32_t>(__cvta_generic_to_shared(&s_tile[i][tid])), tile + static_cast<int64_t>(rg + 16 * i) * V, true);
+    }
+    cp_async_commit();
+
+    const int64_t HK = static_cast<int64_t>(p.Hk) * K;
+    const uint16_t *row = p.qkv + e * p.ld_qkv;
+    uint16_t qb[CPL], kb[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; c++) {
+        qb[c] = row[hk * K + lane + 32 * c];
+        kb[c] = row[HK + hk * K + lane + 32 * c];
+    }
+    const uint16_t *vp = row + 2 * HK + static_cast<int64_t>(h) * V + j0;
+    const float vv[4] = {bf16_to_f32(vp[0]), bf16_to_f32(vp[1]), bf16_to_f32(vp[2]), bf16_to_f32(vp[3])};
+    const float beta = sigmoid_f(bf16_to_f32(p.rb[e * p.ld_beta + h]));
+    const float alpha = expf(log_decay(p, e, h, expf(__ldg(p.A_log + h)), p.dt_bias ? __ldg(p.dt_bias + h) : 0.f));
+    if (tid < K) {
+        uint32_t kq = 0;
+#pragma unroll
+        for (int c = 0; c < CPL; c++)
+            if (c == warp) kq = static_cast<uint32_t>(kb[c]) | (static_cast<uint32_t>(qb[c]) << 16);
+        s_kq[tid] = kq;
+    }
+    float qq = 0.f, kk = 0.f, qk = 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; c++) {
+        const float qf = bf16_to_f32(qb[c]), kf = bf16_to_f32(kb[c]);
+        qq += qf * qf; kk += kf * kf; qk += qf * kf;
+    }
+    qq = warp_sum(qq);
+    kk = warp_sum(kk);
+    qk = warp_sum(qk);
+    cp_async_wait_all();   // this thread's own copies
+    __syncthreads();
+
+    const float rq = p.scale * rsqrtf(qq + p.eps), rk = rsqrtf(kk + p.eps);
+    float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < RPT; i++) {
+        const uint32_t kq = s_kq[rg + 16 * i];
+        const float kr = __uint_as_float(kq << 16), qr = __uint_as_float(kq & 0xffff0000u);
+        const float4 S = has_state ? s_tile[i][tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+        pk[0] += kr * S.x; pk[1] += kr * S.y; pk[2] += kr * S.z; pk[3] += kr * S.w;
+        pq[0] += qr * S.x; pq[1] += qr * S.y; pq[2] += qr * S.z; pq[3] += qr * S.w;
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; jj++) {
+        pk[jj] += __shfl_xor_sync(0xffffffffu, pk[jj], 8);
+        pk[jj] += __shfl_xor_sync(0xffffffffu, pk[jj], 16);
+        pq[jj] += __shfl_xor_sync(0xffffffffu, pq[jj], 8);
+        pq[jj] += __shfl_xor_sync(0xffffffffu, pq[jj], 16);
+    }
+    if (lane < 8) {
+        s_red[warp][0][cg] = make_float4(pk[0], pk[1], pk[2], pk[3]);
+        s_red[warp][1][cg] = make_float4(pq[0], pq[1], pq[2], pq[3]);
+    }
+    __syncthreads();
+
+    float u[4], o[4];
+    const float qkh = qk * rq * rk;
+    {
+        float ks[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            const float4 kw = s_red[w][0][cg], qw = s_red[w][1][cg];
+            ks[0] += kw.x; ks[1] += kw.y; ks[2] += kw.z; ks[3] += kw.w;
+            qs[0] += qw.x; qs[1] += qw.y; qs[2] += qw.z; qs[3] += qw.w;
+        }
+#pragma unroll
+        for (int jj = 0; jj < 4; jj++) {
+            u[jj] = beta * (vv[jj] - alpha * (ks[jj] * rk));
+            o[jj] = alpha * (qs[jj] * rq) + qkh * u[jj];
+        }
+    }
+    if (rg == 0) *reinterpret_cast<uint2 *>(orow) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    if (writable) {
+#pragma unroll
+        for (int i = 0; i < RPT; i++) {
+            const int r = rg + 16 * i;
+            const float kh = __uint_as_float(s_kq[r] << 16) * rk;
+            float4 S = s_tile[i][tid];
+            S.x = fmaf(S.x, alpha, kh * u[0]); S.y = fmaf(S.y, alpha, kh * u[1]);
+            S.z = fmaf(S.z, alpha, kh * u[2]); S.w = fmaf(S.w, alpha, kh * u[3]);
+            *reinterpret_cast<float4 *>(tile + static_cast<int64_t>(r) * V) = S;
+        }
+    }
+}
+
+// ---- mma.sync ----------------------------------------------------------------------------
+
+// d += a b, 16 rows by 8 columns; k = 16, or 8 with a[0], a[1] and b[0] alone.
+template <int KD>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[KD / 4], const uint32_t (&b)[KD / 8])
+{
+    if constexpr (KD == 16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+    else
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(b[0]));
+}
+
+// Four 8 x 8 bf16 tiles, transposed; lane l gives the address of row l % 8 of tile l / 8.
+__device__ __forceinline__ void load_trans(uint32_t (&r)[4], uint32_t saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr));
+}
+
+__device__ __forceinline__ float sum_squares(uint32_t pair)
+{
+    const float x = __uint_as_float(pair << 16), y = __uint_as_float(pair & 0xffff0000u);
+    return x * x + y * y;
+}
+
+// One CTA per (entry, value head): warp w holds value columns 32 w .. 32 w + 31, in registers over all K channels
+// (4 K / 4 floats a thread), and needs nothing of the other warps but the block's T and the query-key products, which warps 0 and
+// 1 form while the others already multiply. TB tokens a step (a multiple of 8).
+template <int K, int V, int TB>
+__global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
+{
+    constexpr int NT = TB / 8, CT = K / 8, PITCH = K + 8, TP = TB + 8;
+    __shared__ __align__(16) uint16_t s_k[TB][PITCH], s_q[TB][PITCH];
+    __shared__ __align__(4) uint16_t s_t[2][TB][TP], s_w[2][TB][TP];   // T diag(beta) and the scaled q k^T, each hi and lo
+    __shared__ float s_a[TB][TB + 1];
+    __shared__ float s_ys[TB], s_qs[TB], s_us[TB];        // scales of k S, q S, and of U on its way into S
+    __shared__ float s_gamma;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+    pdl_wait_then_release();   // no global read before this
+    const int64_t e = blockIdx.x / p.Hv;
+    const int h = static_cast<int>(blockIdx.x % p.Hv), hk = h / (p.Hv / p.Hk);
+    const int j0 = warp * 32 + g * 4;                     // this thread's four value columns
+    int64_t row0 = e * T, row1 = row0 + T;
+    if (cu) {
+        row0 = __ldg(cu + e);
+        row1 = __ldg(cu + e + 1);
+        if (row0 < 0 || row1 < row0 || row1 > rows) {     // not a range of the rows: counts as empty
+            if (tid == 0 && p.err) atomicOr(p.err, kErrLengths);
+            row1 = row0;
+        }
+    }
+    const int64_t slot = load_slot(p, e);
+    uint16_t *out = p.out + static_cast<int64_t>(h) * V + j0;
+    if (slot >= p.num_slots) {                            // out of range: flag, zero outputs
+        if (tid == 0 && p.err) atomicOr(p.err, kErrSlotRange);
+        for (int64_t r = row0 + (lane & 3); r < row1; r += 4) *reinterpret_cast<uint2 *>(out + r * p.ld_out) = make_uint2(0u, 0u);
+        return;
+    }
+    if (row0 == row1) return;
+    const bool has_state = slot >= 0, writable = has_state && slot != p.null_slot;
+    float *tile = has_state ? p.pool + slot * p.slot_stride + static_cast<int64_t>(h) * K * V + j0 : nullptr;
+
+    // S[m][n]: columns j0 + 2m, j0 + 2m + 1 (the MMA's rows g and g + 8 of tile m), channels 8n + t2, 8n + t2 + 1
+    float S[2][CT][4];
+#pragma unroll
+    for (int n = 0; n < CT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            const float4 x = has_state ? *reinterpret_cast<const float4 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) : make_float4(0.f, 0.f, 0.f, 0.f);
+            S[0][n][c] = x.x; S[0][n][2 + c] = x.y; S[1][n][c] = x.z; S[1][n][2 + c] = x.w;
+        }
+
+    const int64_t HK = static_cast<int64_t>(p.Hk) * K;
+    const float expA = expf(__ldg(p.A_log + h)), dtb = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+    for (int64_t r0 = row0; r0 < row1; r0 += TB) {
+        const int n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
+        const uint16_t *in = p.qkv + r0 * p.ld_qkv;
+        // q and k of the block; rows past its end are zeros, and so is their beta
+        if (vec) {
+            for (int i = tid; i < 2 * TB * (K / 8); i += V) {
+                const int part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
+                const uint4 x = r < n ? *reinterpret_cast<const uint4 *>(in + r * p.ld_qkv + part * HK + hk * K + c) : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = x;
+            }
+        } else {
+            for (int i = tid; i < 2 * TB * K; i += V) {
+                const int part = i / (TB * K), r = i / K % TB, c = i % K;
+                const uint16_t x = r < n ? in[r * p.ld_qkv + part * HK + hk * K + c] : static_cast<uint16_t>(0);
+                (part ? s_k : s_q)[r][c] = x;
+            }
+        }
+        // v of this thread's columns and tokens
+        float vv[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < NT; m++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int r = 8 * m + t2 + c;
+                uint2 x = make_uint2(0u, 0u);
+                if (r < n) {
+                    const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
+                    if (vec) x = *reinterpret_cast<const uint2 *>(vp);
+                    else x = make_uint2(vp[0] | static_cast<uint32_t>(vp[1]) << 16, vp[2] | static_cast<uint32_t>(vp[3]) << 16);
+                }
+                vv[0][m][c] = __uint_as_float(x.x << 16); vv[0][m][2 + c] = __uint_as_float(x.x & 0xffff0000u);
+                vv[1][m][c] = __uint_as_float(x.y << 16); vv[1][m][2 + c] = __uint_as_float(x.y & 0xffff0000u);
+            }
+        __syncthreads();
+
+        // Warp 0: the block's scalars and T. Warp 1 (or warp 0 again): the query-key products. Lane r has token r's scalars.
+        if (warp < 2) {
+            float gl = 0.f, beta = 0.f;
+            if (lane < n) {
+                gl = log_decay(p, r0 + lane, h, expA, dtb);
+                beta = sigmoid_f(bf16_to_f32(p.rb[(r0 + lane) * p.ld_beta + h]));
+            }
+            const RunningDecay b(gl, TB);
+            const RunningDecay::At b_end = b.of(TB - 1);
+            for (int qk = warp; qk < 2; qk += V == 32 ? 1 : 2) {
+                const uint16_t(*s_l)[PITCH] = qk ? s_q : s_k;
+                float G[NT][4] = {}, nl[2] = {}, nr[NT] = {};
+#pragma unroll
+                for (int kt = 0; kt < K / 16; kt++) {
+                    uint32_t a[4] = {};
+                    const int c = 16 * kt + t2;
+                    a[0] = *reinterpret_cast<const uint32_t *>(&s_l[g][c]);
+                    a[2] = *reinterpret_cast<const uint32_t *>(&s_l[g][c + 8]);
+                    if (NT > 1) {
+                        a[1] = *reinterpret_cast<const uint32_t *>(&s_l[(g + 8) % TB][c]);
+                        a[3] = *reinterpret_cast<const uint32_t *>(&s_l[(g + 8) % TB][c + 8]);
+                    }
+                    nl[0] += sum_squares(a[0]) + sum_squares(a[2]);
+                    nl[1] += sum_squares(a[1]) + sum_squares(a[3]);
+#pragma unroll
+                    for (int m = 0; m < NT; m++) {
+                        uint32_t kb[2] = {*reinterpret_cast<const uint32_t *>(&s_k[8 * m + g][c]), *reinterpret_cast<const uint32_t *>(&s_k[8 * m + g][c + 8])};
+                        nr[m] += sum_squares(kb[0]) + sum_squares(kb[1]);
+                        mma<16>(G[m], a, kb);
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    nl[0] += __shfl_xor_sync(0xffffffffu, nl[0], o);
+                    nl[1] += __shfl_xor_sync(0xffffffffu, nl[1], o);
+#pragma unroll
+                    for (int m = 0; m < NT; m++) nr[m] += __shfl_xor_sync(0xffffffffu, nr[m], o);
+                }
+                // rows past the block's end have no norm: with eps = 0 theirs would be infinite
+                nl[0] = g < n ? rsqrtf(nl[0] + p.eps) : 0.f;
+                nl[1] = g + 8 < n ? rsqrtf(nl[1] + p.eps) : 0.f;
+#pragma unroll
+                for (int m = 0; m < NT; m++) nr[m] = rsqrtf(nr[m] + p.eps);
+                // entry (r, i) of G: r = g + 8 hh, i = 8 m + t2 + c
+#pragma unroll
+                for (int hh = 0; hh < NT; hh++) {
+                    const int r = g + 8 * hh;
+                    const RunningDecay::At br = b.of(r);
+                    const float beta_r = __shfl_sync(0xffffffffu, beta, r);
+#pragma unroll
+                    for (int m = 0; m < NT; m++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            const int i = 8 * m + t2 + c;
+                            const RunningDecay::At bi = b.of(i);
+                            const float ni = __shfl_sync(0xffffffffu, nr[m], (t2 + c) * 4);
+                            const float x = G[m][2 * hh + c] * nl[hh] * ni;
+                            if (!qk) {
+                                s_a[r][i] = i < r && r < n ? beta_r * x * expf(br - bi) : 0.f;
+                            } else {
+                                const float w = i <= r && r < n ? p.scale * x * expf(br - bi) : 0.f;
+                                const uint16_t hi = f32_to_bf16(w);
+                                s_w[0][r][i] = hi;
+                                s_w[1][r][i] = f32_to_bf16(w - bf16_to_f32(hi));
+                            }
+                        }
+                    if (t2 == 0) {
+                        if (!qk) {
+                            s_ys[r] = expf(br.hi) * nl[hh];
+                            s_us[r] = expf(b_end - br) * nl[hh];
+                        } else {
+                            s_qs[r] = p.scale * expf(br.hi) * nl[hh];
+                        }
+                    }
+                }
+                if (!qk) {
+                    if (lane == 0) s_gamma = expf(b_end.hi);
+                    __syncwarp();
+                    // column `lane` of T by substitution, row after row
+                    float x[TB];
+#pragma unroll
+                    for (int r = 0; r < TB; r++) {
+                        float y = r == lane ? 1.f : 0.f;
+#pragma unroll
+                        for (int i = 0; i < r; i++) y = fmaf(-s_a[r][i], x[i], y);
+                        x[r] = y;
+                    }
+                    if (lane < TB) {
+#pragma unroll
+                        for (int r = 0; r < TB; r++) {
+                            const float w = x[r] * beta;
+                            const uint16_t hi = f32_to_bf16(w);
+                            s_t[0][r][lane] = hi;
+                            s_t[1][r][lane] = f32_to_bf16(w - bf16_to_f32(hi));
+                        }
+                    }
+                }
+            }
+        }
+
+        // k S and q S
+        float P[2][NT][4] = {}, Q[2][NT][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < K / 16; kt++) {
+            uint32_t kb[NT][2], qb[NT][2];
+            const int c = 16 * kt + t2;
+#pragma unroll
+            for (int m = 0; m < NT; m++)
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    kb[m][x] = *reinterpret_cast<const uint32_t *>(&s_k[8 * m + g][c + 8 * x]);
+                    qb[m][x] = *reinterpret_cast<const uint32_t *>(&s_q[8 * m + g][c + 8 * x]);
+                }
+#pragma unroll
+            for (int m = 0; m < 2; m++) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int x = 0; x < 4; x++) split2(S[m][2 * kt + x / 2][2 * (x % 2)], S[m][2 * kt + x / 2][2 * (x % 2) + 1], hi[x], lo[x]);
+#pragma unroll
+                for (int r = 0; r < NT; r++) {
+                    mma<16>(P[m][r], hi, kb[r]);
+                    mma<16>(Q[m][r], hi, qb[r]);
+                    mma<16>(P[m][r], lo, kb[r]);
+                    mma<16>(Q[m][r], lo, qb[r]);
+                }
+            }
+        }
+        __syncthreads();   // T, the query-key products and the scales are there
+
+        const float gamma = s_gamma;
+#pragma unroll
+        for (int m = 0; m < 2; m++) {
+            uint32_t hi[2 * NT], lo[2 * NT];
+            float U[NT][4] = {};
+            // y = v - e^b (k^ S)
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                const float y0 = s_ys[8 * r + t2], y1 = s_ys[8 * r + t2 + 1];
+                split2(vv[m][r][0] - y0 * P[m][r][0], vv[m][r][1] - y1 * P[m][r][1], hi[2 * r], lo[2 * r]);
+                split2(vv[m][r][2] - y0 * P[m][r][2], vv[m][r][3] - y1 * P[m][r][3], hi[2 * r + 1], lo[2 * r + 1]);
+            }
+            auto pairs = [&](const uint16_t(*s)[TP], int r, uint32_t (&x)[NT]) {
+#pragma unroll
+                for (int i = 0; i < NT; i++) x[i] = *reinterpret_cast<const uint32_t *>(&s[8 * r + g][8 * i + t2]);
+            };
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                uint32_t th[NT], tl[NT];
+                pairs(s_t[0], r, th);
+                pairs(s_t[1], r, tl);
+                mma<TB>(U[r], hi, th);
+                mma<TB>(U[r], lo, th);
+                mma<TB>(U[r], hi, tl);
+            }
+            // o = e^b (q^ S) + W U
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                split2(U[r][0], U[r][1], hi[2 * r], lo[2 * r]);
+                split2(U[r][2], U[r][3], hi[2 * r + 1], lo[2 * r + 1]);
+            }
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                const float q0 = s_qs[8 * r + t2], q1 = s_qs[8 * r + t2 + 1];
+                Q[m][r][0] *= q0; Q[m][r][1] *= q1; Q[m][r][2] *= q0; Q[m][r][3] *= q1;
+                uint32_t wh[NT], wl[NT];
+                pairs(s_w[0], r, wh);
+                pairs(s_w[1], r, wl);
+                mma<TB>(Q[m][r], hi, wh);
+                mma<TB>(Q[m][r], lo, wh);
+                mma<TB>(Q[m][r], hi, wl);
+            }
+            // S <- gamma S + (k^ e^{b_n - b})^T U
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                const float u0 = s_us[8 * r + t2], u1 = s_us[8 * r + t2 + 1];
+                split2(U[r][0] * u0, U[r][1] * u1, hi[2 * r], lo[2 * r]);
+                split2(U[r][2] * u0, U[r][3] * u1, hi[2 * r + 1], lo[2 * r + 1]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ct += 4 / NT) {     // four 8 x 8 tiles of k: 4 / NT channel tiles of NT token tiles
+                uint32_t kt[4];
+                const int at = lane / 8;
+                load_trans(kt, static_cast<uint32_t>(__cvta_generic_to_shared(&s_k[8 * (at % NT) + lane % 8][8 * (ct + at / NT)])));
+#pragma unroll
+                for (int x = 0; x < 4 / NT; x++) {
+                    float(&d)[4] = S[m][ct + x];
+                    d[0] *= gamma; d[1] *= gamma; d[2] *= gamma; d[3] *= gamma;
+                    uint32_t kb[NT];
+#pragma unroll
+                    for (int r = 0; r < NT; r++) kb[r] = kt[x * NT + r];
+                    mma<TB>(d, hi, kb);
+                    mma<TB>(d, lo, kb);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NT; r++)
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+                if (8 * r + t2 + c < n)
+                    *reinterpret_cast<uint2 *>(out + (r0 + 8 * r + t2 + c) * p.ld_out) =
+                        make_uint2(pack_bf16x2(Q[0][r][c], Q[0][r][2 + c]), pack_bf16x2(Q[1][r][c], Q[1][r][2 + c]));
+        if (r0 + TB < row1) __syncthreads();   // the next block's q, k, T and scales
+    }
+    if (writable) {
+#pragma unroll
+        for (int n = 0; n < CT; n++)
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+                *reinterpret_cast<float4 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) =
+                    make_float4(S[0][n][c], S[0][n][2 + c], S[1][n][c], S[1][n][2 + c]);
+    }
+}
+
+}  // namespace gdn
+
+#define KDA_GDN_DIMS(RUN) \
+    RUN(32, 32) RUN(32, 64) RUN(32, 128) RUN(64, 32) RUN(64, 64) RUN(64, 128) RUN(128, 32) RUN(128, 64) RUN(128, 128)
+
+cudaError_t launch_gdn_decode(const GdnParams &p, int K, int V, int64_t num_seqs, cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(num_seqs * p.Hv * (V / 32)));
+#define KDA_GDN_RUN(KK, VV) \
+    if (K == KK && V == VV) return launch_pdl(gdn::decode_kernel<KK, VV>, grid, dim3(128), 0, stream, p);
+    KDA_GDN_DIMS(KDA_GDN_RUN)
+#undef KDA_GDN_RUN
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32_t *cu, int64_t rows, int64_t num_entries,
+                            cudaStream_t stream)
+{
+    const dim3 grid(static_cast<unsigned>(num_entries * p.Hv));
+    const int vec = reinterpret_cast<uintptr_t>(p.qkv) % 16 == 0 && p.ld_qkv % 8 == 0;   // K and V are multiples of 8
+    // blocks of 8 rows for requests of at most 8: half the products of 16
+#define KDA_GDN_RUN(KK, VV) \
+    if (K == KK && V == VV) \
+        return !cu && T <= 8 ? launch_pdl(gdn::rows_kernel<KK, VV, 8>, grid, dim3(VV), 0, stream, p, T, cu, rows, vec) \
+                             : launch_pdl(gdn::rows_kernel<KK, VV, 16>, grid, dim3(VV), 0, stream, p, T, cu, rows, vec);
+    KDA_GDN_DIMS(KDA_GDN_RUN)
+#undef KDA_GDN_RUN
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs,
+                               cudaStream_t stream)
+{
+    return launch_gdn_rows(p, K, V, 16, cu, rows, num_seqs, stream);
+}
+
+}  // namespace kda

@@ -47,7 +47,8 @@ EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decod
             "kda_fused_spec_verify", "kda_selftest_bounded_wait", "kda_chunk_prefill_workspace_bytes",
             "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
             "kda_norm_quant", "kda_fp8_matmul", "kda_fp8_matmul_plan",
-            "kda_selftest_fp8_matmul", "kda_batch_maps")
+            "kda_selftest_fp8_matmul", "kda_batch_maps",
+            "kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -73,6 +74,11 @@ class KdaShortConv(ctypes.Structure):
 class KdaGatedNorm(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64), ("weight", ctypes.c_void_p),
                 ("eps", ctypes.c_float)]
+
+
+class KdaGdnHeads(ctypes.Structure):
+    _fields_ = [("Hk", ctypes.c_int32), ("Hv", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("scale", ctypes.c_float), ("l2_eps", ctypes.c_float)]
 
 
 class KdaError(RuntimeError):
@@ -127,6 +133,13 @@ def _load():
     lib.kda_fp8_matmul_plan.argtypes = [P, I64, P, I64, I64, I64, I64, P]
     lib.kda_selftest_fp8_matmul.restype = ctypes.c_int
     lib.kda_selftest_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, I32, P, P]
+    GP = ctypes.POINTER(KdaGdnHeads)
+    lib.kda_gdn_decode.restype = ctypes.c_int
+    lib.kda_gdn_decode.argtypes = [P, I64, P, I64, P, I64, I64, GP, SP, P, I64, P, P]
+    lib.kda_gdn_spec_verify.restype = ctypes.c_int
+    lib.kda_gdn_spec_verify.argtypes = [P, I64, P, I64, P, I64, I64, I32, GP, SP, P, I64, P, P]
+    lib.kda_gdn_chunk_prefill.restype = ctypes.c_int
+    lib.kda_gdn_chunk_prefill.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, GP, SP, P, I64, P, P]
     lib.kda_batch_maps.restype = ctypes.c_int
     lib.kda_batch_maps.argtypes = [P, P, P, I64, I64, P, I64, I64, P, I64, P, I64, I32, I64, P, P, P, P, P, P,
                                    P, P, P]
@@ -532,7 +545,7 @@ class _TorchBinding:
         spec = importlib.util.spec_from_file_location("_kda_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        for f in ("norm_quant", "fp8_matmul", "batch_maps"):
+        for f in ("norm_quant", "fp8_matmul", "batch_maps", "gdn"):
             setattr(self, f, getattr(module, f))
         return getattr(module, name)
 
@@ -637,3 +650,48 @@ def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_page
     if type(r) is int:
         _check(r, "kda_batch_maps")
     return r
+
+
+# ---- the gated delta rule with one decay per head ------------------------------------------
+# Checked in the compiled module too.
+
+
+def _gdn(name, mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads, scale,
+         l2_eps, null_slot, out, err_flags, stream):
+    r = _torch_binding.gdn(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads,
+                           scale, l2_eps, null_slot, out, err_flags, _handle(stream))
+    if type(r) is int:
+        _check(r, name)
+    return r, initial_state
+
+
+def kda_gdn_decode(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, *, num_k_heads=None, scale=None,
+                   l2_eps=1e-6, null_slot=-1, out=None, err_flags=None, stream=None):
+    """One decode token per sequence of the gated delta rule with one decay per token and head.
+
+    mixed_qkv: bf16 [N, >= 2*Hk*K + Hv*V] (row = q | k | v); raw_g, raw_beta: bf16 [N, >= Hv]; A_log: fp32 [Hv]; dt_bias: fp32
+    [Hv] or None; initial_state: fp32 [num_slots, Hv, K, V], advanced in place; state_indices: int32 1-D, any positive stride.
+    num_k_heads: Hk (value head h reads key head h // (Hv // Hk)), by default Hv. Returns (out bf16 [N, Hv*V], initial_state)."""
+    return _gdn("kda_gdn_decode", mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, 0, None, num_k_heads, scale,
+                l2_eps, null_slot, out, err_flags, stream)
+
+
+def kda_gdn_spec_verify(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens_per_req, *, num_k_heads=None,
+                        scale=None, l2_eps=1e-6, null_slot=-1, out=None, err_flags=None, stream=None):
+    """The same over requests of tokens_per_req (1..64) consecutive rows; returns (out, initial_state)."""
+    tokens = int(tokens_per_req)
+    if tokens < 1:
+        raise ValueError(f"tokens_per_req must be in 1..64 (got {tokens})")
+    return _gdn("kda_gdn_spec_verify", mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, None,
+                num_k_heads, scale, l2_eps, null_slot, out, err_flags, stream)
+
+
+def kda_gdn_chunk_prefill(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, cu_seqlens, *, num_k_heads=None,
+                          scale=None, l2_eps=1e-6, null_slot=-1, out=None, err_flags=None, stream=None):
+    """The same over packed sequences, in chunks: sequence s has rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the GPU,
+    never read on the host: no synchronisation, and lengths may change between graph replays). A pair that is no range of
+    the rows counts as empty and sets KDA_ERRFLAG_LENGTHS in err_flags. Returns (out, initial_state)."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor")
+    return _gdn("kda_gdn_chunk_prefill", mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, 0, cu_seqlens,
+                num_k_heads, scale, l2_eps, null_slot, out, err_flags, stream)

@@ -1,0 +1,183 @@
+"""GPU tests of the gated delta rule with one decay per head against its fp64 oracle.
+
+Tolerances, from the arithmetic. Outputs are rounded once to bf16 (half a step is 2^-8 of the value); the products inside
+take fp32 values as two bf16 terms, 2^-18 of a value off at most, a third of that in the mean. On the path of a block's state
+there are six such values (S twice, y, T, U twice): in quadrature 6^(1/2) 2^-18 / 3 = 3.1e-6 of the state's norm, at most
+three times that where the errors of the blocks before still count: 1e-5. The outputs of several tokens may take their
+second terms from single bf16 values (2^-9 of a value off, a third in the mean, three of them in quadrature: 1.1e-3); with the rounding
+of the result (2^-9 / 3^(1/2) = 1.1e-3 to 1.7e-3 in the mean) 2.5e-3 of a row's norm. One token's products are fp32 throughout.
+With one key for all tokens the sum over i of k^_i u_i is of u of alternating effect, and what counts is not its norm but
+the terms': with Y = max |v| + |S_0|, T's rows sum to 2 at most in magnitude (beta (1 + beta + beta (1 - beta) + ..)), so |u_i| <= 2 Y,
+and u_i is off by 2^-18 (3 * 2 Y) (T, y and the product of their second terms) and 2^-18 * 2 Y (its own two terms), each a third of that in
+the mean; over the 64 tokens of a block, in quadrature: 64^(1/2) * 8 Y 2^-18 / 3, and 2.5e-3 of it more in the outputs than of their norm.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn as og
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def kda():
+    assert torch.cuda.is_available()
+    from linear_attention_state_recurrent_gb300 import build
+    build.build()
+    from linear_attention_state_recurrent_gb300 import kda as k
+    return k
+
+
+def f64(t):
+    return t.to(torch.float64).cpu().numpy()
+
+
+class Case:
+    """Inputs of a call, with NaN behind every row and in rows of no sequence."""
+
+    def __init__(self, rows, entries, Hk, Hv, K, V, seed, pad=8, slots=None, spare=4, alike=False, strong=False, dt=True):
+        g = torch.Generator().manual_seed(seed)
+        randn = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        self.Hk, self.Hv, self.K, self.V = Hk, Hv, K, V
+        width = 2 * Hk * K + Hv * V
+        self.qkv = torch.full((rows, width + pad), math.nan, dtype=BF16)
+        x = randn(rows, width)
+        if alike:   # one key for all tokens, and its negative: the largest entries that T can have
+            x[:, Hk * K:2 * Hk * K] = x[:1, Hk * K:2 * Hk * K] * torch.where(torch.arange(rows) % 3 == 1, -1.0, 1.0)[:, None]
+        self.qkv[:, :width] = x.to(BF16)
+        self.rg, self.rb = randn(rows, Hv + 3).to(BF16), (randn(rows, Hv + 1) + (4.0 if alike else 0.0)).to(BF16)
+        self.A_log = torch.rand(Hv, generator=g) * 2.77 + (3.0 if strong else -4.0 if alike else 0.0)
+        self.dt = -3 + randn(Hv) if dt else None
+        n = entries + spare
+        self.pool = torch.full((n, Hv * K * V + 4), math.nan)
+        self.pool[:, :Hv * K * V] = 0.05 * randn(n, Hv * K * V)
+        self.slots = torch.randperm(n, generator=g)[:entries].tolist() if slots is None else slots
+        self.width, self.rows = width, rows
+
+    def gpu(self):
+        self.d_qkv, self.d_rg, self.d_rb = self.qkv.cuda()[:, :self.width], self.rg.cuda()[:, :self.Hv], self.rb.cuda()[:, :self.Hv]
+        self.d_pool = self.pool.cuda()
+        self.state = torch.as_strided(self.d_pool, (len(self.pool), self.Hv, self.K, self.V), (self.d_pool.stride(0), self.K * self.V, self.V, 1))
+        idx = torch.full((max(1, len(self.slots)), 3), 1 << 30, dtype=torch.int32)
+        idx[:len(self.slots), 1] = torch.tensor(self.slots, dtype=torch.int32)
+        self.out = torch.full((self.rows, self.Hv * self.V + 4), 7.0, dtype=BF16, device="cuda")
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        return (self.d_qkv, self.d_rg, self.d_rb, self.A_log.cuda(), None if self.dt is None else self.dt.cuda(), self.state,
+                idx.cuda()[:len(self.slots), 1])
+
+    def check(self, bounds, null_slot=-1, err=0, exact=False, rows=None, alike=False):
+        hkv = self.Hv * self.K * self.V
+        pool = f64(self.pool[:, :hkv]).reshape(-1, self.Hv, self.K, self.V)
+        out, after, flags = og.run(f64(self.qkv[:, :self.width]), f64(self.rg), f64(self.rb), f64(self.A_log),
+                                   None if self.dt is None else f64(self.dt), pool, self.slots, bounds, self.Hk, null_slot=null_slot, rows=rows)
+        assert self.err.item() == flags == err
+        got = f64(self.out)
+        assert (got[:, self.Hv * self.V:] == 7.0).all()                       # behind the rows
+        free = np.isnan(out[:, 0])
+        assert (got[free] == 7.0).all()                                       # rows of no sequence
+        g, o = got[~free, :self.Hv * self.V].reshape(-1, self.V), out[~free].reshape(-1, self.V)
+        if len(o):
+            off = np.linalg.norm(g - o, axis=1) / np.maximum(np.linalg.norm(o, axis=1), 1e-30)
+            off = np.where(np.linalg.norm(o, axis=1) == 0, np.linalg.norm(g, axis=1), off)
+            total = np.linalg.norm(g - o) / max(np.linalg.norm(o), 1e-30)
+            assert total <= 2.5e-3, total
+            rms = np.sqrt((o ** 2).mean(1, keepdims=True))
+            assert (np.abs(g - o) <= 2.0 ** -8 * np.abs(o) + (1e-6 if exact else 1e-2) * rms + 1e-30).all()
+        p = f64(self.d_pool)
+        np.testing.assert_array_equal(p[:, hkv:], f64(self.pool[:, hkv:]))    # behind the slots
+        p = p[:, :hkv].reshape(pool.shape)
+        worst = 0.0
+        for s in range(len(pool)):
+            if (after[s] == pool[s]).all():
+                np.testing.assert_array_equal(p[s], pool[s])
+                continue
+            for h in range(self.Hv):
+                worst = max(worst, np.linalg.norm(p[s, h] - after[s, h]) / np.linalg.norm(after[s, h]))
+        most = 2e-6 if exact else 1e-5
+        if alike:
+            v = f64(self.qkv[:, 2 * self.Hk * self.K:self.width]).reshape(self.rows, self.Hv, self.V)
+            most = 64 ** 0.5 * 8 * 2.0 ** -18 / 3 * (np.linalg.norm(v, axis=2).max() + np.linalg.norm(pool, axis=(2, 3)).max())
+            worst *= max(np.linalg.norm(after[s, h]) for s in range(len(pool)) for h in range(self.Hv))
+        assert worst <= most, (worst, most)
+
+
+HEADS = [(1, 1, 128, 128), (2, 4, 128, 64), (1, 3, 64, 128), (2, 2, 64, 64), (1, 2, 32, 128), (1, 1, 128, 32), (2, 4, 32, 32), (1, 2, 64, 32)]
+
+
+@pytest.mark.parametrize("Hk, Hv, K, V", HEADS)
+@pytest.mark.parametrize("n", [1, 5])
+def test_decode(kda, Hk, Hv, K, V, n):
+    c = Case(n, n, Hk, Hv, K, V, seed=K + V + n)
+    kda.kda_gdn_decode(*c.gpu(), num_k_heads=Hk, out=c.out, err_flags=c.err)
+    c.check([(i, i + 1) for i in range(n)], exact=True)
+
+
+@pytest.mark.parametrize("Hk, Hv, K, V", HEADS)
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 16, 17, 64])
+def test_spec_verify(kda, Hk, Hv, K, V, T):
+    c = Case(3 * T, 3, Hk, Hv, K, V, seed=T, pad=7 if T == 7 else 8)          # rows off 16-byte boundaries too
+    kda.kda_gdn_spec_verify(*c.gpu(), T, num_k_heads=Hk, out=c.out, err_flags=c.err)
+    c.check([(r * T, (r + 1) * T) for r in range(3)])
+
+
+@pytest.mark.parametrize("pad", [7, 8])
+@pytest.mark.parametrize("Hk, Hv, K, V", HEADS)
+def test_prefill(kda, Hk, Hv, K, V, pad):
+    lens = [1, 63, 64, 0, 65, 130, 2, 200]
+    cu = np.concatenate([[2], 2 + np.cumsum(lens)]).tolist()
+    c = Case(cu[-1] + 3, len(lens), Hk, Hv, K, V, seed=4, pad=pad, dt=V != 64)
+    c.qkv[:2] = c.qkv[-3:] = math.nan
+    kda.kda_gdn_chunk_prefill(*c.gpu(), torch.tensor(cu, dtype=torch.int32, device="cuda"), num_k_heads=Hk, out=c.out, err_flags=c.err)
+    c.check(list(zip(cu, cu[1:])))
+
+
+@pytest.mark.parametrize("what", ["alike", "strong"])
+@pytest.mark.parametrize("K, V", [(128, 128), (64, 64), (32, 32)])
+def test_prefill_extremes(kda, what, K, V):
+    """The same key again and again with beta near 1 and little decay; and a decay of thousands of nats in a chunk."""
+    c = Case(300, 2, 1, 2, K, V, seed=9, **{what: True})
+    cu = [0, 170, 300]
+    kda.kda_gdn_chunk_prefill(*c.gpu(), torch.tensor(cu, dtype=torch.int32, device="cuda"), num_k_heads=1, out=c.out, err_flags=c.err)
+    c.check(list(zip(cu, cu[1:])), alike=what == "alike")
+
+
+@pytest.mark.parametrize("call", ["decode", "spec", "prefill", "prefill32"])
+def test_slots(kda, call):
+    T, K = (1 if call == "decode" else 5), (32 if call == "prefill32" else 64)
+    c = Case(5 * T, 5, 1, 2, K, 64, seed=8, slots=[2, -1, 0, 9, 4])           # 9 slots: the fourth is past them, 0 is null
+    a = c.gpu()
+    kw = dict(num_k_heads=1, out=c.out, err_flags=c.err, null_slot=0)
+    bounds = [(i * T, i * T + T) for i in range(5)]
+    if call == "decode":
+        kda.kda_gdn_decode(*a, **kw)
+    elif call == "spec":
+        kda.kda_gdn_spec_verify(*a, T, **kw)
+    else:
+        kda.kda_gdn_chunk_prefill(*a, torch.tensor([0, 5, 10, 15, 20, 25], dtype=torch.int32, device="cuda"), **kw)
+    c.check(bounds, null_slot=0, err=og.ERR_SLOT_RANGE)
+
+
+@pytest.mark.parametrize("K", [32, 128])
+def test_prefill_lengths_out_of_range(kda, K):
+    cu = [0, 70, 60, 60, 400, -5, 20]   # no two ranges share a row
+    c = Case(100, 6, 1, 1, K, 64, seed=12)
+    kda.kda_gdn_chunk_prefill(*c.gpu(), torch.tensor(cu, dtype=torch.int32, device="cuda"), out=c.out, err_flags=c.err)
+    c.check(list(zip(cu, cu[1:])), err=og.ERR_LENGTHS)
+
+
+@pytest.mark.parametrize("K", [32, 128])
+def test_prefill_in_parts_is_prefill(kda, K):
+    """A prompt in two calls, the second from the first one's state, then decoded on: the whole by the oracle."""
+    c = Case(150, 1, 1, 2, K, 64, seed=13, slots=[3])
+    qkv, rg, rb, *rest = c.gpu()
+    for r0, r1 in ((0, 77), (77, 149), (149, 150)):
+        kw = dict(num_k_heads=1, out=c.out[r0:r1], err_flags=c.err)
+        if r1 - r0 == 1:
+            kda.kda_gdn_decode(qkv[r0:r1], rg[r0:r1], rb[r0:r1], *rest, **kw)
+        else:
+            kda.kda_gdn_chunk_prefill(qkv[r0:r1], rg[r0:r1], rb[r0:r1], *rest, torch.tensor([0, r1 - r0], dtype=torch.int32, device="cuda"), **kw)
+    c.check([(0, 150)])
