@@ -494,10 +494,4 @@ cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs,
-                               cudaStream_t stream)
-{
-    return launch_gdn_rows(p, K, V, 16, cu, rows, num_seqs, stream);
-}
-
 }  // namespace kda

@@ -102,8 +102,10 @@ int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint1
     const int s = check(mixed_qkv, ld_qkv, raw_g, ld_g, raw_beta, ld_beta, num_seqs, heads, state, out, ld_out, err_flags, &p);
     if (s) return s;
     if (!cu_seqlens || !aligned(cu_seqlens, 4)) return invalid("cu_seqlens must be non-NULL and 4-byte aligned");
-    if (num_rows < 0 || num_rows > INT32_MAX) return invalid("num_rows must be in [0, 2^31)");
-    if (num_seqs == 0) return set_error(KDA_OK, "%s", "");
+    if (num_rows < 0) return invalid("num_rows must be >= 0");
+    if (num_rows > INT32_MAX - 64)   // a chunk past the last row still has a 32-bit row number
+        return set_error(KDA_ERR_UNSUPPORTED, "num_rows must be below 2^31 - 64 (got %lld)", (long long)num_rows);
+    if (num_seqs == 0 || num_rows == 0) return set_error(KDA_OK, "%s", "");
     return done(kda::launch_gdn_prefill(p, heads->K, heads->V, cu_seqlens, num_rows, num_seqs, static_cast<cudaStream_t>(stream)),
                 "kda_gdn_chunk_prefill launch");
 }

@@ -123,8 +123,8 @@ def test_refusals(kda, name, what, bad, status):
 def test_refusals_of_one_call(kda):
     for T in (0, -1, 65):
         assert call(kda, "kda_gdn_spec_verify", dict(T=T)) == 1
-    for change in (dict(cu=None), dict(cu=FAKE + 2), dict(rows=-1), dict(rows=2 ** 31)):
-        assert call(kda, "kda_gdn_chunk_prefill", change) == 1
+    for change, status in ((dict(cu=None), 1), (dict(cu=FAKE + 2), 1), (dict(rows=-1), 1), (dict(rows=2 ** 31 - 64), 2)):
+        assert call(kda, "kda_gdn_chunk_prefill", change) == status
 
 
 @pytest.mark.parametrize("name", CALLS)
