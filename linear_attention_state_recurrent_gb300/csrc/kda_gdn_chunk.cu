@@ -18,6 +18,7 @@
 #include <atomic>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -37,8 +38,8 @@ constexpr int SCALARS = 8;                             // chunks of row factors:
                                                        // when those of c + 4 are written
 constexpr int ORDER = 256;                             // sequences that are sorted by length
 constexpr int BLK = 16 * 20;                           // floats of a 16 x 16 block, rows 20 apart: no bank conflicts
-// registers: 85 a thread at launch are 80, 61,440 in all; 256 x 144 + 256 x 64 + 128 x 40 + 128 x 24 = 61,440
-constexpr int REG_CHAIN = 144, REG_PREP = 64, REG_OUT = 40, REG_REST = 24;
+// registers: 80 a thread at launch, 61,440 in all; 256 x 136 + 256 x 64 + 2 x 128 x 40 = 61,440
+constexpr int REG_CHAIN = 136, REG_PREP = 64, REG_OUT = 40, REG_REST = 40;
 
 // columns of tensor memory
 constexpr uint32_t T_S = 0;      // first operand of K S and Q S: the halves of the channels one after the other, each hi | lo; then the state's increment
@@ -55,8 +56,8 @@ struct Smem {
     static constexpr int BLOCKS = T + 2 * GROUP;       // per group the ten blocks of A and T
     static constexpr int ROWS = BLOCKS + 2 * 10 * BLK * 4;
     static constexpr int SET = 3 * C + 4;              // floats: ys, us, qs, and gamma
-    static constexpr int COLS = ROWS + SCALARS * SET * 4;   // per group: b hi, b lo (less log2 |k|^-1), beta
-    static constexpr int SORT = COLS + 2 * 3 * C * 4;
+    static constexpr int COLS = ROWS + SCALARS * SET * 4;   // per group: b hi, b lo, beta, and of the keys b lo less the norm's logarithm and e^{p - b} times the norm
+    static constexpr int SORT = COLS + 2 * 5 * C * 4;
     static constexpr int BARS = SORT + ORDER * 2;
     static constexpr int NBARS = 2 * STAGES + 26;
     static constexpr int END = BARS + NBARS * 8 + 16;
@@ -69,28 +70,30 @@ struct Args {
     int rows, num_seqs;
 };
 
-// Matrix descriptors with the 128-byte swizzle, groups of 8 rows at 1024 bytes. K-major: a row of the operand is 128 bytes.
-__device__ __forceinline__ uint64_t desc_k(uint32_t at)
-{
-    constexpr uint32_t HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
-    return static_cast<uint64_t>(HIGH) << 32 | (1u << 16) | (at >> 4);
-}
+// Matrix descriptors with the 128-byte swizzle, groups of 8 rows at 1024 bytes: the low words (the high one is the same for all).
+// K-major: a row of the operand is 128 bytes.
+__device__ __forceinline__ uint32_t desc_k(uint32_t at) { return (1u << 16) | (at >> 4); }
 // The same bytes with the 128-byte rows along the inner axis (K^T from the tile of K): 64 columns, the next 64 at HALF.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t at)
-{
-    constexpr uint32_t HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
-    return static_cast<uint64_t>(HIGH) << 32 | (static_cast<uint32_t>(Smem::HALF >> 4) << 16) | (at >> 4);
-}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t at) { return (static_cast<uint32_t>(Smem::HALF >> 4) << 16) | (at >> 4); }
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
 // bf16 operands, fp32 sums, 128 rows; `mn`: the second operand is stored along its columns
 constexpr uint32_t idesc(int n, bool mn = false)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 // d (+)= a b^T, 16 of the inner axis; a in tensor memory
-__device__ __forceinline__ void mma_t(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add)
+__device__ __forceinline__ void mma_t(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(add ? 1u : 0u));
+    asm volatile("{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n"
+                 :: "r"(d), "r"(a), "r"(b), "n"(DESC_HIGH), "r"(id), "r"(add ? 1u : 0u));
+}
+// The same with both operands from the same place in shared memory.
+__device__ __forceinline__ void mma_gram(uint32_t d, uint32_t ab, uint32_t id, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%1, %2};\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], db, db, %3, p;\n}\n"
+                 :: "r"(d), "r"(ab), "n"(DESC_HIGH), "r"(id), "r"(add ? 1u : 0u));
 }
 
 __device__ __forceinline__ bool elect_one()
@@ -108,6 +111,11 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
@@ -133,6 +141,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
                     "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 // d += a b in fp32 but for 2^-21 of the terms: tf32 products of the operands' two terms
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
@@ -160,23 +173,23 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const Tf32<4> &a, const
 struct Walk {
     const Args *a;
     const uint16_t *order;
-    int64_t item, total;        // chains: sequence (longest first) x value head
+    int item, total;            // chains: sequence (longest first) x value head
     int row, left, h;           // of the current chunk: its first row, the chain's rows from there on, the value head
-    int64_t seq;
+    int seq;
 
-    __device__ __forceinline__ Walk(const Args &args, const uint16_t *sorted, int64_t from = blockIdx.x)
-        : a(&args), order(sorted), item(from), total(static_cast<int64_t>(args.num_seqs) * args.p.Hv) {}
+    __device__ __forceinline__ Walk(const Args &args, const uint16_t *sorted)
+        : a(&args), order(sorted), item(blockIdx.x), total(args.num_seqs * args.p.Hv) {}
     // CTA i's chains are i, 2 G - 1 - i, 2 G + i, ..: the longest with the shortest
     __device__ __forceinline__ void advance()
     {
-        const int64_t g = gridDim.x, at = item % g;
+        const int g = gridDim.x, at = item % g;
         item += 2 * (g - 1 - at) + 1;
     }
     // The chain at `item`: its rows, or none (an empty or bad range, a slot past the pool). *bad: error bits.
     __device__ __forceinline__ bool chain(uint32_t *bad = nullptr, int *all = nullptr)
     {
-        const int64_t s = item / a->p.Hv;
-        h = static_cast<int>(item % a->p.Hv);
+        const int s = item / a->p.Hv;
+        h = item - s * a->p.Hv;
         seq = a->num_seqs <= ORDER ? order[s] : s;
         row = __ldg(a->cu + seq);
         const int end = __ldg(a->cu + seq + 1);
@@ -212,23 +225,22 @@ struct Walk {
 struct Waiter {
     volatile uint32_t *gave_up;
     uint32_t *err;
+    // Asleep for up to 1 ms a try: some twenty warps of a CTA wait at any time, and must not take the others' issue slots.
     __device__ __forceinline__ bool operator()(uint32_t mbar, uint32_t parity) const
     {
         long long start = 0;
-        for (uint32_t it = 1;; it++) {
+        for (bool again = false;; again = true) {
             uint32_t ok;
-            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                         " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity) : "memory");
+            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+                         " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity), "r"(1000000u) : "memory");
             if (ok) return true;
-            if (it % 64 == 0) {
-                if (*gave_up) return false;
-                const long long now = clock64();
-                if (it == 64) start = now;
-                else if (now - start > 4000000000ll) {
-                    *gave_up = 1;
-                    if (err) atomicOr(err, kErrTimeout);
-                    return false;
-                }
+            if (*gave_up) return false;
+            const long long now = clock64();
+            if (!again) start = now;
+            else if (now - start > 4000000000ll) {
+                *gave_up = 1;
+                if (err) atomicOr(err, kErrTimeout);
+                return false;
             }
         }
     }
@@ -239,14 +251,6 @@ struct Waiter {
     }
 };
 
-// T diag(beta) at (r, i), hi and lo
-__device__ __forceinline__ void put_t(unsigned char *tile, int r, int i, float x)
-{
-    const uint32_t at = r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2;
-    const uint16_t hi = f32_to_bf16(x);
-    *reinterpret_cast<uint16_t *>(tile + at) = hi;
-    *reinterpret_cast<uint16_t *>(tile + Smem::TILE + at) = f32_to_bf16(x - bf16_to_f32(hi));
-}
 __device__ __forceinline__ constexpr int block_at(int a, int b) { return (a * (a + 1) / 2 + b) * BLK; }
 
 template <int NH, int V>
@@ -381,29 +385,31 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 // Y = V - e^b K^ S; rows past the chunk's end are zeros, whatever is in memory there
                 if (!wait.warp(ks_done, one)) break;
                 tc::fence_after_sync();
+                // (its terms go where later columns of K S still are: all of them first)
                 {
-                    uint32_t r[32], hi[16], lo[16];
+                    uint32_t r[32];
                     tmem_ld(ty, r);
                     tc::tmem_ld_wait();
                     const float4 *ys = reinterpret_cast<const float4 *>(set + half * 32);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float4 f = ys[i];
+                    for (int q = 0; q < 2; q++) {
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int x = 0; x < 2; x++) {
-                            const int e = 2 * i + x;
-                            const float2 pk = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                            const float2 vv = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
-                            float2 y = ffma2(x ? make_float2(-f.z, -f.w) : make_float2(-f.x, -f.y), pk, vv);
+                        for (int e = 0; e < 8; e++) {
+                            const int at = 8 * q + e;
+                            const float4 f = ys[at / 2];
+                            const float2 pk = make_float2(__uint_as_float(r[2 * at]), __uint_as_float(r[2 * at + 1]));
+                            const float2 vv = make_float2(__uint_as_float(v[at] << 16), __uint_as_float(v[at] & 0xffff0000u));
+                            float2 y = ffma2(at % 2 ? make_float2(-f.z, -f.w) : make_float2(-f.x, -f.y), pk, vv);
                             if (n < C) {
-                                if (half * 32 + 2 * e >= n) y.x = 0.f;
-                                if (half * 32 + 2 * e + 1 >= n) y.y = 0.f;
+                                if (half * 32 + 2 * at >= n) y.x = 0.f;
+                                if (half * 32 + 2 * at + 1 >= n) y.y = 0.f;
                             }
                             split2(y.x, y.y, hi[e], lo[e]);
                         }
+                        tmem_st8(ty + 8 * q, hi);
+                        tmem_st8(ty + 16 + 8 * q, lo);
                     }
-                    tmem_st16(ty, hi);
-                    tmem_st16(ty + 16, lo);
                 }
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
@@ -413,26 +419,33 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 if (!wait.warp(u_done(c & 1), two)) break;
                 tc::fence_after_sync();
                 {
-                    uint32_t r[32], uh[16], ul[16], hi[16], lo[16];
+                    uint32_t r[32];
                     tmem_ld(tu, r);
                     tc::tmem_ld_wait();
                     const float4 *us = reinterpret_cast<const float4 *>(set + C + half * 32);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float4 f = us[i];
+                    for (int q = 0; q < 2; q++) {
+                        uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int x = 0; x < 2; x++) {
-                            const int e = 2 * i + x;
-                            const float2 y = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                            split2(y.x, y.y, uh[e], ul[e]);
-                            const float2 z = fmul2(y, x ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                        for (int e = 0; e < 8; e++) {
+                            const int at = 8 * q + e;
+                            const float4 f = us[at / 2];
+                            const float2 y = make_float2(__uint_as_float(r[2 * at]), __uint_as_float(r[2 * at + 1]));
+                            const float2 z = fmul2(y, at % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
                             split2(z.x, z.y, hi[e], lo[e]);
                         }
+                        tmem_st8(ty + 8 * q, hi);
+                        tmem_st8(ty + 16 + 8 * q, lo);
                     }
-                    tmem_st16(ty, hi);
-                    tmem_st16(ty + 16, lo);
-                    tmem_st16(tu, uh);
-                    tmem_st16(tu + 16, ul);
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            split2(__uint_as_float(r[2 * (8 * q + e)]), __uint_as_float(r[2 * (8 * q + e) + 1]), hi[e], lo[e]);
+                        tmem_st8(tu + 8 * q, hi);
+                        tmem_st8(tu + 16 + 8 * q, lo);
+                    }
                 }
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
@@ -472,7 +485,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         const bool query = t >= 64;
         unsigned char *tile = sm + Smem::T + g * Smem::GROUP;
         float *blocks = reinterpret_cast<float *>(sm + Smem::BLOCKS) + g * 10 * BLK;
-        float *cols = reinterpret_cast<float *>(sm + Smem::COLS) + g * 3 * C;
+        float *cols = reinterpret_cast<float *>(sm + Smem::COLS) + g * 5 * C;
         auto sync = [&] { asm volatile("bar.sync %0, 128;" :: "r"(1 + g) : "memory"); };
         // the same, with one answer to whether every thread's waits have come through
         auto sync_ok = [&](bool ok) {
@@ -483,7 +496,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         };
         const int gq = lane >> 2, tq = lane & 3;
         // raw_g (warp 0) and raw_beta (warp 1) of rows 2 lane, 2 lane + 1 of the chunk at the walk
-        float raw0 = 0.f, raw1 = 0.f;
+        float raw0 = 0.f, raw1 = 0.f, rate = 0.f, dtb = 0.f;
+        int h_of = -1;
         auto fetch = [&] {
             if (pw < 2) {
                 const uint16_t *at = pw == 0 ? p.rg : p.rb;
@@ -504,18 +518,22 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             if (more) fetch();
             float *set = sets + (c % SCALARS) * Smem::SET;
             if (pw == 0) {                                                    // the running decay, in units of log 2
-                const float expA = expf(__ldg(p.A_log + h)) * 1.44269504f, dtb = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
-                const double g0 = 2 * lane < n ? -expA * softplus_f(in0 + dtb) : 0.f, g1 = 2 * lane + 1 < n ? -expA * softplus_f(in1 + dtb) : 0.f;
+                if (h != h_of) {
+                    h_of = h;
+                    rate = expf(__ldg(p.A_log + h)) * -1.44269504f;
+                    dtb = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+                }
+                const double g0 = 2 * lane < n ? rate * softplus_f(in0 + dtb) : 0.f, g1 = 2 * lane + 1 < n ? rate * softplus_f(in1 + dtb) : 0.f;
                 double b = g0 + g1;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const double x = __shfl_up_sync(0xffffffffu, b, o);
                     if (lane >= o) b += x;
                 }
-                const double b1 = b, b0_ = b - g1;
-                const float h0 = static_cast<float>(b0_), h1 = static_cast<float>(b1);
+                const double b0_ = b - g1;
+                const float h0 = static_cast<float>(b0_), h1 = static_cast<float>(b);
                 *reinterpret_cast<float2 *>(cols + 2 * lane) = make_float2(h0, h1);
-                *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(static_cast<float>(b0_ - h0), static_cast<float>(b1 - h1));
+                *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(static_cast<float>(b0_ - h0), static_cast<float>(b - h1));
             } else if (pw == 1) {
                 *reinterpret_cast<float2 *>(cols + 2 * C + 2 * lane) =
                     make_float2(2 * lane < n ? sigmoid_f(in0) : 0.f, 2 * lane + 1 < n ? sigmoid_f(in1) : 0.f);
@@ -544,16 +562,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                     for (int x = 0; x < 8; x++) *reinterpret_cast<uint4 *>(own + hf * Smem::HALF + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
             if (!sync_ok(ok)) break;
-            const float b_hi = cols[r], b_lo = cols[C + r], e_hi = cols[C - 1], e_lo = cols[2 * C - 1], beta = cols[2 * C + r];
+            const float b_hi = cols[r], b_lo = cols[C + r];
+            const float scale = (query ? p.scale : cols[2 * C + r]) * norm;
             if (!query) {
+                const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1];
                 set[r] = ex2(b_hi + b_lo) * norm;
                 set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * norm;
                 if (r == 0) set[3 * C] = ex2(e_hi + e_lo);
+                cols[3 * C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
+                cols[4 * C + r] = ex2((cols[r | 15] - b_hi) + (cols[C + (r | 15)] - b_lo)) * norm;
             } else {
                 set[2 * C + r] = p.scale * ex2(b_hi + b_lo) * norm;
             }
-            sync();                                                           // b lo has been read as it was
-            if (!query) cols[C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
             __syncwarp();
             if (lane == 0) arrive(scaled(c));
             sync();
@@ -561,73 +581,96 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             ok = wait.warp(g_done(g), two);
             tc::fence_after_sync();
             if (query && c >= 2) ok &= wait.warp(o_done(g), two ^ 1);         // the products of this group's last chunk have been used
-            const float scale = (query ? p.scale : beta) * norm;
-            const int blocks_here = (r >> 4) + 1, most = (pw & 1) * 2 + 2;    // of this row, and of the warp's rows
-#pragma unroll 1
-            for (int bl = 0; bl < 4; bl++) {
-                if (bl >= most) {
-                    if (query)
-                        for (int x = 0; x < 4; x++)
-                            *reinterpret_cast<uint4 *>(tile + (2 + x / 2) * Smem::TILE + r * 128 + (((2 * bl + x % 2) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                    continue;
-                }
-                uint32_t x[16];
-                tmem_ld(tmem + T_G + g * 64 + (static_cast<uint32_t>(pw * 32) << 16) + bl * 16, x);
-                tc::tmem_ld_wait();
-                float d[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 ch = *reinterpret_cast<const float4 *>(cols + bl * 16 + i), cl = *reinterpret_cast<const float4 *>(cols + C + bl * 16 + i);
-                    const float hh[4] = {ch.x, ch.y, ch.z, ch.w}, ll[4] = {cl.x, cl.y, cl.z, cl.w};
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const int col = bl * 16 + i + y;
-                        const float f = ex2((b_hi - hh[y]) + (b_lo - ll[y])) * scale * __uint_as_float(x[i + y]);
-                        d[i + y] = r < n && (query ? col <= r : col < r) ? f : 0.f;
-                    }
-                }
+            const int low = (pw & 1) * 2;                                     // the first block with a diagonal in the warp's rows
+            const uint32_t tg = tmem + T_G + g * 64 + (static_cast<uint32_t>(pw * 32) << 16);
+            float2 d[8];
+            auto put = [&](int bl) {
                 if (query) {
 #pragma unroll
                     for (int y = 0; y < 2; y++) {
                         uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int i = 0; i < 4; i++) split2(d[8 * y + 2 * i], d[8 * y + 2 * i + 1], hi[i], lo[i]);
+                        for (int i = 0; i < 4; i++) split2(d[4 * y + i].x, d[4 * y + i].y, hi[i], lo[i]);
                         unsigned char *at = tile + 2 * Smem::TILE + r * 128 + (((2 * bl + y) ^ (r & 7)) << 4);
                         *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4 *>(at + Smem::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                } else if (bl < blocks_here) {
+                } else if (bl <= r >> 4) {
                     float *at = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(at + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+                    for (int i = 0; i < 4; i++)
+                        *reinterpret_cast<float4 *>(at + 4 * i) = make_float4(d[2 * i].x, d[2 * i].y, d[2 * i + 1].x, d[2 * i + 1].y);
                 }
+            };
+            // blocks left of it: e^{b_r - b_i} = e^{b_r - p} e^{p - b_i}, p the sum at the block's last row: neither is above 1
+#pragma unroll 1
+            for (int bl = 0; bl < low; bl++) {
+                uint32_t x[16];
+                tmem_ld(tg + bl * 16, x);
+                const float f = ex2((b_hi - cols[bl * 16 + 15]) + (b_lo - cols[C + bl * 16 + 15])) * scale;
+                const float2 f2 = make_float2(f, f);
+                tc::tmem_ld_wait();
+                if (r >= n) {                                                 // not a row of the chunk: whatever it held
+#pragma unroll
+                    for (int i = 0; i < 16; i++) x[i] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float4 e = *reinterpret_cast<const float4 *>(cols + 4 * C + bl * 16 + 4 * i);
+                    d[2 * i] = fmul2(fmul2(make_float2(e.x, e.y), f2), make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])));
+                    d[2 * i + 1] = fmul2(fmul2(make_float2(e.z, e.w), f2), make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
+                }
+                put(bl);
+            }
+            // and the two with diagonals: entry by entry, the ones above it cut off
+            const int end = r < n ? r + query : 0;
+            const float2 bh = make_float2(b_hi, b_hi), bl2 = make_float2(b_lo, b_lo), sc = make_float2(scale, scale);
+#pragma unroll 1
+            for (int bl = low; bl < low + 2; bl++) {
+                uint32_t x[16];
+                tmem_ld(tg + bl * 16, x);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float4 eh = *reinterpret_cast<const float4 *>(cols + bl * 16 + 4 * i);
+                    const float4 el = *reinterpret_cast<const float4 *>(cols + 3 * C + bl * 16 + 4 * i);
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        const float2 e = fadd2(fsub2(bh, y ? make_float2(eh.z, eh.w) : make_float2(eh.x, eh.y)),
+                                               fsub2(bl2, y ? make_float2(el.z, el.w) : make_float2(el.x, el.y)));
+                        const float2 v = fmul2(fmul2(make_float2(ex2(e.x), ex2(e.y)), sc),
+                                               make_float2(__uint_as_float(x[4 * i + 2 * y]), __uint_as_float(x[4 * i + 2 * y + 1])));
+                        const int col = bl * 16 + 4 * i + 2 * y;
+                        d[2 * i + y] = make_float2(col < end ? v.x : 0.f, col + 1 < end ? v.y : 0.f);
+                    }
+                }
+                put(bl);
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive(g_free(g));
-            if (c >= 2) ok &= wait.warp(u_done(g), two ^ 1);                  // T of this group's last chunk has been used
-            if (!sync_ok(ok)) break;
+            sync();
             // T: the diagonal blocks, a warp each, by substitution; a lane has a column (lanes 16 and up the same again)
             {
                 const float *A = blocks + block_at(pw, pw);
                 float x[16];
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
-                    float y0 = i == (lane & 15) ? 1.f : 0.f, y1 = 0.f;
+                    float y[4] = {i == (lane & 15) ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int k = 0; k < i; k += 2) {
-                        y0 = fmaf(-A[i * 20 + k], x[k], y0);
-                        if (k + 1 < i) y1 = fmaf(-A[i * 20 + k + 1], x[k + 1], y1);
+                    for (int k = 0; k < i; k += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(A + i * 20 + k);
+                        y[0] = fmaf(-f.x, x[k], y[0]);
+                        if (k + 1 < i) y[1] = fmaf(-f.y, x[k + 1], y[1]);
+                        if (k + 2 < i) y[2] = fmaf(-f.z, x[k + 2], y[2]);
+                        if (k + 3 < i) y[3] = fmaf(-f.w, x[k + 3], y[3]);
                     }
-                    x[i] = y0 + y1;
+                    x[i] = (y[0] + y[1]) + (y[2] + y[3]);
                 }
-                const float bj = cols[2 * C + pw * 16 + (lane & 15)];
                 __syncwarp();
+                if (lane < 16)
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    if (lane < 16) blocks[block_at(pw, pw) + i * 20 + lane] = x[i];
-                    else if (i >= (lane & 15)) put_t(tile, pw * 16 + i, pw * 16 + (lane & 15), x[i] * bj);
-                }
+                    for (int i = 0; i < 16; i++) blocks[block_at(pw, pw) + i * 20 + lane] = x[i];
             }
             sync();
             // the blocks below them: [[X, 0], [-Y A X, Y]], first of 32 rows, then of all 64. X^T A^T is the first operand of the
@@ -667,7 +710,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 for (int x = 0; x < 4; x++) {
                     const int col = gq + 8 * (x >> 1), row = 8 * hf + 2 * tq + (x & 1);
                     A[row * 20 + col] = out[x];
-                    put_t(tile, 32 * pr + 16 + row, 32 * pr + col, out[x] * cols[2 * C + 32 * pr + col]);
                 }
             }
             sync();
@@ -713,13 +755,34 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                         }
                     }
                 }
+                sync();                                                       // A has been read
+                float *at = blocks + block_at(2 + hf, mt);
 #pragma unroll
                 for (int rt = 0; rt < 2; rt++)
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                        const int col = 16 * mt + gq + 8 * (x >> 1), row = 32 + 16 * hf + 8 * rt + 2 * tq + (x & 1);
-                        put_t(tile, row, col, out[rt][x] * cols[2 * C + col]);
+                    for (int x = 0; x < 4; x++) at[(8 * rt + 2 * tq + (x & 1)) * 20 + gq + 8 * (x >> 1)] = out[rt][x];
+            }
+            if (c >= 2) ok &= wait.warp(u_done(g), two ^ 1);                  // T of this group's last chunk has been used
+            if (!sync_ok(ok)) break;
+            // T diag(beta), hi and lo: half of row r
+#pragma unroll 1
+            for (int bl = t >> 6 << 1; bl <= r >> 4 && bl < (t >> 6 << 1) + 2; bl++) {
+                const float *from = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const float4 x = *reinterpret_cast<const float4 *>(from + 8 * y + 4 * i);
+                        const float4 e = *reinterpret_cast<const float4 *>(cols + 2 * C + bl * 16 + 8 * y + 4 * i);
+                        const float2 v0 = fmul2(make_float2(x.x, x.y), make_float2(e.x, e.y)), v1 = fmul2(make_float2(x.z, x.w), make_float2(e.z, e.w));
+                        split2(v0.x, v0.y, hi[2 * i], lo[2 * i]);
+                        split2(v1.x, v1.y, hi[2 * i + 1], lo[2 * i + 1]);
                     }
+                    unsigned char *at = tile + r * 128 + (((2 * bl + y) ^ (r & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + Smem::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             tc::fence_proxy_async();
             __syncwarp();
@@ -750,26 +813,32 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 if (!wait.warp(o_done(c & 1), (c >> 1) & 1)) break;
                 tc::fence_after_sync();
                 more = w.next();
+                auto store = [&](auto whole) {
 #pragma unroll
-                for (int i = 0; i < C; i += 16) {
-                    uint32_t x[16], y[16];
-                    tmem_ld(t0 + i, x);
-                    tmem_ld(t0 + C + i, y);
-                    tc::tmem_ld_wait();
-                    if (i == C - 16) {
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) arrive(o_free);
-                    }
+                    for (int i = 0; i < C; i += 8) {
+                        uint32_t x[8], y[8];
+                        tmem_ld8(t0 + i, x);
+                        tmem_ld8(t0 + C + i, y);
+                        tc::tmem_ld_wait();
+                        if (i == C - 8) {
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) arrive(o_free);
+                        }
 #pragma unroll
-                    for (int r = 0; r < 16; r += 2) {
-                        const float2 f = *reinterpret_cast<const float2 *>(qs + i + r);
-                        const uint32_t o2 = pack_bf16x2(fmaf(f.x, __uint_as_float(x[r]), __uint_as_float(y[r])),
-                                                        fmaf(f.y, __uint_as_float(x[r + 1]), __uint_as_float(y[r + 1])));
-                        if (i + r < n) out[static_cast<int64_t>(i + r) * p.ld_out] = static_cast<uint16_t>(o2);
-                        if (i + r + 1 < n) out[static_cast<int64_t>(i + r + 1) * p.ld_out] = static_cast<uint16_t>(o2 >> 16);
+                        for (int r = 0; r < 8; r += 2) {
+                            const float2 o = ffma2(*reinterpret_cast<const float2 *>(qs + i + r), make_float2(__uint_as_float(x[r]), __uint_as_float(x[r + 1])),
+                                                   make_float2(__uint_as_float(y[r]), __uint_as_float(y[r + 1])));
+                            const uint32_t o2 = pack_bf16x2(o.x, o.y);
+                            if (whole || i + r < n) *out = static_cast<uint16_t>(o2);
+                            out += p.ld_out;
+                            if (whole || i + r + 1 < n) *out = static_cast<uint16_t>(o2 >> 16);
+                            out += p.ld_out;
+                        }
                     }
-                }
+                };
+                if (n == C) store(std::true_type{});
+                else store(std::false_type{});
             }
         }
     } else {
@@ -886,10 +955,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 tc::fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < K / 16; k++) {
-                        const uint64_t d = desc_k(at + (k / 4) * Smem::HALF + (k % 4) * 32);
-                        tc::mma_f16(tmem + T_G + g * 64, d, d, idesc(C), k > 0);
-                    }
+                    for (int k = 0; k < K / 16; k++)
+                        mma_gram(tmem + T_G + g * 64, desc_k(at + (k / 4) * Smem::HALF + (k % 4) * 32), idesc(C), k > 0);
                     tc::commit(g_done(g));
                 }
                 __syncwarp();
