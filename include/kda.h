@@ -87,7 +87,8 @@ extern "C" {
                                      met a page id outside [0, num_pages); those tokens' slots are -1 */
 #define KDA_ERRFLAG_LENGTHS 16u   /* bit 4: kda_batch_maps met a negative or too large length (the request
                                      counts as empty) or more tokens than num_tokens (cut off), or
-                                     kda_gdn_chunk_prefill a sequence that is no range of the rows */
+                                     kda_gdn_chunk_prefill a sequence that is no range of the rows
+                                     (counts as empty) */
 
 /* Element types of the calls that take more than one (kda_norm_quant, kda_fp8_matmul). */
 #define KDA_BF16 0
@@ -371,8 +372,7 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
  *   o_t   = S_t^T q^                                                (V, bf16 out)
  * mixed_qkv: bf16 [N, ld_qkv], row t = [ q (Hk*K) | k (Hk*K) | v (Hv*V) ]; raw_g and raw_beta: bf16 [N, ld], Hv used;
  * out: bf16 [N, ld_out], Hv*V written; the state pool holds [Hv][K][V] per slot. Alignment, slots, the null slot, error
- * bits and sizes are those of the calls above with H = Hv. All three calls can be captured in a CUDA graph, and none
- * uses a workspace. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
+ * bits and sizes are those of the calls above with H = Hv. All three calls can be captured in a CUDA graph. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
  * several tokens); values of any magnitude that fp32 holds are accepted.
  */
 typedef struct kda_gdn_heads {
@@ -403,11 +403,18 @@ int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_
  * kda_batch_maps'): lengths may differ from one graph replay to the next. A pair that is no range of the rows
  * (negative, decreasing, past num_rows) counts as an empty sequence and sets KDA_ERRFLAG_LENGTHS. Rows of no sequence
  * are left as they were; the slot of an empty sequence is left untouched (one >= num_slots is still flagged).
+ * Ranges may not share rows. `workspace` (device, 256-byte aligned) must hold
+ * kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, heads) bytes, about 21 KB per 64 rows and value head; its contents are
+ * scratch between calls, and calls that share one (two captured graphs, too) must not overlap on the device. It may be NULL
+ * where that is 0 (K = 32). K of 64 and 128 with mixed_qkv 16-byte aligned and ld_qkv a multiple of 8 take the tensor cores
+ * in chunks of 64 rows; other layouts, and K = 32, blocks of 16 rows that are several times slower.
+ * A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT; what it was to give is not written.
  */
+size_t kda_gdn_chunk_prefill_workspace_bytes(int64_t num_rows, int64_t num_seqs, const kda_gdn_heads *heads);
 int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
                           const uint16_t *raw_beta, int64_t ld_beta, const int32_t *cu_seqlens, int64_t num_seqs,
-                          int64_t num_rows, const kda_gdn_heads *heads, const kda_state *state, uint16_t *out,
-                          int64_t ld_out, uint32_t *err_flags, void *stream);
+                          int64_t num_rows, const kda_gdn_heads *heads, const kda_state *state, void *workspace,
+                          size_t workspace_bytes, uint16_t *out, int64_t ld_out, uint32_t *err_flags, void *stream);
 
 /*
  * The calls below are what a layer's step does around the recurrence: the batch's maps,

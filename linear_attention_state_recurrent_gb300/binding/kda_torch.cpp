@@ -324,19 +324,19 @@ bool rows_of(const Tensor &t, const char *name, ScalarType type, int64_t rows, i
 }
 
 // (mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads, scale, l2_eps,
-//  null_slot, out, err_flags, stream) -> out. tokens: rows per request, 0 for decode; cu_seqlens: the prefill's, else None;
+//  null_slot, out, err_flags, stream, workspace) -> out. tokens: rows per request, 0 for decode; cu_seqlens: the prefill's, else None;
 // num_k_heads, scale: None for one key head per value head and K^-1/2
 PyObject *gdn(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    const Tensor *x, *g, *b, *A, *dt, *pool, *idx, *cu, *out;
+    const Tensor *x, *g, *b, *A, *dt, *pool, *idx, *cu, *out, *ws;
     int64_t tokens, null_slot;
     double scale = 0, eps;
-    if (!count(n, 16) || !tensor(a[0], "mixed_qkv", false, &x) || !tensor(a[1], "raw_g", false, &g) || !tensor(a[2], "raw_beta", false, &b) ||
+    if (!count(n, 17) || !tensor(a[0], "mixed_qkv", false, &x) || !tensor(a[1], "raw_g", false, &g) || !tensor(a[2], "raw_beta", false, &b) ||
         !tensor(a[3], "A_log", false, &A) || !tensor(a[4], "dt_bias", true, &dt) || !tensor(a[5], "initial_state", false, &pool) ||
         !tensor(a[6], "state_indices", false, &idx) || !integer(a[7], &tokens) || !tensor(a[8], "cu_seqlens", true, &cu) ||
         (a[10] != Py_None && !number(a[10], &scale)) || !number(a[11], &eps) || !integer(a[12], &null_slot) ||
-        !tensor(a[13], "out", true, &out))
+        !tensor(a[13], "out", true, &out) || !tensor(a[16], "workspace", true, &ws))
         return nullptr;
     const ScalarType H = ScalarType::BFloat16, F = ScalarType::Float;
     if (pool->scalar_type() != F || pool->dim() != 4) return refuse("initial_state must be fp32 [num_slots, H, K, V]");
@@ -369,10 +369,11 @@ PyObject *gdn(PyObject *, PyObject *const *a, Py_ssize_t n)
     void *stream;
     if (!error_word(a[14], x, &err) || !stream_of(a[15], *x, &stream)) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
-    Tensor made;
-    if (!out) {   // it belongs to the stream that the kernel runs on
-        c10::cuda::OptionalCUDAStreamGuard on;
-        if (a[15] != Py_None) on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), x->device().index()));
+    // what is allocated below belongs to the stream that the kernels run on
+    c10::cuda::OptionalCUDAStreamGuard on;
+    if (a[15] != Py_None) on.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), x->device().index()));
+    Tensor made, made_ws;
+    if (!out) {
         made = at::empty({N, Hv * V}, x->options());
         out = &made;
     }
@@ -382,13 +383,24 @@ PyObject *gdn(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int64_t slot_stride = pool->size(0) > 1 ? pool->stride(0) : Hv * K * V;
     const kda_state state = {static_cast<float *>(pool->data_ptr()), pool->size(0), slot_stride, static_cast<const int32_t *>(idx->data_ptr()),
                              entries > 1 ? idx->stride(0) : 1, static_cast<int32_t>(null_slot)};
+    size_t ws_bytes = 0;
+    if (cu) {
+        const size_t need = kda_gdn_chunk_prefill_workspace_bytes(N, entries, &heads);
+        if (ws && !(on_device(*ws, "workspace", x))) return nullptr;
+        if (ws && !ws->is_contiguous()) return refuse("workspace must be contiguous");
+        if (need > 0 && (!ws || ws->nbytes() < need)) {
+            made_ws = at::empty({static_cast<int64_t>(need)}, x->options().dtype(ScalarType::Byte));
+            ws = &made_ws;
+        }
+        if (ws) ws_bytes = ws->nbytes();
+    }
     auto u16 = [](const Tensor *t) { return static_cast<uint16_t *>(t->data_ptr()); };
     int status = KDA_OK;
     if (N == 0 && !cu) {   // nothing to do, and no rows to point to
     } else if (cu) {
         if (N > 0)
             status = kda_gdn_chunk_prefill(u16(x), ld_x, u16(g), ld_g, u16(b), ld_b, static_cast<const int32_t *>(cu->data_ptr()), entries, N,
-                                           &heads, &state, u16(out), ld_out, err, stream);
+                                           &heads, &state, ws ? ws->data_ptr() : nullptr, ws_bytes, u16(out), ld_out, err, stream);
     } else if (tokens == 0) {
         status = kda_gdn_decode(u16(x), ld_x, u16(g), ld_g, u16(b), ld_b, N, &heads, &state, u16(out), ld_out, err, stream);
     } else {

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(128, K == 128 ? 12 : 8) decode_kernel(GdnParam
     const uint16_t *vp = row + 2 * HK + static_cast<int64_t>(h) * V + j0;
     const float vv[4] = {bf16_to_f32(vp[0]), bf16_to_f32(vp[1]), bf16_to_f32(vp[2]), bf16_to_f32(vp[3])};
     const float beta = sigmoid_f(bf16_to_f32(p.rb[e * p.ld_beta + h]));
-    const float alpha = expf(log_decay(p, e, h, expf(__ldg(p.A_log + h)), p.dt_bias ? __ldg(p.dt_bias + h) : 0.f));
+    const float alpha = expf(log_decay(p, e, h, expf(p.A_log[h]), p.dt_bias ? p.dt_bias[h] : 0.f));
     if (tid < K) {
         uint32_t kq = 0;
 #pragma unroll
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
     const int j0 = warp * 32 + g * 4;                     // this thread's four value columns
     int64_t row0 = e * T, row1 = row0 + T;
     if (cu) {
-        row0 = __ldg(cu + e);
-        row1 = __ldg(cu + e + 1);
+        row0 = cu[e];
+        row1 = cu[e + 1];
         if (row0 < 0 || row1 < row0 || row1 > rows) {     // not a range of the rows: counts as empty
             if (tid == 0 && p.err) atomicOr(p.err, kErrLengths);
             row1 = row0;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
         }
 
     const int64_t HK = static_cast<int64_t>(p.Hk) * K;
-    const float expA = expf(__ldg(p.A_log + h)), dtb = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+    const float expA = expf(p.A_log[h]), dtb = p.dt_bias ? p.dt_bias[h] : 0.f;
     for (int64_t r0 = row0; r0 < row1; r0 += TB) {
         const int n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
         const uint16_t *in = p.qkv + r0 * p.ld_qkv;

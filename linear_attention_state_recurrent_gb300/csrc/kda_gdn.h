@@ -1,6 +1,7 @@
 // Internal parameters and launchers of the gated delta rule with one decay per head, shared by its entry points and kernels.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -26,8 +27,9 @@ cudaError_t launch_gdn_decode(const GdnParams &p, int K, int V, int64_t num_seqs
 cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32_t *cu, int64_t rows, int64_t num_entries,
                             cudaStream_t stream);
 
-// The rows [cu[e], cu[e + 1]) of `rows` packed ones per sequence, in chunks.
-cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs,
+// The rows [cu[e], cu[e + 1]) of `rows` packed ones per sequence, in chunks. Bytes of workspace, and the launches.
+size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K);
+cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs, void *workspace,
                                cudaStream_t stream);
 
 }  // namespace kda

@@ -58,6 +58,16 @@ int check(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int6
     return KDA_OK;
 }
 
+// What a prefill's launches count in 32 bits: rows (a chunk past the last one too), and chunks times heads.
+int check_size(int64_t rows, int64_t seqs, int64_t Hv)
+{
+    if (rows < 0) return invalid("num_rows must be >= 0");
+    if (rows > INT32_MAX - 64) return set_error(KDA_ERR_UNSUPPORTED, "num_rows must be below 2^31 - 64 (got %lld)", (long long)rows);
+    if (rows / 64 + seqs > INT32_MAX / Hv)
+        return set_error(KDA_ERR_UNSUPPORTED, "%lld rows x %lld heads exceed one launch: split the call", (long long)rows, (long long)Hv);
+    return KDA_OK;
+}
+
 int done(cudaError_t e, const char *what)
 {
     return e == cudaSuccess ? set_error(KDA_OK, "%s", "") : set_error(KDA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -93,20 +103,34 @@ int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_
                 "kda_gdn_spec_verify launch");
 }
 
+size_t kda_gdn_chunk_prefill_workspace_bytes(int64_t num_rows, int64_t num_seqs, const kda_gdn_heads *heads)
+{
+    if (!heads) return invalid("heads is NULL"), 0;
+    if (heads->Hk < 1 || heads->Hv < 1 || heads->Hv % heads->Hk != 0 || !supported_dim(heads->K) || !supported_dim(heads->V))
+        return invalid("Hv must be a multiple of Hk, K and V each 32, 64 or 128"), 0;
+    if (num_seqs < 0) return invalid("num_seqs must be >= 0"), 0;
+    if (check_size(num_rows, num_seqs, heads->Hv)) return 0;
+    set_error(KDA_OK, "%s", "");
+    return kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K);
+}
+
 int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
                           const uint16_t *raw_beta, int64_t ld_beta, const int32_t *cu_seqlens, int64_t num_seqs,
-                          int64_t num_rows, const kda_gdn_heads *heads, const kda_state *state, uint16_t *out,
-                          int64_t ld_out, uint32_t *err_flags, void *stream)
+                          int64_t num_rows, const kda_gdn_heads *heads, const kda_state *state, void *workspace,
+                          size_t workspace_bytes, uint16_t *out, int64_t ld_out, uint32_t *err_flags, void *stream)
 {
     kda::GdnParams p;
     const int s = check(mixed_qkv, ld_qkv, raw_g, ld_g, raw_beta, ld_beta, num_seqs, heads, state, out, ld_out, err_flags, &p);
     if (s) return s;
     if (!cu_seqlens || !aligned(cu_seqlens, 4)) return invalid("cu_seqlens must be non-NULL and 4-byte aligned");
-    if (num_rows < 0) return invalid("num_rows must be >= 0");
-    if (num_rows > INT32_MAX - 64)   // a chunk past the last row still has a 32-bit row number
-        return set_error(KDA_ERR_UNSUPPORTED, "num_rows must be below 2^31 - 64 (got %lld)", (long long)num_rows);
+    const int r = check_size(num_rows, num_seqs, heads->Hv);
+    if (r) return r;
     if (num_seqs == 0 || num_rows == 0) return set_error(KDA_OK, "%s", "");
-    return done(kda::launch_gdn_prefill(p, heads->K, heads->V, cu_seqlens, num_rows, num_seqs, static_cast<cudaStream_t>(stream)),
+    const size_t need = kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return set_error(KDA_ERR_WORKSPACE, "kda_gdn_chunk_prefill needs a 256-byte aligned workspace of %zu bytes (got %zu)", need,
+                         workspace ? workspace_bytes : static_cast<size_t>(0));
+    return done(kda::launch_gdn_prefill(p, heads->K, heads->V, cu_seqlens, num_rows, num_seqs, workspace, static_cast<cudaStream_t>(stream)),
                 "kda_gdn_chunk_prefill launch");
 }
 

@@ -2,16 +2,13 @@
 //
 // With b the running log-decay inside a chunk, D[r, i] = e^{b_r - b_i}, A[r, i] = beta_r (k^_r . k^_i) D[r, i] for
 // i < r and T = (I + A)^-1, a chunk is
-//   Y = V - e^b (K^ S),   U = T diag(beta) Y,   O = e^b (Q^ S) + (Q^ K^^T * D, i <= r) U,   S <- e^{b_n} S + (K^ e^{b_n - b})^T U
+//   Y = V - e^b (K^ S),   U = T diag(beta) Y,   O = e^b (Q^ S) + W U,  W = Q^ K^^T * D (i <= r),   S <- e^{b_n} S + (K^ e^{b_n - b})^T U
 // A decay that is the same in all channels leaves the tiles of q and k as they are in memory: every product takes them
-// raw, as TMA brings them, and norms and decays are factors of rows and columns of the products. So nothing but T and the
-// query-key products is computed ahead, and both beside the chain of chunks, in the same CTA: no workspace, one launch.
-//
-// One CTA per SM, persistent; it walks (sequence, value head) chains, longest sequences first. Its warps:
-//   0 - 7    the chain: S in registers (fp32), transposed: a thread has one value column and half of the channels
-//   8 - 15   two groups that take chunks in turn: decays, norms, T and the query-key products
-//   16 - 19  outputs
-//   20, 21   TMA; the chain's MMAs      22  the products K K^T and Q K^T
+// raw, as TMA brings them, and norms and decays are factors of rows and columns of the products. What the chunks need but for
+// S, T diag(beta) and W, is 21 KB a chunk and head (KDA's is 58 KB). Three launches:
+//   map_kernel    where each sequence's chunks are, from cu_seqlens on the device
+//   prep_kernel   T diag(beta), W and the row factors of every chunk at once: a CTA per chunk and key head, for all its value heads
+//   chain_kernel  one CTA per SM walks (sequence, value head) chains, longest sequences first, S in registers
 // The chain's products have value columns as rows (TMEM lanes), so that what depends on a token is a factor per column,
 // and their first operand is written to TMEM by the thread that has the values.
 // What enters the products is exact (q, k, v are bf16) or two bf16 terms, hi + lo = x to 2^-18.
@@ -32,61 +29,52 @@ namespace gdn {
 namespace {
 
 constexpr int C = 64;                                  // rows of a chunk
-constexpr int THREADS = 768;
-constexpr int STAGES = 3;                              // chunks of q and k in shared memory (and two of v, which the chain reads first of all)
-constexpr int SCALARS = 8;                             // chunks of row factors: the outputs may still read those of chunk c
-                                                       // when those of c + 4 are written
 constexpr int ORDER = 256;                             // sequences that are sorted by length
 constexpr int BLK = 16 * 20;                           // floats of a 16 x 16 block, rows 20 apart: no bank conflicts
-// registers: 80 a thread at launch, 61,440 in all; 256 x 136 + 256 x 64 + 2 x 128 x 40 = 61,440
-constexpr int REG_CHAIN = 136, REG_PREP = 64, REG_OUT = 40, REG_REST = 40;
 
-// columns of tensor memory
-constexpr uint32_t T_S = 0;      // first operand of K S and Q S: the halves of the channels one after the other, each hi | lo; then the state's increment
-constexpr uint32_t T_Y = 128;    // K S; then Y and later U (scaled), by halves of the rows, each hi | lo
-constexpr uint32_t T_U = 192;    // U; then as an operand, by halves of the rows, each hi | lo
-constexpr uint32_t T_O = 256;    // Q S and (Q K^T * D) U
-constexpr uint32_t T_G = 384;    // K K^T | Q K^T, one for each of the two groups
-
-struct Smem {
-    static constexpr int HALF = 2 * C * 128;           // 64 channels of the chunk's keys, then of its queries
-    static constexpr int STAGE = 2 * HALF, V = STAGES * STAGE, V_STAGE = C * 256;
-    static constexpr int T = V + 2 * V_STAGE;          // per group T diag(beta), hi and lo, and the query-key products, hi and lo
-    static constexpr int TILE = C * 128, GROUP = 4 * TILE;
-    static constexpr int BLOCKS = T + 2 * GROUP;       // per group the ten blocks of A and T
-    static constexpr int ROWS = BLOCKS + 2 * 10 * BLK * 4;
-    static constexpr int SET = 3 * C + 4;              // floats: ys, us, qs, and gamma
-    static constexpr int COLS = ROWS + SCALARS * SET * 4;   // per group: b hi, b lo, beta, and of the keys b lo less the norm's logarithm and e^{p - b} times the norm
-    static constexpr int SORT = COLS + 2 * 5 * C * 4;
-    static constexpr int BARS = SORT + ORDER * 2;
-    static constexpr int NBARS = 2 * STAGES + 26;
-    static constexpr int END = BARS + NBARS * 8 + 16;
+// A chunk and head's record. Of the 64 x 64 matrices T diag(beta) and W, hi and lo each, the blocks on and below the diagonal: a panel
+// for every 16 columns with the rows from 16 k on, in the order the MMAs read without a swizzle (8 rows of 16 bytes follow each
+// other, the next 8 columns 128 bytes on, the next 8 rows 256). Then the row factors: e^b |k|^-1, e^{b_n - b} |k|^-1,
+// scale e^b |q|^-1 (64 floats each) and e^{b_n}.
+struct Rec {
+    static constexpr int MATRIX = 5120, T = 0, W = 2 * MATRIX, ROWS = 4 * MATRIX, BYTES = ROWS + (3 * C + 4) * 4, STAGE = 21376;
+    __device__ static constexpr int panel(int k) { return k * 2048 - k * (k - 1) * 256; }
 };
-static_assert(Smem::END <= 232448, "shared memory of a CTA");
+static_assert(Rec::BYTES % 16 == 0 && Rec::BYTES <= Rec::STAGE && Rec::STAGE % 128 == 0, "");
 
 struct Args {
     GdnParams p;
     const int32_t *cu;
-    int rows, num_seqs;
+    int rows, num_seqs, V;
+    int chunks;                                        // as many as there can be: rows / 64 + num_seqs
+    int32_t *first;                                    // [num_seqs + 1] each sequence's first chunk, and their number
+    int2 *where;                                       // [chunks] a chunk's first row, and its rows
+    unsigned char *records;                            // [chunks][Hv]
 };
+
+constexpr int HALF = 2 * C * 128;                      // in shared memory, 64 channels of the chunk's keys, then of its queries
 
 // Matrix descriptors with the 128-byte swizzle, groups of 8 rows at 1024 bytes: the low words (the high one is the same for all).
 // K-major: a row of the operand is 128 bytes.
 __device__ __forceinline__ uint32_t desc_k(uint32_t at) { return (1u << 16) | (at >> 4); }
 // The same bytes with the 128-byte rows along the inner axis (K^T from the tile of K): 64 columns, the next 64 at HALF.
-__device__ __forceinline__ uint32_t desc_mn(uint32_t at) { return (static_cast<uint32_t>(Smem::HALF >> 4) << 16) | (at >> 4); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t at) { return (static_cast<uint32_t>(HALF >> 4) << 16) | (at >> 4); }
 constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+// A panel of a record: no swizzle.
+__device__ __forceinline__ uint32_t desc_panel(uint32_t at) { return ((128u >> 4) << 16) | (at >> 4); }
+constexpr uint32_t PANEL_HIGH = (256u >> 4) | (1u << 14);
 // bf16 operands, fp32 sums, 128 rows; `mn`: the second operand is stored along its columns
 constexpr uint32_t idesc(int n, bool mn = false)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 // d (+)= a b^T, 16 of the inner axis; a in tensor memory
+template <uint32_t HIGH = DESC_HIGH>
 __device__ __forceinline__ void mma_t(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add)
 {
     asm volatile("{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
                  " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n"
-                 :: "r"(d), "r"(a), "r"(b), "n"(DESC_HIGH), "r"(id), "r"(add ? 1u : 0u));
+                 :: "r"(d), "r"(a), "r"(b), "n"(HIGH), "r"(id), "r"(add ? 1u : 0u));
 }
 // The same with both operands from the same place in shared memory.
 __device__ __forceinline__ void mma_gram(uint32_t d, uint32_t ab, uint32_t id, bool add)
@@ -112,35 +100,12 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
-}
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N])
-{
-    static_assert(N == 16 || N == 32, "");
-    if constexpr (N == 16)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                       "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(taddr));
-    else
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                       "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-                       "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-                       "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                     : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
@@ -169,35 +134,47 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const Tf32<4> &a, const
     mma_tf32(d, a.hi, b.hi);
 }
 
-// The chunks of this CTA's chains, one after the other, the same for every warp.
-struct Walk {
-    const Args *a;
-    const uint16_t *order;
-    int item, total;            // chains: sequence (longest first) x value head
-    int row, left, h;           // of the current chunk: its first row, the chain's rows from there on, the value head
-    int seq;
+// The bounds of a sequence; a pair that is no range of the rows has none. *bad: error bits.
+__device__ __forceinline__ int2 range(const Args &a, int seq, uint32_t *bad)
+{
+    const int row = a.cu[seq], end = a.cu[seq + 1];
+    if (row >= 0 && end >= row && end <= a.rows) return make_int2(row, end - row);
+    *bad |= kErrLengths;
+    return make_int2(row, 0);
+}
 
-    __device__ __forceinline__ Walk(const Args &args, const uint16_t *sorted)
-        : a(&args), order(sorted), item(blockIdx.x), total(args.num_seqs * args.p.Hv) {}
+// The chunks of this CTA's chains, one after the other, the same for every warp. A chain: a sequence (longest first), a value head
+// and a slice of its columns.
+struct Walk {
+    const Args &a;
+    const uint16_t *order;
+    int item, total, slices;
+    int row, left, h, slice;    // of the current chunk: its first row, the chain's rows from there on
+    int seq, chunk;
+
+    __device__ __forceinline__ Walk(const Args &args, const uint16_t *sorted, int vs)
+        : a(args), order(sorted), item(blockIdx.x), slices(args.V / vs) { total = args.num_seqs * args.p.Hv * slices; }
     // CTA i's chains are i, 2 G - 1 - i, 2 G + i, ..: the longest with the shortest
     __device__ __forceinline__ void advance()
     {
         const int g = gridDim.x, at = item % g;
         item += 2 * (g - 1 - at) + 1;
     }
-    // The chain at `item`: its rows, or none (an empty or bad range, a slot past the pool). *bad: error bits.
+    // The chain at `item`: whether it has rows (and a slot). *bad: error bits; *all: its rows whatever its slot.
     __device__ __forceinline__ bool chain(uint32_t *bad = nullptr, int *all = nullptr)
     {
-        const int s = item / a->p.Hv;
-        h = item - s * a->p.Hv;
-        seq = a->num_seqs <= ORDER ? order[s] : s;
-        row = __ldg(a->cu + seq);
-        const int end = __ldg(a->cu + seq + 1);
-        left = end - row;
+        const int per = a.p.Hv * slices, s = item / per, in = item - s * per;
+        h = in / slices;
+        slice = in - h * slices;
+        seq = a.num_seqs <= ORDER ? order[s] : s;
         uint32_t e = 0;
-        if (row < 0 || end < row || end > a->rows) { left = 0; e |= kErrLengths; }
+        const int2 x = range(a, seq, &e);
+        row = x.x;
+        left = x.y;
+        chunk = a.first[seq];
         if (all) *all = left;
-        if (load_slot(a->p, seq) >= a->p.num_slots) { left = 0; e |= kErrSlotRange; }
+        if (left > 0 && (left - 1) / C >= a.chunks - chunk) { left = 0; e |= kErrLengths; }   // ranges that overlap: more chunks than rows make
+        if (load_slot(a.p, seq) >= a.p.num_slots) { left = 0; e |= kErrSlotRange; }
         if (bad) *bad = e;
         return left > 0;
     }
@@ -214,6 +191,7 @@ struct Walk {
     {
         row += C;
         left -= C;
+        chunk++;
         if (left > 0) return true;
         advance();
         return begin();
@@ -253,66 +231,441 @@ struct Waiter {
 
 __device__ __forceinline__ constexpr int block_at(int a, int b) { return (a * (a + 1) / 2 + b) * BLK; }
 
-template <int NH, int V>
-__global__ void __launch_bounds__(THREADS, 1)
-chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a)
+// One CTA: every sequence's first chunk (their number is not above rows / 64 + num_seqs where the ranges do not overlap; what would
+// pass it is left out) and each chunk's rows. Error bits are the chain's.
+__global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args a)
 {
-    constexpr int K = 64 * NH, KP = K / 2, VW = V / 32;
+    __shared__ int sums[32];
+    __shared__ int base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) base = 0;
+    pdl_wait_then_release();   // no global read before this
+    __syncthreads();
+    for (int s0 = 0; s0 < a.num_seqs; s0 += 1024) {
+        uint32_t bad = 0;
+        const int s = s0 + tid;
+        const int2 x = s < a.num_seqs ? range(a, s, &bad) : make_int2(0, 0);
+        const int n = (x.y + C - 1) / C;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int before = base, all = 0;
+        for (int w = 0; w < 32; w++) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
+        }
+        const int first = before + sum - n;
+        if (s < a.num_seqs) a.first[s] = first;
+        // a warp fills its sequences' chunks together
+        for (int l = 0; l < 32; l++) {
+            const int f = __shfl_sync(0xffffffffu, first, l), row = __shfl_sync(0xffffffffu, x.x, l), left = __shfl_sync(0xffffffffu, x.y, l);
+            for (int i = lane; i * C < left; i += 32)
+                if (f + i < a.chunks) a.where[f + i] = make_int2(row + i * C, left - i * C < C ? left - i * C : C);
+        }
+        __syncthreads();
+        if (tid == 0) base += all;
+        __syncthreads();
+    }
+    if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;
+}
+
+// T diag(beta), W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
+// t - 64 of Q K^T, which one product of 128 x 64 gives. Four CTAs an SM: a warp's path through the inverse is bound by its latencies.
+template <int NH>
+__global__ void __launch_bounds__(128, 4) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
+{
+    constexpr int K = 64 * NH;
+    extern __shared__ __align__(1024) unsigned char sm[];                     // the tiles of q and k
+    __shared__ __align__(16) float blocks[10 * BLK];                          // the blocks of A, then of T, on and below the diagonal
+    __shared__ __align__(16) float cols[5 * C];   // b hi, b lo, beta, and of the keys b lo less the norm's logarithm, and e^{p - b} times the norm
+    __shared__ uint64_t bars[2];
+    __shared__ uint32_t tmem_at;
+    const uint32_t s0 = tc::smem_addr(sm), full = tc::smem_addr(&bars[0]), g_done = tc::smem_addr(&bars[1]);
+    const int t = threadIdx.x, lane = t & 31, pw = t >> 5, r = t & 63;
+    const bool query = t >= 64;
+    const GdnParams &p = a.p;
+    const int chunk = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, per = p.Hv / p.Hk;
+    if (t == 0) {
+        tc::mbar_init(full, 1);
+        tc::mbar_init(g_done, 1);
+        tc::prefetch_tensormap(&tm_qk);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // no global read before this
+    if (chunk >= a.first[a.num_seqs]) return;
+    const int2 at = a.where[chunk];
+    const int n = at.y;
+    if (pw == 0) tc::tmem_alloc<64>(tc::smem_addr(&tmem_at));
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = tmem_at;
+    if (t == 0) {
+        tc::mbar_expect_tx(full, NH * HALF);
+#pragma unroll
+        for (int hf = 0; hf < NH; hf++) {
+            tc::tma_load_2d(s0 + hf * HALF, &tm_qk, (p.Hk + hk) * K + 64 * hf, at.x, full);
+            tc::tma_load_2d(s0 + hf * HALF + C * 128, &tm_qk, hk * K + 64 * hf, at.x, full);
+        }
+    }
+    // raw_g (warp 0) and raw_beta (warp 1) of rows 2 lane, 2 lane + 1
+    float in0 = 0.f, in1 = 0.f, rate = 0.f, dtb = 0.f;
+    auto fetch = [&](int h) {
+        if (pw < 2) {
+            const uint16_t *from = pw == 0 ? p.rg : p.rb;
+            const int64_t ld = pw == 0 ? p.ld_g : p.ld_beta, row = static_cast<int64_t>(at.x) + 2 * lane;
+            if (2 * lane < n) in0 = bf16_to_f32(from[row * ld + h]);
+            if (2 * lane + 1 < n) in1 = bf16_to_f32(from[(row + 1) * ld + h]);
+            if (pw == 0) {
+                rate = p.A_log[h];
+                dtb = p.dt_bias ? p.dt_bias[h] : 0.f;
+            }
+        }
+    };
+    fetch(hk * per);
+    bool ok = tc::mbar_wait(full, 0);
+    if (pw == 0) {
+        if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < K / 16; k++) mma_gram(tmem, desc_k(s0 + (k / 4) * HALF + (k % 4) * 32), idesc(C), k > 0);
+            tc::commit(g_done);
+        }
+        __syncwarp();
+    }
+    // the norm of this thread's row
+    float norm = 0.f;
+    if (r < n) {
+        float2 sum = make_float2(0.f, 0.f);
+        const unsigned char *own = sm + t * 128;
+#pragma unroll
+        for (int hf = 0; hf < NH; hf++)
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(own + hf * HALF + ((x ^ (t & 7)) << 4));
+                const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    const float2 f = make_float2(__uint_as_float(qq[y] << 16), __uint_as_float(qq[y] & 0xffff0000u));
+                    sum = ffma2(f, f, sum);
+                }
+            }
+        norm = rsqrtf(sum.x + sum.y + p.eps);
+    }
+    ok &= tc::mbar_wait(g_done, 0);
+    tc::fence_after_sync();
+    for (int h = hk * per; h < (hk + 1) * per; h++) {
+        unsigned char *rec = a.records + (static_cast<int64_t>(chunk) * p.Hv + h) * Rec::BYTES;
+        float *set = reinterpret_cast<float *>(rec + Rec::ROWS);
+        if (pw == 0) {                                                    // the running decay, in units of log 2
+            rate = expf(rate) * -1.44269504f;
+            const double g0 = 2 * lane < n ? rate * softplus_f(in0 + dtb) : 0.f, g1 = 2 * lane + 1 < n ? rate * softplus_f(in1 + dtb) : 0.f;
+            double b = g0 + g1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, b, o);
+                if (lane >= o) b += x;
+            }
+            const double b0_ = b - g1;
+            const float h0 = static_cast<float>(b0_), h1 = static_cast<float>(b);
+            *reinterpret_cast<float2 *>(cols + 2 * lane) = make_float2(h0, h1);
+            *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(static_cast<float>(b0_ - h0), static_cast<float>(b - h1));
+        } else if (pw == 1) {
+            *reinterpret_cast<float2 *>(cols + 2 * C + 2 * lane) =
+                make_float2(2 * lane < n ? sigmoid_f(in0) : 0.f, 2 * lane + 1 < n ? sigmoid_f(in1) : 0.f);
+        }
+        if (h + 1 < (hk + 1) * per) fetch(h + 1);
+        __syncthreads();
+        const float b_hi = cols[r], b_lo = cols[C + r];
+        const float scale = (query ? p.scale : cols[2 * C + r]) * norm;
+        if (!query) {
+            const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1];
+            set[r] = ex2(b_hi + b_lo) * norm;
+            set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * norm;
+            if (r == 0) set[3 * C] = ex2(e_hi + e_lo);
+            cols[3 * C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
+            cols[4 * C + r] = ex2((cols[r | 15] - b_hi) + (cols[C + (r | 15)] - b_lo)) * norm;
+        } else {
+            set[2 * C + r] = p.scale * ex2(b_hi + b_lo) * norm;
+        }
+        __syncthreads();
+        // row r of A (its blocks up to the diagonal's), or of W
+        const int low = (pw & 1) * 2;                                         // the first block with a diagonal in the warp's rows
+        const uint32_t tg = tmem + (static_cast<uint32_t>(pw * 32) << 16);
+        float2 d[8];
+        auto put = [&](int bl) {
+            if (bl > r >> 4) return;
+            if (query) {
+                unsigned char *to = rec + Rec::W + Rec::panel(bl) + ((r - 16 * bl) >> 3) * 256 + (r & 7) * 16;
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) split2(d[4 * y + i].x, d[4 * y + i].y, hi[i], lo[i]);
+                    *reinterpret_cast<uint4 *>(to + y * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(to + Rec::MATRIX + y * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            } else {
+                float *to = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    *reinterpret_cast<float4 *>(to + 4 * i) = make_float4(d[2 * i].x, d[2 * i].y, d[2 * i + 1].x, d[2 * i + 1].y);
+            }
+        };
+        // blocks left of it: e^{b_r - b_i} = e^{b_r - p} e^{p - b_i}, p the sum at the block's last row: neither is above 1
+#pragma unroll 1
+        for (int bl = 0; bl < low; bl++) {
+            uint32_t x[16];
+            tmem_ld(tg + bl * 16, x);
+            const float f = ex2((b_hi - cols[bl * 16 + 15]) + (b_lo - cols[C + bl * 16 + 15])) * scale;
+            const float2 f2 = make_float2(f, f);
+            tc::tmem_ld_wait();
+            if (r >= n) {                                                     // not a row of the chunk: whatever it held
+#pragma unroll
+                for (int i = 0; i < 16; i++) x[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float4 e = *reinterpret_cast<const float4 *>(cols + 4 * C + bl * 16 + 4 * i);
+                d[2 * i] = fmul2(fmul2(make_float2(e.x, e.y), f2), make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])));
+                d[2 * i + 1] = fmul2(fmul2(make_float2(e.z, e.w), f2), make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
+            }
+            put(bl);
+        }
+        // and the two with diagonals: entry by entry, the ones above it cut off
+        const int end = r < n ? r + query : 0;
+        const float2 bh = make_float2(b_hi, b_hi), bl2 = make_float2(b_lo, b_lo), sc = make_float2(scale, scale);
+#pragma unroll 1
+        for (int bl = low; bl < low + 2; bl++) {
+            uint32_t x[16];
+            tmem_ld(tg + bl * 16, x);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float4 eh = *reinterpret_cast<const float4 *>(cols + bl * 16 + 4 * i);
+                const float4 el = *reinterpret_cast<const float4 *>(cols + 3 * C + bl * 16 + 4 * i);
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    const float2 e = fadd2(fsub2(bh, y ? make_float2(eh.z, eh.w) : make_float2(eh.x, eh.y)),
+                                           fsub2(bl2, y ? make_float2(el.z, el.w) : make_float2(el.x, el.y)));
+                    const float2 v = fmul2(fmul2(make_float2(ex2(e.x), ex2(e.y)), sc),
+                                           make_float2(__uint_as_float(x[4 * i + 2 * y]), __uint_as_float(x[4 * i + 2 * y + 1])));
+                    const int col = bl * 16 + 4 * i + 2 * y;
+                    d[2 * i + y] = make_float2(col < end ? v.x : 0.f, col + 1 < end ? v.y : 0.f);
+                }
+            }
+            put(bl);
+        }
+        __syncthreads();
+        const int gq = lane >> 2, tq = lane & 3;
+        // T: the diagonal blocks, a warp each, by substitution; a lane has a column (lanes 16 and up the same again)
+        {
+            const float *A = blocks + block_at(pw, pw);
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                float y[4] = {i == (lane & 15) ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < i; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(A + i * 20 + k);
+                    y[0] = fmaf(-f.x, x[k], y[0]);
+                    if (k + 1 < i) y[1] = fmaf(-f.y, x[k + 1], y[1]);
+                    if (k + 2 < i) y[2] = fmaf(-f.z, x[k + 2], y[2]);
+                    if (k + 3 < i) y[3] = fmaf(-f.w, x[k + 3], y[3]);
+                }
+                x[i] = (y[0] + y[1]) + (y[2] + y[3]);
+            }
+            __syncwarp();
+            if (lane < 16)
+#pragma unroll
+                for (int i = 0; i < 16; i++) blocks[block_at(pw, pw) + i * 20 + lane] = x[i];
+        }
+        __syncthreads();
+        // the blocks below them: [[X, 0], [-Y A X, Y]], first of 32 rows, then of all 64. X^T A^T is the first operand of the
+        // second product as it leaves the first one: column 2t of a tile counts as k = t, 2t + 1 as k = t + 4.
+        {
+            const int pr = pw >> 1, hf = pw & 1;
+            const float *X = blocks + block_at(2 * pr, 2 * pr), *Y = blocks + block_at(2 * pr + 1, 2 * pr + 1);
+            float *A = blocks + block_at(2 * pr + 1, 2 * pr);
+            float xa[2][4] = {}, out[4] = {};
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                Tf32<4> fx;
+                fx.set(0, X[(8 * k + tq) * 20 + gq]);
+                fx.set(1, X[(8 * k + tq) * 20 + gq + 8]);
+                fx.set(2, X[(8 * k + tq + 4) * 20 + gq]);
+                fx.set(3, X[(8 * k + tq + 4) * 20 + gq + 8]);
+#pragma unroll
+                for (int m = 0; m < 2; m++) {
+                    Tf32<2> fa;
+                    fa.set(0, A[(8 * m + gq) * 20 + 8 * k + tq]);
+                    fa.set(1, A[(8 * m + gq) * 20 + 8 * k + tq + 4]);
+                    mma_split(xa[m], fx, fa);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 2; m++) {
+                Tf32<4> fx;
+                Tf32<2> fy;
+                fx.set(0, -xa[m][0]); fx.set(1, -xa[m][2]); fx.set(2, -xa[m][1]); fx.set(3, -xa[m][3]);
+                const float2 y = *reinterpret_cast<const float2 *>(Y + (8 * hf + gq) * 20 + 8 * m + 2 * tq);
+                fy.set(0, y.x);
+                fy.set(1, y.y);
+                mma_split(out, fx, fy);
+            }
+            __syncthreads();                                                       // A has been read
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const int col = gq + 8 * (x >> 1), row = 8 * hf + 2 * tq + (x & 1);
+                A[row * 20 + col] = out[x];
+            }
+        }
+        __syncthreads();
+        {
+            const int mt = pw >> 1, hf = pw & 1;                          // columns 16 mt .., rows 32 + 16 hf ..
+            float out[2][4] = {};
+#pragma unroll
+            for (int ib = 0; ib < 2; ib++) {
+                if (ib > hf) break;
+                float xa[2][4] = {};
+#pragma unroll
+                for (int kb = 0; kb < 2; kb++) {
+                    if (kb < mt) continue;
+                    const float *X = blocks + block_at(kb, mt), *A = blocks + block_at(2 + ib, kb);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        Tf32<4> fx;
+                        fx.set(0, X[(8 * k + tq) * 20 + gq]);
+                        fx.set(1, X[(8 * k + tq) * 20 + gq + 8]);
+                        fx.set(2, X[(8 * k + tq + 4) * 20 + gq]);
+                        fx.set(3, X[(8 * k + tq + 4) * 20 + gq + 8]);
+#pragma unroll
+                        for (int m = 0; m < 2; m++) {
+                            Tf32<2> fa;
+                            fa.set(0, A[(8 * m + gq) * 20 + 8 * k + tq]);
+                            fa.set(1, A[(8 * m + gq) * 20 + 8 * k + tq + 4]);
+                            mma_split(xa[m], fx, fa);
+                        }
+                    }
+                }
+                const float *Y = blocks + block_at(2 + hf, 2 + ib);
+#pragma unroll
+                for (int m = 0; m < 2; m++) {
+                    Tf32<4> fx;
+                    fx.set(0, -xa[m][0]); fx.set(1, -xa[m][2]); fx.set(2, -xa[m][1]); fx.set(3, -xa[m][3]);
+#pragma unroll
+                    for (int rt = 0; rt < 2; rt++) {
+                        Tf32<2> fy;
+                        const float2 y = *reinterpret_cast<const float2 *>(Y + (8 * rt + gq) * 20 + 8 * m + 2 * tq);
+                        fy.set(0, y.x);
+                        fy.set(1, y.y);
+                        mma_split(out[rt], fx, fy);
+                    }
+                }
+            }
+            __syncthreads();                                                       // A has been read
+            float *at = blocks + block_at(2 + hf, mt);
+#pragma unroll
+            for (int rt = 0; rt < 2; rt++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) at[(8 * rt + 2 * tq + (x & 1)) * 20 + gq + 8 * (x >> 1)] = out[rt][x];
+        }
+        __syncthreads();
+        // T diag(beta), hi and lo: half of row r
+#pragma unroll 1
+        for (int bl = t >> 6 << 1; bl <= r >> 4 && bl < (t >> 6 << 1) + 2; bl++) {
+            const float *from = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
+            unsigned char *to = rec + Rec::T + Rec::panel(bl) + ((r - 16 * bl) >> 3) * 256 + (r & 7) * 16;
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const float4 x = *reinterpret_cast<const float4 *>(from + 8 * y + 4 * i);
+                    const float4 e = *reinterpret_cast<const float4 *>(cols + 2 * C + bl * 16 + 8 * y + 4 * i);
+                    const float2 v0 = fmul2(make_float2(x.x, x.y), make_float2(e.x, e.y)), v1 = fmul2(make_float2(x.z, x.w), make_float2(e.z, e.w));
+                    split2(v0.x, v0.y, hi[2 * i], lo[2 * i]);
+                    split2(v1.x, v1.y, hi[2 * i + 1], lo[2 * i + 1]);
+                }
+                *reinterpret_cast<uint4 *>(to + y * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(to + Rec::MATRIX + y * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        __syncthreads();                                                      // blocks and columns are free again
+    }
+    if (!ok && p.err) atomicOr(p.err, kErrTimeout);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (pw == 0) tc::tmem_dealloc<64>(tmem);
+}
+// ---- the chains ---------------------------------------------------------------------------
+
+constexpr int THREADS = 768;       // warps 0 - 15 the chain, 16 - 19 outputs, 20 copies, 21 MMAs, 22 the rows behind a sequence's end
+constexpr int STAGES = 3;          // chunks in shared memory
+struct Smem {
+    static constexpr int QK = 2 * HALF, V = C * 256;
+    static constexpr int REC = QK + V, STAGE = QK + V + Rec::STAGE;
+    static constexpr int SORT = STAGES * STAGE, BARS = SORT + ORDER * 2, NBARS = 3 * STAGES + 9, END = BARS + NBARS * 8 + 16;
+};
+static_assert(Smem::STAGE % 128 == 0 && Smem::END <= 232448, "shared memory of a CTA");
+
+// columns of tensor memory
+constexpr uint32_t T_S = 0;      // first operand of K S and Q S: the quarters of the channels one after the other, each hi | lo; then the state's increment
+constexpr uint32_t T_Y = 128;    // K S; then Y, later U scaled, as operands, by quarters of the rows, each hi | lo
+constexpr uint32_t T_U = 192;    // U; then as an operand, the same way
+constexpr uint32_t T_O = 256;    // Q S and W U
+
+// Value columns VS at a time (a slice of V), a thread with one of them and a quarter of the channels, or of the rows.
+template <int NH, int VS>
+__global__ void __launch_bounds__(THREADS, 1)
+chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a)
+{
+    constexpr int K = 64 * NH, KP = K / 4, VW = VS / 32;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t s0 = tc::smem_addr(sm), b0 = s0 + Smem::BARS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // barriers
-    auto full = [&](int s) { return b0 + s * 8; };                          // q and k of a chunk have landed
-    auto empty = [&](int s) { return b0 + (STAGES + s) * 8; };              // and are no longer needed
-    const uint32_t bx = b0 + 2 * STAGES * 8;
-    const uint32_t s_ready = bx, ks_done = bx + 8, y_ready = bx + 16, u_ready = bx + 24, s_done = bx + 32, o_free = bx + 40;
-    auto u_done = [&](int g) { return bx + 48 + g * 8; };
-    auto o_done = [&](int g) { return bx + 64 + g * 8; };
-    auto t_ready = [&](int g) { return bx + 80 + g * 8; };
-    auto g_done = [&](int g) { return bx + 96 + g * 8; };
-    auto g_free = [&](int g) { return bx + 112 + g * 8; };
-    // a chunk's row factors are there: four of them, since those of c + 2 may be when the chain has yet to ask for those of c
-    auto scaled = [&](uint32_t c) { return bx + 128 + (c & 3) * 8; };
-    auto drained = [&](int i) { return bx + 160 + i * 8; };                 // the MMA warps' last commits
-    auto v_full = [&](int i) { return bx + 176 + i * 8; };
-    auto v_empty = [&](int i) { return bx + 192 + i * 8; };
+    auto full = [&](int s) { return b0 + s * 8; };                          // a chunk has landed
+    auto empty = [&](int s) { return b0 + (STAGES + s) * 8; };              // and is no longer needed
+    auto clean = [&](int s) { return b0 + (2 * STAGES + s) * 8; };          // its keys behind the sequence's end are zeros
+    const uint32_t bx = b0 + 3 * STAGES * 8;
+    const uint32_t s_ready = bx, ks_done = bx + 8, y_ready = bx + 16, u_done = bx + 24, u_ready = bx + 32, s_done = bx + 40, o_done = bx + 48,
+                   o_free = bx + 56, drained = bx + 64;
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(sm + Smem::BARS + Smem::NBARS * 8);   // tensor memory's base, whether a wait has given up
     uint16_t *order = reinterpret_cast<uint16_t *>(sm + Smem::SORT);
-    float *sets = reinterpret_cast<float *>(sm + Smem::ROWS);
     const GdnParams &p = a.p;
 
     if (tid == 0) {
-        for (int i = 0; i < STAGES; i++) { tc::mbar_init(full(i), 1); tc::mbar_init(empty(i), 1); }
-        tc::mbar_init(s_ready, 2 * VW);
-        tc::mbar_init(ks_done, 1);
-        tc::mbar_init(y_ready, 2 * VW);
-        tc::mbar_init(u_ready, 2 * VW);
-        tc::mbar_init(s_done, 1);
-        tc::mbar_init(o_free, VW);
-        for (int g = 0; g < 2; g++) {
-            tc::mbar_init(u_done(g), 1);
-            tc::mbar_init(o_done(g), 1);
-            tc::mbar_init(scaled(g), 4);
-            tc::mbar_init(scaled(g + 2), 4);
-            tc::mbar_init(drained(g), 1);
-            tc::mbar_init(v_full(g), 1);
-            tc::mbar_init(v_empty(g), 2 * VW);
-            tc::mbar_init(t_ready(g), 4);
-            tc::mbar_init(g_done(g), 1);
-            tc::mbar_init(g_free(g), 4);
+        for (int i = 0; i < STAGES; i++) {
+            tc::mbar_init(full(i), 1);
+            tc::mbar_init(empty(i), 1 + VW);
+            tc::mbar_init(clean(i), 1);
         }
+        tc::mbar_init(s_ready, 4 * VW);
+        tc::mbar_init(ks_done, 1);
+        tc::mbar_init(y_ready, 4 * VW);
+        tc::mbar_init(u_done, 1);
+        tc::mbar_init(u_ready, 4 * VW);
+        tc::mbar_init(s_done, 1);
+        tc::mbar_init(o_done, 1);
+        tc::mbar_init(o_free, VW);
+        tc::mbar_init(drained, 1);
         words[1] = 0;
         tc::prefetch_tensormap(&tm_qk);
         tc::prefetch_tensormap(&tm_v);
     }
-    // above T's diagonal nothing is ever written
-    for (int i = tid; i < 2 * Smem::GROUP / 16; i += THREADS) reinterpret_cast<uint4 *>(sm + Smem::T)[i] = make_uint4(0u, 0u, 0u, 0u);
-    tc::fence_proxy_async();
     asm volatile("griddepcontrol.wait;" ::: "memory");   // no global read before this
     // the sequences by falling length: each finds its place
     if (a.num_seqs <= ORDER) {
         int *len = reinterpret_cast<int *>(sm);           // the first stage's place
-        for (int i = tid; i < a.num_seqs; i += THREADS) len[i] = __ldg(a.cu + i + 1) - __ldg(a.cu + i);
+        for (int i = tid; i < a.num_seqs; i += THREADS) {
+            uint32_t bad = 0;
+            len[i] = range(a, i, &bad).y;
+        }
         __syncthreads();
         for (int i = tid; i < a.num_seqs; i += THREADS) {
             const int own = len[i];
@@ -329,504 +682,174 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = words[0];
     const Waiter wait{words + 1, p.err};
-    Walk w(a, order);
+    Walk w(a, order, VS);
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ---- the chain ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REG_CHAIN));
-        const int quarter = warp & 3, half = warp >> 2;
+        const int quarter = warp & 3, part = warp >> 2;                       // of the value columns; of the channels and rows
         if (quarter < VW) {
-            const int j = quarter * 32 + lane;                                // this thread's value column
+            const int j = quarter * 32 + lane;                                // this thread's value column in the slice
             const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-            const uint32_t ts = t0 + T_S + half * KP, ty = t0 + T_Y + half * 32, tu = t0 + T_U + half * 32;
-            float2 S[KP / 2];                                                 // channels KP half .. of column j
-            auto give_s = [&] {                                               // S as the next products' operand
-#pragma unroll
-                for (int i = 0; i < KP / 2; i += 16) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int x = 0; x < 16; x++) split2(S[i + x].x, S[i + x].y, hi[x], lo[x]);
-                    tmem_st16(ts + i, hi);
-                    tmem_st16(ts + KP / 2 + i, lo);
-                }
+            const uint32_t ts = t0 + T_S + part * KP, ty = t0 + T_Y + part * 16, tu = t0 + T_U + part * 16;
+            float2 S[KP / 2];                                                 // channels KP part .. of column j
+            auto give = [&](uint32_t mbar) {                                  // what the products wait for is in tensor memory
                 tc::tmem_st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive(s_ready);
+                if (lane == 0) arrive(mbar);
+            };
+            auto give_s = [&] {                                               // S as the next products' operand
+#pragma unroll
+                for (int i = 0; i < KP / 2; i += 8) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int x = 0; x < 8; x++) split2(S[i + x].x, S[i + x].y, hi[x], lo[x]);
+                    tmem_st8(ts + i, hi);
+                    tmem_st8(ts + KP / 2 + i, lo);
+                }
+                give(s_ready);
             };
             bool more = w.begin(), first = true;
             for (uint32_t c = 0; more; c++) {
-                const int n = w.n();
-                const uint32_t one = c & 1, two = (c >> 1) & 1;
-                const int64_t slot = load_slot(p, w.seq);
-                float *tile = slot >= 0 ? p.pool + slot * p.slot_stride + (static_cast<int64_t>(w.h) * K + half * KP) * V + j : nullptr;
+                const int s = c % STAGES, n = w.n();
+                const uint32_t one = c & 1;
+                const unsigned char *stage = sm + s * Smem::STAGE;
+                float *tile = nullptr;
+                bool write = false;
+                const bool last = w.left <= C;
+                if (first || last) {
+                    const int64_t slot = load_slot(p, w.seq);
+                    if (slot >= 0) tile = p.pool + slot * p.slot_stride + (static_cast<int64_t>(w.h) * K + part * KP) * a.V + w.slice * VS + j;
+                    write = slot >= 0 && slot != p.null_slot;
+                }
                 if (first) {
 #pragma unroll
                     for (int i = 0; i < KP / 2; i++)
-                        S[i] = slot >= 0 ? make_float2(tile[2 * i * V], tile[(2 * i + 1) * V]) : make_float2(0.f, 0.f);
+                        S[i] = tile ? make_float2(tile[static_cast<int64_t>(2 * i) * a.V], tile[static_cast<int64_t>(2 * i + 1) * a.V]) : make_float2(0.f, 0.f);
                     give_s();
                 }
-                const bool last = w.left <= C;
-                // v of this column, rows 32 half ..
-                if (!wait.warp(v_full(c & 1), two)) break;
-                uint32_t v[16];
+                // v of this column and quarter of the rows
+                if (!wait.warp(full(s), (c / STAGES) & 1)) break;
+                uint32_t v[8];
                 {
-                    const unsigned char *at = sm + Smem::V + (c & 1) * Smem::V_STAGE + half * 32 * (V * 2) + j * 2;
+                    const unsigned char *at = stage + Smem::QK + part * 16 * (VS * 2) + j * 2;
 #pragma unroll
-                    for (int i = 0; i < 16; i++)
-                        v[i] = *reinterpret_cast<const uint16_t *>(at + 2 * i * V * 2) |
-                               static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(at + (2 * i + 1) * V * 2)) << 16;
+                    for (int i = 0; i < 8; i++)
+                        v[i] = *reinterpret_cast<const uint16_t *>(at + 2 * i * VS * 2) |
+                               static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(at + (2 * i + 1) * VS * 2)) << 16;
                 }
-                __syncwarp();
-                if (lane == 0) arrive(v_empty(c & 1));
-                if (!wait.warp(scaled(c), (c >> 2) & 1)) break;
-                const float *set = sets + (c % SCALARS) * Smem::SET;
+                const float *set = reinterpret_cast<const float *>(stage + Smem::REC + Rec::ROWS);
                 const float gamma = set[3 * C];
                 // Y = V - e^b K^ S; rows past the chunk's end are zeros, whatever is in memory there
                 if (!wait.warp(ks_done, one)) break;
                 tc::fence_after_sync();
-                // (its terms go where later columns of K S still are: all of them first)
                 {
-                    uint32_t r[32];
-                    tmem_ld(ty, r);
+                    uint32_t x[16], hi[8], lo[8];
+                    tmem_ld(ty, x);
                     tc::tmem_ld_wait();
-                    const float4 *ys = reinterpret_cast<const float4 *>(set + half * 32);
+                    const float4 *ys = reinterpret_cast<const float4 *>(set + part * 16);
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const int at = 8 * q + e;
-                            const float4 f = ys[at / 2];
-                            const float2 pk = make_float2(__uint_as_float(r[2 * at]), __uint_as_float(r[2 * at + 1]));
-                            const float2 vv = make_float2(__uint_as_float(v[at] << 16), __uint_as_float(v[at] & 0xffff0000u));
-                            float2 y = ffma2(at % 2 ? make_float2(-f.z, -f.w) : make_float2(-f.x, -f.y), pk, vv);
-                            if (n < C) {
-                                if (half * 32 + 2 * at >= n) y.x = 0.f;
-                                if (half * 32 + 2 * at + 1 >= n) y.y = 0.f;
-                            }
-                            split2(y.x, y.y, hi[e], lo[e]);
+                    for (int e = 0; e < 8; e++) {
+                        const float4 f = ys[e / 2];
+                        float2 y = ffma2(e % 2 ? make_float2(-f.z, -f.w) : make_float2(-f.x, -f.y),
+                                         make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                         make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)));
+                        if (n < C) {
+                            if (part * 16 + 2 * e >= n) y.x = 0.f;
+                            if (part * 16 + 2 * e + 1 >= n) y.y = 0.f;
                         }
-                        tmem_st8(ty + 8 * q, hi);
-                        tmem_st8(ty + 16 + 8 * q, lo);
+                        split2(y.x, y.y, hi[e], lo[e]);
                     }
+                    tmem_st8(ty, hi);
+                    tmem_st8(ty + 8, lo);
                 }
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) arrive(y_ready);
-                // U: two terms for the outputs, two of its scaled form for the state
-                if (!wait.warp(u_done(c & 1), two)) break;
+                give(y_ready);
+                // U, for the outputs, and scaled, for the state
+                if (!wait.warp(u_done, one)) break;
                 tc::fence_after_sync();
                 {
-                    uint32_t r[32];
-                    tmem_ld(tu, r);
+                    uint32_t x[16], hi[8], lo[8];
+                    tmem_ld(tu, x);
                     tc::tmem_ld_wait();
-                    const float4 *us = reinterpret_cast<const float4 *>(set + C + half * 32);
+                    const float4 *us = reinterpret_cast<const float4 *>(set + C + part * 16);
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const int at = 8 * q + e;
-                            const float4 f = us[at / 2];
-                            const float2 y = make_float2(__uint_as_float(r[2 * at]), __uint_as_float(r[2 * at + 1]));
-                            const float2 z = fmul2(y, at % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
-                            split2(z.x, z.y, hi[e], lo[e]);
-                        }
-                        tmem_st8(ty + 8 * q, hi);
-                        tmem_st8(ty + 16 + 8 * q, lo);
+                    for (int e = 0; e < 8; e++) {
+                        const float4 f = us[e / 2];
+                        const float2 z = fmul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                               e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                        split2(z.x, z.y, hi[e], lo[e]);
                     }
+                    tmem_st8(ty, hi);
+                    tmem_st8(ty + 8, lo);
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            split2(__uint_as_float(r[2 * (8 * q + e)]), __uint_as_float(r[2 * (8 * q + e) + 1]), hi[e], lo[e]);
-                        tmem_st8(tu + 8 * q, hi);
-                        tmem_st8(tu + 16 + 8 * q, lo);
-                    }
+                    for (int e = 0; e < 8; e++) split2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hi[e], lo[e]);
+                    tmem_st8(tu, hi);
+                    tmem_st8(tu + 8, lo);
                 }
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) arrive(u_ready);
+                give(u_ready);
                 // S <- gamma S + its increment
                 more = w.next();
                 if (!wait.warp(s_done, one)) break;
                 tc::fence_after_sync();
                 const float2 g2 = make_float2(gamma, gamma);
 #pragma unroll
-                for (int i = 0; i < KP / 2; i += 16) {
-                    uint32_t r[32];
-                    tmem_ld(ts + 2 * i, r);
+                for (int i = 0; i < KP / 2; i += 8) {
+                    uint32_t x[16];
+                    tmem_ld(ts + 2 * i, x);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int x = 0; x < 16; x++) S[i + x] = ffma2(g2, S[i + x], make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])));
+                    for (int e = 0; e < 8; e++) S[i + e] = ffma2(g2, S[i + e], make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])));
                 }
                 first = last;
-                if (last) {
-                    if (slot >= 0 && slot != p.null_slot) {
-#pragma unroll
-                        for (int i = 0; i < KP / 2; i++) {
-                            tile[2 * i * V] = S[i].x;
-                            tile[(2 * i + 1) * V] = S[i].y;
-                        }
-                    }
-                } else {
+                if (!last) {
                     give_s();
-                }
-            }
-        }
-    } else if (warp < 16) {
-        // ---- T and the query-key products ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REG_PREP));
-        const int g = (warp - 8) >> 2, t = tid & 127, pw = t >> 5, r = t & 63;   // thread t: row r of the keys (t < 64) or queries
-        const bool query = t >= 64;
-        unsigned char *tile = sm + Smem::T + g * Smem::GROUP;
-        float *blocks = reinterpret_cast<float *>(sm + Smem::BLOCKS) + g * 10 * BLK;
-        float *cols = reinterpret_cast<float *>(sm + Smem::COLS) + g * 5 * C;
-        auto sync = [&] { asm volatile("bar.sync %0, 128;" :: "r"(1 + g) : "memory"); };
-        // the same, with one answer to whether every thread's waits have come through
-        auto sync_ok = [&](bool ok) {
-            uint32_t all;
-            asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-                         : "=r"(all) : "r"(1 + g), "r"(ok ? 1u : 0u) : "memory");
-            return all != 0;
-        };
-        const int gq = lane >> 2, tq = lane & 3;
-        // raw_g (warp 0) and raw_beta (warp 1) of rows 2 lane, 2 lane + 1 of the chunk at the walk
-        float raw0 = 0.f, raw1 = 0.f, rate = 0.f, dtb = 0.f;
-        int h_of = -1;
-        auto fetch = [&] {
-            if (pw < 2) {
-                const uint16_t *at = pw == 0 ? p.rg : p.rb;
-                const int64_t ld = pw == 0 ? p.ld_g : p.ld_beta, row = static_cast<int64_t>(w.row) + 2 * lane;
-                const int n = w.n();
-                if (2 * lane < n) raw0 = bf16_to_f32(__ldg(at + row * ld + w.h));
-                if (2 * lane + 1 < n) raw1 = bf16_to_f32(__ldg(at + (row + 1) * ld + w.h));
-            }
-        };
-        bool more = w.begin();
-        if (more && g == 1) more = w.next();
-        if (more) fetch();
-        for (uint32_t c = g; more; c += 2) {
-            const int s = c % STAGES, n = w.n(), h = w.h;
-            const uint32_t two = (c >> 1) & 1;
-            const float in0 = raw0, in1 = raw1;
-            more = w.next() && w.next();                                     // this group's next chunk
-            if (more) fetch();
-            float *set = sets + (c % SCALARS) * Smem::SET;
-            if (pw == 0) {                                                    // the running decay, in units of log 2
-                if (h != h_of) {
-                    h_of = h;
-                    rate = expf(__ldg(p.A_log + h)) * -1.44269504f;
-                    dtb = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
-                }
-                const double g0 = 2 * lane < n ? rate * softplus_f(in0 + dtb) : 0.f, g1 = 2 * lane + 1 < n ? rate * softplus_f(in1 + dtb) : 0.f;
-                double b = g0 + g1;
+                } else if (write) {
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double x = __shfl_up_sync(0xffffffffu, b, o);
-                    if (lane >= o) b += x;
-                }
-                const double b0_ = b - g1;
-                const float h0 = static_cast<float>(b0_), h1 = static_cast<float>(b);
-                *reinterpret_cast<float2 *>(cols + 2 * lane) = make_float2(h0, h1);
-                *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(static_cast<float>(b0_ - h0), static_cast<float>(b - h1));
-            } else if (pw == 1) {
-                *reinterpret_cast<float2 *>(cols + 2 * C + 2 * lane) =
-                    make_float2(2 * lane < n ? sigmoid_f(in0) : 0.f, 2 * lane + 1 < n ? sigmoid_f(in1) : 0.f);
-            }
-            // the norm of this thread's row
-            bool ok = wait.warp(full(s), (c / STAGES) & 1);
-            float2 sum = make_float2(0.f, 0.f);
-            unsigned char *own = sm + s * Smem::STAGE + t * 128;
-#pragma unroll
-            for (int hf = 0; hf < NH; hf++)
-#pragma unroll
-                for (int x = 0; x < 8; x++) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(own + hf * Smem::HALF + ((x ^ (t & 7)) << 4));
-                    const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const float2 f = make_float2(__uint_as_float(qq[y] << 16), __uint_as_float(qq[y] & 0xffff0000u));
-                        sum = ffma2(f, f, sum);
+                    for (int i = 0; i < KP / 2; i++) {
+                        tile[static_cast<int64_t>(2 * i) * a.V] = S[i].x;
+                        tile[static_cast<int64_t>(2 * i + 1) * a.V] = S[i].y;
                     }
                 }
-            const float norm = r < n ? rsqrtf(sum.x + sum.y + p.eps) : 0.f;
-            if (!query && r >= n) {   // keys of other sequences: 0 times what they may hold is not 0
-#pragma unroll
-                for (int hf = 0; hf < NH; hf++)
-#pragma unroll
-                    for (int x = 0; x < 8; x++) *reinterpret_cast<uint4 *>(own + hf * Smem::HALF + (x << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
-            if (!sync_ok(ok)) break;
-            const float b_hi = cols[r], b_lo = cols[C + r];
-            const float scale = (query ? p.scale : cols[2 * C + r]) * norm;
-            if (!query) {
-                const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1];
-                set[r] = ex2(b_hi + b_lo) * norm;
-                set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * norm;
-                if (r == 0) set[3 * C] = ex2(e_hi + e_lo);
-                cols[3 * C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
-                cols[4 * C + r] = ex2((cols[r | 15] - b_hi) + (cols[C + (r | 15)] - b_lo)) * norm;
-            } else {
-                set[2 * C + r] = p.scale * ex2(b_hi + b_lo) * norm;
-            }
-            __syncwarp();
-            if (lane == 0) arrive(scaled(c));
-            sync();
-            // K K^T and Q K^T: row r of A (its blocks up to the diagonal's), or of the query-key products
-            ok = wait.warp(g_done(g), two);
-            tc::fence_after_sync();
-            if (query && c >= 2) ok &= wait.warp(o_done(g), two ^ 1);         // the products of this group's last chunk have been used
-            const int low = (pw & 1) * 2;                                     // the first block with a diagonal in the warp's rows
-            const uint32_t tg = tmem + T_G + g * 64 + (static_cast<uint32_t>(pw * 32) << 16);
-            float2 d[8];
-            auto put = [&](int bl) {
-                if (query) {
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) split2(d[4 * y + i].x, d[4 * y + i].y, hi[i], lo[i]);
-                        unsigned char *at = tile + 2 * Smem::TILE + r * 128 + (((2 * bl + y) ^ (r & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(at + Smem::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                } else if (bl <= r >> 4) {
-                    float *at = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        *reinterpret_cast<float4 *>(at + 4 * i) = make_float4(d[2 * i].x, d[2 * i].y, d[2 * i + 1].x, d[2 * i + 1].y);
-                }
-            };
-            // blocks left of it: e^{b_r - b_i} = e^{b_r - p} e^{p - b_i}, p the sum at the block's last row: neither is above 1
-#pragma unroll 1
-            for (int bl = 0; bl < low; bl++) {
-                uint32_t x[16];
-                tmem_ld(tg + bl * 16, x);
-                const float f = ex2((b_hi - cols[bl * 16 + 15]) + (b_lo - cols[C + bl * 16 + 15])) * scale;
-                const float2 f2 = make_float2(f, f);
-                tc::tmem_ld_wait();
-                if (r >= n) {                                                 // not a row of the chunk: whatever it held
-#pragma unroll
-                    for (int i = 0; i < 16; i++) x[i] = 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float4 e = *reinterpret_cast<const float4 *>(cols + 4 * C + bl * 16 + 4 * i);
-                    d[2 * i] = fmul2(fmul2(make_float2(e.x, e.y), f2), make_float2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])));
-                    d[2 * i + 1] = fmul2(fmul2(make_float2(e.z, e.w), f2), make_float2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
-                }
-                put(bl);
-            }
-            // and the two with diagonals: entry by entry, the ones above it cut off
-            const int end = r < n ? r + query : 0;
-            const float2 bh = make_float2(b_hi, b_hi), bl2 = make_float2(b_lo, b_lo), sc = make_float2(scale, scale);
-#pragma unroll 1
-            for (int bl = low; bl < low + 2; bl++) {
-                uint32_t x[16];
-                tmem_ld(tg + bl * 16, x);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float4 eh = *reinterpret_cast<const float4 *>(cols + bl * 16 + 4 * i);
-                    const float4 el = *reinterpret_cast<const float4 *>(cols + 3 * C + bl * 16 + 4 * i);
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {
-                        const float2 e = fadd2(fsub2(bh, y ? make_float2(eh.z, eh.w) : make_float2(eh.x, eh.y)),
-                                               fsub2(bl2, y ? make_float2(el.z, el.w) : make_float2(el.x, el.y)));
-                        const float2 v = fmul2(fmul2(make_float2(ex2(e.x), ex2(e.y)), sc),
-                                               make_float2(__uint_as_float(x[4 * i + 2 * y]), __uint_as_float(x[4 * i + 2 * y + 1])));
-                        const int col = bl * 16 + 4 * i + 2 * y;
-                        d[2 * i + y] = make_float2(col < end ? v.x : 0.f, col + 1 < end ? v.y : 0.f);
-                    }
-                }
-                put(bl);
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive(g_free(g));
-            sync();
-            // T: the diagonal blocks, a warp each, by substitution; a lane has a column (lanes 16 and up the same again)
-            {
-                const float *A = blocks + block_at(pw, pw);
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    float y[4] = {i == (lane & 15) ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < i; k += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(A + i * 20 + k);
-                        y[0] = fmaf(-f.x, x[k], y[0]);
-                        if (k + 1 < i) y[1] = fmaf(-f.y, x[k + 1], y[1]);
-                        if (k + 2 < i) y[2] = fmaf(-f.z, x[k + 2], y[2]);
-                        if (k + 3 < i) y[3] = fmaf(-f.w, x[k + 3], y[3]);
-                    }
-                    x[i] = (y[0] + y[1]) + (y[2] + y[3]);
-                }
-                __syncwarp();
-                if (lane < 16)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) blocks[block_at(pw, pw) + i * 20 + lane] = x[i];
-            }
-            sync();
-            // the blocks below them: [[X, 0], [-Y A X, Y]], first of 32 rows, then of all 64. X^T A^T is the first operand of the
-            // second product as it leaves the first one: column 2t of a tile counts as k = t, 2t + 1 as k = t + 4.
-            {
-                const int pr = pw >> 1, hf = pw & 1;
-                const float *X = blocks + block_at(2 * pr, 2 * pr), *Y = blocks + block_at(2 * pr + 1, 2 * pr + 1);
-                float *A = blocks + block_at(2 * pr + 1, 2 * pr);
-                float xa[2][4] = {}, out[4] = {};
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    Tf32<4> fx;
-                    fx.set(0, X[(8 * k + tq) * 20 + gq]);
-                    fx.set(1, X[(8 * k + tq) * 20 + gq + 8]);
-                    fx.set(2, X[(8 * k + tq + 4) * 20 + gq]);
-                    fx.set(3, X[(8 * k + tq + 4) * 20 + gq + 8]);
-#pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        Tf32<2> fa;
-                        fa.set(0, A[(8 * m + gq) * 20 + 8 * k + tq]);
-                        fa.set(1, A[(8 * m + gq) * 20 + 8 * k + tq + 4]);
-                        mma_split(xa[m], fx, fa);
-                    }
-                }
-#pragma unroll
-                for (int m = 0; m < 2; m++) {
-                    Tf32<4> fx;
-                    Tf32<2> fy;
-                    fx.set(0, -xa[m][0]); fx.set(1, -xa[m][2]); fx.set(2, -xa[m][1]); fx.set(3, -xa[m][3]);
-                    const float2 y = *reinterpret_cast<const float2 *>(Y + (8 * hf + gq) * 20 + 8 * m + 2 * tq);
-                    fy.set(0, y.x);
-                    fy.set(1, y.y);
-                    mma_split(out, fx, fy);
-                }
-                sync();                                                       // A has been read
-#pragma unroll
-                for (int x = 0; x < 4; x++) {
-                    const int col = gq + 8 * (x >> 1), row = 8 * hf + 2 * tq + (x & 1);
-                    A[row * 20 + col] = out[x];
-                }
-            }
-            sync();
-            {
-                const int mt = pw >> 1, hf = pw & 1;                          // columns 16 mt .., rows 32 + 16 hf ..
-                float out[2][4] = {};
-#pragma unroll
-                for (int ib = 0; ib < 2; ib++) {
-                    if (ib > hf) break;
-                    float xa[2][4] = {};
-#pragma unroll
-                    for (int kb = 0; kb < 2; kb++) {
-                        if (kb < mt) continue;
-                        const float *X = blocks + block_at(kb, mt), *A = blocks + block_at(2 + ib, kb);
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            Tf32<4> fx;
-                            fx.set(0, X[(8 * k + tq) * 20 + gq]);
-                            fx.set(1, X[(8 * k + tq) * 20 + gq + 8]);
-                            fx.set(2, X[(8 * k + tq + 4) * 20 + gq]);
-                            fx.set(3, X[(8 * k + tq + 4) * 20 + gq + 8]);
-#pragma unroll
-                            for (int m = 0; m < 2; m++) {
-                                Tf32<2> fa;
-                                fa.set(0, A[(8 * m + gq) * 20 + 8 * k + tq]);
-                                fa.set(1, A[(8 * m + gq) * 20 + 8 * k + tq + 4]);
-                                mma_split(xa[m], fx, fa);
-                            }
-                        }
-                    }
-                    const float *Y = blocks + block_at(2 + hf, 2 + ib);
-#pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        Tf32<4> fx;
-                        fx.set(0, -xa[m][0]); fx.set(1, -xa[m][2]); fx.set(2, -xa[m][1]); fx.set(3, -xa[m][3]);
-#pragma unroll
-                        for (int rt = 0; rt < 2; rt++) {
-                            Tf32<2> fy;
-                            const float2 y = *reinterpret_cast<const float2 *>(Y + (8 * rt + gq) * 20 + 8 * m + 2 * tq);
-                            fy.set(0, y.x);
-                            fy.set(1, y.y);
-                            mma_split(out[rt], fx, fy);
-                        }
-                    }
-                }
-                sync();                                                       // A has been read
-                float *at = blocks + block_at(2 + hf, mt);
-#pragma unroll
-                for (int rt = 0; rt < 2; rt++)
-#pragma unroll
-                    for (int x = 0; x < 4; x++) at[(8 * rt + 2 * tq + (x & 1)) * 20 + gq + 8 * (x >> 1)] = out[rt][x];
-            }
-            if (c >= 2) ok &= wait.warp(u_done(g), two ^ 1);                  // T of this group's last chunk has been used
-            if (!sync_ok(ok)) break;
-            // T diag(beta), hi and lo: half of row r
-#pragma unroll 1
-            for (int bl = t >> 6 << 1; bl <= r >> 4 && bl < (t >> 6 << 1) + 2; bl++) {
-                const float *from = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
-#pragma unroll
-                for (int y = 0; y < 2; y++) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const float4 x = *reinterpret_cast<const float4 *>(from + 8 * y + 4 * i);
-                        const float4 e = *reinterpret_cast<const float4 *>(cols + 2 * C + bl * 16 + 8 * y + 4 * i);
-                        const float2 v0 = fmul2(make_float2(x.x, x.y), make_float2(e.x, e.y)), v1 = fmul2(make_float2(x.z, x.w), make_float2(e.z, e.w));
-                        split2(v0.x, v0.y, hi[2 * i], lo[2 * i]);
-                        split2(v1.x, v1.y, hi[2 * i + 1], lo[2 * i + 1]);
-                    }
-                    unsigned char *at = tile + r * 128 + (((2 * bl + y) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(at + Smem::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) arrive(t_ready(g));
-            sync();                                                           // blocks and columns are free again
         }
     } else if (warp < 20) {
         // ---- outputs ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REG_OUT));
         const int quarter = warp & 3, j = quarter * 32 + lane;
         // chains that are skipped: their error bits, and zeros for a slot past the pool
-        for (Walk z(a, order); z.item < z.total; z.advance()) {
+        for (Walk z(a, order, VS); z.item < z.total; z.advance()) {
             uint32_t bad;
             int all;
             z.chain(&bad, &all);
             if (!bad) continue;
             if (p.err && quarter == 0 && lane == 0) atomicOr(p.err, bad);
-            if (j < V)
-                for (int i = 0; i < all; i++) p.out[(static_cast<int64_t>(z.row) + i) * p.ld_out + static_cast<int64_t>(z.h) * V + j] = 0;
+            if (j < VS)
+                for (int i = 0; i < all; i++)
+                    p.out[(static_cast<int64_t>(z.row) + i) * p.ld_out + static_cast<int64_t>(z.h) * a.V + z.slice * VS + j] = 0;
         }
         if (quarter < VW) {
             const uint32_t t0 = tmem + T_O + (static_cast<uint32_t>(quarter * 32) << 16);
             bool more = w.begin();
             for (uint32_t c = 0; more; c++) {
-                const int n = w.n();
-                uint16_t *out = p.out + static_cast<int64_t>(w.row) * p.ld_out + static_cast<int64_t>(w.h) * V + j;
-                const float *qs = sets + (c % SCALARS) * Smem::SET + 2 * C;
-                if (!wait.warp(o_done(c & 1), (c >> 1) & 1)) break;
-                tc::fence_after_sync();
+                const int s = c % STAGES, n = w.n();
+                uint16_t *out = p.out + static_cast<int64_t>(w.row) * p.ld_out + static_cast<int64_t>(w.h) * a.V + w.slice * VS + j;
+                const float *qs = reinterpret_cast<const float *>(sm + s * Smem::STAGE + Smem::REC + Rec::ROWS) + 2 * C;
                 more = w.next();
+                if (!wait.warp(o_done, c & 1)) break;
+                tc::fence_after_sync();
                 auto store = [&](auto whole) {
 #pragma unroll
-                    for (int i = 0; i < C; i += 8) {
-                        uint32_t x[8], y[8];
-                        tmem_ld8(t0 + i, x);
-                        tmem_ld8(t0 + C + i, y);
+                    for (int i = 0; i < C; i += 16) {
+                        uint32_t x[16], y[16];
+                        tmem_ld(t0 + i, x);
+                        tmem_ld(t0 + C + i, y);
                         tc::tmem_ld_wait();
-                        if (i == C - 8) {
+                        if (i == C - 16) {
                             tc::fence_before_sync();
                             __syncwarp();
                             if (lane == 0) arrive(o_free);
                         }
 #pragma unroll
-                        for (int r = 0; r < 8; r += 2) {
+                        for (int r = 0; r < 16; r += 2) {
                             const float2 o = ffma2(*reinterpret_cast<const float2 *>(qs + i + r), make_float2(__uint_as_float(x[r]), __uint_as_float(x[r + 1])),
                                                    make_float2(__uint_as_float(y[r]), __uint_as_float(y[r + 1])));
                             const uint32_t o2 = pack_bf16x2(o.x, o.y);
@@ -839,132 +862,110 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 };
                 if (n == C) store(std::true_type{});
                 else store(std::false_type{});
+                __syncwarp();
+                if (lane == 0) arrive(empty(s));
             }
         }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REG_REST));
-        if (warp == 20) {
-            // ---- TMA ----
-            if (lane == 0) {
-                const int hk = p.Hv / p.Hk;
-                bool more = w.begin();
-                uint32_t c = 0;
-                for (; more; c++) {
-                    const int s = c % STAGES;
-                    if (c >= STAGES && !wait(empty(s), (c / STAGES - 1) & 1)) break;
-                    const uint32_t at = s0 + s * Smem::STAGE;
-                    tc::mbar_expect_tx(full(s), NH * Smem::HALF);
-#pragma unroll
-                    for (int hf = 0; hf < NH; hf++) {
-                        const int x = w.h / hk * K + 64 * hf;
-                        tc::tma_load_2d(at + hf * Smem::HALF, &tm_qk, p.Hk * K + x, w.row, full(s));
-                        tc::tma_load_2d(at + hf * Smem::HALF + C * 128, &tm_qk, x, w.row, full(s));
-                    }
-                    if (c >= 2 && !wait(v_empty(c & 1), ((c >> 1) & 1) ^ 1)) {
-                        (void)tc::mbar_wait(full(s), (c / STAGES) & 1);
-                        break;
-                    }
-                    tc::mbar_expect_tx(v_full(c & 1), C * V * 2);
-                    tc::tma_load_2d(s0 + Smem::V + (c & 1) * Smem::V_STAGE, &tm_v, 2 * p.Hk * K + w.h * V, w.row, v_full(c & 1));
-                    more = w.next();
-                }
-                // no CTA ends with copies in flight
-                for (uint32_t k = c > STAGES ? c - STAGES : 0; k < c; k++) (void)tc::mbar_wait(full(k % STAGES), (k / STAGES) & 1);
-                for (uint32_t k = c > 2 ? c - 2 : 0; k < c; k++) (void)tc::mbar_wait(v_full(k & 1), (k >> 1) & 1);
-            }
-        } else if (warp == 21) {
-            // ---- the chain's MMAs ----
+    } else if (warp == 20) {
+        // ---- copies ----
+        if (lane == 0) {
+            const int per = p.Hv / p.Hk;
             bool more = w.begin();
-            for (uint32_t c = 0; more; c++) {
-                const int s = c % STAGES, g = c & 1;
-                const uint32_t one = c & 1, two = (c >> 1) & 1;
-                const uint32_t at = s0 + s * Smem::STAGE, tt = s0 + Smem::T + g * Smem::GROUP;
-                if (!wait.warp(full(s), (c / STAGES) & 1) || !wait.warp(s_ready, one)) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
-                    // K S, both terms of S
+            uint32_t c = 0;
+            for (; more; c++) {
+                const int s = c % STAGES;
+                if (c >= STAGES && !wait(empty(s), (c / STAGES - 1) & 1)) break;
+                const uint32_t at = s0 + s * Smem::STAGE;
+                tc::mbar_expect_tx(full(s), NH * HALF + C * VS * 2 + Rec::BYTES);
 #pragma unroll
-                    for (int x = 0; x < 2; x++)
-#pragma unroll
-                        for (int k = 0; k < K / 16; k++) {
-                            const int half = k / (KP / 16), kk = k % (KP / 16);
-                            mma_t(tmem + T_Y, tmem + T_S + half * KP + x * (KP / 2) + kk * 8, desc_k(at + (k / 4) * Smem::HALF + (k % 4) * 32), idesc(C), x + k > 0);
-                        }
-                    tc::commit(ks_done);
+                for (int hf = 0; hf < NH; hf++) {
+                    const int x = w.h / per * K + 64 * hf;
+                    tc::tma_load_2d(at + hf * HALF, &tm_qk, p.Hk * K + x, w.row, full(s));
+                    tc::tma_load_2d(at + hf * HALF + C * 128, &tm_qk, x, w.row, full(s));
                 }
-                __syncwarp();
-                if (c > 0 && !wait.warp(o_free, one ^ 1)) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < 2; x++)
-#pragma unroll
-                        for (int k = 0; k < K / 16; k++) {
-                            const int half = k / (KP / 16), kk = k % (KP / 16);
-                            mma_t(tmem + T_O, tmem + T_S + half * KP + x * (KP / 2) + kk * 8, desc_k(at + (k / 4) * Smem::HALF + C * 128 + (k % 4) * 32), idesc(C), x + k > 0);
-                        }
-                }
-                __syncwarp();
-                if (!wait.warp(t_ready(g), two) || !wait.warp(y_ready, one)) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
-                    // U = (T diag(beta)) Y: hi hi, lo hi, hi lo. Rows of T before 16 k are zero in columns 16 k ..
-#pragma unroll
-                    for (int x = 0; x < 3; x++)
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            mma_t(tmem + T_U + 16 * k, tmem + T_Y + (k / 2) * 32 + (x == 1 ? 16 : 0) + (k % 2) * 8,
-                                  desc_k(tt + (x == 2 ? Smem::TILE : 0) + 16 * k * 128 + k * 32), idesc(C - 16 * k), x + k > 0);
-                    tc::commit(u_done(g));
-                }
-                __syncwarp();
-                if (!wait.warp(u_ready, one)) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
-                    // the state's increment, both terms of U
-#pragma unroll
-                    for (int x = 0; x < 2; x++)
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            mma_t(tmem + T_S, tmem + T_Y + (k / 2) * 32 + x * 16 + (k % 2) * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
-                    tc::commit(s_done);
-#pragma unroll
-                    for (int x = 0; x < 3; x++)
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            mma_t(tmem + T_O + C + 16 * k, tmem + T_U + (k / 2) * 32 + (x == 1 ? 16 : 0) + (k % 2) * 8,
-                                  desc_k(tt + (x == 2 ? 3 : 2) * Smem::TILE + 16 * k * 128 + k * 32), idesc(C - 16 * k), x + k > 0);
-                    tc::commit(empty(s));
-                    tc::commit(o_done(g));
-                }
-                __syncwarp();
+                tc::tma_load_2d(at + Smem::QK, &tm_v, 2 * p.Hk * K + w.h * a.V + w.slice * VS, w.row, full(s));
+                tc::bulk_g2s(at + Smem::REC, a.records + (static_cast<int64_t>(w.chunk) * p.Hv + w.h) * Rec::BYTES, Rec::BYTES, full(s));
                 more = w.next();
             }
-            // nor with MMAs
-            if (elect_one()) tc::commit(drained(0));
-            __syncwarp();
-            (void)tc::mbar_wait(drained(0), 0);
-        } else if (warp == 22) {
-            // ---- K K^T and Q K^T ----
-            bool more = w.begin();
-            for (uint32_t c = 0; more; c++) {
-                const int s = c % STAGES, g = c & 1;
-                const uint32_t at = s0 + s * Smem::STAGE;
-                if (!wait.warp(full(s), (c / STAGES) & 1)) break;
-                if (c >= 2 && !wait.warp(g_free(g), ((c >> 1) & 1) ^ 1)) break;
-                tc::fence_after_sync();
-                if (elect_one()) {
+            // no CTA ends with copies in flight
+            for (uint32_t k = c > STAGES ? c - STAGES : 0; k < c; k++) (void)tc::mbar_wait(full(k % STAGES), (k / STAGES) & 1);
+        }
+    } else if (warp == 21) {
+        // ---- MMAs ----
+        bool more = w.begin();
+        for (uint32_t c = 0; more; c++) {
+            const int s = c % STAGES;
+            const uint32_t one = c & 1, at = s0 + s * Smem::STAGE, rec = at + Smem::REC;
+            if (!wait.warp(full(s), (c / STAGES) & 1) || !wait.warp(s_ready, one)) break;
+            tc::fence_after_sync();
+            // S^T times the keys or the queries (the rows `from` on), both terms of S
+            auto times_s = [&](uint32_t d, uint32_t from) {
+#pragma unroll
+                for (int x = 0; x < 2; x++)
 #pragma unroll
                     for (int k = 0; k < K / 16; k++)
-                        mma_gram(tmem + T_G + g * 64, desc_k(at + (k / 4) * Smem::HALF + (k % 4) * 32), idesc(C), k > 0);
-                    tc::commit(g_done(g));
-                }
-                __syncwarp();
-                more = w.next();
+                        mma_t(d, tmem + T_S + k / (KP / 16) * KP + x * (KP / 2) + k % (KP / 16) * 8, desc_k(from + (k / 4) * HALF + (k % 4) * 32), idesc(C), x + k > 0);
+            };
+            // a record's matrix times Y or U: hi hi, lo hi, hi lo; rows before 16 k are zero in columns 16 k ..
+            auto times_rec = [&](uint32_t d, uint32_t from, uint32_t matrix) {
+#pragma unroll
+                for (int x = 0; x < 3; x++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_t<PANEL_HIGH>(d + 16 * k, from + k * 16 + (x == 1 ? 8 : 0), desc_panel(matrix + (x == 2 ? Rec::MATRIX : 0) + Rec::panel(k)), idesc(C - 16 * k), x + k > 0);
+            };
+            if (elect_one()) {
+                times_s(tmem + T_Y, at);
+                tc::commit(ks_done);
             }
-            if (elect_one()) tc::commit(drained(1));
             __syncwarp();
-            (void)tc::mbar_wait(drained(1), 0);
+            if (c > 0 && !wait.warp(o_free, one ^ 1)) break;
+            tc::fence_after_sync();
+            if (elect_one()) times_s(tmem + T_O, at + C * 128);
+            __syncwarp();
+            if (!wait.warp(y_ready, one)) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T);
+                tc::commit(u_done);
+            }
+            __syncwarp();
+            if (!wait.warp(u_ready, one) || (w.left < C && !wait.warp(clean(s), (c / STAGES) & 1))) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                // the state's increment, both terms of U
+#pragma unroll
+                for (int x = 0; x < 2; x++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_t(tmem + T_S, tmem + T_Y + k * 16 + x * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
+                tc::commit(s_done);
+                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W);
+                tc::commit(empty(s));
+                tc::commit(o_done);
+            }
+            __syncwarp();
+            more = w.next();
+        }
+        // nor with MMAs
+        if (elect_one()) tc::commit(drained);
+        __syncwarp();
+        (void)tc::mbar_wait(drained, 0);
+    } else if (warp == 22) {
+        // ---- keys behind a sequence's end: another sequence's, and 0 times what they may hold is not 0 ----
+        bool more = w.begin();
+        for (uint32_t c = 0; more; c++) {
+            const int s = c % STAGES, n = w.n();
+            more = w.next();
+            if (!wait.warp(full(s), (c / STAGES) & 1)) break;
+            if (n < C) {
+                for (int i = n * 8 + lane; i < C * 8; i += 32)
+#pragma unroll
+                    for (int hf = 0; hf < NH; hf++) *reinterpret_cast<uint4 *>(sm + s * Smem::STAGE + hf * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) arrive(clean(s));
         }
     }
     __syncwarp();
@@ -1017,12 +1018,13 @@ cudaError_t this_device(int *sms)
     if (!known[dev].load(std::memory_order_acquire)) {
         const std::lock_guard<std::mutex> one(asking);
         if (!known[dev].load(std::memory_order_relaxed)) {
-            const auto limit = [&](auto kernel) {
-                if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::END);
+            const auto limit = [&](auto kernel, int bytes) {
+                if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             };
             e = cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev);
-            limit(chunk_kernel<1, 32>); limit(chunk_kernel<1, 64>); limit(chunk_kernel<1, 128>);
-            limit(chunk_kernel<2, 32>); limit(chunk_kernel<2, 64>); limit(chunk_kernel<2, 128>);
+            limit(prep_kernel<1>, HALF); limit(prep_kernel<2>, 2 * HALF);
+            limit(chain_kernel<1, 32>, Smem::END); limit(chain_kernel<1, 64>, Smem::END); limit(chain_kernel<1, 128>, Smem::END);
+            limit(chain_kernel<2, 32>, Smem::END); limit(chain_kernel<2, 64>, Smem::END); limit(chain_kernel<2, 128>, Smem::END);
             if (e != cudaSuccess) return e;
             known[dev].store(true, std::memory_order_release);
         }
@@ -1031,10 +1033,20 @@ cudaError_t this_device(int *sms)
     return cudaSuccess;
 }
 
+int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
 }  // namespace
 }  // namespace gdn
 
-cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs,
+size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K)
+{
+    using namespace gdn;
+    if (K == 32 || rows == 0 || num_seqs == 0) return 0;
+    const int64_t chunks = rows / C + num_seqs;
+    return static_cast<size_t>(up((num_seqs + 1) * 4) + up(chunks * 8) + chunks * Hv * Rec::BYTES);
+}
+
+cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs, void *workspace,
                                cudaStream_t stream)
 {
     using namespace gdn;
@@ -1045,14 +1057,22 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     cudaError_t e = this_device(&sms);
     if (e != cudaSuccess) return e;
     CUtensorMap qk, v;
-    const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V;
+    const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
+    const int VS = V;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
-    if ((e = encode(&v, p, rows, cols, V, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;
-    const Args a{p, cu, static_cast<int>(rows), static_cast<int>(num_seqs)};
-    const int64_t chains = num_seqs * p.Hv;
-    const dim3 grid(static_cast<unsigned>(chains < sms ? chains : sms));
-#define KDA_GDN_RUN(NH, VV) \
-    if (K == 64 * NH && V == VV) return launch_pdl(chunk_kernel<NH, VV>, grid, dim3(THREADS), Smem::END, stream, qk, v, a);
+    if ((e = encode(&v, p, rows, cols, VS, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;
+    const int64_t chunks = rows / C + num_seqs;
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    const Args a{p, cu, static_cast<int>(rows), static_cast<int>(num_seqs), V, static_cast<int>(chunks), reinterpret_cast<int32_t *>(w),
+                 reinterpret_cast<int2 *>(w + up((num_seqs + 1) * 4)), w + up((num_seqs + 1) * 4) + up(chunks * 8)};
+    if ((e = launch_pdl(map_kernel, dim3(1), dim3(1024), 0, stream, a)) != cudaSuccess) return e;
+    const dim3 units(static_cast<unsigned>(chunks * p.Hk));
+    e = K == 64 ? launch_pdl(prep_kernel<1>, units, dim3(128), HALF, stream, qk, a) : launch_pdl(prep_kernel<2>, units, dim3(128), 2 * HALF, stream, qk, a);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = chains * (V / VS);
+    const dim3 grid(static_cast<unsigned>(ctas < sms ? ctas : sms));
+#define KDA_GDN_RUN(NH, W) \
+    if (K == 64 * NH && VS == W) return launch_pdl(chain_kernel<NH, W>, grid, dim3(THREADS), Smem::END, stream, qk, v, a);
     KDA_GDN_RUN(1, 32) KDA_GDN_RUN(1, 64) KDA_GDN_RUN(1, 128) KDA_GDN_RUN(2, 32) KDA_GDN_RUN(2, 64) KDA_GDN_RUN(2, 128)
 #undef KDA_GDN_RUN
     return cudaErrorInvalidValue;

@@ -10,10 +10,9 @@ namespace gdn {
 
 constexpr uint32_t kErrLengths = 16u;   // KDA_ERRFLAG_LENGTHS
 
-__device__ __forceinline__ int64_t load_slot(const GdnParams &p, int64_t e)
-{
-    return static_cast<int64_t>(__ldg(p.indices + e * p.index_stride));
-}
+// (Not a read-only load: the compiler may take one ahead of the wait for the kernel that writes the indices. So too with
+// lengths, and with what one of a call's kernels leaves to the next.)
+__device__ __forceinline__ int64_t load_slot(const GdnParams &p, int64_t e) { return static_cast<int64_t>(p.indices[e * p.index_stride]); }
 
 // Log-decay of a token and head: -e^{A_log} softplus(raw_g + dt_bias).
 __device__ __forceinline__ float log_decay(const GdnParams &p, int64_t row, int h, float expA, float dtb)

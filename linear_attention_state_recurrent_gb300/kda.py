@@ -48,7 +48,7 @@ EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decod
             "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
             "kda_norm_quant", "kda_fp8_matmul", "kda_fp8_matmul_plan",
             "kda_selftest_fp8_matmul", "kda_batch_maps",
-            "kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill")
+            "kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill", "kda_gdn_chunk_prefill_workspace_bytes")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -139,7 +139,9 @@ def _load():
     lib.kda_gdn_spec_verify.restype = ctypes.c_int
     lib.kda_gdn_spec_verify.argtypes = [P, I64, P, I64, P, I64, I64, I32, GP, SP, P, I64, P, P]
     lib.kda_gdn_chunk_prefill.restype = ctypes.c_int
-    lib.kda_gdn_chunk_prefill.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, GP, SP, P, I64, P, P]
+    lib.kda_gdn_chunk_prefill.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, GP, SP, P, SZ, P, I64, P, P]
+    lib.kda_gdn_chunk_prefill_workspace_bytes.restype = SZ
+    lib.kda_gdn_chunk_prefill_workspace_bytes.argtypes = [I64, I64, GP]
     lib.kda_batch_maps.restype = ctypes.c_int
     lib.kda_batch_maps.argtypes = [P, P, P, I64, I64, P, I64, I64, P, I64, P, I64, I32, I64, P, P, P, P, P, P,
                                    P, P, P]
@@ -657,9 +659,9 @@ def kda_batch_maps(query_lens, context_lens, state_slots, block_table, free_page
 
 
 def _gdn(name, mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads, scale,
-         l2_eps, null_slot, out, err_flags, stream):
+         l2_eps, null_slot, out, err_flags, stream, workspace=None):
     r = _torch_binding.gdn(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, tokens, cu_seqlens, num_k_heads,
-                           scale, l2_eps, null_slot, out, err_flags, _handle(stream))
+                           scale, l2_eps, null_slot, out, err_flags, _handle(stream), workspace)
     if type(r) is int:
         _check(r, name)
     return r, initial_state
@@ -686,12 +688,22 @@ def kda_gdn_spec_verify(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_stat
                 num_k_heads, scale, l2_eps, null_slot, out, err_flags, stream)
 
 
+def kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, H, K, V, num_k_heads=None):
+    """Bytes of workspace of a kda_gdn_chunk_prefill over num_rows rows (mixed_qkv's, whatever cu_seqlens holds) and num_seqs sequences."""
+    hd = KdaGdnHeads(Hk=H if num_k_heads is None else num_k_heads, Hv=H, K=K, V=V)
+    n = int(lib.kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, ctypes.byref(hd)))
+    if n == 0 and last_error():
+        raise ValueError(f"kda_gdn_chunk_prefill_workspace_bytes: {last_error()}")
+    return n
+
+
 def kda_gdn_chunk_prefill(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, cu_seqlens, *, num_k_heads=None,
-                          scale=None, l2_eps=1e-6, null_slot=-1, out=None, err_flags=None, stream=None):
+                          scale=None, l2_eps=1e-6, null_slot=-1, out=None, workspace=None, err_flags=None, stream=None):
     """The same over packed sequences, in chunks: sequence s has rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the GPU,
     never read on the host: no synchronisation, and lengths may change between graph replays). A pair that is no range of
-    the rows counts as empty and sets KDA_ERRFLAG_LENGTHS in err_flags. Returns (out, initial_state)."""
+    the rows counts as empty and sets KDA_ERRFLAG_LENGTHS in err_flags. workspace: a contiguous tensor of
+    kda_gdn_chunk_prefill_workspace_bytes, allocated where none or a smaller one is given. Returns (out, initial_state)."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor")
     return _gdn("kda_gdn_chunk_prefill", mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_state, state_indices, 0, cu_seqlens,
-                num_k_heads, scale, l2_eps, null_slot, out, err_flags, stream)
+                num_k_heads, scale, l2_eps, null_slot, out, err_flags, stream, workspace)

@@ -83,7 +83,7 @@ def call(kda, name, change=None, heads=None, state=None):
     """The call with sound arguments, but for what is changed; the status."""
     H = dict(Hk=2, Hv=4, K=64, V=128, A_log=FAKE, dt_bias=FAKE, scale=0.1, l2_eps=1e-6)
     S = dict(pool=FAKE, num_slots=8, slot_stride=4 * 64 * 128, indices=FAKE, index_stride=1, null_slot=-1)
-    A = dict(qkv=FAKE, ld_qkv=768, rg=FAKE, ld_g=4, rb=FAKE, ld_beta=4, n=3, T=4, cu=FAKE, rows=12, out=FAKE, ld_out=512, err=FAKE)
+    A = dict(qkv=FAKE, ld_qkv=768, rg=FAKE, ld_g=4, rb=FAKE, ld_beta=4, n=3, T=4, cu=FAKE, rows=12, ws=FAKE, ws_bytes=1 << 20, out=FAKE, ld_out=512, err=FAKE)
     H.update(heads or {})
     S.update(state or {})
     A.update(change or {})
@@ -96,7 +96,7 @@ def call(kda, name, change=None, heads=None, state=None):
         return kda.lib.kda_gdn_decode(*head, A["n"], *tail)
     if name == "kda_gdn_spec_verify":
         return kda.lib.kda_gdn_spec_verify(*head, A["n"], A["T"], *tail)
-    return kda.lib.kda_gdn_chunk_prefill(*head, A["cu"], A["n"], A["rows"], *tail)
+    return kda.lib.kda_gdn_chunk_prefill(*head, A["cu"], A["n"], A["rows"], *tail[:2], A["ws"], A["ws_bytes"], *tail[2:])
 
 
 CALLS = ["kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill"]
@@ -123,8 +123,22 @@ def test_refusals(kda, name, what, bad, status):
 def test_refusals_of_one_call(kda):
     for T in (0, -1, 65):
         assert call(kda, "kda_gdn_spec_verify", dict(T=T)) == 1
-    for change, status in ((dict(cu=None), 1), (dict(cu=FAKE + 2), 1), (dict(rows=-1), 1), (dict(rows=2 ** 31 - 64), 2)):
+    for change, status in ((dict(cu=None), 1), (dict(cu=FAKE + 2), 1), (dict(rows=-1), 1), (dict(rows=2 ** 31 - 64), 2), 
+                           (dict(ws=None), 3), (dict(ws=FAKE + 128), 3), (dict(ws_bytes=0), 3)):
         assert call(kda, "kda_gdn_chunk_prefill", change) == status
+
+
+def test_workspace_bytes(kda):
+    record = 4 * 5120 + (3 * 64 + 4) * 4        # T and W in two terms, blocks on and below the diagonal; the row factors
+    n = kda.kda_gdn_chunk_prefill_workspace_bytes(130, 3, 4, 128, 64, num_k_heads=2)
+    assert n >= (130 // 64 + 3) * 4 * record and n <= (130 // 64 + 3) * 4 * record + 3 * 256 and n % 16 == 0
+    need = kda.kda_gdn_chunk_prefill_workspace_bytes(12, 3, 4, 64, 128, num_k_heads=2)
+    assert call(kda, "kda_gdn_chunk_prefill", dict(ws_bytes=need - 1)) == 3
+    assert kda.kda_gdn_chunk_prefill_workspace_bytes(130, 3, 4, 32, 64) == 0
+    assert kda.kda_gdn_chunk_prefill_workspace_bytes(0, 3, 4, 64, 64) == 0
+    for bad in ((-1, 3, 4, 64, 64), (2 ** 31 - 65, 1, 128, 64, 64), (8, -1, 4, 64, 64), (8, 3, 4, 96, 64), (8, 3, 0, 64, 64)):
+        with pytest.raises(ValueError):
+            kda.kda_gdn_chunk_prefill_workspace_bytes(*bad)
 
 
 @pytest.mark.parametrize("name", CALLS)
