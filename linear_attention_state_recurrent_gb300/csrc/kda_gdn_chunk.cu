@@ -40,7 +40,7 @@ struct Rec {
     static constexpr int MATRIX = 5120, T = 0, W = 2 * MATRIX, ROWS = 4 * MATRIX, BYTES = ROWS + (3 * C + 4) * 4, STAGE = 21376;
     __device__ static constexpr int panel(int k) { return k * 2048 - k * (k - 1) * 256; }
 };
-static_assert(Rec::BYTES % 16 == 0 && Rec::BYTES <= Rec::STAGE && Rec::STAGE % 128 == 0, "");
+static_assert(10 * BLK * 4 <= 2 * C * 128 && Rec::BYTES % 16 == 0 && Rec::BYTES <= Rec::STAGE && Rec::STAGE % 128 == 0, "");
 
 struct Args {
     GdnParams p;
@@ -199,28 +199,36 @@ struct Walk {
     __device__ __forceinline__ int n() const { return left < C ? left : C; }
 };
 
+// Whether a barrier's phase is over, asleep for a while if it is not: some twenty warps of a CTA wait at any time, and must not take
+// the others' issue slots (with a test in place of the try 720 us for 640 at 31,516 tokens x 32 heads).
+__device__ __forceinline__ bool phase_over(uint32_t mbar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity) : "memory");
+    return ok;
+}
+// The rest of a wait whose first try has not come through (out of line: there are many waits, and the instruction cache is small).
+__device__ __noinline__ bool wait_on(uint32_t mbar, uint32_t parity, volatile uint32_t *gave_up, uint32_t *err)
+{
+    const long long start = clock64();
+    while (!phase_over(mbar, parity)) {
+        if (*gave_up) return false;
+        if (clock64() - start > 4000000000ll) {
+            *gave_up = 1;
+            if (err) atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+    return true;
+}
 // A bounded wait that the CTA gives up as a whole: one that has run out (~2 s) says so to all the others.
 struct Waiter {
     volatile uint32_t *gave_up;
     uint32_t *err;
-    // Asleep for up to 1 ms a try: some twenty warps of a CTA wait at any time, and must not take the others' issue slots.
     __device__ __forceinline__ bool operator()(uint32_t mbar, uint32_t parity) const
     {
-        long long start = 0;
-        for (bool again = false;; again = true) {
-            uint32_t ok;
-            asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-                         " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity), "r"(1000000u) : "memory");
-            if (ok) return true;
-            if (*gave_up) return false;
-            const long long now = clock64();
-            if (!again) start = now;
-            else if (now - start > 4000000000ll) {
-                *gave_up = 1;
-                if (err) atomicOr(err, kErrTimeout);
-                return false;
-            }
-        }
+        return phase_over(mbar, parity) || wait_on(mbar, parity, gave_up, err);
     }
     // by a converged warp, one answer for all lanes
     __device__ __forceinline__ bool warp(uint32_t mbar, uint32_t parity) const
@@ -274,14 +282,16 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
     if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;
 }
 
+constexpr int PREP_CTAS = 6;
 // T diag(beta), W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
 // t - 64 of Q K^T, which one product of 128 x 64 gives. Four CTAs an SM: a warp's path through the inverse is bound by its latencies.
 template <int NH>
-__global__ void __launch_bounds__(128, 4) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
+__global__ void __launch_bounds__(128, PREP_CTAS) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
 {
     constexpr int K = 64 * NH;
-    extern __shared__ __align__(1024) unsigned char sm[];                     // the tiles of q and k
-    __shared__ __align__(16) float blocks[10 * BLK];                          // the blocks of A, then of T, on and below the diagonal
+    // the tiles of q and k; once their products and norms are there, the blocks of A, then of T, on and below the diagonal
+    extern __shared__ __align__(1024) unsigned char sm[];
+    float *blocks = reinterpret_cast<float *>(sm);
     __shared__ __align__(16) float cols[5 * C];   // b hi, b lo, beta, and of the keys b lo less the norm's logarithm, and e^{p - b} times the norm
     __shared__ uint64_t bars[2];
     __shared__ uint32_t tmem_at;
@@ -836,18 +846,18 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 more = w.next();
                 if (!wait.warp(o_done, c & 1)) break;
                 tc::fence_after_sync();
-                auto store = [&](auto whole) {
-#pragma unroll
-                    for (int i = 0; i < C; i += 16) {
-                        uint32_t x[16], y[16];
-                        tmem_ld(t0 + i, x);
-                        tmem_ld(t0 + C + i, y);
-                        tc::tmem_ld_wait();
-                        if (i == C - 16) {
-                            tc::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) arrive(o_free);
-                        }
+#pragma unroll 1
+                for (int i = 0; i < C; i += 16) {
+                    uint32_t x[16], y[16];
+                    tmem_ld(t0 + i, x);
+                    tmem_ld(t0 + C + i, y);
+                    tc::tmem_ld_wait();
+                    if (i == C - 16) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) arrive(o_free);
+                    }
+                    auto store = [&](auto whole) {
 #pragma unroll
                         for (int r = 0; r < 16; r += 2) {
                             const float2 o = ffma2(*reinterpret_cast<const float2 *>(qs + i + r), make_float2(__uint_as_float(x[r]), __uint_as_float(x[r + 1])),
@@ -858,10 +868,10 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                             if (whole || i + r + 1 < n) *out = static_cast<uint16_t>(o2 >> 16);
                             out += p.ld_out;
                         }
-                    }
-                };
-                if (n == C) store(std::true_type{});
-                else store(std::false_type{});
+                    };
+                    if (i + 16 <= n) store(std::true_type{});
+                    else store(std::false_type{});
+                }
                 __syncwarp();
                 if (lane == 0) arrive(empty(s));
             }
@@ -1058,7 +1068,9 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     if (e != cudaSuccess) return e;
     CUtensorMap qk, v;
     const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
-    const int VS = V;
+    // few chains: slices of their value columns, as long as there are idle multiprocessors for them
+    int VS = V;
+    while (VS > 32 && chains * (V / VS) * 2 <= sms) VS /= 2;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     if ((e = encode(&v, p, rows, cols, VS, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;
     const int64_t chunks = rows / C + num_seqs;

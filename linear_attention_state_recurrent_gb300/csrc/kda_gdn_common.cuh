@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kda_common.cuh"
+#include "kda_f32x2.cuh"
 #include "kda_gdn.h"
 
 namespace kda {
@@ -25,7 +26,8 @@ __device__ __forceinline__ float log_decay(const GdnParams &p, int64_t row, int 
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
 {
     hi = pack_bf16x2(x, y);
-    lo = pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+    const float2 d = fsub2(make_float2(x, y), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+    lo = pack_bf16x2(d.x, d.y);
 }
 
 // The sum of a warp's log-decays up to each lane. What is needed are differences of such sums, to an absolute error of
