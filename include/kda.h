@@ -474,6 +474,35 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
                    void *out, int64_t ld_out, int32_t out_dtype, uint32_t *err_flags, void *stream);
 
 /*
+ * kda_matmul — a product of 16-bit operands with bias, activation and residual in its epilogue:
+ *   out[m, n] = act(sum_k a[m, k] * w[n, k] + bias[n]) + residual[m, n]
+ * a: [M, ld_a] and w: [N, ld_w] (row n holds output n's weights), both of element type dtype (KDA_BF16 or KDA_FP16), K columns used
+ * of each; bias: [N] of bias_dtype (dtype or KDA_FP32), or NULL; act: KDA_ACT_*; residual: [M, ld_residual] of out_dtype, or NULL; out: [M, ld_out] of out_dtype
+ * (KDA_BF16, KDA_FP16 or KDA_FP32). Sums, bias, activation and residual are held in fp32 and rounded once. residual may be out itself;
+ * no other overlap is allowed. GELU is x (1 + erf(x / 2^(1/2))) / 2, GELU_TANH x (1 + tanh((2 / pi)^(1/2) (x + 0.044715 x^3))) / 2.
+ * Any strides >= the columns and alignments of the element types are accepted; operands whose base and row pitch are multiples
+ * of 16 bytes move by TMA, others by element loads, several times slower (pad rows, or ask kda_matmul_plan). M, N and K may be any
+ * size >= 1 (K = 0: act(bias) + residual; M or N = 0: nothing to do), up to 2^30 each. A split of the inner axis is joined in a fixed order: results
+ * repeat bit for bit. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT in *err_flags (may be NULL); what it was to give is not written.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_RELU 1
+#define KDA_ACT_SILU 2      /* x sigmoid(x) */
+#define KDA_ACT_SIGMOID 3
+#define KDA_ACT_GELU 4
+#define KDA_ACT_GELU_TANH 5
+int kda_matmul(const void *a, int64_t ld_a, const void *w, int64_t ld_w, int32_t dtype, int64_t M, int64_t N, int64_t K, const void *bias,
+               int32_t bias_dtype, int32_t act, const void *residual, int64_t ld_residual, void *out, int64_t ld_out, int32_t out_dtype,
+               uint32_t *err_flags, void *stream);
+
+/*
+ * kda_matmul_plan — how kda_matmul would compute a product on the current device: plan (host int32 [2]) receives the rows of a per
+ * tile (16 .. 128: single CTAs; 256: pairs; 0: element loads, for operands off 16-byte boundaries) and the CTAs that split the inner
+ * axis. Of a and w only the alignment counts; nothing is launched.
+ */
+int kda_matmul_plan(const void *a, int64_t ld_a, const void *w, int64_t ld_w, int64_t M, int64_t N, int64_t K, int32_t *plan);
+
+/*
  * kda_fp8_matmul_plan — how kda_fp8_matmul would compute a product on the current device: plan (host int32
  * [3]) receives the rows of a per tile (16, 32, 64: thin; 128: slim; 256: wide; 0: the slower kernel for
  * operands off 16-byte boundaries), the CTAs that split the inner axis, and the rows of w per tile. Of a

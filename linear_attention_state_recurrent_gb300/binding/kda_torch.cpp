@@ -300,6 +300,40 @@ PyObject *batch_maps(PyObject *, PyObject *const *v, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// (a, w, bias, act, residual, out, err_flags, stream) -> out; act: a KDA_ACT_*
+PyObject *matmul(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const Tensor *a, *w, *bias, *res, *out;
+    int64_t act;
+    if (!count(n, 8) || !tensor(v[0], "a", false, &a) || !tensor(v[1], "w", false, &w) || !tensor(v[2], "bias", true, &bias) ||
+        !integer(v[3], &act) || !tensor(v[4], "residual", true, &res) || !tensor(v[5], "out", false, &out))
+        return nullptr;
+    if (a->dim() != 2 || w->dim() != 2) return refuse("a and w must be 2-D with the same number of columns");
+    const ScalarType type = a->scalar_type();
+    if (type != ScalarType::BFloat16 && type != ScalarType::Half) return refuse("a must be bf16 or fp16");
+    const int64_t M = a->size(0), K = a->size(1), N = w->size(0);
+    const int code = code_of(out->scalar_type());
+    if (code < 0) return refuse("out must be bf16, fp16 or fp32");
+    int64_t ld_a, ld_w, ld_out, ld_res = 0;
+    uint32_t *err;
+    void *stream;
+    if (!matrix(*a, "a", type, M, K, nullptr, &ld_a) || !matrix(*w, "w", type, N, K, a, &ld_w) ||
+        !matrix(*out, "out", out->scalar_type(), M, N, a, &ld_out) || (res && !matrix(*res, "residual", out->scalar_type(), M, N, a, &ld_res)))
+        return nullptr;
+    if (bias && bias->scalar_type() != ScalarType::Float && !of_type(*bias, "bias", type)) return nullptr;
+    if (bias && (!vector(*bias, "bias", bias->scalar_type(), N, a) || bias->size(0) != N))
+        return PyErr_Occurred() ? nullptr : refuse("bias must have %lld entries", (long long)N);
+    if (!error_word(v[6], a, &err) || !stream_of(v[7], *a, &stream)) return nullptr;
+    const c10::cuda::CUDAGuard guard(a->device());
+    const int status = kda_matmul(a->data_ptr(), ld_a, w->data_ptr(), ld_w, code_of(type), M, N, K, bias ? bias->data_ptr() : nullptr,
+                                  bias ? code_of(bias->scalar_type()) : 0, static_cast<int32_t>(act), res ? res->data_ptr() : nullptr, ld_res,
+                                  out->data_ptr(), ld_out, code, err, stream);
+    if (status != KDA_OK) return PyLong_FromLong(status);
+    return Py_NewRef(v[5]);
+    END_HANDLE_TH_ERRORS
+}
+
 // A float argument.
 bool number(PyObject *o, double *v)
 {
@@ -417,6 +451,7 @@ PyMethodDef methods[] = {{"norm_quant", FAST(norm_quant), nullptr},
                          {"fp8_matmul", FAST(fp8_matmul), nullptr},
                          {"batch_maps", FAST(batch_maps), nullptr},
                          {"gdn", FAST(gdn), nullptr},
+                         {"matmul", FAST(matmul), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -16,17 +16,19 @@
 #include <climits>
 #include <mutex>
 #include <type_traits>
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "kda_f32x2.cuh"
 #include "kda_gdn_common.cuh"
+#include "kda_mma.cuh"
 #include "kda_pdl.cuh"
-#include "kda_tc.cuh"
 
 namespace kda {
 namespace gdn {
 namespace {
+
+using mma::arrive;
+using mma::elect_one;
+using mma::phase_over;
 
 constexpr int C = 64;                                  // rows of a chunk
 constexpr int ORDER = 256;                             // sequences that are sorted by length
@@ -84,16 +86,6 @@ __device__ __forceinline__ void mma_gram(uint32_t d, uint32_t ab, uint32_t id, b
                  :: "r"(d), "r"(ab), "n"(DESC_HIGH), "r"(id), "r"(add ? 1u : 0u));
 }
 
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ void arrive(uint32_t mbar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(mbar) : "memory");
-}
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -199,16 +191,9 @@ struct Walk {
     __device__ __forceinline__ int n() const { return left < C ? left : C; }
 };
 
-// Whether a barrier's phase is over, asleep for a while if it is not: some twenty warps of a CTA wait at any time, and must not take
-// the others' issue slots (with a test in place of the try 720 us for 640 at 31,516 tokens x 32 heads).
-__device__ __forceinline__ bool phase_over(uint32_t mbar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(mbar), "r"(parity) : "memory");
-    return ok;
-}
 // The rest of a wait whose first try has not come through (out of line: there are many waits, and the instruction cache is small).
+// Some twenty warps of a CTA wait at any time and must not take the others' issue slots: the tries sleep (with tests in their place
+// 720 us for 640 at 31,516 tokens x 32 heads).
 __device__ __noinline__ bool wait_on(uint32_t mbar, uint32_t parity, volatile uint32_t *gave_up, uint32_t *err)
 {
     const long long start = clock64();
@@ -987,31 +972,10 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
 
 // ---- host ---------------------------------------------------------------------------------
 
-// cuTensorMapEncodeTiled, fetched once through the runtime
-PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
 // Boxes of 64 rows by `box` columns of the packed q | k | v rows.
 cudaError_t encode(CUtensorMap *m, const GdnParams &p, int64_t rows, int64_t cols, int box, CUtensorMapSwizzle swizzle)
 {
-    const auto enc = encoder();
-    if (!enc) return cudaErrorSymbolNotFound;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ld_qkv) * 2};
-    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), C}, steps[2] = {1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(p.qkv), dims, strides, boxes, steps,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    return mma::encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.qkv, cols, rows, p.ld_qkv, box, C, swizzle);
 }
 
 // The multiprocessors of the current device, the kernels' shared-memory limits set there, once; kept only on success.

@@ -48,7 +48,8 @@ EXPORTED = ("kda_last_error", "kda_status_string", "kda_gate", "kda_packed_decod
             "kda_chunk_prefill", "kda_mixed_batch", "kda_chunk_prefill_no_alloc",
             "kda_norm_quant", "kda_fp8_matmul", "kda_fp8_matmul_plan",
             "kda_selftest_fp8_matmul", "kda_batch_maps",
-            "kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill", "kda_gdn_chunk_prefill_workspace_bytes")
+            "kda_gdn_decode", "kda_gdn_spec_verify", "kda_gdn_chunk_prefill", "kda_gdn_chunk_prefill_workspace_bytes",
+            "kda_matmul", "kda_matmul_plan")
 
 KDA_NO_ALLOC_SCRATCH_BYTES = 64 * 1024 * 1024   # the fixed scratch of kda_chunk_prefill_no_alloc
 
@@ -133,6 +134,10 @@ def _load():
     lib.kda_fp8_matmul_plan.argtypes = [P, I64, P, I64, I64, I64, I64, P]
     lib.kda_selftest_fp8_matmul.restype = ctypes.c_int
     lib.kda_selftest_fp8_matmul.argtypes = [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, P, I64, I32, I32, P, P]
+    lib.kda_matmul.restype = ctypes.c_int
+    lib.kda_matmul.argtypes = [P, I64, P, I64, I32, I64, I64, I64, P, I32, I32, P, I64, P, I64, I32, P, P]
+    lib.kda_matmul_plan.restype = ctypes.c_int
+    lib.kda_matmul_plan.argtypes = [P, I64, P, I64, I64, I64, I64, P]
     GP = ctypes.POINTER(KdaGdnHeads)
     lib.kda_gdn_decode.restype = ctypes.c_int
     lib.kda_gdn_decode.argtypes = [P, I64, P, I64, P, I64, I64, GP, SP, P, I64, P, P]
@@ -547,7 +552,7 @@ class _TorchBinding:
         spec = importlib.util.spec_from_file_location("_kda_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        for f in ("norm_quant", "fp8_matmul", "batch_maps", "gdn"):
+        for f in ("norm_quant", "fp8_matmul", "batch_maps", "gdn", "matmul"):
             setattr(self, f, getattr(module, f))
         return getattr(module, name)
 
@@ -615,6 +620,41 @@ def kda_selftest_fp8_matmul(a, a_scales, w, w_scales, out, err_flags, stalled=0,
     if type(r) is int:
         _check(r, "kda_selftest_fp8_matmul")
     return r
+
+
+_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "sigmoid": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+def kda_matmul(a, w, *, bias=None, activation=None, residual=None, out=None, out_dtype=None, err_flags=None, stream=None):
+    """out[m, n] = activation(sum_k a[m, k] w[n, k] + bias[n]) + residual[m, n], rounded once.
+
+    a: bf16 or fp16 [M, K]; w: [N, K] of the same type; bias: [N] of that type or fp32; activation: None, "relu", "silu",
+    "sigmoid", "gelu" (erf) or "gelu_tanh"; residual: [M, N] of out's type (it may be out itself); out: bf16, fp16 or fp32 [M, N],
+    allocated as out_dtype (a's type by default) when not given. Operands with rows on 16-byte boundaries move by TMA, others
+    several times slower (kda_matmul_plan tells). Returns out."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(map(repr, _ACTIVATIONS))} (got {activation!r})")
+    if out is None:
+        out_dtype = a.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be bf16, fp16 or fp32")
+        with _on(stream):
+            out = torch.empty(a.shape[0], w.shape[0], dtype=out_dtype, device=a.device)
+    r = _torch_binding.matmul(a, w, bias, _ACTIVATIONS[activation], residual, out, err_flags, _handle(stream))
+    if type(r) is int:
+        _check(r, "kda_matmul")
+    return r
+
+
+def kda_matmul_plan(a, w):
+    """How kda_matmul would compute a product of these operands on the current device: (rows of a per tile, CTAs that split the inner
+    axis); 0 rows: element loads, for operands off 16-byte boundaries."""
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a and w must be 2-D with the same number of columns")
+    plan = (ctypes.c_int32 * 2)()
+    ld = [max(t.stride(0), t.shape[1]) if t.shape[0] == 1 else t.stride(0) for t in (a, w)]   # the stride of a single row says nothing
+    _check(lib.kda_matmul_plan(_ptr(a), ld[0], _ptr(w), ld[1], a.shape[0], w.shape[0], a.shape[1], plan), "kda_matmul_plan")
+    return tuple(plan)
 
 
 BatchMaps = collections.namedtuple("BatchMaps", "order cu_seqlens state_indices num_decodes positions slot_map "
