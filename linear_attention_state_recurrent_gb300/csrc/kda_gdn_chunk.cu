@@ -36,7 +36,7 @@ constexpr int BLK = 16 * 20;                           // floats of a 16 x 16 bl
 
 // A chunk and head's record. Of the 64 x 64 matrices T diag(beta) and W, hi and lo each, the blocks on and below the diagonal: a panel
 // for every 16 columns with the rows from 16 k on, in the order the MMAs read without a swizzle (8 rows of 16 bytes follow each
-// other, the next 8 columns 128 bytes on, the next 8 rows 256). Then the row factors: e^b |k|^-1, e^{b_n - b} |k|^-1,
+// other, the next 8 columns 128 bytes on, the next 8 rows 256). Then the row factors: -e^b |k|^-1, e^{b_n - b} |k|^-1,
 // scale e^b |q|^-1 (64 floats each) and e^{b_n}.
 struct Rec {
     static constexpr int MATRIX = 5120, T = 0, W = 2 * MATRIX, ROWS = 4 * MATRIX, BYTES = ROWS + (3 * C + 4) * 4, STAGE = 21376;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(128, PREP_CTAS) prep_kernel(const __grid_const
         const float scale = (query ? p.scale : cols[2 * C + r]) * norm;
         if (!query) {
             const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1];
-            set[r] = ex2(b_hi + b_lo) * norm;
+            set[r] = -ex2(b_hi + b_lo) * norm;
             set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * norm;
             if (r == 0) set[3 * C] = ex2(e_hi + e_lo);
             cols[3 * C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
@@ -605,7 +605,7 @@ constexpr int STAGES = 3;          // chunks in shared memory
 struct Smem {
     static constexpr int QK = 2 * HALF, V = C * 256;
     static constexpr int REC = QK + V, STAGE = QK + V + Rec::STAGE;
-    static constexpr int SORT = STAGES * STAGE, BARS = SORT + ORDER * 2, NBARS = 3 * STAGES + 9, END = BARS + NBARS * 8 + 16;
+    static constexpr int SORT = STAGES * STAGE, BARS = SORT + ORDER * 2, NBARS = 3 * STAGES + 13, END = BARS + NBARS * 8 + 16;
 };
 static_assert(Smem::STAGE % 128 == 0 && Smem::END <= 232448, "shared memory of a CTA");
 
@@ -628,8 +628,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     auto empty = [&](int s) { return b0 + (STAGES + s) * 8; };              // and is no longer needed
     auto clean = [&](int s) { return b0 + (2 * STAGES + s) * 8; };          // its keys behind the sequence's end are zeros
     const uint32_t bx = b0 + 3 * STAGES * 8;
-    const uint32_t s_ready = bx, ks_done = bx + 8, y_ready = bx + 16, u_done = bx + 24, u_ready = bx + 32, s_done = bx + 40, o_done = bx + 48,
-                   o_free = bx + 56, drained = bx + 64;
+    const uint32_t s_hi = bx, s_lo = bx + 8, ks_done = bx + 16, y_hi = bx + 24, y_lo = bx + 32, u_done = bx + 40, u_hi = bx + 48, u_lo = bx + 56,
+                   w_ready = bx + 64, s_done = bx + 72, o_done = bx + 80, o_free = bx + 88, drained = bx + 96;
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(sm + Smem::BARS + Smem::NBARS * 8);   // tensor memory's base, whether a wait has given up
     uint16_t *order = reinterpret_cast<uint16_t *>(sm + Smem::SORT);
     const GdnParams &p = a.p;
@@ -640,11 +640,9 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             tc::mbar_init(empty(i), 1 + VW);
             tc::mbar_init(clean(i), 1);
         }
-        tc::mbar_init(s_ready, 4 * VW);
+        for (const uint32_t b : {s_hi, s_lo, y_hi, y_lo, u_hi, u_lo, w_ready}) tc::mbar_init(b, 4 * VW);
         tc::mbar_init(ks_done, 1);
-        tc::mbar_init(y_ready, 4 * VW);
         tc::mbar_init(u_done, 1);
-        tc::mbar_init(u_ready, 4 * VW);
         tc::mbar_init(s_done, 1);
         tc::mbar_init(o_done, 1);
         tc::mbar_init(o_free, VW);
@@ -693,16 +691,33 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) arrive(mbar);
             };
-            auto give_s = [&] {                                               // S as the next products' operand
+            // Operands are given term by term: the products of the first are under way while the second is formed.
+            auto give_s = [&] {
+                uint32_t hi[KP / 2];
+#pragma unroll
+                for (int i = 0; i < KP / 2; i++) hi[i] = pack_bf16x2(S[i].x, S[i].y);
+#pragma unroll
+                for (int i = 0; i < KP / 2; i += 8) tmem_st8(ts + i, *reinterpret_cast<const uint32_t(*)[8]>(hi + i));
+                give(s_hi);
 #pragma unroll
                 for (int i = 0; i < KP / 2; i += 8) {
-                    uint32_t hi[8], lo[8];
+                    uint32_t lo[8];
 #pragma unroll
-                    for (int x = 0; x < 8; x++) split2(S[i + x].x, S[i + x].y, hi[x], lo[x]);
-                    tmem_st8(ts + i, hi);
+                    for (int x = 0; x < 8; x++) lo[x] = rest2(S[i + x].x, S[i + x].y, hi[i + x]);
                     tmem_st8(ts + KP / 2 + i, lo);
                 }
-                give(s_ready);
+                give(s_lo);
+            };
+            auto give2 = [&](const float2 (&y)[8], uint32_t at, uint32_t hi_bar, uint32_t lo_bar) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) hi[e] = pack_bf16x2(y[e].x, y[e].y);
+                tmem_st8(at, hi);
+                give(hi_bar);
+#pragma unroll
+                for (int e = 0; e < 8; e++) lo[e] = rest2(y[e].x, y[e].y, hi[e]);
+                tmem_st8(at + 8, lo);
+                give(lo_bar);
             };
             bool more = w.begin(), first = true;
             for (uint32_t c = 0; more; c++) {
@@ -739,49 +754,49 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 if (!wait.warp(ks_done, one)) break;
                 tc::fence_after_sync();
                 {
-                    uint32_t x[16], hi[8], lo[8];
+                    uint32_t x[16];
+                    float2 y[8];
                     tmem_ld(ty, x);
-                    tc::tmem_ld_wait();
                     const float4 *ys = reinterpret_cast<const float4 *>(set + part * 16);
+                    tc::tmem_ld_wait();
+                    if (n - part * 16 < 16) {
+#pragma unroll
+                        for (int e = 0; e < 16; e++)
+                            if (part * 16 + e >= n) {
+                                x[e] = 0u;
+                                v[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
+                            }
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const float4 f = ys[e / 2];
-                        float2 y = ffma2(e % 2 ? make_float2(-f.z, -f.w) : make_float2(-f.x, -f.y),
-                                         make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                         make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)));
-                        if (n < C) {
-                            if (part * 16 + 2 * e >= n) y.x = 0.f;
-                            if (part * 16 + 2 * e + 1 >= n) y.y = 0.f;
-                        }
-                        split2(y.x, y.y, hi[e], lo[e]);
+                        y[e] = ffma2(e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                     make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)));
                     }
-                    tmem_st8(ty, hi);
-                    tmem_st8(ty + 8, lo);
+                    give2(y, ty, y_hi, y_lo);
                 }
-                give(y_ready);
-                // U, for the outputs, and scaled, for the state
+                // U scaled, for the state, and then as it is, for the outputs
                 if (!wait.warp(u_done, one)) break;
                 tc::fence_after_sync();
                 {
-                    uint32_t x[16], hi[8], lo[8];
+                    uint32_t x[16];
+                    float2 z[8];
                     tmem_ld(tu, x);
-                    tc::tmem_ld_wait();
                     const float4 *us = reinterpret_cast<const float4 *>(set + C + part * 16);
+                    tc::tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const float4 f = us[e / 2];
-                        const float2 z = fmul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                               e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
-                        split2(z.x, z.y, hi[e], lo[e]);
+                        z[e] = fmul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
                     }
-                    tmem_st8(ty, hi);
-                    tmem_st8(ty + 8, lo);
+                    give2(z, ty, u_hi, u_lo);
+                    uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 8; e++) split2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hi[e], lo[e]);
                     tmem_st8(tu, hi);
                     tmem_st8(tu + 8, lo);
+                    give(w_ready);
                 }
-                give(u_ready);
                 // S <- gamma S + its increment
                 more = w.next();
                 if (!wait.warp(s_done, one)) break;
@@ -891,51 +906,72 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         for (uint32_t c = 0; more; c++) {
             const int s = c % STAGES;
             const uint32_t one = c & 1, at = s0 + s * Smem::STAGE, rec = at + Smem::REC;
-            if (!wait.warp(full(s), (c / STAGES) & 1) || !wait.warp(s_ready, one)) break;
+            if (!wait.warp(full(s), (c / STAGES) & 1) || !wait.warp(s_hi, one)) break;
             tc::fence_after_sync();
-            // S^T times the keys or the queries (the rows `from` on), both terms of S
-            auto times_s = [&](uint32_t d, uint32_t from) {
+            // a term (x) of S^T times the keys or the queries (the rows `from` on)
+            auto times_s = [&](uint32_t d, uint32_t from, int x) {
 #pragma unroll
-                for (int x = 0; x < 2; x++)
-#pragma unroll
-                    for (int k = 0; k < K / 16; k++)
-                        mma_t(d, tmem + T_S + k / (KP / 16) * KP + x * (KP / 2) + k % (KP / 16) * 8, desc_k(from + (k / 4) * HALF + (k % 4) * 32), idesc(C), x + k > 0);
+                for (int k = 0; k < K / 16; k++)
+                    mma_t(d, tmem + T_S + k / (KP / 16) * KP + x * (KP / 2) + k % (KP / 16) * 8, desc_k(from + (k / 4) * HALF + (k % 4) * 32), idesc(C), x + k > 0);
             };
-            // a record's matrix times Y or U: hi hi, lo hi, hi lo; rows before 16 k are zero in columns 16 k ..
-            auto times_rec = [&](uint32_t d, uint32_t from, uint32_t matrix) {
+            // a term of a record's matrix (y) times one (x) of Y or U; rows before 16 k are zero in columns 16 k ..
+            auto times_rec = [&](uint32_t d, uint32_t from, uint32_t matrix, int x, int y, bool first) {
 #pragma unroll
-                for (int x = 0; x < 3; x++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_t<PANEL_HIGH>(d + 16 * k, from + k * 16 + (x == 1 ? 8 : 0), desc_panel(matrix + (x == 2 ? Rec::MATRIX : 0) + Rec::panel(k)), idesc(C - 16 * k), x + k > 0);
+                for (int k = 0; k < 4; k++)
+                    mma_t<PANEL_HIGH>(d + 16 * k, from + k * 16 + x * 8, desc_panel(matrix + y * Rec::MATRIX + Rec::panel(k)), idesc(C - 16 * k), !first || k > 0);
             };
+            if (elect_one()) times_s(tmem + T_Y, at, 0);
+            __syncwarp();
+            if (!wait.warp(s_lo, one)) break;
+            tc::fence_after_sync();
             if (elect_one()) {
-                times_s(tmem + T_Y, at);
+                times_s(tmem + T_Y, at, 1);
                 tc::commit(ks_done);
             }
             __syncwarp();
             if (c > 0 && !wait.warp(o_free, one ^ 1)) break;
             tc::fence_after_sync();
-            if (elect_one()) times_s(tmem + T_O, at + C * 128);
+            if (elect_one()) {
+                times_s(tmem + T_O, at + C * 128, 0);
+                times_s(tmem + T_O, at + C * 128, 1);
+            }
             __syncwarp();
-            if (!wait.warp(y_ready, one)) break;
+            if (!wait.warp(y_hi, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T);
+                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 0, 0, true);
+                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 0, 1, false);
+            }
+            __syncwarp();
+            if (!wait.warp(y_lo, one)) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 1, 0, false);
                 tc::commit(u_done);
             }
             __syncwarp();
-            if (!wait.warp(u_ready, one) || (w.left < C && !wait.warp(clean(s), (c / STAGES) & 1))) break;
+            // the state's increment
+            auto increment = [&](int x) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) mma_t(tmem + T_S, tmem + T_Y + k * 16 + x * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
+            };
+            if (!wait.warp(u_hi, one) || (w.left < C && !wait.warp(clean(s), (c / STAGES) & 1))) break;
+            tc::fence_after_sync();
+            if (elect_one()) increment(0);
+            __syncwarp();
+            if (!wait.warp(u_lo, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                // the state's increment, both terms of U
-#pragma unroll
-                for (int x = 0; x < 2; x++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_t(tmem + T_S, tmem + T_Y + k * 16 + x * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
+                increment(1);
                 tc::commit(s_done);
-                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W);
+            }
+            __syncwarp();
+            if (!wait.warp(w_ready, one)) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 0, 0, true);
+                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 1, 0, false);
+                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 0, 1, false);
                 tc::commit(empty(s));
                 tc::commit(o_done);
             }

@@ -13,6 +13,7 @@
 #include <atomic>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 #include <cuda_fp16.h>
 
 #include "kda.h"
@@ -123,26 +124,26 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
 // LOOSE: operands on any boundaries, loaded by eight warps more.
 template <int NT, bool LOOSE>
 struct Tile {
-    static constexpr int THREADS = LOOSE ? 448 : 192;               // copies, MMAs, four epilogue warps
+    static constexpr int EW = 8;                                    // epilogue warps: two for each quarter of the TMEM lanes
+    static constexpr int THREADS = (2 + EW + (LOOSE ? 8 : 0)) * 32; // copies, MMAs, the epilogue's, and the loose operands' copies
     static constexpr int STAGE = 128 * 128 + NT * 128;
-    static constexpr int STAGES = NT > 64 ? 3 : NT > 32 ? 4 : NT > 16 ? 5 : 6;
-    static constexpr int SMEM = STAGES * STAGE;                     // and the split's sums once it is drained: two CTAs per SM
+    static constexpr int TWO = 113 * 1024 / STAGE, ONE = 226 * 1024 / STAGE < 10 ? 226 * 1024 / STAGE : 10;   // stages with two CTAs per SM, with one
     static constexpr int COLS = NT < 32 ? 32 : NT;                  // of tensor memory
 };
 
 template <int NT, bool LOOSE>
 __global__ void __launch_bounds__(Tile<NT, LOOSE>::THREADS, LOOSE ? 1 : 2)
-tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MatmulParams p, const int split)
+tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MatmulParams p, const int split, const int stages)
 {
     using T = Tile<NT, LOOSE>;
-    static_assert(NT * 132 * 4 <= T::SMEM, "a split's sums");
+    static_assert(NT * 132 * 4 <= T::TWO * T::STAGE, "a split's sums, in the ring once it is drained");
     extern __shared__ __align__(1024) unsigned char sm[];
-    __shared__ uint64_t bars[2 * T::STAGES + 1];
+    __shared__ uint64_t bars[2 * T::ONE + 1];
     __shared__ uint32_t tmem_at, failed;
     const uint32_t s0 = tc::smem_addr(sm), b0 = tc::smem_addr(bars);
     auto full = [&](int s) { return b0 + s * 8; };
-    auto empty = [&](int s) { return b0 + (T::STAGES + s) * 8; };
-    const uint32_t done = b0 + 2 * T::STAGES * 8;
+    auto empty = [&](int s) { return b0 + (T::ONE + s) * 8; };
+    const uint32_t done = b0 + 2 * T::ONE * 8;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = blockIdx.x % split, n0 = blockIdx.x / split * 128, m0 = blockIdx.y * NT;
     const int steps = (p.K + BK - 1) / BK;
@@ -154,7 +155,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         tc::tma_load_2d(at + 128 * 128, &tm_a, k * BK, m0, full(s));
     };
     if (threadIdx.x == 0) {
-        for (int s = 0; s < T::STAGES; s++) {
+        for (int s = 0; s < stages; s++) {
             tc::mbar_init(full(s), LOOSE ? 8 : 1);
             tc::mbar_init(empty(s), 1);
         }
@@ -166,7 +167,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // no global read before this
-    const int ahead = min(T::STAGES, k1 - k0);
+    const int ahead = min(stages, k1 - k0);
     if (!LOOSE && threadIdx.x == 0)                        // the ring's first turn needs nothing but the barriers of this thread
         for (int i = 0; i < ahead; i++) load(k0 + i, i);
     if (warp == 1) tc::tmem_alloc<T::COLS>(tc::smem_addr(&tmem_at));
@@ -178,40 +179,44 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 
     if (warp == 0) {
         if (!LOOSE && lane == 0) {
-            int k = k0 + ahead, c = ahead;
-            for (; k < k1; k++, c++) {
-                const int s = c % T::STAGES;
-                if (!wait(empty(s), (c / T::STAGES - 1) & 1)) { report(p); break; }
+            int s = 0;
+            uint32_t phase = 0;
+            for (int k = k0 + ahead; k < k1; k++) {
+                if (!wait(empty(s), phase)) { report(p); break; }
                 load(k, s);
+                if (++s == stages) { s = 0; phase ^= 1; }
             }
-            for (int i = c > T::STAGES ? c - T::STAGES : 0; i < c; i++) (void)wait(full(i % T::STAGES), (i / T::STAGES) & 1);   // none in flight
+            for (int i = 0; i < ahead; i++) (void)wait(full(i), i < s ? phase ^ 1u : phase);   // none in flight
         }
         __syncwarp();
     } else if (warp == 1) {
         const uint32_t id = (1u << 4) | (p.dtype == KDA_BF16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(NT >> 3) << 17) | (8u << 24);
-        for (int c = 0; c < k1 - k0; c++) {
-            const int s = c % T::STAGES;
-            if (!wait_warp(full(s), (c / T::STAGES) & 1)) { report(p); failed = 1; break; }
+        int s = 0;
+        uint32_t phase = 0;
+        for (int k = k0; k < k1; k++) {
+            if (!wait_warp(full(s), phase)) { report(p); failed = 1; break; }
             tc::fence_after_sync();
             const uint32_t at = s0 + s * T::STAGE;
             if (elect_one()) {
-                mma_stage<1>(tmem, at, at + 128 * 128, id, c > 0);
+                mma_stage<1>(tmem, at, at + 128 * 128, id, k > k0);
                 tc::commit(empty(s));
             }
             __syncwarp();
+            if (++s == stages) { s = 0; phase ^= 1; }
         }
         if (elect_one()) tc::commit(done);
         __syncwarp();
-    } else if (LOOSE && warp >= 6) {
+    } else if (LOOSE && warp >= 2 + T::EW) {
         // lanes along the inner axis, two elements each; rows and columns past the matrices are zeros
         const uint16_t *pa = static_cast<const uint16_t *>(p.a), *pw = static_cast<const uint16_t *>(p.w);
-        for (int c = 0; c < k1 - k0; c++) {
-            const int s = c % T::STAGES;
-            if (c >= T::STAGES && !wait_warp(empty(s), (c / T::STAGES - 1) & 1)) { report(p); break; }
-            const int64_t k = static_cast<int64_t>(k0 + c) * BK + 2 * lane;
+        int s = 0;
+        uint32_t phase = 1;
+        for (int c = k0; c < k1; c++) {
+            if (!wait_warp(empty(s), phase)) { report(p); break; }
+            const int64_t k = static_cast<int64_t>(c) * BK + 2 * lane;
             unsigned char *at = sm + s * T::STAGE;
 #pragma unroll 8
-            for (int r = warp - 6; r < 128 + NT; r += 8) {
+            for (int r = warp - 2 - T::EW; r < 128 + NT; r += 8) {
                 const int64_t row = r < 128 ? n0 + r : m0 + r - 128;
                 const uint16_t *from = r < 128 ? pw + row * p.ld_w : pa + row * p.ld_a;
                 const bool in = row < (r < 128 ? p.N : p.M);
@@ -221,11 +226,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(full(s));
+            if (++s == stages) { s = 0; phase ^= 1; }
         }
     }
     // the sums: a thread has one row of W, a column of the output
     const int quarter = warp % 4, n = n0 + quarter * 32 + lane;
-    const bool epilogue = warp >= 2 && warp < 6;
+    const bool epilogue = warp >= 2 && warp < 2 + T::EW;
+    const int i0 = 16 * ((warp - 2) / 4), step = 16 * (T::EW / 4);          // rows of A in turn
     auto finish = [&](float (&v)[16], int m) {             // outputs m .. m + 15 of column n
         if (n >= p.N) return;
         if (p.bias) {
@@ -249,7 +256,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         tc::fence_after_sync();
         ok &= *static_cast<volatile uint32_t *>(&failed) == 0;
         if (!ok) report(p);
-        for (int i = 0; ok && i < NT && m0 + i < p.M; i += 16) {
+        for (int i = i0; ok && i < NT && m0 + i < p.M; i += step) {
             float v[16];
             tc::tmem_ld16(tq + i, v);
             tc::tmem_ld_wait();
@@ -268,7 +275,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             tc::fence_after_sync();
             if (!ok) failed = 1;
 #pragma unroll 1
-            for (int i = 0; ok && i < NT; i += 16) {
+            for (int i = i0; ok && i < NT && m0 + i < p.M; i += step) {
                 float v[16];
                 tc::tmem_ld16(tq + i, v);
                 tc::tmem_ld_wait();
@@ -287,16 +294,20 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             }
             if (bad) report(p);
             const int per = (NT / 16 + split - 1) / split * 16;
-            for (int i = rank * per; !bad && i < min(NT, (rank + 1) * per) && m0 + i < p.M; i += 16) {
+            for (int i = rank * per + i0; !bad && i < min(NT, (rank + 1) * per) && m0 + i < p.M; i += step) {
                 float v[16] = {};
+                const int rows = min(16, p.M - m0 - i);
+#pragma unroll 2
                 for (int k = 0; k < split; k++) {
                     const uint32_t at = in_cta(tc::smem_addr(sums + i * 132 + quarter * 32 + lane), k);
+                    float y[16];
 #pragma unroll
                     for (int x = 0; x < 16; x++) {
-                        float y;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(at + x * 132 * 4));
-                        v[x] += y;
+                        y[x] = 0.f;
+                        if (x < rows) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y[x]) : "r"(at + x * 132 * 4));
                     }
+#pragma unroll
+                    for (int x = 0; x < 16; x++) v[x] += y[x];
                 }
                 finish(v, m0 + i);
             }
@@ -451,6 +462,25 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 }
                 __syncwarp();
             };
+            // box x between memory and shared memory where TMA cannot: row after row, lanes along the columns
+            auto loose = [&](auto in, int x) {
+                unsigned char *from = boxes + (x & 1) * T::BOX;
+                const int cols = min(wide, p.N - n0 - x * wide), rows = min(32, p.M - m0);
+#pragma unroll 4
+                for (int r = 0; r < rows; r++) {
+                    const int64_t at = static_cast<int64_t>(m0 + r) * (in ? p.ld_res : p.ld_out) + n0 + x * wide;
+                    for (int c = lane; c < cols; c += 32) {
+                        unsigned char *e = from + r * 128 + (((c * es >> 4) ^ (r & 7)) << 4) + (c * es & 15);
+                        if (es == 4) {
+                            if (in) *reinterpret_cast<uint32_t *>(e) = static_cast<const uint32_t *>(p.res)[at + c];
+                            else static_cast<uint32_t *>(p.out)[at + c] = *reinterpret_cast<const uint32_t *>(e);
+                        } else {
+                            if (in) *reinterpret_cast<uint16_t *>(e) = static_cast<const uint16_t *>(p.res)[at + c];
+                            else static_cast<uint16_t *>(p.out)[at + c] = *reinterpret_cast<const uint16_t *>(e);
+                        }
+                    }
+                }
+            };
             if (p.res && blocks > 0 && by_tma(0)) fetch(0);
             if (!wait_warp(tfull(b), tphase)) {
                 report(p);
@@ -478,6 +508,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
                     }
+                } else {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+                    if (p.res) loose(std::true_type{}, x);
+                    __syncwarp();
                 }
 #pragma unroll 1
                 for (int h = 0; h < wide; h += 32) {
@@ -490,47 +525,37 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                         for (int j = 0; j < 32; j++) v[j] += __shfl_sync(0xffffffffu, own, j);
                     }
                     activate(v, p.act);
-                    if (tma) {
-                        // 16-byte piece j of the row is at j ^ (row % 8)
-                        if (es == 4) {
+                    // 16-byte piece j of the row is at j ^ (row % 8)
+                    if (es == 4) {
 #pragma unroll
-                            for (int j = 0; j < 8; j++) {
-                                float4 *to = reinterpret_cast<float4 *>(box + ((j ^ (lane & 7)) << 4));
-                                float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                                if (p.res) { const float4 r = *to; o.x += r.x; o.y += r.y; o.z += r.z; o.w += r.w; }
-                                *to = o;
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                uint4 *to = reinterpret_cast<uint4 *>(box + (((h / 8 + j) ^ (lane & 7)) << 4));
-                                uint32_t o[4];
-                                if (p.res) {
-                                    const uint4 r = *to;
-                                    const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                                    for (int q = 0; q < 4; q++) {
-                                        float2 f;
-                                        if (p.out_dtype == KDA_BF16) f = make_float2(__uint_as_float(rr[q] << 16), __uint_as_float(rr[q] & 0xffff0000u));
-                                        else f = __half22float2(*reinterpret_cast<const __half2 *>(&rr[q]));
-                                        v[8 * j + 2 * q] += f.x;
-                                        v[8 * j + 2 * q + 1] += f.y;
-                                    }
-                                }
-#pragma unroll
-                                for (int q = 0; q < 4; q++)
-                                    o[q] = p.out_dtype == KDA_BF16 ? pack_bf16x2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]) : tc::pack_f16x2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]);
-                                *to = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                        for (int j = 0; j < 8; j++) {
+                            float4 *to = reinterpret_cast<float4 *>(box + ((j ^ (lane & 7)) << 4));
+                            float4 o = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                            if (p.res) { const float4 r = *to; o.x += r.x; o.y += r.y; o.z += r.z; o.w += r.w; }
+                            *to = o;
                         }
-                    } else if (m0 + lane < p.M) {
-                        const int64_t row = m0 + lane;
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            if (n + j < p.N) {
-                                const float r = p.res ? load_as(p.res, row * p.ld_res + n + j, p.out_dtype) : 0.f;
-                                store_as(p.out, row * p.ld_out + n + j, p.out_dtype, p.res ? v[j] + r : v[j]);
+                        for (int j = 0; j < 4; j++) {
+                            uint4 *to = reinterpret_cast<uint4 *>(box + (((h / 8 + j) ^ (lane & 7)) << 4));
+                            uint32_t o[4];
+                            if (p.res) {
+                                const uint4 r = *to;
+                                const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                                for (int q = 0; q < 4; q++) {
+                                    float2 f;
+                                    if (p.out_dtype == KDA_BF16) f = make_float2(__uint_as_float(rr[q] << 16), __uint_as_float(rr[q] & 0xffff0000u));
+                                    else f = __half22float2(*reinterpret_cast<const __half2 *>(&rr[q]));
+                                    v[8 * j + 2 * q] += f.x;
+                                    v[8 * j + 2 * q + 1] += f.y;
+                                }
                             }
+#pragma unroll
+                            for (int q = 0; q < 4; q++)
+                                o[q] = p.out_dtype == KDA_BF16 ? pack_bf16x2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]) : tc::pack_f16x2(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]);
+                            *to = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
                     }
                 }
                 if (tma) {
@@ -541,6 +566,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                                      :: "l"(&tm_out), "r"(n0 + x * wide), "r"(m0), "r"(tc::smem_addr(boxes + (x & 1) * T::BOX)) : "memory");
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
+                    __syncwarp();
+                } else {
+                    __syncwarp();
+                    loose(std::false_type{}, x);
+                    tc::fence_proxy_async();   // the box may be TMA's next
                     __syncwarp();
                 }
             }
@@ -601,10 +631,10 @@ struct Device {
     cudaError_t ask_tile(int which)
     {
         using T = Tile<NT, LOOSE>;
-        cudaError_t e = cudaFuncSetAttribute(tile_kernel<NT, LOOSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(tile_kernel<NT, LOOSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::ONE * T::STAGE);
         fit[which][1] = sms * (LOOSE ? 1 : 2);
         for (int split = 2; split <= 8 && e == cudaSuccess; split++) {
-            Launch l(dim3(split), T::THREADS, T::SMEM, split, nullptr);
+            Launch l(dim3(split), T::THREADS, T::TWO * T::STAGE, split, nullptr);
             l.at[0] = l.at[1];     // the cluster alone
             l.cfg.numAttrs = 1;
             int n = 0;
@@ -717,8 +747,11 @@ cudaError_t run_tile(const MatmulParams &p, const Choice &c, cudaStream_t stream
         if ((e = encode(&tw, type_of(p.dtype), 2, p.w, p.K, p.N, c.ld_w, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
         if ((e = encode(&ta, type_of(p.dtype), 2, p.a, p.K, p.M, c.ld_a, BK, NT, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     }
-    Launch l(dim3(static_cast<unsigned>((p.N - 1) / 128 + 1) * c.split, static_cast<unsigned>((p.M - 1) / NT + 1)), T::THREADS, T::SMEM, c.split, stream);
-    return cudaLaunchKernelEx(&l.cfg, tile_kernel<NT, LOOSE>, ta, tw, p, c.split);
+    const dim3 grid(static_cast<unsigned>((p.N - 1) / 128 + 1) * c.split, static_cast<unsigned>((p.M - 1) / NT + 1));
+    // a CTA that has a multiprocessor to itself takes all of its shared memory: what is in flight is what its stream is bound by
+    const int stages = static_cast<int64_t>(grid.x) * grid.y <= c.device->sms ? T::ONE : T::TWO;
+    Launch l(grid, T::THREADS, stages * T::STAGE, c.split, stream);
+    return cudaLaunchKernelEx(&l.cfg, tile_kernel<NT, LOOSE>, ta, tw, p, c.split, stages);
 }
 
 cudaError_t run_pair(const MatmulParams &p, const Choice &c, cudaStream_t stream)
