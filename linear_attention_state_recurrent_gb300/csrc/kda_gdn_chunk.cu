@@ -228,12 +228,10 @@ __device__ __forceinline__ constexpr int block_at(int a, int b) { return (a * (a
 // pass it is left out) and each chunk's rows. Error bits are the chain's.
 __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args a)
 {
-    __shared__ int sums[32];
-    __shared__ int base;
+    __shared__ int sums[32], firsts[1024], starts[1024], lens[1024];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) base = 0;
     pdl_wait_then_release();   // no global read before this
-    __syncthreads();
+    int base = 0;
     for (int s0 = 0; s0 < a.num_seqs; s0 += 1024) {
         uint32_t bad = 0;
         const int s = s0 + tid;
@@ -247,21 +245,29 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
         }
         if (lane == 31) sums[warp] = sum;
         __syncthreads();
-        int before = base, all = 0;
-        for (int w = 0; w < 32; w++) {
-            if (w < warp) before += sums[w];
-            all += sums[w];
+        int before = sums[lane];                          // every warp scans the warps' sums
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
         }
-        const int first = before + sum - n;
+        const int all = __shfl_sync(0xffffffffu, before, 31), here = warp > 0 ? __shfl_sync(0xffffffffu, before, warp - 1) : 0;
+        const int first = base + here + sum - n;
+        firsts[tid] = first;
+        starts[tid] = x.x;
+        lens[tid] = x.y;
         if (s < a.num_seqs) a.first[s] = first;
-        // a warp fills its sequences' chunks together
-        for (int l = 0; l < 32; l++) {
-            const int f = __shfl_sync(0xffffffffu, first, l), row = __shfl_sync(0xffffffffu, x.x, l), left = __shfl_sync(0xffffffffu, x.y, l);
-            for (int i = lane; i * C < left; i += 32)
-                if (f + i < a.chunks) a.where[f + i] = make_int2(row + i * C, left - i * C < C ? left - i * C : C);
-        }
         __syncthreads();
-        if (tid == 0) base += all;
+        // each chunk finds its sequence: the last one that begins at it or before it, which has rows
+        for (int i = base + tid; i < base + all && i < a.chunks; i += 1024) {
+            int low = 0;
+#pragma unroll
+            for (int step = 512; step > 0; step >>= 1)
+                if (firsts[low + step] <= i) low += step;
+            const int at = (i - firsts[low]) * C;
+            a.where[i] = make_int2(starts[low] + at, lens[low] - at < C ? lens[low] - at : C);
+        }
+        base += all;
         __syncthreads();
     }
     if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;
@@ -983,10 +989,23 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         __syncwarp();
         (void)tc::mbar_wait(drained, 0);
     } else if (warp == 22) {
-        // ---- keys behind a sequence's end: another sequence's, and 0 times what they may hold is not 0 ----
+        // ---- keys behind a sequence's end: another sequence's, and 0 times what they may hold is not 0; the next chain's state to L2 ----
         bool more = w.begin();
+        Walk z(a, order, VS);
+        bool another = z.begin();
+        int item = -1;
         for (uint32_t c = 0; more; c++) {
             const int s = c % STAGES, n = w.n();
+            if (w.item != item) {
+                item = w.item;
+                if (another) { z.advance(); another = z.begin(); }
+                const int64_t slot = another ? load_slot(p, z.seq) : -1;
+                if (slot >= 0) {
+                    const float *tile = p.pool + slot * p.slot_stride + static_cast<int64_t>(z.h) * K * a.V + z.slice * VS;
+                    for (int i = lane; i < K * VW; i += 32)
+                        asm volatile("prefetch.global.L2 [%0];" :: "l"(tile + static_cast<int64_t>(i / VW) * a.V + i % VW * 32));
+                }
+            }
             more = w.next();
             if (!wait.warp(full(s), (c / STAGES) & 1)) break;
             if (n < C) {
@@ -1068,9 +1087,9 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     if (e != cudaSuccess) return e;
     CUtensorMap qk, v;
     const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
-    // few chains: slices of their value columns, as long as there are idle multiprocessors for them
-    int VS = V;
-    while (VS > 32 && chains * (V / VS) * 2 <= sms) VS /= 2;
+    // few chains: halves of their value columns, if there are idle multiprocessors for them (16,384 tokens x 32 heads 779 us, whole 818,
+    // quarters 812: a chain is bound by its latencies, not by what a multiprocessor issues)
+    const int VS = V == 128 && chains * 2 <= sms ? 64 : V;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     if ((e = encode(&v, p, rows, cols, VS, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;
     const int64_t chunks = rows / C + num_seqs;
