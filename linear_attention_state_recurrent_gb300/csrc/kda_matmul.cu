@@ -111,12 +111,38 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
     };
     switch (act) {
     case KDA_ACT_RELU: each([](float x) { return x < 0.f ? 0.f : x; }); break;   // a NaN stays one
-    case KDA_ACT_SILU: each([](float x) { return x / (1.f + expf(-x)); }); break;
-    case KDA_ACT_SIGMOID: each([](float x) { return 1.f / (1.f + expf(-x)); }); break;
+    // (a quotient to two steps: the exact one takes a slow path where e^-x is large, 36 us for 24 at 128 x 12,288 x 4096)
+    case KDA_ACT_SILU: each([](float x) { return __fdividef(x, 1.f + expf(-x)); }); break;
+    case KDA_ACT_SIGMOID: each([](float x) { return __fdividef(1.f, 1.f + expf(-x)); }); break;
     case KDA_ACT_GELU: each([](float x) { return 0.5f * x * erfcf(-0.70710678118654752f * x); }); break;
     // x (1 + tanh u) / 2 = x / (1 + e^{-2u}), u = (2 / pi)^(1/2) (x + 0.044715 x^3)
-    case KDA_ACT_GELU_TANH: each([](float x) { return x / (1.f + expf(-1.5957691216057308f * (x + 0.044715f * x * x * x))); }); break;
+    case KDA_ACT_GELU_TANH: each([](float x) { return __fdividef(x, 1.f + expf(-1.5957691216057308f * (x + 0.044715f * x * x * x))); }); break;
     }
+}
+
+// The residuals of outputs m .. m + 15 of column n.
+__device__ __forceinline__ void fetch(const MatmulParams &p, float (&r)[16], int m, int n)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i++) r[i] = p.res && n < p.N && m + i < p.M ? load_as(p.res, static_cast<int64_t>(m + i) * p.ld_res + n, p.out_dtype) : 0.f;
+}
+// Outputs m .. m + 15 of column n, from their sums.
+__device__ __forceinline__ void finish(const MatmulParams &p, float (&v)[16], const float (&r)[16], int m, int n)
+{
+    if (n >= p.N) return;
+    if (p.bias) {
+        const float b = load_as(p.bias, n, p.bias_dtype);
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] += b;
+    }
+    activate(v, p.act);
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] += r[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        if (m + i < p.M) store_as(p.out, static_cast<int64_t>(m + i) * p.ld_out + n, p.out_dtype, v[i]);
 }
 
 // ---- tiles of 128 rows of W by NT rows of A -------------------------------------------------
@@ -215,13 +241,24 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             if (!wait_warp(empty(s), phase)) { report(p); break; }
             const int64_t k = static_cast<int64_t>(c) * BK + 2 * lane;
             unsigned char *at = sm + s * T::STAGE;
-#pragma unroll 8
-            for (int r = warp - 2 - T::EW; r < 128 + NT; r += 8) {
-                const int64_t row = r < 128 ? n0 + r : m0 + r - 128;
-                const uint16_t *from = r < 128 ? pw + row * p.ld_w : pa + row * p.ld_a;
-                const bool in = row < (r < 128 ? p.N : p.M);
-                const uint32_t x = in && k < p.K ? from[k] : 0u, y = in && k + 1 < p.K ? from[k + 1] : 0u;
-                *reinterpret_cast<uint32_t *>(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x | y << 16;
+            static_assert((128 + NT) % 96 == 0 || !LOOSE, "");
+#pragma unroll 1
+            for (int r0 = warp - 2 - T::EW; r0 < 128 + NT; r0 += 96) {   // twelve rows' loads at once
+                uint32_t x[12];
+#pragma unroll
+                for (int i = 0; i < 12; i++) {
+                    const int r = r0 + 8 * i;
+                    const int64_t row = r < 128 ? n0 + r : m0 + r - 128;
+                    const uint16_t *from = r < 128 ? pw + row * p.ld_w : pa + row * p.ld_a;
+                    const bool in = row < (r < 128 ? p.N : p.M);
+                    const uint32_t lo = in && k < p.K ? from[k] : 0u, hi = in && k + 1 < p.K ? from[k + 1] : 0u;
+                    x[i] = lo | hi << 16;
+                }
+#pragma unroll
+                for (int i = 0; i < 12; i++) {
+                    const int r = r0 + 8 * i;
+                    *reinterpret_cast<uint32_t *>(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = x[i];
+                }
             }
             tc::fence_proxy_async();
             __syncwarp();
@@ -233,25 +270,10 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
     const int quarter = warp % 4, n = n0 + quarter * 32 + lane;
     const bool epilogue = warp >= 2 && warp < 2 + T::EW;
     const int i0 = 16 * ((warp - 2) / 4), step = 16 * (T::EW / 4);          // rows of A in turn
-    auto finish = [&](float (&v)[16], int m) {             // outputs m .. m + 15 of column n
-        if (n >= p.N) return;
-        if (p.bias) {
-            const float b = load_as(p.bias, n, p.bias_dtype);
-#pragma unroll
-            for (int i = 0; i < 16; i++) v[i] += b;
-        }
-        activate(v, p.act);
-        if (p.res) {
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (m + i < p.M) v[i] += load_as(p.res, static_cast<int64_t>(m + i) * p.ld_res + n, p.out_dtype);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i++)
-            if (m + i < p.M) store_as(p.out, static_cast<int64_t>(m + i) * p.ld_out + n, p.out_dtype, v[i]);
-    };
     const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     if (epilogue && split == 1) {
+        float r[16];
+        fetch(p, r, m0 + i0, n);                           // beside the products
         bool ok = wait_warp(done, 0);
         tc::fence_after_sync();
         ok &= *static_cast<volatile uint32_t *>(&failed) == 0;
@@ -264,7 +286,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 #pragma unroll
                 for (int x = 0; x < 16; x++) v[x] = 0.f;
             }
-            finish(v, m0 + i);
+            finish(p, v, r, m0 + i, n);
+            if (i + step < NT) fetch(p, r, m0 + i + step, n);
         }
     }
     if (split > 1) {
@@ -295,8 +318,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             if (bad) report(p);
             const int per = (NT / 16 + split - 1) / split * 16;
             for (int i = rank * per + i0; !bad && i < min(NT, (rank + 1) * per) && m0 + i < p.M; i += step) {
-                float v[16] = {};
+                float v[16] = {}, r[16];
                 const int rows = min(16, p.M - m0 - i);
+                fetch(p, r, m0 + i, n);
 #pragma unroll 2
                 for (int k = 0; k < split; k++) {
                     const uint32_t at = in_cta(tc::smem_addr(sums + i * 132 + quarter * 32 + lane), k);
@@ -309,7 +333,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
 #pragma unroll
                     for (int x = 0; x < 16; x++) v[x] += y[x];
                 }
-                finish(v, m0 + i);
+                finish(p, v, r, m0 + i, n);
             }
         }
         cluster_sync();    // no CTA ends while another reads its sums
@@ -686,26 +710,29 @@ struct Choice {
     const Device *device = nullptr;
 };
 
-// Plans are compared by their time in nanoseconds: start and end of a wave of CTAs, then its steps of 64 of the inner axis, each by the slowest of
-// the MMAs, the stream from HBM (5.7 kB/ns over all multiprocessors) and the copies into a multiprocessor (85 B/ns), then the join.
+// Plans are compared by their time in nanoseconds, fitted to the measured splits of products of 1 to 8192 rows, N and K of 64 to 12,288:
+// start and end of a wave of CTAs, then its steps of 64 of the inner axis, each by the slowest of the MMAs, the stream from HBM (5.7 kB/ns
+// over all multiprocessors) and the copies into a multiprocessor (107 B/ns), then the join of a split.
 double time_tile(const MatmulParams &p, const int (&fit)[9], int nt, int split)
 {
     if (fit[split] == 0) return 1e30;
     const int64_t tn = (p.N - 1) / 128 + 1, tm = (p.M - 1) / nt + 1, ctas = tn * tm * split;
     const int steps = (p.K + BK - 1) / BK;
     const double at_once = ctas < fit[split] ? ctas : fit[split], stage = (128 + nt) * 128.;
-    const double hbm = at_once * 128 * 128 / tm / 5700., l2 = (at_once > fit[1] / 2 ? 2 : 1) * stage / 85.;
-    double step = 110. + 0.5 * nt;
+    const double hbm = at_once * 128 * 128 / tm / 5700., l2 = (at_once > fit[1] / 2 ? 2 : 1) * stage / 107.;
+    double step = 264.;                                    // what one CTA's ring brings of W
     if (step < hbm) step = hbm;
     if (step < l2) step = l2;
     const double waves = static_cast<double>((ctas + fit[split] - 1) / fit[split]);
-    return waves * (2800. + 8. * nt + step * ((steps + split - 1) / split)) + (split > 1 ? 1100. + 6. * nt : 0.);
+    return waves * (3200. + 14. * nt + step * ((steps + split - 1) / split)) + (split > 1 ? 1100. + 6. * nt : 0.);
 }
-double time_pair(const MatmulParams &p, int sms)
+// The pairs' epilogues are beside the next tile's MMAs; where TMA cannot write the outputs they take three times as long.
+double time_pair(const MatmulParams &p, int sms, bool tma_out)
 {
     const int64_t tiles = ((p.M - 1) / 256 + 1) * static_cast<int64_t>((p.N - 1) / 256 + 1);
     const int pairs = sms / 2, steps = (p.K + BK - 1) / BK;
-    return 6000. + (270. * steps + 300.) * static_cast<double>((tiles + pairs - 1) / pairs);
+    const double end = tma_out ? 3000. : 9000., main = 270. * steps;
+    return 3000. + static_cast<double>((tiles + pairs - 1) / pairs) * (main > end ? main : end) + end;
 }
 
 cudaError_t choose(const MatmulParams &p, Choice *c)
@@ -727,13 +754,13 @@ cudaError_t choose(const MatmulParams &p, Choice *c)
         tile(4, 64, 0);
         return least < 1e30 ? cudaSuccess : cudaErrorInvalidConfiguration;
     }
-    if (p.M <= 16) tile(0, 16, 16);
-    else if (p.M <= 32) tile(1, 32, 32);
-    else {
-        tile(2, 64, 64);
-        if (p.M > 64) tile(3, 128, 128);
-    }
-    if (p.M > 128 && time_pair(p, d->sms) < least) { c->rows = 256; c->split = 1; }
+    if (p.M <= 512) tile(0, 16, 16);
+    if (p.M > 16 && p.M <= 1024) tile(1, 32, 32);
+    if (p.M > 32) tile(2, 64, 64);
+    if (p.M > 64) tile(3, 128, 128);
+    int64_t ld_out = p.ld_out;
+    const bool tma_out = !p.out || tma_rows(p.out, &ld_out, p.M, p.N, p.out_dtype == KDA_FP32 ? 4 : 2);
+    if (p.M > 128 && time_pair(p, d->sms, tma_out) < least) { c->rows = 256; c->split = 1; }
     return cudaSuccess;
 }
 
