@@ -21,7 +21,7 @@ namespace kda {
 namespace gdn {
 
 template <int K, int V>
-__global__ void __launch_bounds__(128, K == 128 ? 12 : 8) decode_kernel(GdnParams p)
+__global__ void __launch_bounds__(128, 12) decode_kernel(GdnParams p)
 {
     constexpr int VT = 32, VS = V / VT, RPT = K / 16, CPL = K / 32;
     // Thread (rg, cg) copies, reads and stores rows rg, rg + 16, .. of four columns: no register holds the slice, and
@@ -165,13 +165,18 @@ __device__ __forceinline__ float sum_squares(uint32_t pair)
     return x * x + y * y;
 }
 
-// One CTA per (entry, value head): warp w holds value columns 32 w .. 32 w + 31, in registers over all K channels
-// (4 K / 4 floats a thread), and needs nothing of the other warps but the block's T and the query-key products, which warps 0 and
-// 1 form while the others already multiply. TB tokens a step (a multiple of 8).
-template <int K, int V, int TB>
-__global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
+// One CTA per (entry, value head, 64 value columns): a warp holds 16 of them, in registers over all K channels (K / 2 floats a
+// thread), and needs nothing of the other warps but the block's T and the query-key products, which warps 0 and 1 form while the
+// others already multiply. TB tokens a step (a multiple of 8). Bound by the latency of a CTA's load, products and store, one after the other, so
+// by how many CTAs are on an SM: with 32 columns a warp (three CTAs of a whole head an SM) 16 requests of 8 rows x 32 heads took 23 us.
+template <int V>
+constexpr int COLS = V < 64 ? V : 64;
+// GROUPS: 128 threads each that an SM has to hold (four of them without spills at K = 128, 128 registers a thread).
+template <int K, int V, int TB, int GROUPS>
+__global__ void __launch_bounds__(2 * COLS<V>, GROUPS * 128 / (2 * COLS<V>))
+rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
 {
-    constexpr int NT = TB / 8, CT = K / 8, PITCH = K + 8, TP = TB + 8;
+    constexpr int NT = TB / 8, CT = K / 8, PITCH = K + 8, TP = TB + 8, THREADS = 2 * COLS<V>, SLICES = V / COLS<V>;
     __shared__ __align__(16) uint16_t s_k[TB][PITCH], s_q[TB][PITCH];
     __shared__ __align__(4) uint16_t s_t[2][TB][TP], s_w[2][TB][TP];   // T diag(beta) and the scaled q k^T, each hi and lo
     __shared__ float s_a[TB][TB + 1];
@@ -180,9 +185,9 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
     pdl_wait_then_release();   // no global read before this
-    const int64_t e = blockIdx.x / p.Hv;
-    const int h = static_cast<int>(blockIdx.x % p.Hv), hk = h / (p.Hv / p.Hk);
-    const int j0 = warp * 32 + g * 4;                     // this thread's four value columns
+    const int64_t e = blockIdx.x / (SLICES * p.Hv);
+    const int h = static_cast<int>(blockIdx.x / SLICES % p.Hv), hk = h / (p.Hv / p.Hk);
+    const int j0 = static_cast<int>(blockIdx.x % SLICES) * COLS<V> + warp * 16 + g * 2;   // this thread's two value columns
     int64_t row0 = e * T, row1 = row0 + T;
     if (cu) {
         row0 = cu[e];
@@ -196,21 +201,21 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
     uint16_t *out = p.out + static_cast<int64_t>(h) * V + j0;
     if (slot >= p.num_slots) {                            // out of range: flag, zero outputs
         if (tid == 0 && p.err) atomicOr(p.err, kErrSlotRange);
-        for (int64_t r = row0 + (lane & 3); r < row1; r += 4) *reinterpret_cast<uint2 *>(out + r * p.ld_out) = make_uint2(0u, 0u);
+        for (int64_t r = row0 + (lane & 3); r < row1; r += 4) *reinterpret_cast<uint32_t *>(out + r * p.ld_out) = 0u;
         return;
     }
     if (row0 == row1) return;
     const bool has_state = slot >= 0, writable = has_state && slot != p.null_slot;
     float *tile = has_state ? p.pool + slot * p.slot_stride + static_cast<int64_t>(h) * K * V + j0 : nullptr;
 
-    // S[m][n]: columns j0 + 2m, j0 + 2m + 1 (the MMA's rows g and g + 8 of tile m), channels 8n + t2, 8n + t2 + 1
-    float S[2][CT][4];
+    // S[n]: columns j0, j0 + 1 (the MMA's rows g and g + 8), channels 8n + t2, 8n + t2 + 1
+    float S[CT][4];
 #pragma unroll
     for (int n = 0; n < CT; n++)
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-            const float4 x = has_state ? *reinterpret_cast<const float4 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) : make_float4(0.f, 0.f, 0.f, 0.f);
-            S[0][n][c] = x.x; S[0][n][2 + c] = x.y; S[1][n][c] = x.z; S[1][n][2 + c] = x.w;
+            const float2 x = has_state ? *reinterpret_cast<const float2 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) : make_float2(0.f, 0.f);
+            S[n][c] = x.x; S[n][2 + c] = x.y;
         }
 
     const int64_t HK = static_cast<int64_t>(p.Hk) * K;
@@ -220,37 +225,35 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
         const uint16_t *in = p.qkv + r0 * p.ld_qkv;
         // q and k of the block; rows past its end are zeros, and so is their beta
         if (vec) {
-            for (int i = tid; i < 2 * TB * (K / 8); i += V) {
+            for (int i = tid; i < 2 * TB * (K / 8); i += THREADS) {
                 const int part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
                 const uint4 x = r < n ? *reinterpret_cast<const uint4 *>(in + r * p.ld_qkv + part * HK + hk * K + c) : make_uint4(0u, 0u, 0u, 0u);
                 *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = x;
             }
         } else {
-            for (int i = tid; i < 2 * TB * K; i += V) {
+            for (int i = tid; i < 2 * TB * K; i += THREADS) {
                 const int part = i / (TB * K), r = i / K % TB, c = i % K;
                 const uint16_t x = r < n ? in[r * p.ld_qkv + part * HK + hk * K + c] : static_cast<uint16_t>(0);
                 (part ? s_k : s_q)[r][c] = x;
             }
         }
         // v of this thread's columns and tokens
-        float vv[2][NT][4];
+        float vv[NT][4];
 #pragma unroll
         for (int m = 0; m < NT; m++)
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 const int r = 8 * m + t2 + c;
-                uint2 x = make_uint2(0u, 0u);
+                uint32_t x = 0u;
                 if (r < n) {
                     const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
-                    if (vec) x = *reinterpret_cast<const uint2 *>(vp);
-                    else x = make_uint2(vp[0] | static_cast<uint32_t>(vp[1]) << 16, vp[2] | static_cast<uint32_t>(vp[3]) << 16);
+                    x = vec ? *reinterpret_cast<const uint32_t *>(vp) : vp[0] | static_cast<uint32_t>(vp[1]) << 16;
                 }
-                vv[0][m][c] = __uint_as_float(x.x << 16); vv[0][m][2 + c] = __uint_as_float(x.x & 0xffff0000u);
-                vv[1][m][c] = __uint_as_float(x.y << 16); vv[1][m][2 + c] = __uint_as_float(x.y & 0xffff0000u);
+                vv[m][c] = __uint_as_float(x << 16); vv[m][2 + c] = __uint_as_float(x & 0xffff0000u);
             }
         __syncthreads();
 
-        // Warp 0: the block's scalars and T. Warp 1 (or warp 0 again): the query-key products. Lane r has token r's scalars.
+        // Warp 0: the block's scalars and T. Warp 1: the query-key products. Lane r has token r's scalars.
         if (warp < 2) {
             float gl = 0.f, beta = 0.f;
             if (lane < n) {
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
             }
             const RunningDecay b(gl, TB);
             const RunningDecay::At b_end = b.of(TB - 1);
-            for (int qk = warp; qk < 2; qk += V == 32 ? 1 : 2) {
+            for (int qk = warp; qk < 2; qk += 2) {
                 const uint16_t(*s_l)[PITCH] = qk ? s_q : s_k;
                 float G[NT][4] = {}, nl[2] = {}, nr[NT] = {};
 #pragma unroll
@@ -351,98 +354,90 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
         }
 
         // k S and q S
-        float P[2][NT][4] = {}, Q[2][NT][4] = {};
+        float P[NT][4] = {}, Q[NT][4] = {};
 #pragma unroll
         for (int kt = 0; kt < K / 16; kt++) {
-            uint32_t kb[NT][2], qb[NT][2];
             const int c = 16 * kt + t2;
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int m = 0; m < NT; m++)
+            for (int x = 0; x < 4; x++) split2(S[2 * kt + x / 2][2 * (x % 2)], S[2 * kt + x / 2][2 * (x % 2) + 1], hi[x], lo[x]);
+#pragma unroll
+            for (int r = 0; r < NT; r++) {
+                uint32_t kb[2], qb[2];
 #pragma unroll
                 for (int x = 0; x < 2; x++) {
-                    kb[m][x] = *reinterpret_cast<const uint32_t *>(&s_k[8 * m + g][c + 8 * x]);
-                    qb[m][x] = *reinterpret_cast<const uint32_t *>(&s_q[8 * m + g][c + 8 * x]);
+                    kb[x] = *reinterpret_cast<const uint32_t *>(&s_k[8 * r + g][c + 8 * x]);
+                    qb[x] = *reinterpret_cast<const uint32_t *>(&s_q[8 * r + g][c + 8 * x]);
                 }
-#pragma unroll
-            for (int m = 0; m < 2; m++) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int x = 0; x < 4; x++) split2(S[m][2 * kt + x / 2][2 * (x % 2)], S[m][2 * kt + x / 2][2 * (x % 2) + 1], hi[x], lo[x]);
-#pragma unroll
-                for (int r = 0; r < NT; r++) {
-                    mma<16>(P[m][r], hi, kb[r]);
-                    mma<16>(Q[m][r], hi, qb[r]);
-                    mma<16>(P[m][r], lo, kb[r]);
-                    mma<16>(Q[m][r], lo, qb[r]);
-                }
+                mma<16>(P[r], hi, kb);
+                mma<16>(Q[r], hi, qb);
+                mma<16>(P[r], lo, kb);
+                mma<16>(Q[r], lo, qb);
             }
         }
         __syncthreads();   // T, the query-key products and the scales are there
 
         const float gamma = s_gamma;
+        uint32_t hi[2 * NT], lo[2 * NT];
+        float U[NT][4] = {};
+        // y = v - e^b (k^ S)
 #pragma unroll
-        for (int m = 0; m < 2; m++) {
-            uint32_t hi[2 * NT], lo[2 * NT];
-            float U[NT][4] = {};
-            // y = v - e^b (k^ S)
+        for (int r = 0; r < NT; r++) {
+            const float y0 = s_ys[8 * r + t2], y1 = s_ys[8 * r + t2 + 1];
+            split2(vv[r][0] - y0 * P[r][0], vv[r][1] - y1 * P[r][1], hi[2 * r], lo[2 * r]);
+            split2(vv[r][2] - y0 * P[r][2], vv[r][3] - y1 * P[r][3], hi[2 * r + 1], lo[2 * r + 1]);
+        }
+        auto pairs = [&](const uint16_t(*s)[TP], int r, uint32_t (&x)[NT]) {
 #pragma unroll
-            for (int r = 0; r < NT; r++) {
-                const float y0 = s_ys[8 * r + t2], y1 = s_ys[8 * r + t2 + 1];
-                split2(vv[m][r][0] - y0 * P[m][r][0], vv[m][r][1] - y1 * P[m][r][1], hi[2 * r], lo[2 * r]);
-                split2(vv[m][r][2] - y0 * P[m][r][2], vv[m][r][3] - y1 * P[m][r][3], hi[2 * r + 1], lo[2 * r + 1]);
-            }
-            auto pairs = [&](const uint16_t(*s)[TP], int r, uint32_t (&x)[NT]) {
+            for (int i = 0; i < NT; i++) x[i] = *reinterpret_cast<const uint32_t *>(&s[8 * r + g][8 * i + t2]);
+        };
 #pragma unroll
-                for (int i = 0; i < NT; i++) x[i] = *reinterpret_cast<const uint32_t *>(&s[8 * r + g][8 * i + t2]);
-            };
+        for (int r = 0; r < NT; r++) {
+            uint32_t th[NT], tl[NT];
+            pairs(s_t[0], r, th);
+            pairs(s_t[1], r, tl);
+            mma<TB>(U[r], hi, th);
+            mma<TB>(U[r], lo, th);
+            mma<TB>(U[r], hi, tl);
+        }
+        // o = e^b (q^ S) + W U
 #pragma unroll
-            for (int r = 0; r < NT; r++) {
-                uint32_t th[NT], tl[NT];
-                pairs(s_t[0], r, th);
-                pairs(s_t[1], r, tl);
-                mma<TB>(U[r], hi, th);
-                mma<TB>(U[r], lo, th);
-                mma<TB>(U[r], hi, tl);
-            }
-            // o = e^b (q^ S) + W U
+        for (int r = 0; r < NT; r++) {
+            split2(U[r][0], U[r][1], hi[2 * r], lo[2 * r]);
+            split2(U[r][2], U[r][3], hi[2 * r + 1], lo[2 * r + 1]);
+        }
 #pragma unroll
-            for (int r = 0; r < NT; r++) {
-                split2(U[r][0], U[r][1], hi[2 * r], lo[2 * r]);
-                split2(U[r][2], U[r][3], hi[2 * r + 1], lo[2 * r + 1]);
-            }
+        for (int r = 0; r < NT; r++) {
+            const float q0 = s_qs[8 * r + t2], q1 = s_qs[8 * r + t2 + 1];
+            Q[r][0] *= q0; Q[r][1] *= q1; Q[r][2] *= q0; Q[r][3] *= q1;
+            uint32_t wh[NT], wl[NT];
+            pairs(s_w[0], r, wh);
+            pairs(s_w[1], r, wl);
+            mma<TB>(Q[r], hi, wh);
+            mma<TB>(Q[r], lo, wh);
+            mma<TB>(Q[r], hi, wl);
+        }
+        // S <- gamma S + (k^ e^{b_n - b})^T U
 #pragma unroll
-            for (int r = 0; r < NT; r++) {
-                const float q0 = s_qs[8 * r + t2], q1 = s_qs[8 * r + t2 + 1];
-                Q[m][r][0] *= q0; Q[m][r][1] *= q1; Q[m][r][2] *= q0; Q[m][r][3] *= q1;
-                uint32_t wh[NT], wl[NT];
-                pairs(s_w[0], r, wh);
-                pairs(s_w[1], r, wl);
-                mma<TB>(Q[m][r], hi, wh);
-                mma<TB>(Q[m][r], lo, wh);
-                mma<TB>(Q[m][r], hi, wl);
-            }
-            // S <- gamma S + (k^ e^{b_n - b})^T U
+        for (int r = 0; r < NT; r++) {
+            const float u0 = s_us[8 * r + t2], u1 = s_us[8 * r + t2 + 1];
+            split2(U[r][0] * u0, U[r][1] * u1, hi[2 * r], lo[2 * r]);
+            split2(U[r][2] * u0, U[r][3] * u1, hi[2 * r + 1], lo[2 * r + 1]);
+        }
 #pragma unroll
-            for (int r = 0; r < NT; r++) {
-                const float u0 = s_us[8 * r + t2], u1 = s_us[8 * r + t2 + 1];
-                split2(U[r][0] * u0, U[r][1] * u1, hi[2 * r], lo[2 * r]);
-                split2(U[r][2] * u0, U[r][3] * u1, hi[2 * r + 1], lo[2 * r + 1]);
-            }
+        for (int ct = 0; ct < CT; ct += 4 / NT) {         // four 8 x 8 tiles of k: 4 / NT channel tiles of NT token tiles
+            uint32_t kt[4];
+            const int at = lane / 8;
+            load_trans(kt, static_cast<uint32_t>(__cvta_generic_to_shared(&s_k[8 * (at % NT) + lane % 8][8 * (ct + at / NT)])));
 #pragma unroll
-            for (int ct = 0; ct < CT; ct += 4 / NT) {     // four 8 x 8 tiles of k: 4 / NT channel tiles of NT token tiles
-                uint32_t kt[4];
-                const int at = lane / 8;
-                load_trans(kt, static_cast<uint32_t>(__cvta_generic_to_shared(&s_k[8 * (at % NT) + lane % 8][8 * (ct + at / NT)])));
+            for (int x = 0; x < 4 / NT; x++) {
+                float(&d)[4] = S[ct + x];
+                d[0] *= gamma; d[1] *= gamma; d[2] *= gamma; d[3] *= gamma;
+                uint32_t kb[NT];
 #pragma unroll
-                for (int x = 0; x < 4 / NT; x++) {
-                    float(&d)[4] = S[m][ct + x];
-                    d[0] *= gamma; d[1] *= gamma; d[2] *= gamma; d[3] *= gamma;
-                    uint32_t kb[NT];
-#pragma unroll
-                    for (int r = 0; r < NT; r++) kb[r] = kt[x * NT + r];
-                    mma<TB>(d, hi, kb);
-                    mma<TB>(d, lo, kb);
-                }
+                for (int r = 0; r < NT; r++) kb[r] = kt[x * NT + r];
+                mma<TB>(d, hi, kb);
+                mma<TB>(d, lo, kb);
             }
         }
 #pragma unroll
@@ -450,8 +445,7 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
 #pragma unroll
             for (int c = 0; c < 2; c++)
                 if (8 * r + t2 + c < n)
-                    *reinterpret_cast<uint2 *>(out + (r0 + 8 * r + t2 + c) * p.ld_out) =
-                        make_uint2(pack_bf16x2(Q[0][r][c], Q[0][r][2 + c]), pack_bf16x2(Q[1][r][c], Q[1][r][2 + c]));
+                    *reinterpret_cast<uint32_t *>(out + (r0 + 8 * r + t2 + c) * p.ld_out) = pack_bf16x2(Q[r][c], Q[r][2 + c]);
         if (r0 + TB < row1) __syncthreads();   // the next block's q, k, T and scales
     }
     if (writable) {
@@ -459,8 +453,7 @@ __global__ void __launch_bounds__(V, 384 / V) rows_kernel(GdnParams p, int T, co
         for (int n = 0; n < CT; n++)
 #pragma unroll
             for (int c = 0; c < 2; c++)
-                *reinterpret_cast<float4 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) =
-                    make_float4(S[0][n][c], S[0][n][2 + c], S[1][n][c], S[1][n][2 + c]);
+                *reinterpret_cast<float2 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) = make_float2(S[n][c], S[n][2 + c]);
     }
 }
 
@@ -482,15 +475,28 @@ cudaError_t launch_gdn_decode(const GdnParams &p, int K, int V, int64_t num_seqs
 cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32_t *cu, int64_t rows, int64_t num_entries,
                             cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>(num_entries * p.Hv));
+    const dim3 grid(static_cast<unsigned>(num_entries * p.Hv * (V > 64 ? V / 64 : 1)));
     const int vec = reinterpret_cast<uintptr_t>(p.qkv) % 16 == 0 && p.ld_qkv % 8 == 0;   // K and V are multiples of 8
+    // Four groups of 128 threads an SM at K = 128, five where that saves a wave: 16 requests x 32 heads x 128 columns (1024 groups, two waves either way)
+    // 20.2 us with four, 22.1 with five; 61 x 12 x 64 (732 groups) 14.1 with four, 12.7 with five.
+    const int64_t groups = static_cast<int64_t>(grid.x) * (V < 64 ? V : 64) / 64;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const bool five = (groups + 5 * sms - 1) / (5 * sms) < (groups + 4 * sms - 1) / (4 * sms);
     // blocks of 8 rows for requests of at most 8: half the products of 16
+    const bool small = !cu && T <= 8;
+#define KDA_GDN_LAUNCH(KK, VV, TB, G) return launch_pdl(gdn::rows_kernel<KK, VV, TB, G>, grid, dim3(2 * gdn::COLS<VV>), 0, stream, p, T, cu, rows, vec);
 #define KDA_GDN_RUN(KK, VV) \
-    if (K == KK && V == VV) \
-        return !cu && T <= 8 ? launch_pdl(gdn::rows_kernel<KK, VV, 8>, grid, dim3(VV), 0, stream, p, T, cu, rows, vec) \
-                             : launch_pdl(gdn::rows_kernel<KK, VV, 16>, grid, dim3(VV), 0, stream, p, T, cu, rows, vec);
+    if (K == KK && V == VV) { \
+        if (!small) KDA_GDN_LAUNCH(KK, VV, 16, KK == 128 ? 4 : 5) \
+        if (five) KDA_GDN_LAUNCH(KK, VV, 8, KK == 128 ? 5 : 6) \
+        KDA_GDN_LAUNCH(KK, VV, 8, KK == 128 ? 4 : 6) \
+    }
     KDA_GDN_DIMS(KDA_GDN_RUN)
 #undef KDA_GDN_RUN
+#undef KDA_GDN_LAUNCH
     return cudaErrorInvalidValue;
 }
 
