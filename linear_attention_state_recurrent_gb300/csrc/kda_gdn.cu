@@ -13,7 +13,7 @@
 //   U = T diag(beta) (v - e^b (k^ S)),  o = e^b (q^ S) + (q^ k^^T * D) U,  S <- e^{b_n} S + (k^ e^{b_n - b})^T U
 // so a state is read from memory once, kept in registers as the MMAs' accumulators, and written once. It is held
 // transposed (rows of an MMA = value columns, columns = key channels): the accumulator layout is then the layout of the
-// first operand of the next product. fp32 values enter the MMAs as two bf16 terms (2^-18 of the value); q and k are bf16 already.
+// first operand of the next product. fp32 values enter the MMAs as two bf16 terms (2^-17 of the value); q and k are bf16 already.
 #include "kda_gdn_common.cuh"
 #include "kda_pdl.cuh"
 

@@ -11,7 +11,7 @@
 //   chain_kernel  one CTA per SM walks (sequence, value head) chains, longest sequences first, S in registers
 // The chain's products have value columns as rows (TMEM lanes), so that what depends on a token is a factor per column,
 // and their first operand is written to TMEM by the thread that has the values.
-// What enters the products is exact (q, k, v are bf16) or two bf16 terms, hi + lo = x to 2^-18.
+// What enters the products is exact (q, k, v are bf16) or two bf16 terms, hi + lo = x to 2^-17.
 #include <atomic>
 #include <climits>
 #include <mutex>

@@ -22,7 +22,7 @@ __device__ __forceinline__ float log_decay(const GdnParams &p, int64_t row, int 
 }
 
 // x and y as packed bf16 pairs hi + lo: hi is x rounded to bf16 and lo what is left, rounded again, so that
-// |x - hi - lo| <= 2^-18 |x|.
+// |x - hi - lo| <= 2^-17 |x|.
 __device__ __forceinline__ uint32_t rest2(float x, float y, uint32_t hi)
 {
     const float2 d = fsub2(make_float2(x, y), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));

@@ -1,15 +1,15 @@
 """GPU tests of the gated delta rule with one decay per head against its fp64 oracle.
 
 Tolerances, from the arithmetic. Outputs are rounded once to bf16 (half a step is 2^-8 of the value); the products inside
-take fp32 values as two bf16 terms, 2^-18 of a value off at most, a third of that in the mean. On the path of a block's state
-there are six such values (S twice, y, T, U twice): in quadrature 6^(1/2) 2^-18 / 3 = 3.1e-6 of the state's norm, at most
-three times that where the errors of the blocks before still count: 1e-5. Outputs come by the same kind of products: in a row's norm
-the rounding of the result (2^-9 / 3^(1/2) = 1.1e-3 to 1.7e-3 in the mean) and little else, 2e-3 in all; one value is off by half a step and, where a row is
+take fp32 values as two bf16 terms: 8 bits of x, 8 bits of the rest, so 2^-17 of the value off at most and 2^-18.7 = 2.3e-6 in the mean. On the path
+of a block's state there are six such values (S twice, y, T, U twice): in quadrature 6^(1/2) 2.3e-6 = 5.8e-6 of the state's norm, and
+1e-5 with what is left of the errors of the blocks before. Outputs come by the same kind of products: in a row's norm
+the rounding of the result (1.1e-3 to 1.7e-3 in the mean) and little else, 2e-3 in all; one value is off by half a step and, where a row is
 small beside the terms that cancelled in it, by 1e-2 of the row's mean size. One token's products are fp32 throughout.
 With one key for all tokens the sum over i of k^_i u_i is of u of alternating effect, and what counts is not its norm but
 the terms': with Y = max |v| + |S_0|, T's rows sum to 2 at most in magnitude (beta (1 + beta + beta (1 - beta) + ..)), so |u_i| <= 2 Y,
-and u_i is off by 2^-18 (3 * 2 Y) (T, y and the product of their second terms) and 2^-18 * 2 Y (its own two terms), each a third of that in
-the mean; over the 64 tokens of a block, in quadrature: 64^(1/2) * 8 Y 2^-18 / 3.
+and u_i is off by 3 * 2 Y (T, y and the product of their second terms) and 2 Y (its own two terms) times 2^-18.7; over the 64 tokens of
+a block, in quadrature: 64^(1/2) * 8 Y 2^-18.7.
 """
 import math
 
@@ -100,7 +100,7 @@ class Case:
         most = 2e-6 if exact else 1e-5
         if alike:
             v = f64(self.qkv[:, 2 * self.Hk * self.K:self.width]).reshape(self.rows, self.Hv, self.V)
-            most = 64 ** 0.5 * 8 * 2.0 ** -18 / 3 * (np.linalg.norm(v, axis=2).max() + np.linalg.norm(pool, axis=(2, 3)).max())
+            most = 64 ** 0.5 * 8 * 2.0 ** -18.7 * (np.linalg.norm(v, axis=2).max() + np.linalg.norm(pool, axis=(2, 3)).max())
             worst *= max(np.linalg.norm(after[s, h]) for s in range(len(pool)) for h in range(self.Hv))
         assert worst <= most, (worst, most)
 
@@ -181,3 +181,99 @@ def test_prefill_in_parts_is_prefill(kda, K):
         else:
             kda.kda_gdn_chunk_prefill(qkv[r0:r1], rg[r0:r1], rb[r0:r1], *rest, torch.tensor([0, r1 - r0], dtype=torch.int32, device="cuda"), **kw)
     c.check([(0, 150)])
+
+
+@pytest.mark.parametrize("n, Hk, Hv, K, V, top", [(40, 2, 4, 128, 128, 150), (300, 1, 1, 64, 64, 90), (1100, 1, 1, 64, 32, 3)])
+def test_prefill_many_sequences(kda, n, Hk, Hv, K, V, top):
+    """More chains than multiprocessors; more sequences than are sorted, and than one turn of the chunks' map takes."""
+    g = torch.Generator().manual_seed(n)
+    cu = [0] + torch.cumsum(torch.randint(0, top, (n,), generator=g), 0).tolist()
+    c = Case(cu[-1], n, Hk, Hv, K, V, seed=n)
+    args, d_cu = c.gpu(), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kda.kda_gdn_chunk_prefill(*args, d_cu, num_k_heads=Hk, out=c.out, err_flags=c.err)
+    c.check(list(zip(cu, cu[1:])))
+    # the same bits again, and from a workspace that held something else
+    first, out = c.d_pool.clone(), c.out.clone()
+    c.d_pool.copy_(c.pool)
+    ws = torch.full((kda.kda_gdn_chunk_prefill_workspace_bytes(cu[-1], n, Hv, K, V, Hk),), 255, dtype=torch.uint8, device="cuda")
+    kda.kda_gdn_chunk_prefill(*args, d_cu, num_k_heads=Hk, out=c.out, err_flags=c.err, workspace=ws)
+    assert torch.equal(first.view(torch.int32), c.d_pool.view(torch.int32)) and torch.equal(out, c.out)
+
+
+def test_prefill_is_untouched_by_what_lies_around(kda):
+    """Infinities and NaN in rows of other sequences, and in the rows behind the last, stay there."""
+    lens = [70, 50, 100]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    c = Case(cu[-1] + 40, 3, 1, 2, 128, 64, seed=21)
+    c.qkv[cu[1]:cu[2]] = math.inf
+    c.qkv[cu[1] + 7] = math.nan
+    c.qkv[cu[3]:] = math.nan
+    args, d_cu = c.gpu(), torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kda.kda_gdn_chunk_prefill(*args, d_cu, num_k_heads=1, out=c.out, err_flags=c.err)
+    spoilt = c.slots[1]
+    c.pool[spoilt], c.d_pool[spoilt] = 0.0, 0.0
+    keep = c.out[cu[1]:cu[2]].clone()
+    c.out[cu[1]:cu[2]] = 7.0
+    c.check([(cu[0], cu[1]), (0, 0), (cu[2], cu[3])])
+    assert not torch.isfinite(keep[:, :128].float()).any()
+
+
+@pytest.mark.parametrize("call", ["decode", "spec", "prefill"])
+def test_offsets_past_32_bits(kda, call):
+    """Slots and rows whose offsets pass 2^31 elements."""
+    T = 1 if call == "decode" else 8 if call == "spec" else 70
+    n = 2
+    c = Case(n * T, n, 1, 1, 64, 64, seed=31, slots=[3, 1], spare=2)
+    qkv, rg, rb, A, dt, state, idx = c.gpu()
+    pitch = (1 << 31) // (n * T) * 2 + 8 & ~7
+    big = torch.empty(n * T * pitch, dtype=BF16, device="cuda").view(n * T, pitch)
+    big[:, :c.width] = qkv
+    slot = 1 << 30
+    pool = torch.empty(4 * slot, dtype=torch.float32, device="cuda").view(4, slot)
+    pool[:, :64 * 64] = c.d_pool[:, :64 * 64]
+    view = pool.as_strided((4, 1, 64, 64), (slot, 64 * 64, 64, 1))
+    wide = big[:, c.width + 8 & ~7:][:, :64]
+    kw = dict(out=wide, err_flags=c.err)
+    if call == "decode":
+        kda.kda_gdn_decode(big[:, :c.width], rg, rb, A, dt, view, idx, **kw)
+    elif call == "spec":
+        kda.kda_gdn_spec_verify(big[:, :c.width], rg, rb, A, dt, view, idx, T, **kw)
+    else:
+        kda.kda_gdn_chunk_prefill(big[:, :c.width], rg, rb, A, dt, view, idx, torch.tensor([0, 70, 140], dtype=torch.int32, device="cuda"), **kw)
+    c.out[:, :64] = wide
+    c.d_pool[:, :64 * 64] = pool[:, :64 * 64]
+    c.check([(0, T), (T, 2 * T)])
+
+
+def test_streams_and_graphs(kda):
+    """Every call on another stream with outputs and workspaces of its own, and captured; two graphs with a workspace each."""
+    c = Case(3 * 80, 3, 1, 2, 128, 128, seed=41)
+    args = c.gpu()
+    cu = torch.tensor([0, 80, 160, 240], dtype=torch.int32, device="cuda")
+    start = c.d_pool.clone()
+
+    def calls(stream=None, ws=None):
+        a, _ = kda.kda_gdn_chunk_prefill(*args, cu, num_k_heads=1, workspace=ws, stream=stream)
+        b, _ = kda.kda_gdn_spec_verify(*[t[:24] for t in args[:3]], *args[3:], 8, num_k_heads=1, stream=stream)
+        d, _ = kda.kda_gdn_decode(*[t[:3] for t in args[:3]], *args[3:], num_k_heads=1, stream=stream)
+        return a, b, d
+
+    want = [t.clone() for t in calls()] + [c.d_pool.clone()]
+    s = torch.cuda.Stream()
+    c.d_pool.copy_(start)
+    s.wait_stream(torch.cuda.current_stream())
+    got = calls(s)
+    torch.cuda.current_stream().wait_stream(s)
+    same = lambda got: all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip([*got, c.d_pool], want))  # noqa: E731
+    assert same(got)
+    graphs = []
+    for _ in range(2):
+        ws = torch.empty(kda.kda_gdn_chunk_prefill_workspace_bytes(240, 3, 2, 128, 128, 1), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = calls(ws=ws)
+        graphs.append((g, got, ws))
+    for g, got, _ in graphs * 2:
+        c.d_pool.copy_(start)
+        g.replay()
+        assert same(got)
