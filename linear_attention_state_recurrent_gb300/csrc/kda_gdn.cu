@@ -165,6 +165,12 @@ __device__ __forceinline__ float sum_squares(uint32_t pair)
     return x * x + y * y;
 }
 
+// Whether one of a pair of bf16 values is an infinity or NaN.
+__device__ __forceinline__ bool not_finite(uint32_t pair)
+{
+    return (pair & 0x7f80u) == 0x7f80u || (pair & 0x7f800000u) == 0x7f800000u;
+}
+
 // One CTA per (entry, value head, 64 value columns): a warp holds 16 of them, in registers over all K channels (K / 2 floats a
 // thread), and needs nothing of the other warps but the block's T and the query-key products, which warps 0 and 1 form while the
 // others already multiply. TB tokens a step (a multiple of 8). Bound by the latency of a CTA's load, products and store, one after the other, so
@@ -220,46 +226,60 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
 
     const int64_t HK = static_cast<int64_t>(p.Hk) * K;
     const float expA = expf(p.A_log[h]), dtb = p.dt_bias ? p.dt_bias[h] : 0.f;
-    for (int64_t r0 = row0; r0 < row1; r0 += TB) {
-        const int n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
+    // A block's products take zeros for the rows behind a row, and 0 times what is not finite is not 0: where a block's keys, values
+    // or gates are not all finite, its rows go one by one, and those ahead of such a row stay as they are.
+    int n;
+    for (int64_t r0 = row0; r0 < row1; r0 += n) {
+        n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
         const uint16_t *in = p.qkv + r0 * p.ld_qkv;
-        // q and k of the block; rows past its end are zeros, and so is their beta
-        if (vec) {
-            for (int i = tid; i < 2 * TB * (K / 8); i += THREADS) {
-                const int part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
-                const uint4 x = r < n ? *reinterpret_cast<const uint4 *>(in + r * p.ld_qkv + part * HK + hk * K + c) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = x;
-            }
-        } else {
-            for (int i = tid; i < 2 * TB * K; i += THREADS) {
-                const int part = i / (TB * K), r = i / K % TB, c = i % K;
-                const uint16_t x = r < n ? in[r * p.ld_qkv + part * HK + hk * K + c] : static_cast<uint16_t>(0);
-                (part ? s_k : s_q)[r][c] = x;
-            }
-        }
-        // v of this thread's columns and tokens
-        float vv[NT][4];
-#pragma unroll
-        for (int m = 0; m < NT; m++)
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
-                const int r = 8 * m + t2 + c;
-                uint32_t x = 0u;
-                if (r < n) {
-                    const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
-                    x = vec ? *reinterpret_cast<const uint32_t *>(vp) : vp[0] | static_cast<uint32_t>(vp[1]) << 16;
+        float vv[NT][4], gl, beta;
+#pragma unroll 1
+        for (;;) {
+            bool odd = false;
+            // q and k of the block; rows past its end are zeros, and so is their beta
+            if (vec) {
+                for (int i = tid; i < 2 * TB * (K / 8); i += THREADS) {
+                    const int part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
+                    const uint4 x = r < n ? *reinterpret_cast<const uint4 *>(in + r * p.ld_qkv + part * HK + hk * K + c) : make_uint4(0u, 0u, 0u, 0u);
+                    odd |= part && (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w));
+                    *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = x;
                 }
-                vv[m][c] = __uint_as_float(x << 16); vv[m][2 + c] = __uint_as_float(x & 0xffff0000u);
+            } else {
+                for (int i = tid; i < 2 * TB * K; i += THREADS) {
+                    const int part = i / (TB * K), r = i / K % TB, c = i % K;
+                    const uint16_t x = r < n ? in[r * p.ld_qkv + part * HK + hk * K + c] : static_cast<uint16_t>(0);
+                    odd |= part && not_finite(x);
+                    (part ? s_k : s_q)[r][c] = x;
+                }
             }
-        __syncthreads();
-
-        // Warp 0: the block's scalars and T. Warp 1: the query-key products. Lane r has token r's scalars.
-        if (warp < 2) {
-            float gl = 0.f, beta = 0.f;
-            if (lane < n) {
+            // v of this thread's columns and tokens
+#pragma unroll
+            for (int m = 0; m < NT; m++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    const int r = 8 * m + t2 + c;
+                    uint32_t x = 0u;
+                    if (r < n) {
+                        const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
+                        x = vec ? *reinterpret_cast<const uint32_t *>(vp) : vp[0] | static_cast<uint32_t>(vp[1]) << 16;
+                    }
+                    odd |= not_finite(x);
+                    vv[m][c] = __uint_as_float(x << 16); vv[m][2 + c] = __uint_as_float(x & 0xffff0000u);
+                }
+            // the gates, in the two warps that use them: lane r has token r's
+            gl = 0.f;
+            beta = 0.f;
+            if (warp < 2 && lane < n) {
                 gl = log_decay(p, r0 + lane, h, expA, dtb);
                 beta = sigmoid_f(bf16_to_f32(p.rb[(r0 + lane) * p.ld_beta + h]));
+                odd |= !(fabsf(gl) <= 1000.f && beta <= 1.f);
             }
+            if (!__syncthreads_or(odd) || n == 1) break;
+            n = 1;
+        }
+
+        // Warp 0: the block's scalars and T. Warp 1: the query-key products.
+        if (warp < 2) {
             const RunningDecay b(gl, TB);
             const RunningDecay::At b_end = b.of(TB - 1);
             for (int qk = warp; qk < 2; qk += 2) {
@@ -446,7 +466,7 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
             for (int c = 0; c < 2; c++)
                 if (8 * r + t2 + c < n)
                     *reinterpret_cast<uint32_t *>(out + (r0 + 8 * r + t2 + c) * p.ld_out) = pack_bf16x2(Q[r][c], Q[r][2 + c]);
-        if (r0 + TB < row1) __syncthreads();   // the next block's q, k, T and scales
+        if (r0 + n < row1) __syncthreads();   // the next block's q, k, T and scales
     }
     if (writable) {
 #pragma unroll

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(128, PREP_CTAS) prep_kernel(const __grid_const
         float *set = reinterpret_cast<float *>(rec + Rec::ROWS);
         if (pw == 0) {                                                    // the running decay, in units of log 2
             rate = expf(rate) * -1.44269504f;
-            const double g0 = 2 * lane < n ? rate * softplus_f(in0 + dtb) : 0.f, g1 = 2 * lane + 1 < n ? rate * softplus_f(in1 + dtb) : 0.f;
+            const double g0 = 2 * lane < n ? bounded(rate * softplus_f(in0 + dtb)) : 0.f, g1 = 2 * lane + 1 < n ? bounded(rate * softplus_f(in1 + dtb)) : 0.f;
             double b = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

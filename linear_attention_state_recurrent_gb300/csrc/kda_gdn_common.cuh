@@ -15,10 +15,14 @@ constexpr uint32_t kErrLengths = 16u;   // KDA_ERRFLAG_LENGTHS
 // lengths, and with what one of a call's kernels leaves to the next.)
 __device__ __forceinline__ int64_t load_slot(const GdnParams &p, int64_t e) { return static_cast<int64_t>(p.indices[e * p.index_stride]); }
 
+// A log-decay that differences of sums are taken of: below -1000 e^x and 2^x are 0 in fp32, and sums of what is below it
+// (-inf, for a large A_log or raw_g) have no differences. NaN stays NaN.
+__device__ __forceinline__ float bounded(float g) { return g < -1000.f ? -1000.f : g; }
+
 // Log-decay of a token and head: -e^{A_log} softplus(raw_g + dt_bias).
 __device__ __forceinline__ float log_decay(const GdnParams &p, int64_t row, int h, float expA, float dtb)
 {
-    return -expA * softplus_f(bf16_to_f32(p.rg[row * p.ld_g + h]) + dtb);
+    return bounded(-expA * softplus_f(bf16_to_f32(p.rg[row * p.ld_g + h]) + dtb));
 }
 
 // x and y as packed bf16 pairs hi + lo: hi is x rounded to bf16 and lo what is left, rounded again, so that

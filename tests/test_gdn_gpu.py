@@ -277,3 +277,58 @@ def test_streams_and_graphs(kda):
         c.d_pool.copy_(start)
         g.replay()
         assert same(got)
+
+
+def run(kda, c, call, cu):
+    kw = dict(num_k_heads=c.Hk, out=c.out, err_flags=c.err)
+    if call == "spec":
+        kda.kda_gdn_spec_verify(*c.gpu_args, cu[1], **kw)
+    else:
+        kda.kda_gdn_chunk_prefill(*c.gpu_args, torch.tensor(cu, dtype=torch.int32, device="cuda"), **kw)
+
+
+@pytest.mark.parametrize("where", ["key", "value", "gate", "beta"])
+@pytest.mark.parametrize("call, K, V, T, at", [("spec", 128, 128, 5, 3), ("spec", 64, 64, 16, 0), ("spec", 128, 32, 20, 17), ("prefill", 32, 64, 40, 9),
+                                               ("prefill", 128, 128, 150, 127), ("prefill", 64, 64, 70, 66)])
+def test_what_is_not_finite_reaches_no_earlier_token(kda, call, K, V, T, at, where):
+    """A row's outputs are finite where the oracle's are, and right; of the chunked form, those of the chunks before."""
+    c = Case(2 * T, 2, 1, 2, K, V, seed=31)
+    bad = T + at                                                              # in the second sequence
+    if where == "key":
+        c.qkv[bad, K + 3] = math.nan
+    elif where == "value":
+        c.qkv[bad, 2 * K + 5], c.qkv[bad, 2 * K + V + 1] = math.inf, math.nan
+    elif where == "gate":
+        c.rg[bad, 1] = math.nan
+    else:
+        c.rb[bad, 1] = math.nan
+    c.gpu_args = c.gpu()
+    run(kda, c, call, [0, T, 2 * T])
+    with np.errstate(invalid="ignore"):
+        out, after, _ = og.run(f64(c.qkv[:, :c.width]), f64(c.rg), f64(c.rb), f64(c.A_log), f64(c.dt), f64(c.pool[:, :2 * K * V]).reshape(-1, 2, K, V),
+                               c.slots, [(0, T), (T, 2 * T)], 1)
+    got, state = f64(c.out)[:, :2 * V], f64(c.state)[c.slots[1]]
+    np.testing.assert_array_equal(np.isfinite(state), np.isfinite(after[c.slots[1]]))
+    seen = np.ones(2 * T, bool)
+    if call == "prefill" and K > 32:
+        seen[T + at // 64 * 64:bad] = False                                   # its chunk's rows ahead of it
+    fine = np.isfinite(out)
+    np.testing.assert_array_equal(np.isfinite(got[seen]), fine[seen])
+    for h in range(2):
+        rows = seen & fine[:, h * V]
+        o = np.where(fine, out, 0.0)[rows, h * V:(h + 1) * V]
+        rms = np.sqrt((o ** 2).mean(1, keepdims=True))
+        g = np.where(fine, got, 0.0)[rows, h * V:(h + 1) * V]
+        assert (np.abs(g - o) <= 2.0 ** -8 * np.abs(o) + 1e-2 * rms + 1e-30).all()
+
+
+@pytest.mark.parametrize("call, K, T", [("spec", 128, 7), ("spec", 64, 16), ("prefill", 32, 50), ("prefill", 128, 150), ("prefill", 64, 90)])
+def test_decays_without_end(kda, call, K, T):
+    """exp(A_log) past fp32's range, and an infinite raw_g: alpha is 0, and the tokens behind go on as ever."""
+    c = Case(2 * T, 2, 1, 3, K, 64, seed=32)
+    c.A_log[0] = 100.0
+    c.rg[T // 2, 1] = c.rg[T + 2, 2] = math.inf
+    c.rg[T - 1, 1] = -math.inf                                                # and one without any
+    c.gpu_args = c.gpu()
+    run(kda, c, call, [0, T, 2 * T])
+    c.check([(0, T), (T, 2 * T)])
