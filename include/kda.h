@@ -372,7 +372,8 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
  *   o_t   = S_t^T q^                                                (V, bf16 out)
  * mixed_qkv: bf16 [N, ld_qkv], row t = [ q (Hk*K) | k (Hk*K) | v (Hv*V) ]; raw_g and raw_beta: bf16 [N, ld], Hv used;
  * out: bf16 [N, ld_out], Hv*V written; the state pool holds [Hv][K][V] per slot. Alignment, slots, the null slot, error
- * bits and sizes are those of the calls above with H = Hv. All three calls can be captured in a CUDA graph. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
+ * bits and sizes are those of the calls above with H = Hv, and a row of mixed_qkv has fewer than 2^31 columns in use. out may not
+ * overlap an input. All three calls can be captured in a CUDA graph. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
  * several tokens); squares, products and sums are fp32 too. A log-decay below -1000 is taken as -1000: alpha is 0 either way.
  * An infinity or NaN in a key, value or gate reaches its own token and the later ones of its sequence; in
  * kda_gdn_chunk_prefill's chunks of 64 rows (counted from the sequence's start) also the earlier ones of its chunk.

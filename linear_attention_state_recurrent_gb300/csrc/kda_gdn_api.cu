@@ -32,6 +32,8 @@ int check(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int6
     if (!(hd->l2_eps >= 0.f) || !std::isfinite(hd->l2_eps)) return invalid("l2_eps must be finite and >= 0");
     const int64_t Hk = hd->Hk, Hv = hd->Hv, K = hd->K, V = hd->V;
     if (!mixed_qkv || !raw_g || !raw_beta || !out) return invalid("mixed_qkv, raw_g, raw_beta and out must be non-NULL");
+    if (2 * Hk * K + Hv * V > INT32_MAX)   // columns are counted in 32 bits
+        return set_error(KDA_ERR_UNSUPPORTED, "2*Hk*K + Hv*V must be below 2^31 (got %lld)", (long long)(2 * Hk * K + Hv * V));
     if (ld_qkv < 2 * Hk * K + Hv * V)
         return set_error(KDA_ERR_INVALID_ARGUMENT, "ld_qkv (%lld) < 2*Hk*K + Hv*V (%lld)", (long long)ld_qkv, (long long)(2 * Hk * K + Hv * V));
     if (ld_g < Hv || ld_beta < Hv) return invalid("ld_g and ld_beta must be >= Hv");

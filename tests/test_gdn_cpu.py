@@ -184,3 +184,11 @@ def test_binding_refuses_counts(kda):
         kda.kda_gdn_chunk_prefill(*tensors(), None)
     with pytest.raises(ValueError, match="cu_seqlens"):
         kda.kda_gdn_chunk_prefill(*tensors(), torch.zeros(2, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_refuses_columns_past_32_bits(kda, name):
+    big = dict(ld_qkv=1 << 40, ld_g=1 << 24, ld_beta=1 << 24, ld_out=1 << 32, n=1, rows=1, T=1)
+    state = dict(slot_stride=1 << 40)
+    assert call(kda, name, big, dict(Hk=1 << 24, Hv=1 << 24), state) == 2
+    assert "2^31" in kda.last_error()
