@@ -104,28 +104,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
-// d += a b in fp32 but for 2^-21 of the terms: tf32 products of the operands' two terms
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
-{
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-template <int N>
-struct Tf32 {
-    uint32_t hi[N], lo[N];
-    __device__ __forceinline__ void set(int i, float x)
-    {
-        hi[i] = __float_as_uint(x) & 0xffffe000u;
-        lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
-    }
-};
-__device__ __forceinline__ void mma_split(float (&d)[4], const Tf32<4> &a, const Tf32<2> &b)
-{
-    mma_tf32(d, a.lo, b.hi);
-    mma_tf32(d, a.hi, b.lo);
-    mma_tf32(d, a.hi, b.hi);
-}
-
 // The bounds of a sequence; a pair that is no range of the rows has none. *bad: error bits.
 __device__ __forceinline__ int2 range(const Args &a, int seq, uint32_t *bad)
 {

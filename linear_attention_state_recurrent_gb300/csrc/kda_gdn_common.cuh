@@ -38,6 +38,29 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = rest2(x, y, hi);
 }
 
+// fp32 values as two tf32 terms, truncated: |x - hi - lo| <= 2^-20 |x|. (Not volatile: the order of products of different sums is free,
+// 61 x 5 rows x 12 heads 14.4 us for 15.0.)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int N>
+struct Tf32 {
+    uint32_t hi[N], lo[N];
+    __device__ __forceinline__ void set(int i, float x)
+    {
+        hi[i] = __float_as_uint(x) & 0xffffe000u;
+        lo[i] = __float_as_uint(x - __uint_as_float(hi[i]));
+    }
+};
+__device__ __forceinline__ void mma_split(float (&d)[4], const Tf32<4> &a, const Tf32<2> &b)
+{
+    mma_tf32(d, a.lo, b.hi);
+    mma_tf32(d, a.hi, b.lo);
+    mma_tf32(d, a.hi, b.hi);
+}
+
 // The sum of a warp's log-decays up to each lane. What is needed are differences of such sums, to an absolute error of
 // 2^-24: a few tokens with little decay may follow thousands of nats. So the sums are taken in 64 bits and kept as two floats.
 struct RunningDecay {

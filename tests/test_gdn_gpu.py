@@ -332,3 +332,18 @@ def test_decays_without_end(kda, call, K, T):
     c.gpu_args = c.gpu()
     run(kda, c, call, [0, T, 2 * T])
     c.check([(0, T), (T, 2 * T)])
+
+
+@pytest.mark.parametrize("Hk, Hv, K, V", HEADS)
+def test_spec_verify_states_to_tf32_pairs(kda, Hk, Hv, K, V):
+    """fp32 values enter the products of a few rows as two truncated tf32 terms: six of them on a state's path, each off by 2^-20 at most,
+    6^(1/2) 2^-20 = 2.4e-6 of the norm, and fp32 sums of up to 128 terms, 128^(1/2) 2^-24 = 0.7e-6."""
+    T = 8
+    c = Case(4 * T, 4, Hk, Hv, K, V, seed=41)
+    kda.kda_gdn_spec_verify(*c.gpu(), T, num_k_heads=Hk, out=c.out, err_flags=c.err)
+    pool = f64(c.pool[:, :Hv * K * V]).reshape(-1, Hv, K, V)
+    _, after, _ = og.run(f64(c.qkv[:, :c.width]), f64(c.rg), f64(c.rb), f64(c.A_log), f64(c.dt), pool, c.slots, [(r * T, (r + 1) * T) for r in range(4)], Hk)
+    got = f64(c.state)
+    for s in c.slots:
+        for h in range(Hv):
+            assert np.linalg.norm(got[s, h] - after[s, h]) <= 3.1e-6 * np.linalg.norm(after[s, h])
