@@ -14,7 +14,7 @@
 // so a state is read from memory once, kept in registers as the MMAs' accumulators, and written once. It is held
 // transposed (rows of an MMA = value columns, columns = key channels): the accumulator layout is then the layout of the
 // first operand of the next product. fp32 values enter the MMAs as two tf32 terms (2^-20 of the value); q and k are bf16, exact in one. (With
-// two bf16 terms, 2^-17, the states were off by 2e-6 to 6e-6 of their norm, for 17.2 us instead of 18.6 at 16 x 8 rows x 32 heads.)
+// two bf16 terms, 2^-17, the states were off by 2e-6 to 6e-6 of their norm, for 20.4 us instead of 21.4 at 16 x 8 rows x 32 heads.)
 #include "kda_gdn_common.cuh"
 #include "kda_pdl.cuh"
 
@@ -184,10 +184,10 @@ __device__ __forceinline__ bool not_finite(uint32_t pair)
 // One CTA per (entry, value head, 64 value columns): a warp holds 16 of them, in registers over all K channels (K / 2 floats a
 // thread), and needs nothing of the other warps but the block's T and the query-key products, which warps 0 and 1 form while the
 // others already multiply. TB tokens a step (a multiple of 8). Bound by the latency of a CTA's load, products and store, one after the other, so
-// by how many CTAs are on an SM: with 32 columns a warp (three CTAs of a whole head an SM) 16 requests of 8 rows x 32 heads took 23 us.
+// by how many CTAs are on an SM: with 32 columns a warp (three CTAs of a whole head an SM) 16 requests of 8 rows x 32 heads took a tenth longer.
 template <int V>
 constexpr int COLS = V < 64 ? V : 64;
-// GROUPS: 128 threads each that an SM has to hold (four of them without spills at K = 128, 128 registers a thread).
+// GROUPS: 128 threads each that an SM has to hold (four of them at K = 128: 128 registers a thread, hardly a spill).
 template <int K, int V, int TB, int GROUPS>
 __global__ void __launch_bounds__(2 * COLS<V>, GROUPS * 128 / (2 * COLS<V>))
 rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
@@ -476,7 +476,7 @@ cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32
     const dim3 grid(static_cast<unsigned>(num_entries * p.Hv * (V > 64 ? V / 64 : 1)));
     const int vec = reinterpret_cast<uintptr_t>(p.qkv) % 16 == 0 && p.ld_qkv % 8 == 0;   // K and V are multiples of 8
     // Four groups of 128 threads an SM at K = 128, five where that saves a wave: 16 requests x 32 heads x 128 columns (1024 groups, two waves either way)
-    // 20.2 us with four, 22.1 with five; 61 x 12 x 64 (732 groups) 14.1 with four, 12.7 with five.
+    // 21.5 us with four, 24.2 with five; 61 x 12 x 64 (732 groups) 15.3 with four, 14.1 with five.
     const int64_t groups = static_cast<int64_t>(grid.x) * (V < 64 ? V : 64) / 64;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
