@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(128, 12) decode_kernel(GdnParams p)
     const uint16_t *vp = row + 2 * HK + static_cast<int64_t>(h) * V + j0;
     const float vv[4] = {bf16_to_f32(vp[0]), bf16_to_f32(vp[1]), bf16_to_f32(vp[2]), bf16_to_f32(vp[3])};
     const float beta = sigmoid_f(bf16_to_f32(p.rb[e * p.ld_beta + h]));
-    const float alpha = expf(log_decay(p, e, h, expf(p.A_log[h]), p.dt_bias ? p.dt_bias[h] : 0.f));
+    const float alpha = expf(log_decay(p.rg[e * p.ld_g + h], expf(p.A_log[h]), p.dt_bias ? p.dt_bias[h] : 0.f));
     if (tid < K) {
         uint32_t kq = 0;
 #pragma unroll
@@ -213,6 +213,51 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
             row1 = row0;
         }
     }
+    const int64_t HK = static_cast<int64_t>(p.Hk) * K;
+    const float rate = p.A_log[h], dtb = p.dt_bias ? p.dt_bias[h] : 0.f;
+    // A block's inputs, asked for before anything is waited for: q and k, v of this thread's columns and tokens, and the gates, in the two
+    // warps that use them (lane r has token r's). Rows past the block's end are zeros.
+    constexpr int QK = 2 * TB * (K / 8), PER = (QK + THREADS - 1) / THREADS;
+    int n;
+    uint4 qk[PER];
+    uint32_t vr[NT][2];
+    uint16_t raw_g, raw_b;
+    auto fetch = [&](int64_t r0) {
+        const uint16_t *in = p.qkv + r0 * p.ld_qkv;
+#pragma unroll
+        for (int x = 0; x < PER; x++) {
+            const int i = tid + x * THREADS, part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
+            qk[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < QK && r < n) {
+                const uint16_t *from = in + r * p.ld_qkv + part * HK + hk * K + c;
+                if (vec) {
+                    qk[x] = *reinterpret_cast<const uint4 *>(from);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; y++) w[y] = from[2 * y] | static_cast<uint32_t>(from[2 * y + 1]) << 16;
+                    qk[x] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NT; m++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int r = 8 * m + t2 + c;
+                vr[m][c] = 0u;
+                if (r < n) {
+                    const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
+                    vr[m][c] = vec ? *reinterpret_cast<const uint32_t *>(vp) : vp[0] | static_cast<uint32_t>(vp[1]) << 16;
+                }
+            }
+        if (warp < 2 && lane < n) {
+            raw_g = p.rg[(r0 + lane) * p.ld_g + h];
+            raw_b = p.rb[(r0 + lane) * p.ld_beta + h];
+        }
+    };
+    n = row1 - row0 < TB ? static_cast<int>(row1 - row0) : TB;
+    fetch(row0);
     const int64_t slot = load_slot(p, e);
     uint16_t *out = p.out + static_cast<int64_t>(h) * V + j0;
     if (slot >= p.num_slots) {                            // out of range: flag, zero outputs
@@ -227,73 +272,53 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
     // S[n]: columns j0, j0 + 1 (the MMA's rows g and g + 8), channels 8n + t2, 8n + t2 + 1
     float S[CT][4];
 #pragma unroll
-    for (int n = 0; n < CT; n++)
+    for (int i = 0; i < CT; i++)
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-            const float2 x = has_state ? *reinterpret_cast<const float2 *>(tile + static_cast<int64_t>(8 * n + t2 + c) * V) : make_float2(0.f, 0.f);
-            S[n][c] = x.x; S[n][2 + c] = x.y;
+            const float2 x = has_state ? *reinterpret_cast<const float2 *>(tile + static_cast<int64_t>(8 * i + t2 + c) * V) : make_float2(0.f, 0.f);
+            S[i][c] = x.x; S[i][2 + c] = x.y;
         }
 
-    const int64_t HK = static_cast<int64_t>(p.Hk) * K;
-    const float expA = expf(p.A_log[h]), dtb = p.dt_bias ? p.dt_bias[h] : 0.f;
     // A block's products take zeros for the rows behind a row, and 0 times what is not finite is not 0: where a block's keys, values
     // or gates are not all finite, its rows go one by one, and those ahead of such a row stay as they are.
-    int n;
-    for (int64_t r0 = row0; r0 < row1; r0 += n) {
-        n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
-        const uint16_t *in = p.qkv + r0 * p.ld_qkv;
+    for (int64_t r0 = row0;;) {
         float vv[NT][4], gl, beta;
 #pragma unroll 1
         for (;;) {
             bool odd = false;
-            // q and k of the block; rows past its end are zeros, and so is their beta
-            if (vec) {
-                for (int i = tid; i < 2 * TB * (K / 8); i += THREADS) {
-                    const int part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
-                    const uint4 x = r < n ? *reinterpret_cast<const uint4 *>(in + r * p.ld_qkv + part * HK + hk * K + c) : make_uint4(0u, 0u, 0u, 0u);
-                    odd |= part && (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w));
-                    *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = x;
-                }
-            } else {
-                for (int i = tid; i < 2 * TB * K; i += THREADS) {
-                    const int part = i / (TB * K), r = i / K % TB, c = i % K;
-                    const uint16_t x = r < n ? in[r * p.ld_qkv + part * HK + hk * K + c] : static_cast<uint16_t>(0);
-                    odd |= part && not_finite(x);
-                    (part ? s_k : s_q)[r][c] = x;
-                }
+#pragma unroll
+            for (int x = 0; x < PER; x++) {
+                const int i = tid + x * THREADS, part = i / (TB * (K / 8)), r = i / (K / 8) % TB, c = i % (K / 8) * 8;
+                if (i >= QK) break;
+                odd |= part && (not_finite(qk[x].x) || not_finite(qk[x].y) || not_finite(qk[x].z) || not_finite(qk[x].w));
+                *reinterpret_cast<uint4 *>(part ? &s_k[r][c] : &s_q[r][c]) = qk[x];
             }
-            // v of this thread's columns and tokens
 #pragma unroll
             for (int m = 0; m < NT; m++)
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const int r = 8 * m + t2 + c;
-                    uint32_t x = 0u;
-                    if (r < n) {
-                        const uint16_t *vp = in + r * p.ld_qkv + 2 * HK + static_cast<int64_t>(h) * V + j0;
-                        x = vec ? *reinterpret_cast<const uint32_t *>(vp) : vp[0] | static_cast<uint32_t>(vp[1]) << 16;
-                    }
-                    odd |= not_finite(x);
-                    vv[m][c] = __uint_as_float(x << 16); vv[m][2 + c] = __uint_as_float(x & 0xffff0000u);
+                    odd |= not_finite(vr[m][c]);
+                    vv[m][c] = __uint_as_float(vr[m][c] << 16); vv[m][2 + c] = __uint_as_float(vr[m][c] & 0xffff0000u);
                 }
-            // the gates, in the two warps that use them: lane r has token r's
             gl = 0.f;
             beta = 0.f;
             if (warp < 2 && lane < n) {
-                gl = log_decay(p, r0 + lane, h, expA, dtb);
-                beta = sigmoid_f(bf16_to_f32(p.rb[(r0 + lane) * p.ld_beta + h]));
+                gl = log_decay(raw_g, expf(rate), dtb);
+                beta = sigmoid_f(bf16_to_f32(raw_b));
                 odd |= !(fabsf(gl) <= 1000.f && beta <= 1.f);
             }
             if (!__syncthreads_or(odd) || n == 1) break;
             n = 1;
+            fetch(r0);
         }
 
         // Warp 0: the block's scalars and T. Warp 1: the query-key products.
         if (warp < 2) {
             const RunningDecay b(gl, TB);
             const RunningDecay::At b_end = b.of(TB - 1);
-            for (int qk = warp; qk < 2; qk += 2) {
-                const uint16_t(*s_l)[PITCH] = qk ? s_q : s_k;
+            {
+                const bool query = warp == 1;
+                const uint16_t(*s_l)[PITCH] = query ? s_q : s_k;
                 float G[NT][4] = {}, nl[2] = {}, nr[NT] = {};
 #pragma unroll
                 for (int kt = 0; kt < K / 16; kt++) {
@@ -340,14 +365,14 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
                             const RunningDecay::At bi = b.of(i);
                             const float ni = __shfl_sync(0xffffffffu, nr[m], (t2 + c) * 4);
                             const float x = G[m][2 * hh + c] * nl[hh] * ni;
-                            if (!qk) {
+                            if (!query) {
                                 s_a[r][i] = i < r && r < n ? beta_r * x * expf(br - bi) : 0.f;
                             } else {
                                 s_w[r][i] = i <= r && r < n ? p.scale * x * expf(br - bi) : 0.f;
                             }
                         }
                     if (t2 == 0) {
-                        if (!qk) {
+                        if (!query) {
                             s_ys[r] = expf(br.hi) * nl[hh];
                             s_us[r] = expf(b_end - br) * nl[hh];
                         } else {
@@ -355,7 +380,7 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
                         }
                     }
                 }
-                if (!qk) {
+                if (!query) {
                     if (lane == 0) s_gamma = expf(b_end.hi);
                     __syncwarp();
                     // column `lane` of T by substitution, row after row
@@ -444,7 +469,11 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
             for (int c = 0; c < 2; c++)
                 if (8 * r + t2 + c < n)
                     *reinterpret_cast<uint32_t *>(out + (r0 + 8 * r + t2 + c) * p.ld_out) = pack_bf16x2(Q[r][c], Q[r][2 + c]);
-        if (r0 + n < row1) __syncthreads();   // the next block's q, k, T and scales
+        r0 += n;
+        if (r0 >= row1) break;
+        n = row1 - r0 < TB ? static_cast<int>(row1 - r0) : TB;
+        fetch(r0);
+        __syncthreads();   // the block's q, k, T and scales have been read
     }
     if (writable) {
 #pragma unroll

@@ -20,10 +20,7 @@ __device__ __forceinline__ int64_t load_slot(const GdnParams &p, int64_t e) { re
 __device__ __forceinline__ float bounded(float g) { return g < -1000.f ? -1000.f : g; }
 
 // Log-decay of a token and head: -e^{A_log} softplus(raw_g + dt_bias).
-__device__ __forceinline__ float log_decay(const GdnParams &p, int64_t row, int h, float expA, float dtb)
-{
-    return bounded(-expA * softplus_f(bf16_to_f32(p.rg[row * p.ld_g + h]) + dtb));
-}
+__device__ __forceinline__ float log_decay(uint16_t raw_g, float expA, float dtb) { return bounded(-expA * softplus_f(bf16_to_f32(raw_g) + dtb)); }
 
 // x and y as packed bf16 pairs hi + lo: hi is x rounded to bf16 and lo what is left, rounded again, so that
 // |x - hi - lo| <= 2^-17 |x|.
