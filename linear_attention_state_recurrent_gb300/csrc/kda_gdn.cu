@@ -190,7 +190,7 @@ constexpr int COLS = V < 64 ? V : 64;
 // GROUPS: 128 threads each that an SM has to hold (four of them at K = 128: 128 registers a thread, hardly a spill).
 template <int K, int V, int TB, int GROUPS>
 __global__ void __launch_bounds__(2 * COLS<V>, GROUPS * 128 / (2 * COLS<V>))
-rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
+rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec, int ahead)
 {
     constexpr int NT = TB / 8, CT = K / 8, PITCH = K + 8, TP = TB + 8, THREADS = 2 * COLS<V>, SLICES = V / COLS<V>;
     __shared__ __align__(16) uint16_t s_k[TB][PITCH], s_q[TB][PITCH];
@@ -312,6 +312,16 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec)
             fetch(r0);
         }
 
+        if (r0 == row0 && warp >= THREADS / 64) {
+            // the state of the CTA that will follow this one on its multiprocessor, to L2
+            const int64_t later = blockIdx.x + static_cast<int64_t>(ahead);
+            const int64_t next = later < gridDim.x ? load_slot(p, later / (SLICES * p.Hv)) : -1;
+            if (next >= 0 && next < p.num_slots) {
+                const float *from = p.pool + next * p.slot_stride + (later / SLICES % p.Hv) * K * V + later % SLICES * COLS<V>;
+                for (int i = tid - THREADS / 2; i < K * COLS<V> / 32; i += THREADS / 2)
+                    asm volatile("prefetch.global.L2 [%0];" :: "l"(from + static_cast<int64_t>(i / (COLS<V> / 32)) * V + i % (COLS<V> / 32) * 32));
+            }
+        }
         // Warp 0: the block's scalars and T. Warp 1: the query-key products.
         if (warp < 2) {
             const RunningDecay b(gl, TB);
@@ -511,10 +521,11 @@ cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    const auto ahead = [&](int threads, int g) { return sms * (g * 128 / threads); };
     const bool five = (groups + 5 * sms - 1) / (5 * sms) < (groups + 4 * sms - 1) / (4 * sms);
     // blocks of 8 rows for requests of at most 8: half the products of 16
     const bool small = !cu && T <= 8;
-#define KDA_GDN_LAUNCH(KK, VV, TB, G) return launch_pdl(gdn::rows_kernel<KK, VV, TB, G>, grid, dim3(2 * gdn::COLS<VV>), 0, stream, p, T, cu, rows, vec);
+#define KDA_GDN_LAUNCH(KK, VV, TB, G) return launch_pdl(gdn::rows_kernel<KK, VV, TB, G>, grid, dim3(2 * gdn::COLS<VV>), 0, stream, p, T, cu, rows, vec, ahead(2 * gdn::COLS<VV>, G));
 #define KDA_GDN_RUN(KK, VV) \
     if (K == KK && V == VV) { \
         if (!small) KDA_GDN_LAUNCH(KK, VV, 16, KK == 128 ? 4 : 5) \
