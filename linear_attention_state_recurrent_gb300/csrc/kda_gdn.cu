@@ -383,15 +383,15 @@ rows_kernel(GdnParams p, int T, const int32_t *cu, int64_t rows, int vec, int ah
                         }
                     if (t2 == 0) {
                         if (!query) {
-                            s_ys[r] = expf(br.hi) * nl[hh];
+                            s_ys[r] = expf(br) * nl[hh];
                             s_us[r] = expf(b_end - br) * nl[hh];
                         } else {
-                            s_qs[r] = p.scale * expf(br.hi) * nl[hh];
+                            s_qs[r] = p.scale * expf(br) * nl[hh];
                         }
                     }
                 }
                 if (!query) {
-                    if (lane == 0) s_gamma = expf(b_end.hi);
+                    if (lane == 0) s_gamma = expf(b_end);
                     __syncwarp();
                     // column `lane` of T by substitution, row after row
                     float x[TB];
@@ -515,7 +515,7 @@ cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32
     const dim3 grid(static_cast<unsigned>(num_entries * p.Hv * (V > 64 ? V / 64 : 1)));
     const int vec = reinterpret_cast<uintptr_t>(p.qkv) % 16 == 0 && p.ld_qkv % 8 == 0;   // K and V are multiples of 8
     // Four groups of 128 threads an SM at K = 128, five where that saves a wave: 16 requests x 32 heads x 128 columns (1024 groups, two waves either way)
-    // 21.5 us with four, 24.2 with five; 61 x 12 x 64 (732 groups) 15.3 with four, 14.1 with five.
+    // 18.9 us with four, 21.7 with five; 61 x 12 x 64 (732 groups) 15.5 with four, 13.7 with five.
     const int64_t groups = static_cast<int64_t>(grid.x) * (V < 64 ? V : 64) / 64;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

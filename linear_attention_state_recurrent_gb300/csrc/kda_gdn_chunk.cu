@@ -342,17 +342,12 @@ __global__ void __launch_bounds__(128, PREP_CTAS) prep_kernel(const __grid_const
         float *set = reinterpret_cast<float *>(rec + Rec::ROWS);
         if (pw == 0) {                                                    // the running decay, in units of log 2
             rate = expf(rate) * -1.44269504f;
-            const double g0 = 2 * lane < n ? bounded(rate * softplus_f(in0 + dtb)) : 0.f, g1 = 2 * lane + 1 < n ? bounded(rate * softplus_f(in1 + dtb)) : 0.f;
-            double b = g0 + g1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, b, o);
-                if (lane >= o) b += x;
-            }
-            const double b0_ = b - g1;
-            const float h0 = static_cast<float>(b0_), h1 = static_cast<float>(b);
-            *reinterpret_cast<float2 *>(cols + 2 * lane) = make_float2(h0, h1);
-            *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(static_cast<float>(b0_ - h0), static_cast<float>(b - h1));
+            const float g0 = 2 * lane < n ? bounded(rate * softplus_f(in0 + dtb)) : 0.f, g1 = 2 * lane + 1 < n ? bounded(rate * softplus_f(in1 + dtb)) : 0.f;
+            const FixedDecay f0 = FixedDecay::of(g0), f1 = FixedDecay::of(g1), b = (f0 + f1).up_to(32);
+            const bool nan = any_below(g0 != g0 || g1 != g1) || g0 != g0;
+            const float2 x0 = FixedDecay{b.hi - f1.hi, b.lo - f1.lo}.get(nan), x1 = b.get(nan || g1 != g1);
+            *reinterpret_cast<float2 *>(cols + 2 * lane) = make_float2(x0.x, x1.x);
+            *reinterpret_cast<float2 *>(cols + C + 2 * lane) = make_float2(x0.y, x1.y);
         } else if (pw == 1) {
             *reinterpret_cast<float2 *>(cols + 2 * C + 2 * lane) =
                 make_float2(2 * lane < n ? sigmoid_f(in0) : 0.f, 2 * lane + 1 < n ? sigmoid_f(in1) : 0.f);
