@@ -251,11 +251,12 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
     if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;
 }
 
-constexpr int PREP_CTAS = 6;
 // T diag(beta), W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
-// t - 64 of Q K^T, which one product of 128 x 64 gives. Four CTAs an SM: a warp's path through the inverse is bound by its latencies.
+// t - 64 of Q K^T, which one product of 128 x 64 gives. A warp's path through the inverse is bound by
+// its latencies: as many CTAs an SM as there is shared memory for at K = 128, and registers at 64 (257 sequences of 1 to 342 tokens x 8 heads:
+// the three launches 187 us, with six CTAs 189, with five 192).
 template <int NH>
-__global__ void __launch_bounds__(128, PREP_CTAS) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
+__global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
 {
     constexpr int K = 64 * NH;
     // the tiles of q and k; once their products and norms are there, the blocks of A, then of T, on and below the diagonal
