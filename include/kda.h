@@ -407,7 +407,9 @@ int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_
  * (negative, decreasing, past num_rows) counts as an empty sequence and sets KDA_ERRFLAG_LENGTHS. Rows of no sequence
  * are left as they were; the slot of an empty sequence is left untouched (one >= num_slots is still flagged).
  * Ranges may not share rows. `workspace` (device, 256-byte aligned) must hold
- * kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, heads) bytes, about 21 KB per 64 rows and value head; its contents are
+ * kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, heads) bytes, about 21 KB per 64 rows and value head (where few long sequences
+ * are cut into parts, with K = V, at most 50 sequences x value heads and 4096 rows a sequence or more, up to 4 (K + V) bytes per row and value head
+ * and 65 KB per part and value head more); its contents are
  * scratch between calls, and calls that share one (two captured graphs, too) must not overlap on the device. It may be NULL
  * where that is 0 (K = 32). K of 64 and 128 with mixed_qkv 16-byte aligned and ld_qkv a multiple of 8 take the tensor cores
  * in chunks of 64 rows; other layouts, and K = 32, blocks of 16 rows that are several times slower.

@@ -28,7 +28,7 @@ cudaError_t launch_gdn_rows(const GdnParams &p, int K, int V, int T, const int32
                             cudaStream_t stream);
 
 // The rows [cu[e], cu[e + 1]) of `rows` packed ones per sequence, in chunks. Bytes of workspace, and the launches.
-size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K);
+size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K, int V);
 cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs, void *workspace,
                                cudaStream_t stream);
 

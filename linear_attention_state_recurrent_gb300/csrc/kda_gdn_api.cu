@@ -113,7 +113,7 @@ size_t kda_gdn_chunk_prefill_workspace_bytes(int64_t num_rows, int64_t num_seqs,
     if (num_seqs < 0) return invalid("num_seqs must be >= 0"), 0;
     if (check_size(num_rows, num_seqs, heads->Hv)) return 0;
     set_error(KDA_OK, "%s", "");
-    return kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K);
+    return kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K, heads->V);
 }
 
 int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,
@@ -128,7 +128,7 @@ int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint1
     const int r = check_size(num_rows, num_seqs, heads->Hv);
     if (r) return r;
     if (num_seqs == 0 || num_rows == 0) return set_error(KDA_OK, "%s", "");
-    const size_t need = kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K);
+    const size_t need = kda::gdn_prefill_workspace(num_rows, num_seqs, heads->Hv, heads->K, heads->V);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return set_error(KDA_ERR_WORKSPACE, "kda_gdn_chunk_prefill needs a 256-byte aligned workspace of %zu bytes (got %zu)", need,
                          workspace ? workspace_bytes : static_cast<size_t>(0));

@@ -5,10 +5,12 @@
 //   Y = V - e^b (K^ S),   U = T diag(beta) Y,   O = e^b (Q^ S) + W U,  W = Q^ K^^T * D (i <= r),   S <- e^{b_n} S + (K^ e^{b_n - b})^T U
 // A decay that is the same in all channels leaves the tiles of q and k as they are in memory: every product takes them
 // raw, as TMA brings them, and norms and decays are factors of rows and columns of the products. What the chunks need but for
-// S, T diag(beta) and W, is 21 KB a chunk and head (KDA's is 58 KB). Three launches:
+// S, T diag(beta) and W, is 21 KB a chunk and head (KDA's is 58 KB). Three launches, and two more
+// where few long sequences are cut into parts that go side by side:
 //   map_kernel    where each sequence's chunks are, from cu_seqlens on the device
 //   prep_kernel   T diag(beta), W and the row factors of every chunk at once: a CTA per chunk and key head, for all its value heads
 //   chain_kernel  one CTA per SM walks (sequence, value head) chains, longest sequences first, S in registers
+//   ends_kernel, outputs_kernel   join the parts
 // The chain's products have value columns as rows (TMEM lanes), so that what depends on a token is a factor per column,
 // and their first operand is written to TMEM by the thread that has the values.
 // What enters the products is exact (q, k, v are bf16) or two bf16 terms, hi + lo = x to 2^-17.
@@ -52,7 +54,16 @@ struct Args {
     int32_t *first;                                    // [num_seqs + 1] each sequence's first chunk, and their number
     int2 *where;                                       // [chunks] a chunk's first row, and its rows
     unsigned char *records;                            // [chunks][Hv]
+    // Long sequences in parts, where there are few:
+    int parts;                                         // 1: none
+    float *states;                                     // [num_seqs][Hv][2 parts - 1][K][V] what the parts' chains end with
+    float *units;                                      // [num_seqs][Hv][2 parts - 1][V] of the states that parts start from, a power of two per column
+    float *partial;                                    // [rows (parts - 1) / parts][Hv][V + K] of parts 1 .., outputs and rows of transitions
 };
+
+// A sequence of `chunks` chunks in parts: the chunks of each but the last, or 0: it is too short.
+constexpr int CUT_CHUNKS = 64, MOST_PARTS = 8;
+__device__ __forceinline__ int part_chunks(const Args &a, int chunks) { return a.parts > 1 && chunks >= CUT_CHUNKS ? (chunks + a.parts - 1) / a.parts : 0; }
 
 constexpr int HALF = 2 * C * 128;                      // in shared memory, 64 channels of the chunk's keys, then of its queries
 
@@ -115,15 +126,19 @@ __device__ __forceinline__ int2 range(const Args &a, int seq, uint32_t *bad)
 
 // The chunks of this CTA's chains, one after the other, the same for every warp. A chain: a sequence (longest first), a value head
 // and a slice of its columns.
+template <bool PARTS>
 struct Walk {
     const Args &a;
     const uint16_t *order;
     int item, total, slices;
     int row, left, h, slice;    // of the current chunk: its first row, the chain's rows from there on
     int seq, chunk;
+    int kind;                   // 0: from the sequence's state; then for each further part its chain from zeros, and its transition's from the identity
+    bool cut = false;           // the sequence is in parts
+    int64_t partial = 0;        // the chunk's first row in Args::partial
 
     __device__ __forceinline__ Walk(const Args &args, const uint16_t *sorted, int vs)
-        : a(args), order(sorted), item(blockIdx.x), slices(args.V / vs) { total = args.num_seqs * args.p.Hv * slices; }
+        : a(args), order(sorted), item(blockIdx.x), slices(args.V / vs) { total = args.num_seqs * args.p.Hv * slices * (PARTS ? 2 * args.parts - 1 : 1); }
     // CTA i's chains are i, 2 G - 1 - i, 2 G + i, ..: the longest with the shortest
     __device__ __forceinline__ void advance()
     {
@@ -133,7 +148,8 @@ struct Walk {
     // The chain at `item`: whether it has rows (and a slot). *bad: error bits; *all: its rows whatever its slot.
     __device__ __forceinline__ bool chain(uint32_t *bad = nullptr, int *all = nullptr)
     {
-        const int per = a.p.Hv * slices, s = item / per, in = item - s * per;
+        const int kinds = PARTS ? 2 * a.parts - 1 : 1, per = a.p.Hv * slices * kinds, s = item / per, in = (item - s * per) / kinds;
+        kind = PARTS ? item % kinds : 0;
         h = in / slices;
         slice = in - h * slices;
         seq = a.num_seqs <= ORDER ? order[s] : s;
@@ -142,10 +158,22 @@ struct Walk {
         row = x.x;
         left = x.y;
         chunk = a.first[seq];
-        if (all) *all = left;
+        if (all) *all = kind == 0 ? left : 0;
         if (left > 0 && (left - 1) / C >= a.chunks - chunk) { left = 0; e |= kErrLengths; }   // ranges that overlap: more chunks than rows make
         if (load_slot(a.p, seq) >= a.p.num_slots) { left = 0; e |= kErrSlotRange; }
         if (bad) *bad = e;
+        if (!PARTS) return left > 0;
+        const int each = part_chunks(a, (left + C - 1) / C);
+        cut = each > 0;
+        if (cut) {
+            const int64_t ahead = static_cast<int64_t>((kind + 1) / 2) * each * C;
+            partial = static_cast<int64_t>(row) * (a.parts - 1) / a.parts + ahead - each * C;
+            row += static_cast<int>(ahead < left ? ahead : 0);
+            chunk += (kind + 1) / 2 * each;
+            left = ahead < left ? (left - static_cast<int>(ahead) < each * C ? left - static_cast<int>(ahead) : each * C) : 0;
+        } else if (kind > 0) {
+            left = 0;
+        }
         return left > 0;
     }
     // To the first chunk at or after `item`; false: there is none.
@@ -162,6 +190,7 @@ struct Walk {
         row += C;
         left -= C;
         chunk++;
+        if (PARTS) partial += C;
         if (left > 0) return true;
         advance();
         return begin();
@@ -598,8 +627,8 @@ constexpr uint32_t T_Y = 128;    // K S; then Y, later U scaled, as operands, by
 constexpr uint32_t T_U = 192;    // U; then as an operand, the same way
 constexpr uint32_t T_O = 256;    // Q S and W U
 
-// Value columns VS at a time (a slice of V), a thread with one of them and a quarter of the channels, or of the rows.
-template <int NH, int VS>
+// Value columns VS at a time (a slice of V), a thread with one of them and a quarter of the channels, or of the rows. PARTS: long sequences are in parts.
+template <int NH, int VS, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
 chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a)
 {
@@ -658,7 +687,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = words[0];
     const Waiter wait{words + 1, p.err};
-    Walk w(a, order, VS);
+    Walk<PARTS> w(a, order, VS);
 
     if (warp < 16) {
         // ---- the chain ----
@@ -709,17 +738,24 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 const unsigned char *stage = sm + s * Smem::STAGE;
                 float *tile = nullptr;
                 bool write = false;
-                const bool last = w.left <= C;
+                const bool last = w.left <= C, transition = PARTS && w.kind > 0 && w.kind % 2 == 0;
                 if (first || last) {
                     const int64_t slot = load_slot(p, w.seq);
                     if (slot >= 0) tile = p.pool + slot * p.slot_stride + (static_cast<int64_t>(w.h) * K + part * KP) * a.V + w.slice * VS + j;
                     write = slot >= 0 && slot != p.null_slot;
                 }
                 if (first) {
+                    if (PARTS && w.kind > 0) tile = nullptr;
 #pragma unroll
-                    for (int i = 0; i < KP / 2; i++)
+                    for (int i = 0; i < KP / 2; i++) {
                         S[i] = tile ? make_float2(tile[static_cast<int64_t>(2 * i) * a.V], tile[static_cast<int64_t>(2 * i + 1) * a.V]) : make_float2(0.f, 0.f);
+                        if (transition) S[i] = make_float2(part * KP + 2 * i == j ? 1.f : 0.f, part * KP + 2 * i + 1 == j ? 1.f : 0.f);
+                    }
                     give_s();
+                }
+                if (PARTS && last && w.cut) {   // the parts are joined later
+                    tile = a.states + ((static_cast<int64_t>(w.seq) * p.Hv + w.h) * (2 * a.parts - 1) + w.kind) * K * a.V + part * KP * a.V + j;
+                    write = true;
                 }
                 // v of this column and quarter of the rows
                 if (!wait.warp(full(s), (c / STAGES) & 1)) break;
@@ -728,7 +764,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                     const unsigned char *at = stage + Smem::QK + part * 16 * (VS * 2) + j * 2;
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        v[i] = *reinterpret_cast<const uint16_t *>(at + 2 * i * VS * 2) |
+                        v[i] = transition ? 0u : *reinterpret_cast<const uint16_t *>(at + 2 * i * VS * 2) |
                                static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(at + (2 * i + 1) * VS * 2)) << 16;
                 }
                 const float *set = reinterpret_cast<const float *>(stage + Smem::REC + Rec::ROWS);
@@ -809,7 +845,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         // ---- outputs ----
         const int quarter = warp & 3, j = quarter * 32 + lane;
         // chains that are skipped: their error bits, and zeros for a slot past the pool
-        for (Walk z(a, order, VS); z.item < z.total; z.advance()) {
+        for (Walk<PARTS> z(a, order, VS); z.item < z.total; z.advance()) {
             uint32_t bad;
             int all;
             z.chain(&bad, &all);
@@ -826,6 +862,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 const int s = c % STAGES, n = w.n();
                 uint16_t *out = p.out + static_cast<int64_t>(w.row) * p.ld_out + static_cast<int64_t>(w.h) * a.V + w.slice * VS + j;
                 const float *qs = reinterpret_cast<const float *>(sm + s * Smem::STAGE + Smem::REC + Rec::ROWS) + 2 * C;
+                float *part = PARTS && w.kind > 0 ? a.partial + (w.partial * p.Hv + w.h) * (a.V + K) + (w.kind % 2 ? 0 : a.V) + j : nullptr;
                 more = w.next();
                 if (!wait.warp(o_done, c & 1)) break;
                 tc::fence_after_sync();
@@ -852,7 +889,13 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                             out += p.ld_out;
                         }
                     };
-                    if (i + 16 <= n) store(std::true_type{});
+                    if (PARTS && part) {
+#pragma unroll
+                        for (int r = 0; r < 16; r++) {
+                            if (i + r < n) *part = fmaf(qs[i + r], __uint_as_float(x[r]), __uint_as_float(y[r]));
+                            part += static_cast<int64_t>(p.Hv) * (a.V + K);
+                        }
+                    } else if (i + 16 <= n) store(std::true_type{});
                     else store(std::false_type{});
                 }
                 __syncwarp();
@@ -968,7 +1011,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     } else if (warp == 22) {
         // ---- keys behind a sequence's end: another sequence's, and 0 times what they may hold is not 0; the next chain's state to L2 ----
         bool more = w.begin();
-        Walk z(a, order, VS);
+        Walk<PARTS> z(a, order, VS);
         bool another = z.begin();
         int item = -1;
         for (uint32_t c = 0; more; c++) {
@@ -976,7 +1019,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             if (w.item != item) {
                 item = w.item;
                 if (another) { z.advance(); another = z.begin(); }
-                const int64_t slot = another ? load_slot(p, z.seq) : -1;
+                const int64_t slot = another && (!PARTS || z.kind == 0) ? load_slot(p, z.seq) : -1;
                 if (slot >= 0) {
                     const float *tile = p.pool + slot * p.slot_stride + static_cast<int64_t>(z.h) * K * a.V + z.slice * VS;
                     for (int i = lane; i < K * VW; i += 32)
@@ -1002,7 +1045,220 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     if (warp == 23) tc::tmem_dealloc<512>(tmem);
 }
 
+// ---- joining the parts ----------------------------------------------------------------------
+// A part's tokens take the state it starts from, S, to A S + B: B is where its chain from zeros ends, A (its transition) where the one from the
+// identity with v = 0 does. An output is that chain's own and the transition's row times S.
+
+// 2^e for the e that x is in [2^e, 2^{e+1}) of, within what fp32 and its reciprocal hold
+__device__ __forceinline__ float power_below(float x)
+{
+    const int e = static_cast<int>(__float_as_uint(x) >> 23 & 255);
+    return __int_as_float((e < 16 ? 16 : e > 240 ? 240 : e) << 23);
+}
+// A CTA per (sequence, value head, 32 value columns): each part's end from its start, in order; the last is the sequence's. A thread has a
+// column and K / 8 channels. The next part's transition is on its way while one is applied.
+template <int K>
+__global__ void __launch_bounds__(256) ends_kernel(const __grid_constant__ Args a)
+{
+    constexpr int R = K / 8;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    float *start = reinterpret_cast<float *>(sm), *trans = start + K * 32, *most = trans + 2 * K * K;   // [K][32], [2][K][K], [8][32]
+    const GdnParams &p = a.p;
+    const int slices = K / 32, slice = blockIdx.x % slices, h = blockIdx.x / slices % p.Hv, seq = blockIdx.x / slices / p.Hv, kinds = 2 * a.parts - 1;
+    const int tid = threadIdx.x, v = tid % 32, warp = tid / 32, c0 = warp * R;
+    pdl_wait_then_release();   // no global read before this
+    uint32_t bad = 0;
+    const int2 x = range(a, seq, &bad);
+    const int chunks = (x.y + C - 1) / C, each = part_chunks(a, chunks);
+    const int64_t slot = load_slot(p, seq), at = static_cast<int64_t>(seq) * p.Hv + h;
+    if (each == 0 || slot >= p.num_slots || chunks > a.chunks - a.first[seq]) return;
+    float *states = a.states + at * kinds * K * K, *own = states + c0 * K + slice * 32 + v, *units = a.units + at * kinds * K + slice * 32 + v;
+    auto fetch = [&](int part) {
+        if (part * each < chunks) {
+            const float *from = states + 2 * part * K * K;
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(trans + part % 2 * K * K));
+#pragma unroll
+            for (int i = 0; i < K * K / 1024; i++) cp_async16(to + (tid + 256 * i) * 16, from + (tid + 256 * i) * 4, true);
+        }
+        cp_async_commit();
+    };
+    fetch(1);
+    float s[R];
+#pragma unroll
+    for (int c = 0; c < R; c++) s[c] = own[c * K];
+    for (int part = 1; part * each < chunks; part++) {
+        float *B = own + (2 * part - 1) * K * K;
+        float next[R], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < R; c++) {
+            next[c] = B[c * K];
+            start[(c0 + c) * 32 + v] = s[c];
+            const float x = fabsf(s[c]);
+            if (x > top && x <= 3.4028234e38f) top = x;
+        }
+        most[warp * 32 + v] = top;
+        cp_async_wait_all();                               // this part's transition
+        __syncthreads();
+        fetch(part + 1);
+        if (warp == 0) {                                   // the columns' largest finite values, in fp16's upper range
+            for (int i = 1; i < 8; i++) top = fmaxf(top, most[i * 32 + v]);
+            units[(part == 1 ? 0 : 2 * part - 3) * K] = power_below(top) * 0.0001220703125f;
+        }
+        const float *A = trans + part % 2 * K * K + c0 * K;
+#pragma unroll 2
+        for (int k = 0; k < K; k += 4) {
+            const float x0 = start[k * 32 + v], x1 = start[(k + 1) * 32 + v], x2 = start[(k + 2) * 32 + v], x3 = start[(k + 3) * 32 + v];
+#pragma unroll
+            for (int c = 0; c < R; c++) {
+                const float4 f = *reinterpret_cast<const float4 *>(A + c * K + k);
+                next[c] = fmaf(f.x, x0, fmaf(f.y, x1, fmaf(f.z, x2, fmaf(f.w, x3, next[c]))));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < R; c++) {
+            s[c] = next[c];
+            B[c * K] = s[c];
+        }
+    }
+    cp_async_wait_all();
+    if (slot >= 0 && slot != p.null_slot) {
+        float *to = p.pool + slot * p.slot_stride + static_cast<int64_t>(h) * K * K + c0 * K + slice * 32 + v;
+#pragma unroll
+        for (int c = 0; c < R; c++) to[c * K] = s[c];
+    }
+}
+
+// d += a b, 16 rows by 8 columns, 16 of the inner axis
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A CTA per (two chunks, value head): the outputs of chunks of parts 1 .., 16 rows a warp, by fp16 products: 2^-12 of a term, where the
+// outputs are rounded to 2^-9. A transition only shrinks what it is given, so a row of one is at most `scale` long; the states are in units of
+// their columns' largest values. 113 us at 8192 rows x 32 heads (with tf32 products
+// 133), bound by its loads' latencies.
+template <int K>
+__global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__ Args a)
+{
+    constexpr int LD = K + 8;                              // pairs of a row of the state: no bank conflicts
+    constexpr int AHEAD = 2;                               // steps of the inner axis whose operands are on their way together
+    extern __shared__ __align__(1024) unsigned char sm[];
+    uint32_t *state = reinterpret_cast<uint32_t *>(sm);    // [K / 2][LD]: of two rows each, fp16
+    __shared__ __align__(16) float units[K];
+    const GdnParams &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+    const int h = blockIdx.x % p.Hv, kinds = 2 * a.parts - 1;
+    pdl_wait_then_release();   // no global read before this
+    // the two chunks' states, where they are joined (NULL: not), and of this warp's the sequence, its row and its place among the partial outputs
+    const float *from[2], *unit[2];
+    int2 own = make_int2(0, 0);
+    int row = 0;
+    const float *mine = nullptr;
+    const int64_t ld = static_cast<int64_t>(p.Hv) * 2 * K;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int chunk = 2 * (blockIdx.x / p.Hv) + i;
+        from[i] = unit[i] = nullptr;
+        if (chunk >= a.first[a.num_seqs]) continue;
+        int seq = 0;
+        while (seq + 1 < a.num_seqs && a.first[seq + 1] <= chunk) seq++;
+        uint32_t bad = 0;
+        const int2 x = range(a, seq, &bad);
+        const int chunks = (x.y + C - 1) / C, each = part_chunks(a, chunks), at = chunk - a.first[seq];
+        if (each == 0 || at < each || at >= chunks || chunks > a.chunks - a.first[seq] || load_slot(p, seq) >= p.num_slots) continue;
+        const int part = at / each;
+        const int64_t start = (static_cast<int64_t>(seq) * p.Hv + h) * kinds + (part == 1 ? 0 : 2 * part - 3);
+        from[i] = a.states + start * K * K;
+        unit[i] = a.units + start * K;
+        if (warp / 4 == i) {
+            own = x;
+            row = at * C + warp % 4 * 16;
+            mine = a.partial + ((static_cast<int64_t>(x.x) * (a.parts - 1) / a.parts + row - each * C) * p.Hv + h) * 2 * K;
+        }
+    }
+    const bool in[2] = {row + g < own.y, row + g + 8 < own.y};
+    auto pair = [&](int r, int c) {                        // two of row g + 8 r's floats
+        return in[r] ? *reinterpret_cast<const float2 *>(mine + (g + 8 * r) * ld + c) : make_float2(0.f, 0.f);
+    };
+    const float whole = 2.f * power_below(fabsf(p.scale)), part = 1.f / whole;
+    auto half2 = [&](float2 x) { return tc::pack_f16x2(x.x * part, x.y * part); };
+    // what the next steps of the inner axis take: rows g and g + 8, columns t2 and t2 + 8
+    float2 u[AHEAD][4];
+    auto fetch = [&](float2 (&u)[4], int k) {
+#pragma unroll
+        for (int x = 0; x < 4; x++) u[x] = pair(x % 2, K + 16 * k + x / 2 * 8 + t2);
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++) fetch(u[k], k);
+    float o[K / 8][4] = {};
+#pragma unroll 1
+    for (int i = 0; i < 2; i++) {
+        if (!from[i] || (i == 1 && from[1] == from[0])) continue;
+        __syncthreads();
+        if (tid < K) units[tid] = unit[i][tid];
+        __syncthreads();
+#pragma unroll 4
+        for (int x = tid; x < K * K / 8; x += 256) {
+            const int j = x / (K / 4), c = x % (K / 4) * 4;
+            const float4 f0 = *reinterpret_cast<const float4 *>(from[i] + 2 * j * K + c), f1 = *reinterpret_cast<const float4 *>(from[i] + (2 * j + 1) * K + c);
+            const float4 z = *reinterpret_cast<const float4 *>(units + c);
+            const float4 r = make_float4(1.f / z.x, 1.f / z.y, 1.f / z.z, 1.f / z.w);
+            *reinterpret_cast<uint4 *>(state + j * LD + c) = make_uint4(tc::pack_f16x2(f0.x * r.x, f1.x * r.x), tc::pack_f16x2(f0.y * r.y, f1.y * r.y),
+                                                                        tc::pack_f16x2(f0.z * r.z, f1.z * r.z), tc::pack_f16x2(f0.w * r.w, f1.w * r.w));
+        }
+        __syncthreads();
+        if (from[warp / 4] != from[i]) continue;
+#pragma unroll 1
+        for (int k0 = 0; k0 < K / 16; k0 += AHEAD) {
+            float2 next[AHEAD][4];
+#pragma unroll
+            for (int k = 0; k < AHEAD; k++)
+                if (k0 + AHEAD < K / 16) fetch(next[k], k0 + AHEAD + k);
+#pragma unroll
+            for (int k = 0; k < AHEAD; k++) {
+                const uint32_t f[4] = {half2(u[k][0]), half2(u[k][1]), half2(u[k][2]), half2(u[k][3])};
+                const uint32_t *s = state + (8 * (k0 + k) + t2 / 2) * LD + g;
+#pragma unroll
+                for (int n = 0; n < K / 8; n++) mma_f16(o[n], f, s[8 * n], s[4 * LD + 8 * n]);
+#pragma unroll
+                for (int x = 0; x < 4; x++) u[k][x] = next[k][x];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < K / 8; n++) {
+            const float2 z = *reinterpret_cast<const float2 *>(units + 8 * n + t2);
+            const float2 x = pair(0, 8 * n + t2), y = pair(1, 8 * n + t2);
+            o[n][0] = fmaf(o[n][0] * whole, z.x, x.x); o[n][1] = fmaf(o[n][1] * whole, z.y, x.y);
+            o[n][2] = fmaf(o[n][2] * whole, z.x, y.x); o[n][3] = fmaf(o[n][3] * whole, z.y, y.y);
+        }
+    }
+    if (!mine) return;
+    uint16_t *out = p.out + (static_cast<int64_t>(own.x) + row + g) * p.ld_out + static_cast<int64_t>(h) * K + t2;
+#pragma unroll
+    for (int n = 0; n < K / 8; n++)
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+            if (in[r]) *reinterpret_cast<uint32_t *>(out + 8 * r * p.ld_out + 8 * n) = pack_bf16x2(o[n][2 * r], o[n][2 * r + 1]);
+}
+
 // ---- host ---------------------------------------------------------------------------------
+
+// Shared memory of ends_kernel.
+constexpr int ends_bytes(int K) { return (K * 32 + 2 * K * K + 8 * 32) * 4; }
+
+// The parts of long sequences: as many as give every chain a multiprocessor (152 of them), with two chains for each part behind the first.
+// Sequences that cannot have CUT_CHUNKS chunks on average stay whole: the joining costs 20 us and more. One sequence of K = V = 128, in parts and whole:
+// 2048 tokens x 32 heads 111 and 107 us, 4096 x 32 188 and 202, 16,384 x 32 645 and 761, 4096 x 8 112 and 180, 16,384 x 8 239 and 682.
+int parts_of(int64_t rows, int64_t num_seqs, int Hv, int K, int V)
+{
+    const int64_t chains = num_seqs * Hv;
+    if (K != V || rows / num_seqs < CUT_CHUNKS * C) return 1;
+    int64_t parts = (152 / chains + 1) / 2;
+    if (parts > MOST_PARTS) parts = MOST_PARTS;
+    return parts < 2 ? 1 : static_cast<int>(parts);
+}
 
 // Boxes of 64 rows by `box` columns of the packed q | k | v rows.
 cudaError_t encode(CUtensorMap *m, const GdnParams &p, int64_t rows, int64_t cols, int box, CUtensorMapSwizzle swizzle)
@@ -1029,8 +1285,10 @@ cudaError_t this_device(int *sms)
             };
             e = cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev);
             limit(prep_kernel<1>, HALF); limit(prep_kernel<2>, 2 * HALF);
-            limit(chain_kernel<1, 32>, Smem::END); limit(chain_kernel<1, 64>, Smem::END); limit(chain_kernel<1, 128>, Smem::END);
-            limit(chain_kernel<2, 32>, Smem::END); limit(chain_kernel<2, 64>, Smem::END); limit(chain_kernel<2, 128>, Smem::END);
+            limit(ends_kernel<64>, ends_bytes(64)); limit(ends_kernel<128>, ends_bytes(128)); limit(outputs_kernel<64>, 32 * 72 * 4); limit(outputs_kernel<128>, 64 * 136 * 4);
+            limit(chain_kernel<1, 32, false>, Smem::END); limit(chain_kernel<1, 64, false>, Smem::END); limit(chain_kernel<1, 128, false>, Smem::END);
+            limit(chain_kernel<2, 32, false>, Smem::END); limit(chain_kernel<2, 64, false>, Smem::END); limit(chain_kernel<2, 128, false>, Smem::END);
+            limit(chain_kernel<1, 64, true>, Smem::END); limit(chain_kernel<2, 128, true>, Smem::END);
             if (e != cudaSuccess) return e;
             known[dev].store(true, std::memory_order_release);
         }
@@ -1044,12 +1302,30 @@ int64_t up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 }  // namespace
 }  // namespace gdn
 
-size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K)
+namespace gdn {
+namespace {
+// Where a call's arrays begin in its workspace.
+struct Layout {
+    int parts;
+    int64_t where, records, states, units, partial, end;
+    Layout(int64_t rows, int64_t num_seqs, int Hv, int K, int V) : parts(parts_of(rows, num_seqs, Hv, K, V))
+    {
+        const int64_t chunks = rows / C + num_seqs;
+        where = up((num_seqs + 1) * 4);
+        records = where + up(chunks * 8);
+        states = records + up(chunks * Hv * Rec::BYTES);
+        units = states + (parts > 1 ? num_seqs * Hv * (2 * parts - 1) * K * V * 4 : 0);
+        partial = units + (parts > 1 ? num_seqs * Hv * (2 * parts - 1) * V * 4 : 0);
+        end = partial + (parts > 1 ? rows * (parts - 1) / parts * Hv * (V + K) * 4 : 0);
+    }
+};
+}  // namespace
+}  // namespace gdn
+
+size_t gdn_prefill_workspace(int64_t rows, int64_t num_seqs, int Hv, int K, int V)
 {
-    using namespace gdn;
     if (K == 32 || rows == 0 || num_seqs == 0) return 0;
-    const int64_t chunks = rows / C + num_seqs;
-    return static_cast<size_t>(up((num_seqs + 1) * 4) + up(chunks * 8) + chunks * Hv * Rec::BYTES);
+    return static_cast<size_t>(gdn::Layout(rows, num_seqs, Hv, K, V).end);
 }
 
 cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *cu, int64_t rows, int64_t num_seqs, void *workspace,
@@ -1064,26 +1340,34 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     if (e != cudaSuccess) return e;
     CUtensorMap qk, v;
     const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
+    const Layout at(rows, num_seqs, p.Hv, K, V);
     // few chains: halves of their value columns, if there are idle multiprocessors for them (16,384 tokens x 32 heads 779 us, whole 818,
     // quarters 812: a chain is bound by its latencies, not by what a multiprocessor issues)
-    const int VS = V == 128 && chains * 2 <= sms ? 64 : V;
+    const int VS = V == 128 && at.parts == 1 && chains * 2 <= sms ? 64 : V;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     if ((e = encode(&v, p, rows, cols, VS, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;
     const int64_t chunks = rows / C + num_seqs;
     unsigned char *w = static_cast<unsigned char *>(workspace);
     const Args a{p, cu, static_cast<int>(rows), static_cast<int>(num_seqs), V, static_cast<int>(chunks), reinterpret_cast<int32_t *>(w),
-                 reinterpret_cast<int2 *>(w + up((num_seqs + 1) * 4)), w + up((num_seqs + 1) * 4) + up(chunks * 8)};
+                 reinterpret_cast<int2 *>(w + at.where), w + at.records, at.parts, reinterpret_cast<float *>(w + at.states),
+                 reinterpret_cast<float *>(w + at.units), reinterpret_cast<float *>(w + at.partial)};
     if ((e = launch_pdl(map_kernel, dim3(1), dim3(1024), 0, stream, a)) != cudaSuccess) return e;
     const dim3 units(static_cast<unsigned>(chunks * p.Hk));
     e = K == 64 ? launch_pdl(prep_kernel<1>, units, dim3(128), HALF, stream, qk, a) : launch_pdl(prep_kernel<2>, units, dim3(128), 2 * HALF, stream, qk, a);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = chains * (V / VS);
+    const int64_t ctas = chains * (V / VS) * (2 * at.parts - 1);
     const dim3 grid(static_cast<unsigned>(ctas < sms ? ctas : sms));
-#define KDA_GDN_RUN(NH, W) \
-    if (K == 64 * NH && VS == W) return launch_pdl(chain_kernel<NH, W>, grid, dim3(THREADS), Smem::END, stream, qk, v, a);
-    KDA_GDN_RUN(1, 32) KDA_GDN_RUN(1, 64) KDA_GDN_RUN(1, 128) KDA_GDN_RUN(2, 32) KDA_GDN_RUN(2, 64) KDA_GDN_RUN(2, 128)
+#define KDA_GDN_RUN(NH, W, PARTS) \
+    if (K == 64 * NH && VS == W && (at.parts > 1) == PARTS) e = launch_pdl(chain_kernel<NH, W, PARTS>, grid, dim3(THREADS), Smem::END, stream, qk, v, a);
+    KDA_GDN_RUN(1, 32, false) KDA_GDN_RUN(1, 64, false) KDA_GDN_RUN(1, 128, false) KDA_GDN_RUN(2, 32, false) KDA_GDN_RUN(2, 64, false)
+    KDA_GDN_RUN(2, 128, false) KDA_GDN_RUN(1, 64, true) KDA_GDN_RUN(2, 128, true)
 #undef KDA_GDN_RUN
-    return cudaErrorInvalidValue;
+    if (e != cudaSuccess || at.parts == 1) return e;
+    const dim3 slices(static_cast<unsigned>(chains * (V / 32)));
+    e = K == 64 ? launch_pdl(ends_kernel<64>, slices, dim3(256), ends_bytes(K), stream, a) : launch_pdl(ends_kernel<128>, slices, dim3(256), ends_bytes(K), stream, a);
+    if (e != cudaSuccess) return e;
+    const dim3 pairs(static_cast<unsigned>((chunks + 1) / 2 * p.Hv));
+    return K == 64 ? launch_pdl(outputs_kernel<64>, pairs, dim3(256), 32 * 72 * 4, stream, a) : launch_pdl(outputs_kernel<128>, pairs, dim3(256), 64 * 136 * 4, stream, a);
 }
 
 }  // namespace kda

@@ -192,3 +192,14 @@ def test_refuses_columns_past_32_bits(kda, name):
     state = dict(slot_stride=1 << 40)
     assert call(kda, name, big, dict(Hk=1 << 24, Hv=1 << 24), state) == 2
     assert "2^31" in kda.last_error()
+
+
+def test_workspace_bytes_of_parts(kda):
+    """One long sequence is cut into parts (two at 32 heads, eight at 4), whose ends, units and partial outputs follow the records."""
+    record = 4 * 5120 + (3 * 64 + 4) * 4
+    for rows, H, K, parts in ((16384, 32, 128, 2), (4097, 4, 64, 8), (4095, 4, 64, 1), (8192, 51, 64, 1)):
+        more = H * (2 * parts - 1) * (K * K + K) * 4 + rows * (parts - 1) // parts * H * 2 * K * 4 if parts > 1 else 0
+        n = kda.kda_gdn_chunk_prefill_workspace_bytes(rows, 1, H, K, K)
+        least = (rows // 64 + 1) * (8 + H * record) + more
+        assert least <= n <= least + 4 * 256
+    assert kda.kda_gdn_chunk_prefill_workspace_bytes(16384, 1, 32, 128, 64) < (16384 // 64 + 1) * (8 + 32 * record) + 4 * 256   # K = V alone

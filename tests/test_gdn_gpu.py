@@ -347,3 +347,58 @@ def test_spec_verify_states_to_tf32_pairs(kda, Hk, Hv, K, V):
     for s in c.slots:
         for h in range(Hv):
             assert np.linalg.norm(got[s, h] - after[s, h]) <= 3.1e-6 * np.linalg.norm(after[s, h])
+
+
+@pytest.mark.parametrize("Hk, Hv, K, lens, slots", [
+    (1, 2, 64, [4100], [0]), (1, 2, 64, [4096, 6300, 0, 4200], [3, -1, 2, 0]), (2, 4, 64, [9000, 100], [9, 1]), (1, 1, 128, [4097, 8200], [1, 0]),
+    (1, 1, 128, [5000], [-1]), (19, 38, 64, [4200], [2])])
+def test_prefill_in_joined_parts(kda, Hk, Hv, K, lens, slots):
+    """Few long sequences, whose parts go side by side and are joined; with short ones, no state, a null slot and one past the pool among them.
+    A part's end is A S + B: as many products of the same errors on the state's path, and a joined output two terms of 2^-11 of tf32 operands
+    beside its rounding of 2^-9 in the mean, below 2e-3 of the norm still."""
+    cu = np.concatenate([[3], 3 + np.cumsum(lens)]).tolist()
+    rows = max(cu[-1] + 5, 4096 * len(lens))
+    c = Case(rows, len(lens), Hk, Hv, K, K, seed=51, slots=slots)
+    c.A_log -= 6.0                                                            # little decay: the parts depend on one another
+    args = c.gpu()
+    kda.kda_gdn_chunk_prefill(*args, torch.tensor(cu, dtype=torch.int32, device="cuda"), num_k_heads=Hk, out=c.out, err_flags=c.err, null_slot=2)
+    c.check(list(zip(cu, cu[1:])), null_slot=2, err=og.ERR_SLOT_RANGE if max(slots) >= 4 + len(lens) else 0)
+
+
+def test_one_graph_cuts_and_leaves_whole(kda):
+    """A captured call over one long row range serves lengths that are cut into parts, and such as are not."""
+    c = Case(9000, 2, 1, 2, 64, 64, seed=52)
+    args, cu = c.gpu(), torch.tensor([0, 9000, 9000], dtype=torch.int32, device="cuda")
+    ws = torch.empty(kda.kda_gdn_chunk_prefill_workspace_bytes(9000, 2, 2, 64, 64, num_k_heads=1), dtype=torch.uint8, device="cuda")
+    run = lambda: kda.kda_gdn_chunk_prefill(*args, cu, num_k_heads=1, out=c.out, err_flags=c.err, workspace=ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for bounds in ([5, 70, 5000], [0, 4096, 4100], [0, 4095, 8191], [0, 0, 9000]):
+        c.d_pool.copy_(c.pool)
+        c.out.fill_(7.0)
+        ws.fill_(255)
+        cu.copy_(torch.tensor(bounds, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(list(zip(bounds, bounds[1:])))
+
+
+def test_parts_keep_what_is_not_finite(kda):
+    """A NaN in the third of the parts reaches no row ahead of its chunk, and every state and row behind it."""
+    c = Case(4500, 1, 1, 1, 64, 64, seed=53)
+    bad = 2 * 9 * 64 + 70                                                     # eight parts of nine chunks
+    c.qkv[bad, 64 + 7] = math.nan
+    kda.kda_gdn_chunk_prefill(*c.gpu(), torch.tensor([0, 4500], dtype=torch.int32, device="cuda"), num_k_heads=1, out=c.out, err_flags=c.err)
+    got = f64(c.out)[:, :64]
+    first = bad // 64 * 64
+    assert np.isfinite(got[:first]).all() and not np.isfinite(got[bad:]).any() and not np.isfinite(f64(c.state)[c.slots[0]]).any()
+    out, _, _ = og.run(f64(c.qkv[:, :c.width]), f64(c.rg), f64(c.rb), f64(c.A_log), f64(c.dt), f64(c.pool[:, :64 * 64]).reshape(-1, 1, 64, 64), c.slots,
+                       [(0, first)], 1)
+    o = out[:first]
+    assert (np.abs(got[:first] - o) <= 2.0 ** -8 * np.abs(o) + 1e-2 * np.sqrt((o ** 2).mean(1, keepdims=True)) + 1e-30).all()
