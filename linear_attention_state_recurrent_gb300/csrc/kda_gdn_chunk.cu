@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
 
 // warps 0 - 15 the chain, 16 - 19 outputs, 20 copies, 22 the rows behind a sequence's end, 23 MMAs. A warp reads the quarter of tensor
 // memory that its number modulo 4 names and runs on that quarter of the multiprocessor: with halves of the value columns the chain's are 0
-// and 1, and the MMAs' warp stays out of their way (16,384 tokens x 32 heads 764 us, as warp 21 781).
+// and 1, and the MMAs' warp stays out of their way (16,384 tokens x 32 heads in one part 764 us, as warp 21 781).
 constexpr int THREADS = 768;
 constexpr int STAGES = 3;          // chunks in shared memory
 struct Smem {
@@ -1341,7 +1341,7 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     CUtensorMap qk, v;
     const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
     const Layout at(rows, num_seqs, p.Hv, K, V);
-    // few chains: halves of their value columns, if there are idle multiprocessors for them (16,384 tokens x 32 heads 779 us, whole 818,
+    // few chains: halves of their value columns, if there are idle multiprocessors for them (16,384 tokens x 32 heads in one part 779 us, whole columns 818,
     // quarters 812: a chain is bound by its latencies, not by what a multiprocessor issues)
     const int VS = V == 128 && at.parts == 1 && chains * 2 <= sms ? 64 : V;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
