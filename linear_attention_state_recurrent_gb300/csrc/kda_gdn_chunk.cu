@@ -1342,7 +1342,7 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     const int64_t cols = 2 * static_cast<int64_t>(p.Hk) * K + static_cast<int64_t>(p.Hv) * V, chains = num_seqs * p.Hv;
     const Layout at(rows, num_seqs, p.Hv, K, V);
     // few chains: halves of their value columns, if there are idle multiprocessors for them (16,384 tokens x 32 heads in one part 779 us, whole columns 818,
-    // quarters 812: a chain is bound by its latencies, not by what a multiprocessor issues)
+    // quarters 812: the warps of the columns that are left use as many of the multiprocessor's quarters fewer, each as loaded as before)
     const int VS = V == 128 && at.parts == 1 && chains * 2 <= sms ? 64 : V;
     if ((e = encode(&qk, p, rows, cols, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     if ((e = encode(&v, p, rows, cols, VS, CU_TENSOR_MAP_SWIZZLE_NONE)) != cudaSuccess) return e;

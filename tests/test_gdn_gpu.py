@@ -402,3 +402,23 @@ def test_parts_keep_what_is_not_finite(kda):
                        [(0, first)], 1)
     o = out[:first]
     assert (np.abs(got[:first] - o) <= 2.0 ** -8 * np.abs(o) + 1e-2 * np.sqrt((o ** 2).mean(1, keepdims=True)) + 1e-30).all()
+
+
+@pytest.mark.parametrize("scale", [-2.0e5, 1e-12, 0.0])
+def test_parts_with_columns_of_any_size(kda, scale):
+    """Joined outputs of value columns from 1e-15 to 1e15, and any scale: each column as near as its own size lets it be, and each state.
+    Of a state, a column takes the six two-term values of the norm's bound by itself: 1e-5 of it."""
+    K = V = 64
+    c = Case(4500, 1, 1, 1, K, V, seed=54)
+    c.A_log -= 6.0
+    size = torch.logspace(-15, 15, V)
+    c.qkv[:, 2 * K:c.width] *= size.to(BF16)
+    c.pool[:, :K * V] *= size.repeat(K)
+    kda.kda_gdn_chunk_prefill(*c.gpu(), torch.tensor([0, 4500], dtype=torch.int32, device="cuda"), num_k_heads=1, scale=scale, out=c.out, err_flags=c.err)
+    out, after, _ = og.run(f64(c.qkv[:, :c.width]), f64(c.rg), f64(c.rb), f64(c.A_log), f64(c.dt), f64(c.pool[:, :K * V]).reshape(-1, 1, K, V), c.slots,
+                           [(0, 4500)], 1, scale=float(np.float32(scale)))
+    got, state = f64(c.out)[:, :V], f64(c.state)[c.slots[0]][0]
+    off = np.linalg.norm(got - out, axis=0)
+    assert (off <= 2e-3 * np.linalg.norm(out, axis=0)).all(), off / np.linalg.norm(out, axis=0)
+    want = after[c.slots[0]][0]
+    assert (np.linalg.norm(state - want, axis=0) <= 1e-5 * np.linalg.norm(want, axis=0)).all()
