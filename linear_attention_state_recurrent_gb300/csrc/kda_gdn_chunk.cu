@@ -1137,18 +1137,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 }
 // A CTA per (two chunks, value head): the outputs of chunks of parts 1 .., 16 rows a warp, by fp16 products: 2^-12 of a term, where the
 // outputs are rounded to 2^-9. A transition only shrinks what it is given, so a row of one is at most `scale` long; the states are in units of
-// their columns' largest values. 113 us at 8192 rows x 32 heads (with tf32 products
+// their columns' largest values. 102 us at 8192 rows x 32 heads (with two columns a load 113, with tf32 products
 // 133), bound by its loads' latencies.
 template <int K>
 __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__ Args a)
 {
-    constexpr int LD = K + 8;                              // pairs of a row of the state: no bank conflicts
+    constexpr int LD = K + 4;                              // pairs of a row of the state; with its columns' bit 1 turned in half of the rows, no bank conflicts
     constexpr int AHEAD = 2;                               // steps of the inner axis whose operands are on their way together
     extern __shared__ __align__(1024) unsigned char sm[];
     uint32_t *state = reinterpret_cast<uint32_t *>(sm);    // [K / 2][LD]: of two rows each, fp16
     __shared__ __align__(16) float units[K];
     const GdnParams &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = (lane & 3) * 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.x % p.Hv, kinds = 2 * a.parts - 1;
     pdl_wait_then_release();   // no global read before this
     // the two chunks' states, where they are joined (NULL: not), and of this warp's the sequence, its row and its place among the partial outputs
@@ -1179,17 +1179,14 @@ __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__
         }
     }
     const bool in[2] = {row + g < own.y, row + g + 8 < own.y};
-    auto pair = [&](int r, int c) {                        // two of row g + 8 r's floats
-        return in[r] ? *reinterpret_cast<const float2 *>(mine + (g + 8 * r) * ld + c) : make_float2(0.f, 0.f);
+    auto four = [&](int r, int c) {                        // columns c + 4 t .. of row g + 8 r
+        return in[r] ? *reinterpret_cast<const float4 *>(mine + (g + 8 * r) * ld + c + 4 * t) : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     const float whole = 2.f * power_below(fabsf(p.scale)), part = 1.f / whole;
-    auto half2 = [&](float2 x) { return tc::pack_f16x2(x.x * part, x.y * part); };
-    // what the next steps of the inner axis take: rows g and g + 8, columns t2 and t2 + 8
-    float2 u[AHEAD][4];
-    auto fetch = [&](float2 (&u)[4], int k) {
-#pragma unroll
-        for (int x = 0; x < 4; x++) u[x] = pair(x % 2, K + 16 * k + x / 2 * 8 + t2);
-    };
+    auto half2 = [&](float x, float y) { return tc::pack_f16x2(x * part, y * part); };
+    // Of 16 of the inner axis a lane has columns 4 t .. 4 t + 3, which count as k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9; so too with the outputs' columns.
+    float4 u[AHEAD][2];
+    auto fetch = [&](float4 (&u)[2], int k) { u[0] = four(0, K + 16 * k); u[1] = four(1, K + 16 * k); };
 #pragma unroll
     for (int k = 0; k < AHEAD; k++) fetch(u[k], k);
     float o[K / 8][4] = {};
@@ -1205,42 +1202,53 @@ __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__
             const float4 f0 = *reinterpret_cast<const float4 *>(from[i] + 2 * j * K + c), f1 = *reinterpret_cast<const float4 *>(from[i] + (2 * j + 1) * K + c);
             const float4 z = *reinterpret_cast<const float4 *>(units + c);
             const float4 r = make_float4(1.f / z.x, 1.f / z.y, 1.f / z.z, 1.f / z.w);
-            *reinterpret_cast<uint4 *>(state + j * LD + c) = make_uint4(tc::pack_f16x2(f0.x * r.x, f1.x * r.x), tc::pack_f16x2(f0.y * r.y, f1.y * r.y),
-                                                                        tc::pack_f16x2(f0.z * r.z, f1.z * r.z), tc::pack_f16x2(f0.w * r.w, f1.w * r.w));
+            const uint4 y = make_uint4(tc::pack_f16x2(f0.x * r.x, f1.x * r.x), tc::pack_f16x2(f0.y * r.y, f1.y * r.y), tc::pack_f16x2(f0.z * r.z, f1.z * r.z),
+                                       tc::pack_f16x2(f0.w * r.w, f1.w * r.w));
+            *reinterpret_cast<uint4 *>(state + j * LD + c) = j & 2 ? make_uint4(y.z, y.w, y.x, y.y) : y;
         }
         __syncthreads();
         if (from[warp / 4] != from[i]) continue;
 #pragma unroll 1
         for (int k0 = 0; k0 < K / 16; k0 += AHEAD) {
-            float2 next[AHEAD][4];
+            float4 next[AHEAD][2];
 #pragma unroll
             for (int k = 0; k < AHEAD; k++)
                 if (k0 + AHEAD < K / 16) fetch(next[k], k0 + AHEAD + k);
 #pragma unroll
             for (int k = 0; k < AHEAD; k++) {
-                const uint32_t f[4] = {half2(u[k][0]), half2(u[k][1]), half2(u[k][2]), half2(u[k][3])};
-                const uint32_t *s = state + (8 * (k0 + k) + t2 / 2) * LD + g;
+                const uint32_t f[4] = {half2(u[k][0].x, u[k][0].y), half2(u[k][1].x, u[k][1].y), half2(u[k][0].z, u[k][0].w), half2(u[k][1].z, u[k][1].w)};
+                const uint32_t *s = state + (8 * (k0 + k) + 2 * t) * LD + (((g >> 1) * 4 + (g & 1)) ^ (t & 1) * 2);
 #pragma unroll
-                for (int n = 0; n < K / 8; n++) mma_f16(o[n], f, s[8 * n], s[4 * LD + 8 * n]);
-#pragma unroll
-                for (int x = 0; x < 4; x++) u[k][x] = next[k][x];
+                for (int n = 0; n < K / 8; n++) {
+                    const uint32_t *at = n % 2 ? s + 8 * n - 8 + (t & 1 ? -2 : 2) : s + 8 * n;
+                    mma_f16(o[n], f, at[0], at[LD]);
+                }
+                u[k][0] = next[k][0];
+                u[k][1] = next[k][1];
             }
         }
 #pragma unroll
-        for (int n = 0; n < K / 8; n++) {
-            const float2 z = *reinterpret_cast<const float2 *>(units + 8 * n + t2);
-            const float2 x = pair(0, 8 * n + t2), y = pair(1, 8 * n + t2);
-            o[n][0] = fmaf(o[n][0] * whole, z.x, x.x); o[n][1] = fmaf(o[n][1] * whole, z.y, x.y);
-            o[n][2] = fmaf(o[n][2] * whole, z.x, y.x); o[n][3] = fmaf(o[n][3] * whole, z.y, y.y);
+        for (int n = 0; n < K / 8; n += 2) {
+            const float4 z = *reinterpret_cast<const float4 *>(units + 8 * n + 4 * t);
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float4 x = four(r, 8 * n);
+                o[n][2 * r] = fmaf(o[n][2 * r] * whole, z.x, x.x);
+                o[n][2 * r + 1] = fmaf(o[n][2 * r + 1] * whole, z.y, x.y);
+                o[n + 1][2 * r] = fmaf(o[n + 1][2 * r] * whole, z.z, x.z);
+                o[n + 1][2 * r + 1] = fmaf(o[n + 1][2 * r + 1] * whole, z.w, x.w);
+            }
         }
     }
     if (!mine) return;
-    uint16_t *out = p.out + (static_cast<int64_t>(own.x) + row + g) * p.ld_out + static_cast<int64_t>(h) * K + t2;
+    uint16_t *out = p.out + (static_cast<int64_t>(own.x) + row + g) * p.ld_out + static_cast<int64_t>(h) * K + 4 * t;
 #pragma unroll
-    for (int n = 0; n < K / 8; n++)
+    for (int n = 0; n < K / 8; n += 2)
 #pragma unroll
         for (int r = 0; r < 2; r++)
-            if (in[r]) *reinterpret_cast<uint32_t *>(out + 8 * r * p.ld_out + 8 * n) = pack_bf16x2(o[n][2 * r], o[n][2 * r + 1]);
+            if (in[r])
+                *reinterpret_cast<uint2 *>(out + 8 * r * p.ld_out + 8 * n) =
+                    make_uint2(pack_bf16x2(o[n][2 * r], o[n][2 * r + 1]), pack_bf16x2(o[n + 1][2 * r], o[n + 1][2 * r + 1]));
 }
 
 // ---- host ---------------------------------------------------------------------------------
@@ -1285,7 +1293,7 @@ cudaError_t this_device(int *sms)
             };
             e = cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev);
             limit(prep_kernel<1>, HALF); limit(prep_kernel<2>, 2 * HALF);
-            limit(ends_kernel<64>, ends_bytes(64)); limit(ends_kernel<128>, ends_bytes(128)); limit(outputs_kernel<64>, 32 * 72 * 4); limit(outputs_kernel<128>, 64 * 136 * 4);
+            limit(ends_kernel<64>, ends_bytes(64)); limit(ends_kernel<128>, ends_bytes(128)); limit(outputs_kernel<64>, 32 * 68 * 4); limit(outputs_kernel<128>, 64 * 132 * 4);
             limit(chain_kernel<1, 32, false>, Smem::END); limit(chain_kernel<1, 64, false>, Smem::END); limit(chain_kernel<1, 128, false>, Smem::END);
             limit(chain_kernel<2, 32, false>, Smem::END); limit(chain_kernel<2, 64, false>, Smem::END); limit(chain_kernel<2, 128, false>, Smem::END);
             limit(chain_kernel<1, 64, true>, Smem::END); limit(chain_kernel<2, 128, true>, Smem::END);
@@ -1367,7 +1375,7 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     e = K == 64 ? launch_pdl(ends_kernel<64>, slices, dim3(256), ends_bytes(K), stream, a) : launch_pdl(ends_kernel<128>, slices, dim3(256), ends_bytes(K), stream, a);
     if (e != cudaSuccess) return e;
     const dim3 pairs(static_cast<unsigned>((chunks + 1) / 2 * p.Hv));
-    return K == 64 ? launch_pdl(outputs_kernel<64>, pairs, dim3(256), 32 * 72 * 4, stream, a) : launch_pdl(outputs_kernel<128>, pairs, dim3(256), 64 * 136 * 4, stream, a);
+    return K == 64 ? launch_pdl(outputs_kernel<64>, pairs, dim3(256), 32 * 68 * 4, stream, a) : launch_pdl(outputs_kernel<128>, pairs, dim3(256), 64 * 132 * 4, stream, a);
 }
 
 }  // namespace kda
