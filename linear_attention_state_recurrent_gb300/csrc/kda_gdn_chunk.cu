@@ -890,11 +890,20 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                         }
                     };
                     if (PARTS && part) {
+                        const int64_t ld = static_cast<int64_t>(p.Hv) * (a.V + K);
+                        auto keep = [&](auto whole) {
 #pragma unroll
-                        for (int r = 0; r < 16; r++) {
-                            if (i + r < n) *part = fmaf(qs[i + r], __uint_as_float(x[r]), __uint_as_float(y[r]));
-                            part += static_cast<int64_t>(p.Hv) * (a.V + K);
-                        }
+                            for (int r = 0; r < 16; r += 2) {
+                                const float2 o = ffma2(*reinterpret_cast<const float2 *>(qs + i + r), make_float2(__uint_as_float(x[r]), __uint_as_float(x[r + 1])),
+                                                       make_float2(__uint_as_float(y[r]), __uint_as_float(y[r + 1])));
+                                if (whole || i + r < n) *part = o.x;
+                                part += ld;
+                                if (whole || i + r + 1 < n) *part = o.y;
+                                part += ld;
+                            }
+                        };
+                        if (i + 16 <= n) keep(std::true_type{});
+                        else keep(std::false_type{});
                     } else if (i + 16 <= n) store(std::true_type{});
                     else store(std::false_type{});
                 }
