@@ -1267,7 +1267,7 @@ constexpr int ends_bytes(int K) { return (K * 32 + 2 * K * K + 8 * 32) * 4; }
 
 // The parts of long sequences: as many as give every chain a multiprocessor (152 of them), with two chains for each part behind the first.
 // Sequences that cannot have CUT_CHUNKS chunks on average stay whole: the joining costs 20 us and more. One sequence of K = V = 128, in parts and whole:
-// 2048 tokens x 32 heads 111 and 107 us, 4096 x 32 188 and 202, 16,384 x 32 645 and 761, 4096 x 8 112 and 180, 16,384 x 8 239 and 682.
+// 2048 tokens x 32 heads 111 and 107 us, 4096 x 32 188 and 202, 16,384 x 32 620 and 757, 4096 x 8 112 and 180, 16,384 x 8 239 and 682.
 int parts_of(int64_t rows, int64_t num_seqs, int Hv, int K, int V)
 {
     const int64_t chains = num_seqs * Hv;
