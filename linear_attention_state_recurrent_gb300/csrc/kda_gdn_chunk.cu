@@ -649,7 +649,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     if (tid == 0) {
         for (int i = 0; i < STAGES; i++) {
             tc::mbar_init(full(i), 1);
-            tc::mbar_init(empty(i), 1 + VW);
+            tc::mbar_init(empty(i), 2 + VW);                           // the MMAs, the outputs' warps and the one that clears keys
             tc::mbar_init(clean(i), 1);
         }
         for (const uint32_t b : {s_hi, s_lo, y_hi, y_lo, u_hi, u_lo, w_ready}) tc::mbar_init(b, 4 * VW);
@@ -1025,6 +1025,19 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         int item = -1;
         for (uint32_t c = 0; more; c++) {
             const int s = c % STAGES, n = w.n();
+            if (!wait.warp(full(s), (c / STAGES) & 1)) break;
+            if (n < C) {
+                for (int i = n * 8 + lane; i < C * 8; i += 32)
+#pragma unroll
+                    for (int hf = 0; hf < NH; hf++) *reinterpret_cast<uint4 *>(sm + s * Smem::STAGE + hf * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                arrive(clean(s));
+                arrive(empty(s));   // the stage is held until here: this warp cannot fall behind by a turn of the ring
+            }
+            // the walks past sequences without rows come after what others wait for
             if (w.item != item) {
                 item = w.item;
                 if (another) { z.advance(); another = z.begin(); }
@@ -1036,15 +1049,6 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 }
             }
             more = w.next();
-            if (!wait.warp(full(s), (c / STAGES) & 1)) break;
-            if (n < C) {
-                for (int i = n * 8 + lane; i < C * 8; i += 32)
-#pragma unroll
-                    for (int hf = 0; hf < NH; hf++) *reinterpret_cast<uint4 *>(sm + s * Smem::STAGE + hf * HALF + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                tc::fence_proxy_async();
-            }
-            __syncwarp();
-            if (lane == 0) arrive(clean(s));
         }
     }
     __syncwarp();

@@ -1,0 +1,101 @@
+"""GPU tests of the gated delta rule's chunked prefill at the edges of its batches, against its fp64 oracle. Tolerances as in
+test_gdn_gpu.py: a state within 1e-5 of its norm, an output within its rounding (2^-8 of it) and 1e-2 of its row's mean size, 2e-3 of the norm in all."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn as og
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def kda():
+    assert torch.cuda.is_available()
+    from linear_attention_state_recurrent_gb300 import build
+    build.build()
+    from linear_attention_state_recurrent_gb300 import kda as k
+    return k
+
+
+def f64(t):
+    return t.to(torch.float64).cpu().numpy()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Batch:
+    """A prefill's inputs on the GPU: sequences of `lens` rows one after the other."""
+
+    def __init__(self, lens, Hk, Hv, K, V, slots, num_slots, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        randn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+        n = self.cu[-1]
+        self.Hk, self.K, self.V, self.slots = Hk, K, V, slots
+        self.qkv = randn(n, 2 * Hk * K + Hv * V).to(BF16)
+        self.rg, self.rb = randn(n, Hv).to(BF16), randn(n, Hv).to(BF16)
+        self.A_log, self.dt = torch.rand(Hv, generator=g, device="cuda"), -3 + randn(Hv)
+        self.pool = 0.05 * randn(num_slots, Hv, K, V)
+        self.start = self.pool.clone()
+        self.out = torch.full((n, Hv * V), 7.0, dtype=BF16, device="cuda")
+        self.err = i32([0])
+
+    def run(self, kda, **kw):
+        kda.kda_gdn_chunk_prefill(self.qkv, self.rg, self.rb, self.A_log, self.dt, self.pool, i32(self.slots), i32(self.cu), num_k_heads=self.Hk, out=self.out,
+                                  err_flags=self.err, **kw)
+
+    def check(self, entries):
+        """The given sequences' outputs and states; those of their slots alone have changed."""
+        assert self.err.item() == 0
+        slots, bounds = [self.slots[e] for e in entries], [(self.cu[e], self.cu[e + 1]) for e in entries]
+        out, after, _ = og.run(*map(f64, (self.qkv, self.rg, self.rb, self.A_log, self.dt, self.start)), slots, bounds, self.Hk)
+        rows = np.concatenate([np.arange(*b) for b in bounds])
+        g, o = (x[rows].reshape(-1, self.V) for x in (f64(self.out), out))
+        assert np.linalg.norm(g - o) <= 2e-3 * np.linalg.norm(o)
+        assert (np.abs(g - o) <= 2.0 ** -8 * np.abs(o) + 1e-2 * np.sqrt((o ** 2).mean(1, keepdims=True))).all()
+        off = np.linalg.norm(f64(self.pool) - after, axis=(2, 3)) / np.linalg.norm(after, axis=(2, 3))
+        assert off.max() <= 1e-5, off.max()
+        same = sorted(set(range(len(after))) - set(slots))
+        assert torch.equal(self.pool[same], self.start[same])
+
+
+@pytest.mark.parametrize("K, V", [(64, 64), (128, 32)])
+def test_long_runs_of_empty_sequences(kda, K, V):
+    """Thousands of entries without rows between the chains of each multiprocessor; every sequence ends inside a chunk and has rows of NaN behind it."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    r = np.random.default_rng(1)
+    lens, live = [], []
+    for part in range(2):
+        for _ in range(sms):
+            live.append(len(lens))
+            lens += [64 * int(r.integers(2, 5)) + int(r.integers(1, 64)), 70]
+        if part == 0:
+            lens += [0] * (60 * sms)
+    slots = [-1] * len(lens)
+    for i, e in enumerate(live):
+        slots[e] = i
+    b = Batch(lens, 1, 1, K, V, slots, len(live) + 2, seed=K)
+    for e in live:
+        b.qkv[b.cu[e + 1]:b.cu[e + 2]] = math.nan
+    b.run(kda)
+    b.check(live)
+
+
+def test_few_sequences_with_rows_among_many_heads(kda):
+    """A step of 256 entries of which 16 have rows, with 64 heads: a hundred chains without rows behind each multiprocessor's own."""
+    r = np.random.default_rng(2)
+    lens = np.zeros(256, int)
+    live = r.permutation(256)[:16].tolist()
+    lens[live] = r.integers(65, 128, 16)
+    slots = [-1] * 256
+    for i, e in enumerate(live):
+        slots[e] = i
+    b = Batch(lens.tolist(), 2, 64, 64, 32, slots, 17, seed=3)
+    b.run(kda)
+    b.check(live)
