@@ -469,26 +469,27 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
         const int es = p.out_dtype == KDA_FP32 ? 4 : 2, wide = 128 / es;         // columns of a box
         unsigned char *boxes = sm + T::BOXES + e * 2 * T::BOX;
         auto landed = [&](int x) { return b0 + (2 * T::STAGES + 4 + e * 2 + x) * 8; };
-        uint32_t rphase[2] = {0, 0};
-        int b = 0;
+        uint32_t rphase = 0;                                                     // a bit for each box
+        int b = 0, turn = 0;                                                     // boxes used so far: they take turns across tiles too
         uint32_t tphase = 0;
         for (int i = pair; i < total; i += pairs) {
             int tm, tn;
             tile_at(tiles, i, &tm, &tn);
             const int m0 = tm * 256 + rank * 128 + quarter * 32, n0 = tn * 256 + c0;
-            const int blocks = m0 >= p.M ? 0 : (min(128, p.N - n0) + wide - 1) / wide;   // of boxes that hold outputs
+            const int blocks = m0 >= p.M || n0 >= p.N ? 0 : (min(128, p.N - n0) + wide - 1) / wide;   // of boxes that hold outputs
+            auto side = [&](int x) { return (turn + x) & 1; };
             auto by_tma = [&](int x) { return n0 + (x + 1) * wide <= tma_n || (n0 + x * wide < tma_n && tma_n == p.N); };
             auto fetch = [&](int x) {                                             // the residual of box x
                 if (lane == 0) {
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the box's last outputs are on their way
-                    tc::mbar_expect_tx(landed(x & 1), T::BOX);
-                    tc::tma_load_2d(tc::smem_addr(boxes + (x & 1) * T::BOX), &tm_res, n0 + x * wide, m0, landed(x & 1));
+                    tc::mbar_expect_tx(landed(side(x)), T::BOX);
+                    tc::tma_load_2d(tc::smem_addr(boxes + side(x) * T::BOX), &tm_res, n0 + x * wide, m0, landed(side(x)));
                 }
                 __syncwarp();
             };
             // box x between memory and shared memory where TMA cannot: row after row, lanes along the columns
             auto loose = [&](auto in, int x) {
-                unsigned char *from = boxes + (x & 1) * T::BOX;
+                unsigned char *from = boxes + side(x) * T::BOX;
                 const int cols = min(wide, p.N - n0 - x * wide), rows = min(32, p.M - m0);
 #pragma unroll 4
                 for (int r = 0; r < rows; r++) {
@@ -508,7 +509,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             if (p.res && blocks > 0 && by_tma(0)) fetch(0);
             if (!wait_warp(tfull(b), tphase)) {
                 report(p);
-                if (p.res && blocks > 0 && by_tma(0)) (void)wait_warp(landed(0), rphase[0]);   // no CTA ends with copies in flight
+                if (p.res && blocks > 0 && by_tma(0)) (void)wait_warp(landed(side(0)), rphase >> side(0) & 1);   // no CTA ends with copies in flight
                 break;
             }
             tc::fence_after_sync();
@@ -516,20 +517,20 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
             bool gone = false;
 #pragma unroll 1
             for (int x = 0; x < blocks; x++) {
-                unsigned char *box = boxes + (x & 1) * T::BOX + lane * 128;
+                unsigned char *box = boxes + side(x) * T::BOX + lane * 128;
                 const bool tma = by_tma(x);
                 if (p.res && x + 1 < blocks && by_tma(x + 1)) fetch(x + 1);
                 if (tma) {
                     if (p.res) {
-                        if (!wait_warp(landed(x & 1), rphase[x & 1])) {
+                        if (!wait_warp(landed(side(x)), rphase >> side(x) & 1)) {
                             report(p);
-                            if (x + 1 < blocks && by_tma(x + 1)) (void)wait_warp(landed((x + 1) & 1), rphase[(x + 1) & 1]);
+                            if (x + 1 < blocks && by_tma(x + 1)) (void)wait_warp(landed(side(x + 1)), rphase >> side(x + 1) & 1);
                             gone = true;
                             break;
                         }
-                        rphase[x & 1] ^= 1;
+                        rphase ^= 1u << side(x);
                     } else {
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the last outputs but one: this box's
                         __syncwarp();
                     }
                 } else {
@@ -587,7 +588,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                     __syncwarp();
                     if (lane == 0) {
                         asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
-                                     :: "l"(&tm_out), "r"(n0 + x * wide), "r"(m0), "r"(tc::smem_addr(boxes + (x & 1) * T::BOX)) : "memory");
+                                     :: "l"(&tm_out), "r"(n0 + x * wide), "r"(m0), "r"(tc::smem_addr(boxes + side(x) * T::BOX)) : "memory");
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                     __syncwarp();
@@ -599,6 +600,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CU
                 }
             }
             if (gone) break;
+            turn += blocks;
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(in_cta(tempty(b), 0)) : "memory");

@@ -1,0 +1,52 @@
+"""GPU tests of the 16-bit product's large tiles at the edges of what they write, against 64-bit torch. Tolerances as in test_matmul_gpu.py."""
+import pytest
+import torch
+
+from tests.test_matmul_gpu import BF16, FP16, FP32, check, rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kda():
+    assert torch.cuda.is_available()
+    from linear_attention_state_recurrent_gb300 import build
+    build.build()
+    from linear_attention_state_recurrent_gb300 import kda as k
+    return k
+
+
+@pytest.mark.parametrize("N, out", [(320, BF16), (320, FP16), (288, FP32), (352, FP32), (64, BF16), (328, BF16), (300, FP32)])
+@pytest.mark.parametrize("act, bias", [(None, False), ("relu", True)])
+def test_odd_boxes_of_many_tiles(kda, N, out, act, bias):
+    """A short inner axis, so that the epilogue is what a pair waits for; every pair has several tiles of an odd number of boxes, one after the other,
+    and neither a residual nor time between their stores. Element by element, several times over."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    M, K = 33494, 256 if N > 64 else 64
+    a, w = rows(M, K, BF16, g, 0), rows(N, K, BF16, g, 0, K ** -0.5)
+    b = torch.randn(N, generator=g, device="cuda") if bias else None
+    if N > 64:
+        assert kda.kda_matmul_plan(a, w)[0] == 256
+    first = None
+    for _ in range(5):
+        o = torch.full((M, N + -N % 8 + 8), 7.0, dtype=out, device="cuda")
+        kda.kda_matmul(a, w, bias=b, activation=act, out=o[:, :N])
+        assert (o[:, N:] == 7.0).all()
+        if first is None:
+            first = o
+            check(o[:, :N], a, w, b, act)
+        assert torch.equal(o, first)
+
+
+@pytest.mark.parametrize("N, out, pad", [(320, BF16, 0), (288, FP32, 0), (353, FP16, 7), (329, FP32, 3)])
+def test_odd_boxes_with_a_residual_in_place(kda, N, out, pad):
+    """The boxes take turns across tiles where residuals come into them too, and where the last columns are stored by rows."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    a, w = rows(33494, 256, FP16, g, 0), rows(N, 256, FP16, g, 0, 1 / 16)
+    assert kda.kda_matmul_plan(a, w)[0] == 256
+    res = rows(33494, N, out, g, pad)
+    for _ in range(3):
+        o = torch.empty(33494, N + pad, dtype=out, device="cuda")[:, :N]
+        o.copy_(res)
+        kda.kda_matmul(a, w, residual=o, activation="relu", out=o)
+        check(o, a, w, None, "relu", res)
