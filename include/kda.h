@@ -503,7 +503,8 @@ int kda_matmul(const void *a, int64_t ld_a, const void *w, int64_t ld_w, int32_t
 /*
  * kda_matmul_plan — how kda_matmul would compute a product on the current device: plan (host int32 [2]) receives the rows of a per
  * tile (16 .. 128: single CTAs; 256: pairs; 0: element loads, for operands off 16-byte boundaries) and the CTAs that split the inner
- * axis. Of a and w only the alignment counts; nothing is launched.
+ * axis. Of a and w only the alignment counts; outputs and a residual are taken as on 16-byte boundaries too (for others kda_matmul
+ * may choose smaller tiles). Nothing is launched.
  */
 int kda_matmul_plan(const void *a, int64_t ld_a, const void *w, int64_t ld_w, int64_t M, int64_t N, int64_t K, int32_t *plan);
 

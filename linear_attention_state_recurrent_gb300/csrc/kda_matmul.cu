@@ -709,8 +709,17 @@ struct Choice {
     int rows = 0;              // of A per tile: 16 .. 128 (tile_kernel), 256 (pair_kernel), 0: 64 loose ones
     int split = 1;
     int64_t ld_a, ld_w;
+    bool boxes = false;        // the pairs' outputs, and residuals, move by TMA
     const Device *device = nullptr;
 };
+
+// Whether TMA can move the outputs, and the residual where there is one. (A plan without outputs takes them as such.)
+bool outputs_by_tma(const MatmulParams &p)
+{
+    const int es = p.out_dtype == KDA_FP32 ? 4 : 2;
+    int64_t ld_out = p.ld_out, ld_res = p.ld_res;
+    return !p.out || (tma_rows(p.out, &ld_out, p.M, p.N, es) && (!p.res || tma_rows(p.res, &ld_res, p.M, p.N, es)));
+}
 
 // Plans are compared by their time in nanoseconds, fitted to the measured splits of products of 1 to 8192 rows, N and K of 64 to 12,288:
 // start and end of a wave of CTAs, then its steps of 64 of the inner axis, each by the slowest of the MMAs, the stream from HBM (5.7 kB/ns
@@ -728,12 +737,13 @@ double time_tile(const MatmulParams &p, const int (&fit)[9], int nt, int split)
     const double waves = static_cast<double>((ctas + fit[split] - 1) / fit[split]);
     return waves * (3200. + 14. * nt + step * ((steps + split - 1) / split)) + (split > 1 ? 1100. + 6. * nt : 0.);
 }
-// The pairs' epilogues are beside the next tile's MMAs; where TMA cannot write the outputs they take three times as long.
-double time_pair(const MatmulParams &p, int sms, bool tma_out)
+// The pairs' epilogues are beside the next tile's MMAs. Where TMA cannot move outputs or residuals they go by rows through shared memory: a tile of
+// 16-bit outputs then takes 7 to 9 us, of fp32 ones 11 to 20; with residuals 16 and 30 from L2, 48 and 90 from HBM, a row's latency after the other's.
+double time_pair(const MatmulParams &p, int sms, bool boxes)
 {
     const int64_t tiles = ((p.M - 1) / 256 + 1) * static_cast<int64_t>((p.N - 1) / 256 + 1);
     const int pairs = sms / 2, steps = (p.K + BK - 1) / BK;
-    const double end = tma_out ? 3000. : 9000., main = 270. * steps;
+    const double end = boxes ? 3000. : p.out_dtype == KDA_FP32 ? (p.res ? 90000. : 16000.) : (p.res ? 48000. : 9000.), main = 270. * steps;
     return 3000. + static_cast<double>((tiles + pairs - 1) / pairs) * (main > end ? main : end) + end;
 }
 
@@ -760,9 +770,8 @@ cudaError_t choose(const MatmulParams &p, Choice *c)
     if (p.M > 16 && p.M <= 1024) tile(1, 32, 32);
     if (p.M > 32) tile(2, 64, 64);
     if (p.M > 64) tile(3, 128, 128);
-    int64_t ld_out = p.ld_out;
-    const bool tma_out = !p.out || tma_rows(p.out, &ld_out, p.M, p.N, p.out_dtype == KDA_FP32 ? 4 : 2);
-    if (p.M > 128 && time_pair(p, d->sms, tma_out) < least) { c->rows = 256; c->split = 1; }
+    c->boxes = outputs_by_tma(p);
+    if (p.M > 128 && time_pair(p, d->sms, c->boxes) < least) { c->rows = 256; c->split = 1; }
     return cudaSuccess;
 }
 
@@ -790,13 +799,10 @@ cudaError_t run_pair(const MatmulParams &p, const Choice &c, cudaStream_t stream
     if ((e = encode(&tw, type_of(p.dtype), 2, p.w, p.K, p.N, c.ld_w, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     if ((e = encode(&ta, type_of(p.dtype), 2, p.a, p.K, p.M, c.ld_a, BK, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
     const int es = p.out_dtype == KDA_FP32 ? 4 : 2, wide = 128 / es;
-    int64_t ld_out = p.ld_out, ld_res = p.ld_res;
     // TMA writes whole 16-byte pieces, also where the map ends inside one: then the last columns are stored without it
-    int tma_n = 0;
-    if (tma_rows(p.out, &ld_out, p.M, p.N, es) && (!p.res || tma_rows(p.res, &ld_res, p.M, p.N, es)))
-        tma_n = static_cast<int64_t>(p.N) * es % 16 == 0 ? p.N : p.N / wide * wide;
-    if (tma_n > 0 && (e = encode(&to, type_of(p.out_dtype), es, p.out, p.N, p.M, ld_out, wide, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
-    if (tma_n > 0 && p.res && (e = encode(&tr, type_of(p.out_dtype), es, p.res, p.N, p.M, ld_res, wide, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
+    const int tma_n = !c.boxes ? 0 : static_cast<int64_t>(p.N) * es % 16 == 0 ? p.N : p.N / wide * wide;
+    if (tma_n > 0 && (e = encode(&to, type_of(p.out_dtype), es, p.out, p.N, p.M, p.ld_out, wide, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess) return e;
+    if (tma_n > 0 && p.res && (e = encode(&tr, type_of(p.out_dtype), es, p.res, p.N, p.M, p.ld_res, wide, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != cudaSuccess)
         return e;
     const int sms = c.device->sms;
     const Tiles t{(p.M - 1) / 256 + 1, (p.N - 1) / 256 + 1, sms / 4};   // the pairs at work share two tiles of W

@@ -648,7 +648,7 @@ def kda_matmul(a, w, *, bias=None, activation=None, residual=None, out=None, out
 
 def kda_matmul_plan(a, w):
     """How kda_matmul would compute a product of these operands on the current device: (rows of a per tile, CTAs that split the inner
-    axis); 0 rows: element loads, for operands off 16-byte boundaries."""
+    axis); 0 rows: element loads, for operands off 16-byte boundaries. Outputs and a residual are taken as on such boundaries."""
     if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
         raise ValueError("a and w must be 2-D with the same number of columns")
     plan = (ctypes.c_int32 * 2)()

@@ -50,3 +50,17 @@ def test_odd_boxes_with_a_residual_in_place(kda, N, out, pad):
         o.copy_(res)
         kda.kda_matmul(a, w, residual=o, activation="relu", out=o)
         check(o, a, w, None, "relu", res)
+
+
+@pytest.mark.parametrize("out_at, res_at", [((0, 0), (3, 0)), ((0, 0), (0, 1)), ((1, 0), (0, 0)), ((0, 1), (5, 1)), ((0, 0), None), ((7, 0), None)])
+@pytest.mark.parametrize("M, N, K, out", [(2048, 8192, 16384, BF16), (2048, 8192, 16384, FP32), (8001, 600, 512, FP32), (1500, 1304, 4096, BF16)])
+def test_outputs_and_residuals_on_boundaries_of_their_own(kda, M, N, K, out, out_at, res_at):
+    """Either off 16-byte boundaries, both or none (how many elements longer than the columns rows are, and where the first begins): where pairs take such outputs as
+    well (256 tiles of 256 steps of 270 ns each), and where smaller tiles take them."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, w = rows(M, K, BF16, g, 0), rows(N, K, BF16, g, 0, K ** -0.5)
+    assert kda.kda_matmul_plan(a, w)[0] == 256
+    o = rows(M, N, out, g, out_at[0], 1.0, out_at[1])
+    res = None if res_at is None else rows(M, N, out, g, res_at[0], 1.0, res_at[1])
+    kda.kda_matmul(a, w, residual=res, out=o)
+    check(o, a, w, None, None, res)
