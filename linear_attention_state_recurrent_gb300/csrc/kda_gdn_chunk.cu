@@ -158,8 +158,8 @@ struct Walk {
         row = x.x;
         left = x.y;
         chunk = a.first[seq];
-        if (all) *all = kind == 0 ? left : 0;
         if (left > 0 && (left - 1) / C >= a.chunks - chunk) { left = 0; e |= kErrLengths; }   // ranges that overlap: more chunks than rows make
+        if (all) *all = kind == 0 ? left : 0;
         if (load_slot(a.p, seq) >= a.p.num_slots) { left = 0; e |= kErrSlotRange; }
         if (bad) *bad = e;
         if (!PARTS) return left > 0;
@@ -231,6 +231,12 @@ struct Waiter {
 
 __device__ __forceinline__ constexpr int block_at(int a, int b) { return (a * (a + 1) / 2 + b) * BLK; }
 
+// Chunks are counted up to here: ranges that overlap can have more than 32 bits hold, a workspace (21 KB each) never.
+__device__ __forceinline__ int count(int x, int y)
+{
+    constexpr int MOST = (1 << 30) - 1;
+    return x + y < MOST ? x + y : MOST;
+}
 // One CTA: every sequence's first chunk (their number is not above rows / 64 + num_seqs where the ranges do not overlap; what would
 // pass it is left out) and each chunk's rows. Error bits are the chain's.
 __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args a)
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            if (lane >= o) sum = count(sum, y);
         }
         if (lane == 31) sums[warp] = sum;
         __syncthreads();
@@ -256,10 +262,10 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += y;
+            if (lane >= o) before = count(before, y);
         }
         const int all = __shfl_sync(0xffffffffu, before, 31), here = warp > 0 ? __shfl_sync(0xffffffffu, before, warp - 1) : 0;
-        const int first = base + here + sum - n;
+        const int first = count(count(base, here), sum) - n;
         firsts[tid] = first;
         starts[tid] = x.x;
         lens[tid] = x.y;
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
             const int at = (i - firsts[low]) * C;
             a.where[i] = make_int2(starts[low] + at, lens[low] - at < C ? lens[low] - at : C);
         }
-        base += all;
+        base = count(base, all);
         __syncthreads();
     }
     if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;

@@ -99,3 +99,20 @@ def test_few_sequences_with_rows_among_many_heads(kda):
     b = Batch(lens.tolist(), 2, 64, 64, 32, slots, 17, seed=3)
     b.run(kda)
     b.check(live)
+
+
+def test_overlapping_ranges_count_no_further_than_the_workspace(kda):
+    """Ranges over all rows again and again, 2^31 chunks and more between them: those that the workspace has chunks for are computed, the others count as empty, and
+    the lengths' bit says so."""
+    rows, n, K, V = 1 << 22, 65600, 64, 32
+    b = Batch([rows], 1, 1, K, V, [0], 3, seed=5)
+    b.run(kda)
+    assert b.err.item() == 0
+    want = b.pool[0].clone()
+    b.pool.copy_(b.start)
+    b.cu = [0, rows] * (n // 2) + [0]
+    b.slots = [0, 2, 1] + [2] * (n - 3)
+    b.pool[1] = b.pool[0]
+    b.run(kda)
+    assert b.err.item() == og.ERR_LENGTHS
+    assert torch.equal(b.pool[0], want) and torch.equal(b.pool[1], want) and torch.equal(b.pool[2], b.start[2])
