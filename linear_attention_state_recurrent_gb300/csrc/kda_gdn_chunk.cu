@@ -1068,12 +1068,16 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
 // A part's tokens take the state it starts from, S, to A S + B: B is where its chain from zeros ends, A (its transition) where the one from the
 // identity with v = 0 does. An output is that chain's own and the transition's row times S.
 
-// 2^e for the e that x is in [2^e, 2^{e+1}) of, within what fp32 and its reciprocal hold
-__device__ __forceinline__ float power_below(float x)
+// The unit of values up to `top`, a power of two that puts them into fp16's upper range (2^13 and more), within what fp32 and its reciprocal hold.
+__device__ __forceinline__ float unit_of(float top)
 {
-    const int e = static_cast<int>(__float_as_uint(x) >> 23 & 255);
-    return __int_as_float((e < 16 ? 16 : e > 240 ? 240 : e) << 23);
+    const int e = static_cast<int>(__float_as_uint(top) >> 23 & 255);
+    return __int_as_float(((e < 16 ? 16 : e > 254 ? 254 : e) - 13) << 23);
 }
+// One over a power of two.
+__device__ __forceinline__ float over(float unit) { return __int_as_float(0x7f000000 - __float_as_int(unit)); }
+// The larger of `top` and |x|, where that is finite.
+__device__ __forceinline__ float with(float top, float x) { return fabsf(x) > top && fabsf(x) <= 3.4028234e38f ? fabsf(x) : top; }
 // A CTA per (sequence, value head, 32 value columns): each part's end from its start, in order; the last is the sequence's. A thread has a
 // column and K / 8 channels. The next part's transition is on its way while one is applied.
 template <int K>
@@ -1112,16 +1116,15 @@ __global__ void __launch_bounds__(256) ends_kernel(const __grid_constant__ Args 
         for (int c = 0; c < R; c++) {
             next[c] = B[c * K];
             start[(c0 + c) * 32 + v] = s[c];
-            const float x = fabsf(s[c]);
-            if (x > top && x <= 3.4028234e38f) top = x;
+            top = with(top, s[c]);
         }
         most[warp * 32 + v] = top;
         cp_async_wait_all();                               // this part's transition
         __syncthreads();
         fetch(part + 1);
-        if (warp == 0) {                                   // the columns' largest finite values, in fp16's upper range
+        if (warp == 0) {                                   // the columns' largest finite values
             for (int i = 1; i < 8; i++) top = fmaxf(top, most[i * 32 + v]);
-            units[(part == 1 ? 0 : 2 * part - 3) * K] = power_below(top) * 0.0001220703125f;
+            units[(part == 1 ? 0 : 2 * part - 3) * K] = unit_of(top);
         }
         const float *A = trans + part % 2 * K * K + c0 * K;
 #pragma unroll 2
@@ -1155,20 +1158,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // A CTA per (two chunks, value head): the outputs of chunks of parts 1 .., 16 rows a warp, by fp16 products: 2^-12 of a term, where the
-// outputs are rounded to 2^-9. A transition only shrinks what it is given, so a row of one is at most `scale` long; the states are in units of
-// their columns' largest values. 102 us at 8192 rows x 32 heads (with two columns a load 113, with tf32 products
-// 133), bound by its loads' latencies.
+// outputs are rounded to 2^-9. fp16's range is short, and both factors shrink with the decays over a part: a transition's rows are in units of
+// their own largest values, the states in those of their columns'. The rows are copied to shared memory whole, so that they are on chip for both their largest
+// values and the products (read again from L1 instead 10 us more). The CTAs of the first parts' chunks, which have nothing to do, take turns with the others.
 template <int K>
 __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__ Args a)
 {
     constexpr int LD = K + 4;                              // pairs of a row of the state; with its columns' bit 1 turned in half of the rows, no bank conflicts
-    constexpr int AHEAD = 2;                               // steps of the inner axis whose operands are on their way together
+    constexpr int ROW = K + 16;                            // floats from one row of a transition to the next: no bank conflicts
     extern __shared__ __align__(1024) unsigned char sm[];
     uint32_t *state = reinterpret_cast<uint32_t *>(sm);    // [K / 2][LD]: of two rows each, fp16
+    float *rows = reinterpret_cast<float *>(state + K / 2 * LD) + (threadIdx.x >> 5) * 16 * ROW;   // this warp's 16 of the transitions
     __shared__ __align__(16) float units[K];
     const GdnParams &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.x % p.Hv, kinds = 2 * a.parts - 1;
+    const int pairs = gridDim.x / p.Hv, pair_at = blockIdx.x / p.Hv, pair = pair_at & 1 ? pair_at >> 1 : (pairs >> 1) + (pair_at >> 1);
     pdl_wait_then_release();   // no global read before this
     // the two chunks' states, where they are joined (NULL: not), and of this warp's the sequence, its row and its place among the partial outputs
     const float *from[2], *unit[2];
@@ -1178,7 +1183,7 @@ __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__
     const int64_t ld = static_cast<int64_t>(p.Hv) * 2 * K;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int chunk = 2 * (blockIdx.x / p.Hv) + i;
+        const int chunk = 2 * pair + i;
         from[i] = unit[i] = nullptr;
         if (chunk >= a.first[a.num_seqs]) continue;
         int seq = 0;
@@ -1198,17 +1203,21 @@ __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__
         }
     }
     const bool in[2] = {row + g < own.y, row + g + 8 < own.y};
-    auto four = [&](int r, int c) {                        // columns c + 4 t .. of row g + 8 r
-        return in[r] ? *reinterpret_cast<const float4 *>(mine + (g + 8 * r) * ld + c + 4 * t) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    const float whole = 2.f * power_below(fabsf(p.scale)), part = 1.f / whole;
-    auto half2 = [&](float x, float y) { return tc::pack_f16x2(x * part, y * part); };
-    // Of 16 of the inner axis a lane has columns 4 t .. 4 t + 3, which count as k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9; so too with the outputs' columns.
-    float4 u[AHEAD][2];
-    auto fetch = [&](float4 (&u)[2], int k) { u[0] = four(0, K + 16 * k); u[1] = four(1, K + 16 * k); };
+    if (mine) {                                            // the part's own outputs to L2
 #pragma unroll
-    for (int k = 0; k < AHEAD; k++) fetch(u[k], k);
-    float o[K / 8][4] = {};
+        for (int x = lane; x < 16 * (K / 32); x += 32) {
+            const int r = x / (K / 32);
+            if (row + r < own.y) asm volatile("prefetch.global.L2 [%0];" :: "l"(mine + r * ld + x % (K / 32) * 32));
+        }
+    }
+    // the rows of the transition, all on their way beside the state
+#pragma unroll
+    for (int x = lane; x < 16 * (K / 4); x += 32) {
+        const int r = x / (K / 4), c = x % (K / 4) * 4;
+        const bool is = row + r < own.y;
+        cp_async16(tc::smem_addr(rows + r * ROW + c), is ? mine + r * ld + K + c : a.partial, is);
+    }
+    cp_async_commit();
 #pragma unroll 1
     for (int i = 0; i < 2; i++) {
         if (!from[i] || (i == 1 && from[1] == from[0])) continue;
@@ -1220,60 +1229,70 @@ __global__ void __launch_bounds__(256, 2) outputs_kernel(const __grid_constant__
             const int j = x / (K / 4), c = x % (K / 4) * 4;
             const float4 f0 = *reinterpret_cast<const float4 *>(from[i] + 2 * j * K + c), f1 = *reinterpret_cast<const float4 *>(from[i] + (2 * j + 1) * K + c);
             const float4 z = *reinterpret_cast<const float4 *>(units + c);
-            const float4 r = make_float4(1.f / z.x, 1.f / z.y, 1.f / z.z, 1.f / z.w);
+            const float4 r = make_float4(over(z.x), over(z.y), over(z.z), over(z.w));
             const uint4 y = make_uint4(tc::pack_f16x2(f0.x * r.x, f1.x * r.x), tc::pack_f16x2(f0.y * r.y, f1.y * r.y), tc::pack_f16x2(f0.z * r.z, f1.z * r.z),
                                        tc::pack_f16x2(f0.w * r.w, f1.w * r.w));
             *reinterpret_cast<uint4 *>(state + j * LD + c) = j & 2 ? make_uint4(y.z, y.w, y.x, y.y) : y;
         }
         __syncthreads();
         if (from[warp / 4] != from[i]) continue;
-#pragma unroll 1
-        for (int k0 = 0; k0 < K / 16; k0 += AHEAD) {
-            float4 next[AHEAD][2];
+        // Of 16 of the inner axis a lane has columns 4 t .. 4 t + 3, which count as k = 2 t, 2 t + 1, 2 t + 8, 2 t + 9; so too with the outputs' columns.
+        auto four = [&](int r, int k) { return *reinterpret_cast<const float4 *>(rows + (g + 8 * r) * ROW + 16 * k + 4 * t); };
+        cp_async_wait_all();
+        __syncwarp();
+        float whole[2] = {}, part[2];                      // the units of rows g and g + 8, and one over them
 #pragma unroll
-            for (int k = 0; k < AHEAD; k++)
-                if (k0 + AHEAD < K / 16) fetch(next[k], k0 + AHEAD + k);
+        for (int r = 0; r < 2; r++) {
 #pragma unroll
-            for (int k = 0; k < AHEAD; k++) {
-                const uint32_t f[4] = {half2(u[k][0].x, u[k][0].y), half2(u[k][1].x, u[k][1].y), half2(u[k][0].z, u[k][0].w), half2(u[k][1].z, u[k][1].w)};
-                const uint32_t *s = state + (8 * (k0 + k) + 2 * t) * LD + (((g >> 1) * 4 + (g & 1)) ^ (t & 1) * 2);
+            for (int k = 0; k < K / 16; k++) {
+                const float4 x = four(r, k);
+                whole[r] = fmaxf(fmaxf(whole[r], fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+            }
 #pragma unroll
-                for (int n = 0; n < K / 8; n++) {
-                    const uint32_t *at = n % 2 ? s + 8 * n - 8 + (t & 1 ? -2 : 2) : s + 8 * n;
-                    mma_f16(o[n], f, at[0], at[LD]);
-                }
-                u[k][0] = next[k][0];
-                u[k][1] = next[k][1];
+            for (int x = 1; x < 4; x <<= 1) whole[r] = fmaxf(whole[r], __shfl_xor_sync(0xffffffffu, whole[r], x));
+            whole[r] = unit_of(whole[r]);
+            part[r] = over(whole[r]);
+        }
+        float o[K / 8][4] = {};
+#pragma unroll 2
+        for (int k = 0; k < K / 16; k++) {
+            uint32_t f[4];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float4 x = four(r, k);
+                f[r] = tc::pack_f16x2(x.x * part[r], x.y * part[r]);
+                f[2 + r] = tc::pack_f16x2(x.z * part[r], x.w * part[r]);
+            }
+            const uint32_t *s = state + (8 * k + 2 * t) * LD + (((g >> 1) * 4 + (g & 1)) ^ (t & 1) * 2);
+#pragma unroll
+            for (int n = 0; n < K / 8; n++) {
+                const uint32_t *at = n % 2 ? s + 8 * n - 8 + (t & 1 ? -2 : 2) : s + 8 * n;
+                mma_f16(o[n], f, at[0], at[LD]);
             }
         }
+        const float *add = mine + g * ld + 4 * t;
+        uint16_t *out = p.out + (static_cast<int64_t>(own.x) + row + g) * p.ld_out + static_cast<int64_t>(h) * K + 4 * t;
 #pragma unroll
         for (int n = 0; n < K / 8; n += 2) {
             const float4 z = *reinterpret_cast<const float4 *>(units + 8 * n + 4 * t);
 #pragma unroll
             for (int r = 0; r < 2; r++) {
-                const float4 x = four(r, 8 * n);
-                o[n][2 * r] = fmaf(o[n][2 * r] * whole, z.x, x.x);
-                o[n][2 * r + 1] = fmaf(o[n][2 * r + 1] * whole, z.y, x.y);
-                o[n + 1][2 * r] = fmaf(o[n + 1][2 * r] * whole, z.z, x.z);
-                o[n + 1][2 * r + 1] = fmaf(o[n + 1][2 * r + 1] * whole, z.w, x.w);
+                const float4 x = in[r] ? *reinterpret_cast<const float4 *>(add + 8 * r * ld + 8 * n) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float y[4] = {fmaf(o[n][2 * r] * whole[r], z.x, x.x), fmaf(o[n][2 * r + 1] * whole[r], z.y, x.y),
+                                    fmaf(o[n + 1][2 * r] * whole[r], z.z, x.z), fmaf(o[n + 1][2 * r + 1] * whole[r], z.w, x.w)};
+                if (in[r]) *reinterpret_cast<uint2 *>(out + 8 * r * p.ld_out + 8 * n) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
             }
         }
     }
-    if (!mine) return;
-    uint16_t *out = p.out + (static_cast<int64_t>(own.x) + row + g) * p.ld_out + static_cast<int64_t>(h) * K + 4 * t;
-#pragma unroll
-    for (int n = 0; n < K / 8; n += 2)
-#pragma unroll
-        for (int r = 0; r < 2; r++)
-            if (in[r])
-                *reinterpret_cast<uint2 *>(out + 8 * r * p.ld_out + 8 * n) =
-                    make_uint2(pack_bf16x2(o[n][2 * r], o[n][2 * r + 1]), pack_bf16x2(o[n + 1][2 * r], o[n + 1][2 * r + 1]));
+    cp_async_wait_all();                                   // a warp without a state to multiply has copies too
 }
 
 // ---- host ---------------------------------------------------------------------------------
 
 // Shared memory of ends_kernel.
 constexpr int ends_bytes(int K) { return (K * 32 + 2 * K * K + 8 * 32) * 4; }
+// And of outputs_kernel.
+constexpr int outputs_bytes(int K) { return (K / 2 * (K + 4) + 128 * (K + 16)) * 4; }
 
 // The parts of long sequences: as many as give every chain a multiprocessor (152 of them), with two chains for each part behind the first.
 // Sequences that cannot have CUT_CHUNKS chunks on average stay whole: the joining costs 20 us and more. One sequence of K = V = 128, in parts and whole:
@@ -1312,7 +1331,7 @@ cudaError_t this_device(int *sms)
             };
             e = cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev);
             limit(prep_kernel<1>, HALF); limit(prep_kernel<2>, 2 * HALF);
-            limit(ends_kernel<64>, ends_bytes(64)); limit(ends_kernel<128>, ends_bytes(128)); limit(outputs_kernel<64>, 32 * 68 * 4); limit(outputs_kernel<128>, 64 * 132 * 4);
+            limit(ends_kernel<64>, ends_bytes(64)); limit(ends_kernel<128>, ends_bytes(128)); limit(outputs_kernel<64>, outputs_bytes(64)); limit(outputs_kernel<128>, outputs_bytes(128));
             limit(chain_kernel<1, 32, false>, Smem::END); limit(chain_kernel<1, 64, false>, Smem::END); limit(chain_kernel<1, 128, false>, Smem::END);
             limit(chain_kernel<2, 32, false>, Smem::END); limit(chain_kernel<2, 64, false>, Smem::END); limit(chain_kernel<2, 128, false>, Smem::END);
             limit(chain_kernel<1, 64, true>, Smem::END); limit(chain_kernel<2, 128, true>, Smem::END);
@@ -1394,7 +1413,7 @@ cudaError_t launch_gdn_prefill(const GdnParams &p, int K, int V, const int32_t *
     e = K == 64 ? launch_pdl(ends_kernel<64>, slices, dim3(256), ends_bytes(K), stream, a) : launch_pdl(ends_kernel<128>, slices, dim3(256), ends_bytes(K), stream, a);
     if (e != cudaSuccess) return e;
     const dim3 pairs(static_cast<unsigned>((chunks + 1) / 2 * p.Hv));
-    return K == 64 ? launch_pdl(outputs_kernel<64>, pairs, dim3(256), 32 * 68 * 4, stream, a) : launch_pdl(outputs_kernel<128>, pairs, dim3(256), 64 * 132 * 4, stream, a);
+    return K == 64 ? launch_pdl(outputs_kernel<64>, pairs, dim3(256), outputs_bytes(64), stream, a) : launch_pdl(outputs_kernel<128>, pairs, dim3(256), outputs_bytes(128), stream, a);
 }
 
 }  // namespace kda

@@ -40,7 +40,7 @@ class Batch:
         self.Hk, self.K, self.V, self.slots = Hk, K, V, slots
         self.qkv = randn(n, 2 * Hk * K + Hv * V).to(BF16)
         self.rg, self.rb = randn(n, Hv).to(BF16), randn(n, Hv).to(BF16)
-        self.A_log, self.dt = torch.rand(Hv, generator=g, device="cuda"), -3 + randn(Hv)
+        self.A_log, self.dt = torch.rand(Hv, generator=g, device="cuda"), -3 + randn(Hv)   # dt: None for zeros
         self.pool = 0.05 * randn(num_slots, Hv, K, V)
         self.start = self.pool.clone()
         self.out = torch.full((n, Hv * V), 7.0, dtype=BF16, device="cuda")
@@ -50,11 +50,30 @@ class Batch:
         kda.kda_gdn_chunk_prefill(self.qkv, self.rg, self.rb, self.A_log, self.dt, self.pool, i32(self.slots), i32(self.cu), num_k_heads=self.Hk, out=self.out,
                                   err_flags=self.err, **kw)
 
+    def oracle(self, slots, bounds):
+        return og.run(*(None if x is None else f64(x) for x in (self.qkv, self.rg, self.rb, self.A_log, self.dt, self.start)), slots, bounds, self.Hk)
+
+    def run_and_check_rows(self, kda, least=1e-30):
+        """One sequence: every row by itself, down to `least`, and every head's state."""
+        self.run(kda)
+        out, after, err = self.oracle(self.slots, [(0, self.cu[1])])
+        assert self.err.item() == err == 0
+        g, o = (x.reshape(-1, self.V) for x in (f64(self.out), out))
+        norms = np.linalg.norm(o, axis=1)
+        off = np.linalg.norm(g - o, axis=1)
+        seen = norms > least
+        assert (off[seen] <= 4e-3 * norms[seen]).all(), (off[seen] / norms[seen]).max()
+        assert (off[~seen] <= least).all()
+        slot = self.slots[0]
+        size = np.linalg.norm(after[slot], axis=(1, 2))
+        rel = np.linalg.norm(f64(self.pool)[slot] - after[slot], axis=(1, 2)) / np.maximum(size, least)
+        assert rel.max() <= 1e-5, rel.max()
+
     def check(self, entries):
         """The given sequences' outputs and states; those of their slots alone have changed."""
         assert self.err.item() == 0
         slots, bounds = [self.slots[e] for e in entries], [(self.cu[e], self.cu[e + 1]) for e in entries]
-        out, after, _ = og.run(*map(f64, (self.qkv, self.rg, self.rb, self.A_log, self.dt, self.start)), slots, bounds, self.Hk)
+        out, after, _ = self.oracle(slots, bounds)
         rows = np.concatenate([np.arange(*b) for b in bounds])
         g, o = (x[rows].reshape(-1, self.V) for x in (f64(self.out), out))
         assert np.linalg.norm(g - o) <= 2e-3 * np.linalg.norm(o)
@@ -116,3 +135,30 @@ def test_overlapping_ranges_count_no_further_than_the_workspace(kda):
     b.run(kda)
     assert b.err.item() == og.ERR_LENGTHS
     assert torch.equal(b.pool[0], want) and torch.equal(b.pool[1], want) and torch.equal(b.pool[2], b.start[2])
+
+
+@pytest.mark.parametrize("K, Hv, rows", [(64, 1, 4500), (128, 1, 4300), (64, 40, 4200)])
+@pytest.mark.parametrize("decay, beta", [(0.03, -30.0), (0.012, -4.0)])
+def test_parts_whose_outputs_are_what_is_left_of_the_state(kda, K, Hv, rows, decay, beta):
+    """Sequences in joined parts whose values end with the first 500 rows: from there on an output is the transition's row times the part's start, and both shrink, by
+    e^-7 to e^-60 within a part. Each row is as near as any: rounded to bf16, 2^-8 of its norm at most (1.7e-3 in the mean), and of terms whose two factors are off by
+    half a step of fp16, 2^-11 at most and 2.0e-4 in the mean each, of random signs (little is written, so that the state keeps its rank): 4e-3 in quadrature."""
+    b = Batch([rows], 1, Hv, K, K, [1], 3, seed=K + Hv)
+    b.A_log.zero_()
+    b.dt = None
+    b.rg.fill_(math.log(math.expm1(decay)))
+    b.rb.fill_(beta)
+    b.rb[:500] = 0.0
+    b.qkv[500:, 2 * K:] = 0.0
+    b.run_and_check_rows(kda)
+
+
+@pytest.mark.parametrize("size", [2e35, 1e-30])
+def test_parts_with_states_near_the_ends_of_fp32(kda, size):
+    """Joined outputs where every value is above 2^114, or small: rows as near as any (tolerance as above; little decay, so that the parts depend on one another)."""
+    b = Batch([4500], 1, 1, 64, 64, [1], 3, seed=9)
+    b.A_log -= 6.0
+    b.qkv[:, 128:] *= size
+    b.pool *= size
+    b.start = b.pool.clone()
+    b.run_and_check_rows(kda, least=1e-3 * size)
