@@ -1,19 +1,20 @@
 // The gated delta rule with one decay per head over packed sequences, in chunks of 64 rows on the tensor cores.
 //
-// With b the running log-decay inside a chunk, D[r, i] = e^{b_r - b_i}, A[r, i] = beta_r (k^_r . k^_i) D[r, i] for
+// With b the running log-decay inside a chunk, D[r, i] = e^{b_r - b_i}, A[r, i] = (k^_r . k^_i) D[r, i] beta_i for
 // i < r and T = (I + A)^-1, a chunk is
-//   Y = V - e^b (K^ S),   U = T diag(beta) Y,   O = e^b (Q^ S) + W U,  W = Q^ K^^T * D (i <= r),   S <- e^{b_n} S + (K^ e^{b_n - b})^T U
+//   Y = V - e^b (K^ S),   Z = T Y,   O = e^b (Q^ S) + W Z,  W = (Q^ K^^T * D) diag(beta) (i <= r),   S <- e^{b_n} S + (K^ e^{b_n - b} beta)^T Z
+// (beta stands behind T, whose diagonal is then one: Y goes into Z's sums as it is, in fp32, and through products only what is off the diagonal.)
 // A decay that is the same in all channels leaves the tiles of q and k as they are in memory: every product takes them
 // raw, as TMA brings them, and norms and decays are factors of rows and columns of the products. What the chunks need but for
-// S, T diag(beta) and W, is 21 KB a chunk and head (KDA's is 58 KB). Three launches, and two more
+// S, T and W, is 21 KB a chunk and head (KDA's is 58 KB). Three launches, and two more
 // where few long sequences are cut into parts that go side by side:
 //   map_kernel    where each sequence's chunks are, from cu_seqlens on the device
-//   prep_kernel   T diag(beta), W and the row factors of every chunk at once: a CTA per chunk and key head, for all its value heads
+//   prep_kernel   T, W and the row factors of every chunk at once: a CTA per chunk and key head, for all its value heads
 //   chain_kernel  one CTA per SM walks (sequence, value head) chains, longest sequences first, S in registers
 //   ends_kernel, outputs_kernel   join the parts
 // The chain's products have value columns as rows (TMEM lanes), so that what depends on a token is a factor per column,
 // and their first operand is written to TMEM by the thread that has the values.
-// What enters the products is exact (q, k, v are bf16) or two bf16 terms, hi + lo = x to 2^-17.
+// What enters the products is exact (q, k, v are bf16), two bf16 terms, hi + lo = x to 2^-17, or, of Z on its way into the state, three (2^-25).
 #include <atomic>
 #include <climits>
 #include <mutex>
@@ -36,9 +37,9 @@ constexpr int C = 64;                                  // rows of a chunk
 constexpr int ORDER = 256;                             // sequences that are sorted by length
 constexpr int BLK = 16 * 20;                           // floats of a 16 x 16 block, rows 20 apart: no bank conflicts
 
-// A chunk and head's record. Of the 64 x 64 matrices T diag(beta) and W, hi and lo each, the blocks on and below the diagonal: a panel
+// A chunk and head's record. Of the 64 x 64 matrices T - I and W, hi and lo each, the blocks on and below the diagonal: a panel
 // for every 16 columns with the rows from 16 k on, in the order the MMAs read without a swizzle (8 rows of 16 bytes follow each
-// other, the next 8 columns 128 bytes on, the next 8 rows 256). Then the row factors: -e^b |k|^-1, e^{b_n - b} |k|^-1,
+// other, the next 8 columns 128 bytes on, the next 8 rows 256). Then the row factors: -e^b |k|^-1, beta e^{b_n - b} |k|^-1,
 // scale e^b |q|^-1 (64 floats each) and e^{b_n}.
 struct Rec {
     static constexpr int MATRIX = 5120, T = 0, W = 2 * MATRIX, ROWS = 4 * MATRIX, BYTES = ROWS + (3 * C + 4) * 4, STAGE = 21376;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
     if (tid == 0) a.first[a.num_seqs] = base < a.chunks ? base : a.chunks;
 }
 
-// T diag(beta), W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
+// T, W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
 // t - 64 of Q K^T, which one product of 128 x 64 gives. A warp's path through the inverse is bound by
 // its latencies: as many CTAs an SM as there is shared memory for at K = 128, and registers at 64 (257 sequences of 1 to 342 tokens x 8 heads:
 // the three launches 187 us, with six CTAs 189, with five 192).
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
     // the tiles of q and k; once their products and norms are there, the blocks of A, then of T, on and below the diagonal
     extern __shared__ __align__(1024) unsigned char sm[];
     float *blocks = reinterpret_cast<float *>(sm);
-    __shared__ __align__(16) float cols[5 * C];   // b hi, b lo, beta, and of the keys b lo less the norm's logarithm, and e^{p - b} times the norm
+    __shared__ __align__(16) float cols[5 * C];   // b hi, b lo, beta, and of the keys b lo less the logarithm of norm and beta, and e^{p - b} times both
     __shared__ uint64_t bars[2];
     __shared__ uint32_t tmem_at;
     const uint32_t s0 = tc::smem_addr(sm), full = tc::smem_addr(&bars[0]), g_done = tc::smem_addr(&bars[1]);
@@ -391,14 +392,14 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
         if (h + 1 < (hk + 1) * per) fetch(h + 1);
         __syncthreads();
         const float b_hi = cols[r], b_lo = cols[C + r];
-        const float scale = (query ? p.scale : cols[2 * C + r]) * norm;
+        const float scale = (query ? p.scale : 1.f) * norm;
         if (!query) {
-            const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1];
+            const float e_hi = cols[C - 1], e_lo = cols[2 * C - 1], own = norm * cols[2 * C + r];
             set[r] = -ex2(b_hi + b_lo) * norm;
-            set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * norm;
+            set[C + r] = ex2((e_hi - b_hi) + (e_lo - b_lo)) * own;
             if (r == 0) set[3 * C] = ex2(e_hi + e_lo);
-            cols[3 * C + r] = b_lo - (r < n ? __log2f(norm) : 0.f);
-            cols[4 * C + r] = ex2((cols[r | 15] - b_hi) + (cols[C + (r | 15)] - b_lo)) * norm;
+            cols[3 * C + r] = b_lo - (r < n ? __log2f(own) : 0.f);
+            cols[4 * C + r] = ex2((cols[r | 15] - b_hi) + (cols[C + (r | 15)] - b_lo)) * own;
         } else {
             set[2 * C + r] = p.scale * ex2(b_hi + b_lo) * norm;
         }
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
                 for (int x = 0; x < 4; x++) at[(8 * rt + 2 * tq + (x & 1)) * 20 + gq + 8 * (x >> 1)] = out[rt][x];
         }
         __syncthreads();
-        // T diag(beta), hi and lo: half of row r
+        // T - I, hi and lo: half of row r
 #pragma unroll 1
         for (int bl = t >> 6 << 1; bl <= r >> 4 && bl < (t >> 6 << 1) + 2; bl++) {
             const float *from = blocks + block_at(r >> 4, bl) + (r & 15) * 20;
@@ -595,11 +596,11 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    const float4 x = *reinterpret_cast<const float4 *>(from + 8 * y + 4 * i);
-                    const float4 e = *reinterpret_cast<const float4 *>(cols + 2 * C + bl * 16 + 8 * y + 4 * i);
-                    const float2 v0 = fmul2(make_float2(x.x, x.y), make_float2(e.x, e.y)), v1 = fmul2(make_float2(x.z, x.w), make_float2(e.z, e.w));
-                    split2(v0.x, v0.y, hi[2 * i], lo[2 * i]);
-                    split2(v1.x, v1.y, hi[2 * i + 1], lo[2 * i + 1]);
+                    float4 x = *reinterpret_cast<const float4 *>(from + 8 * y + 4 * i);
+                    const int one = r - bl * 16 - 8 * y - 4 * i;                  // the diagonal's column of the four
+                    x.x = one == 0 ? 0.f : x.x; x.y = one == 1 ? 0.f : x.y; x.z = one == 2 ? 0.f : x.z; x.w = one == 3 ? 0.f : x.w;
+                    split2(x.x, x.y, hi[2 * i], lo[2 * i]);
+                    split2(x.z, x.w, hi[2 * i + 1], lo[2 * i + 1]);
                 }
                 *reinterpret_cast<uint4 *>(to + y * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(to + Rec::MATRIX + y * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -623,15 +624,16 @@ constexpr int STAGES = 3;          // chunks in shared memory
 struct Smem {
     static constexpr int QK = 2 * HALF, V = C * 256;
     static constexpr int REC = QK + V, STAGE = QK + V + Rec::STAGE;
-    static constexpr int SORT = STAGES * STAGE, BARS = SORT + ORDER * 2, NBARS = 3 * STAGES + 13, END = BARS + NBARS * 8 + 16;
+    static constexpr int SORT = STAGES * STAGE, BARS = SORT + ORDER * 2, NBARS = 3 * STAGES + 14, END = BARS + NBARS * 8 + 16;
 };
 static_assert(Smem::STAGE % 128 == 0 && Smem::END <= 232448, "shared memory of a CTA");
 
 // columns of tensor memory
 constexpr uint32_t T_S = 0;      // first operand of K S and Q S: the quarters of the channels one after the other, each hi | lo; then the state's increment
-constexpr uint32_t T_Y = 128;    // K S; then Y, later U scaled, as operands, by quarters of the rows, each hi | lo
-constexpr uint32_t T_U = 192;    // U; then as an operand, the same way
-constexpr uint32_t T_O = 256;    // Q S and W U
+constexpr uint32_t T_Y = 128;    // K S; then Y, later Z scaled, as operands, by quarters of the rows, each hi | lo
+constexpr uint32_t T_Z = 192;    // Y, to which its product is added: Z; then as an operand, the same way
+constexpr uint32_t T_O = 256;    // Q S and W Z
+constexpr uint32_t T_3 = 384;    // the scaled Z's third terms
 
 // Value columns VS at a time (a slice of V), a thread with one of them and a quarter of the channels, or of the rows. PARTS: long sequences are in parts.
 template <int NH, int VS, bool PARTS>
@@ -646,8 +648,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
     auto empty = [&](int s) { return b0 + (STAGES + s) * 8; };              // and is no longer needed
     auto clean = [&](int s) { return b0 + (2 * STAGES + s) * 8; };          // its keys behind the sequence's end are zeros
     const uint32_t bx = b0 + 3 * STAGES * 8;
-    const uint32_t s_hi = bx, s_lo = bx + 8, ks_done = bx + 16, y_hi = bx + 24, y_lo = bx + 32, u_done = bx + 40, u_hi = bx + 48, u_lo = bx + 56,
-                   w_ready = bx + 64, s_done = bx + 72, o_done = bx + 80, o_free = bx + 88, drained = bx + 96;
+    const uint32_t s_hi = bx, s_lo = bx + 8, ks_done = bx + 16, y_hi = bx + 24, y_lo = bx + 32, z_done = bx + 40, z_hi = bx + 48, z_lo = bx + 56,
+                   w_ready = bx + 64, s_done = bx + 72, o_done = bx + 80, o_free = bx + 88, drained = bx + 96, z_3 = bx + 104;
     volatile uint32_t *words = reinterpret_cast<volatile uint32_t *>(sm + Smem::BARS + Smem::NBARS * 8);   // tensor memory's base, whether a wait has given up
     uint16_t *order = reinterpret_cast<uint16_t *>(sm + Smem::SORT);
     const GdnParams &p = a.p;
@@ -658,9 +660,9 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             tc::mbar_init(empty(i), 2 + VW);                           // the MMAs, the outputs' warps and the one that clears keys
             tc::mbar_init(clean(i), 1);
         }
-        for (const uint32_t b : {s_hi, s_lo, y_hi, y_lo, u_hi, u_lo, w_ready}) tc::mbar_init(b, 4 * VW);
+        for (const uint32_t b : {s_hi, s_lo, y_hi, y_lo, z_hi, z_lo, z_3, w_ready}) tc::mbar_init(b, 4 * VW);
         tc::mbar_init(ks_done, 1);
-        tc::mbar_init(u_done, 1);
+        tc::mbar_init(z_done, 1);
         tc::mbar_init(s_done, 1);
         tc::mbar_init(o_done, 1);
         tc::mbar_init(o_free, VW);
@@ -701,7 +703,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
         if (quarter < VW) {
             const int j = quarter * 32 + lane;                                // this thread's value column in the slice
             const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-            const uint32_t ts = t0 + T_S + part * KP, ty = t0 + T_Y + part * 16, tu = t0 + T_U + part * 16;
+            const uint32_t ts = t0 + T_S + part * KP, ty = t0 + T_Y + part * 16, tz = t0 + T_Z + part * 16, t3 = t0 + T_3 + part * 8;
             float2 S[KP / 2];                                                 // channels KP part .. of column j
             auto give = [&](uint32_t mbar) {                                  // what the products wait for is in tensor memory
                 tc::tmem_st_wait();
@@ -725,17 +727,6 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                     tmem_st8(ts + KP / 2 + i, lo);
                 }
                 give(s_lo);
-            };
-            auto give2 = [&](const float2 (&y)[8], uint32_t at, uint32_t hi_bar, uint32_t lo_bar) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) hi[e] = pack_bf16x2(y[e].x, y[e].y);
-                tmem_st8(at, hi);
-                give(hi_bar);
-#pragma unroll
-                for (int e = 0; e < 8; e++) lo[e] = rest2(y[e].x, y[e].y, hi[e]);
-                tmem_st8(at + 8, lo);
-                give(lo_bar);
             };
             bool more = w.begin(), first = true;
             for (uint32_t c = 0; more; c++) {
@@ -798,28 +789,56 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                         y[e] = ffma2(e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                      make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u)));
                     }
-                    give2(y, ty, y_hi, y_lo);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) hi[e] = pack_bf16x2(y[e].x, y[e].y);
+                    tmem_st8(ty, hi);
+                    // Z's sums begin with Y (the products that read the last chunk's operand there are over when K S is)
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4)
+                        tmem_st8(tz + 2 * e, {__float_as_uint(y[e].x), __float_as_uint(y[e].y), __float_as_uint(y[e + 1].x), __float_as_uint(y[e + 1].y),
+                                              __float_as_uint(y[e + 2].x), __float_as_uint(y[e + 2].y), __float_as_uint(y[e + 3].x), __float_as_uint(y[e + 3].y)});
+                    give(y_hi);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) lo[e] = rest2(y[e].x, y[e].y, hi[e]);
+                    tmem_st8(ty + 8, lo);
+                    give(y_lo);
                 }
-                // U scaled, for the state, and then as it is, for the outputs
-                if (!wait.warp(u_done, one)) break;
+                // Z scaled, for the state, in three terms (with two the states were off by 2.5e-6 of their norm instead of 1.1e-6 to 1.4e-6, 31,516 tokens x 32 heads
+                // 544 us instead of 569; with two, and T's diagonal in the products, 4.5e-6 and 550), and then as it is, for the outputs
+                if (!wait.warp(z_done, one)) break;
                 tc::fence_after_sync();
                 {
-                    uint32_t x[16];
+                    uint32_t x[16], hi[8], lo[8];
                     float2 z[8];
-                    tmem_ld(tu, x);
-                    const float4 *us = reinterpret_cast<const float4 *>(set + C + part * 16);
+                    tmem_ld(tz, x);
+                    const float4 *zs = reinterpret_cast<const float4 *>(set + C + part * 16);
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const float4 f = us[e / 2];
+                        const float4 f = zs[e / 2];
                         z[e] = fmul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), e % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                        hi[e] = pack_bf16x2(z[e].x, z[e].y);
                     }
-                    give2(z, ty, u_hi, u_lo);
-                    uint32_t hi[8], lo[8];
+                    tmem_st8(ty, hi);
+                    give(z_hi);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        z[e] = left(z[e], hi[e]);
+                        lo[e] = pack_bf16x2(z[e].x, z[e].y);
+                    }
+                    tmem_st8(ty + 8, lo);
+                    if (NH == 2) give(z_lo);               // at K = 64 the products take no longer than a barrier: the second term with the third
+#pragma unroll
+                    for (int e = 0; e < 8; e++) lo[e] = rest2(z[e].x, z[e].y, lo[e]);
+                    tmem_st8(t3, lo);
+                    give(z_3);
+                    tmem_ld(tz, x);                        // again: it is not kept in registers meanwhile
+                    tc::tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 8; e++) split2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hi[e], lo[e]);
-                    tmem_st8(tu, hi);
-                    tmem_st8(tu + 8, lo);
+                    tmem_st8(tz, hi);
+                    tmem_st8(tz + 8, lo);
                     give(w_ready);
                 }
                 // S <- gamma S + its increment
@@ -955,7 +974,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
                 for (int k = 0; k < K / 16; k++)
                     mma_t(d, tmem + T_S + k / (KP / 16) * KP + x * (KP / 2) + k % (KP / 16) * 8, desc_k(from + (k / 4) * HALF + (k % 4) * 32), idesc(C), x + k > 0);
             };
-            // a term of a record's matrix (y) times one (x) of Y or U; rows before 16 k are zero in columns 16 k ..
+            // a term of a record's matrix (y) times one (x) of Y or Z; rows before 16 k are zero in columns 16 k ..
             auto times_rec = [&](uint32_t d, uint32_t from, uint32_t matrix, int x, int y, bool first) {
 #pragma unroll
                 for (int k = 0; k < 4; k++)
@@ -980,39 +999,46 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ 
             if (!wait.warp(y_hi, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 0, 0, true);
-                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 0, 1, false);
+                times_rec(tmem + T_Z, tmem + T_Y, rec + Rec::T, 0, 0, false);
+                times_rec(tmem + T_Z, tmem + T_Y, rec + Rec::T, 0, 1, false);
             }
             __syncwarp();
             if (!wait.warp(y_lo, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                times_rec(tmem + T_U, tmem + T_Y, rec + Rec::T, 1, 0, false);
-                tc::commit(u_done);
+                times_rec(tmem + T_Z, tmem + T_Y, rec + Rec::T, 1, 0, false);
+                tc::commit(z_done);
             }
             __syncwarp();
             // the state's increment
             auto increment = [&](int x) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) mma_t(tmem + T_S, tmem + T_Y + k * 16 + x * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
+                for (int k = 0; k < 4; k++)
+                    mma_t(tmem + T_S, x < 2 ? tmem + T_Y + k * 16 + x * 8 : tmem + T_3 + k * 8, desc_mn(at + k * 16 * 128), idesc(K, true), x + k > 0);
             };
-            if (!wait.warp(u_hi, one) || (w.left < C && !wait.warp(clean(s), (c / STAGES) & 1))) break;
+            if (!wait.warp(z_hi, one) || (w.left < C && !wait.warp(clean(s), (c / STAGES) & 1))) break;
             tc::fence_after_sync();
             if (elect_one()) increment(0);
             __syncwarp();
-            if (!wait.warp(u_lo, one)) break;
+            if (!wait.warp(NH == 2 ? z_lo : z_3, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
                 increment(1);
+            }
+            __syncwarp();
+            if (NH == 2 && !wait.warp(z_3, one)) break;
+            if (NH == 2) tc::fence_after_sync();
+            if (elect_one()) {
+                increment(2);
                 tc::commit(s_done);
             }
             __syncwarp();
             if (!wait.warp(w_ready, one)) break;
             tc::fence_after_sync();
             if (elect_one()) {
-                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 0, 0, true);
-                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 1, 0, false);
-                times_rec(tmem + T_O + C, tmem + T_U, rec + Rec::W, 0, 1, false);
+                times_rec(tmem + T_O + C, tmem + T_Z, rec + Rec::W, 0, 0, true);
+                times_rec(tmem + T_O + C, tmem + T_Z, rec + Rec::W, 1, 0, false);
+                times_rec(tmem + T_O + C, tmem + T_Z, rec + Rec::W, 0, 1, false);
                 tc::commit(empty(s));
                 tc::commit(o_done);
             }

@@ -24,9 +24,13 @@ __device__ __forceinline__ float log_decay(uint16_t raw_g, float expA, float dtb
 
 // x and y as packed bf16 pairs hi + lo: hi is x rounded to bf16 and lo what is left, rounded again, so that
 // |x - hi - lo| <= 2^-17 |x|.
+__device__ __forceinline__ float2 left(float2 x, uint32_t hi)
+{
+    return fsub2(x, make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+}
 __device__ __forceinline__ uint32_t rest2(float x, float y, uint32_t hi)
 {
-    const float2 d = fsub2(make_float2(x, y), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+    const float2 d = left(make_float2(x, y), hi);
     return pack_bf16x2(d.x, d.y);
 }
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)

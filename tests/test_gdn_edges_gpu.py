@@ -162,3 +162,16 @@ def test_parts_with_states_near_the_ends_of_fp32(kda, size):
     b.pool *= size
     b.start = b.pool.clone()
     b.run_and_check_rows(kda, least=1e-3 * size)
+
+
+@pytest.mark.parametrize("K, V, most", [(128, 128, 2.0e-6), (128, 64, 2.0e-6), (64, 64, 2.5e-6)])
+def test_states_to_the_products_terms(kda, K, V, most):
+    """What is off in a state, of its norm: a bf16 pair is off by 2.3e-6 of a value in the mean. Below T's diagonal its product with Y has three such errors (T's pair, Y's, and the
+    second terms' product), and is beta (32 / K)^(1/2) = 0.25 to 0.35 of Z: 1.0e-6 to 1.4e-6. S as the first operand of K S: 2.3e-6 of what is half of Y at most. Sums of 12 steps
+    of the products, each cut at 2^-24 of them: 0.5e-6. In quadrature 1.6e-6 to 1.9e-6."""
+    b = Batch([700, 65, 640], 1, 2, K, V, [0, 1, 2], 4, seed=K + V)
+    b.run(kda)
+    _, after, _ = b.oracle(b.slots, list(zip(b.cu, b.cu[1:])))
+    got = f64(b.pool)
+    for s in b.slots:
+        assert np.linalg.norm(got[s] - after[s]) <= most * np.linalg.norm(after[s]), (s, np.linalg.norm(got[s] - after[s]) / np.linalg.norm(after[s]))
