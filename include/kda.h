@@ -413,7 +413,8 @@ int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_
  * scratch between calls, and calls that share one (two captured graphs, too) must not overlap on the device. It may be NULL
  * where that is 0 (K = 32). K of 64 and 128 with mixed_qkv 16-byte aligned and ld_qkv a multiple of 8 take the tensor cores
  * in chunks of 64 rows; other layouts, and K = 32, blocks of 16 rows that are several times slower.
- * A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT; what it was to give is not written (of a sequence in parts: not right).
+ * A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT; what it was to give is not written or, where it was a chunk's factors or a
+ * sequence is in parts, not right.
  */
 size_t kda_gdn_chunk_prefill_workspace_bytes(int64_t num_rows, int64_t num_seqs, const kda_gdn_heads *heads);
 int kda_gdn_chunk_prefill(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_t *raw_g, int64_t ld_g,

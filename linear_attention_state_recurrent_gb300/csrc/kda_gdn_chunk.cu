@@ -608,7 +608,11 @@ __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid
         }
         __syncthreads();                                                      // blocks and columns are free again
     }
-    if (!ok && p.err) atomicOr(p.err, kErrTimeout);
+    if (!ok) {                                             // no CTA ends with copies or MMAs in flight
+        if (p.err) atomicOr(p.err, kErrTimeout);
+        (void)tc::mbar_wait(full, 0);
+        (void)tc::mbar_wait(g_done, 0);
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
