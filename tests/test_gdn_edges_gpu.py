@@ -175,3 +175,18 @@ def test_states_to_the_products_terms(kda, K, V, most):
     got = f64(b.pool)
     for s in b.slots:
         assert np.linalg.norm(got[s] - after[s]) <= most * np.linalg.norm(after[s]), (s, np.linalg.norm(got[s] - after[s]) / np.linalg.norm(after[s]))
+
+
+@pytest.mark.parametrize("call", ["decode", "spec", "prefill"])
+def test_betas_of_zero_and_one(kda, call):
+    """raw_beta without bounds: a token that writes nothing at all, and one that replaces what its key reads. Tolerance as at the top."""
+    b = Batch([90, 1, 200] if call == "prefill" else [1] * 24 if call == "decode" else [8] * 3, 1, 2, 128, 64, list(range(24 if call == "decode" else 3)), 25, seed=6)
+    b.rb[::3], b.rb[1::3] = -math.inf, math.inf
+    b.rb[5::7], b.rb[6::7] = -200.0, 200.0
+    if call == "prefill":
+        b.run(kda)
+    else:
+        args = (b.qkv, b.rg, b.rb, b.A_log, b.dt, b.pool, i32(b.slots))
+        kw = dict(num_k_heads=1, out=b.out, err_flags=b.err)
+        kda.kda_gdn_decode(*args, **kw) if call == "decode" else kda.kda_gdn_spec_verify(*args, 8, **kw)
+    b.check(range(len(b.slots)))
