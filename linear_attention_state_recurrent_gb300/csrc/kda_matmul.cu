@@ -101,6 +101,13 @@ __device__ __forceinline__ void store_as(void *p, int64_t i, int dtype, float v)
     else static_cast<float *>(p)[i] = v;
 }
 
+// y / (1 + e^-x), by e^-|x|: the divisor is at most 2 (from 2^126 on, x below -87, the quotient to two steps would be 0).
+__device__ __forceinline__ float gated(float y, float x)
+{
+    const float e = expf(-fabsf(x));
+    return __fdividef(x < 0.f ? y * e : y, 1.f + e);
+}
+
 // The activation over values held in registers. The one branch is around all of them.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act)
@@ -112,11 +119,11 @@ __device__ __forceinline__ void activate(float (&v)[N], int act)
     switch (act) {
     case KDA_ACT_RELU: each([](float x) { return x < 0.f ? 0.f : x; }); break;   // a NaN stays one
     // (a quotient to two steps: the exact one takes a slow path where e^-x is large, 36 us for 24 at 128 x 12,288 x 4096)
-    case KDA_ACT_SILU: each([](float x) { return __fdividef(x, 1.f + expf(-x)); }); break;
-    case KDA_ACT_SIGMOID: each([](float x) { return __fdividef(1.f, 1.f + expf(-x)); }); break;
+    case KDA_ACT_SILU: each([](float x) { return gated(x, x); }); break;
+    case KDA_ACT_SIGMOID: each([](float x) { return gated(1.f, x); }); break;
     case KDA_ACT_GELU: each([](float x) { return 0.5f * x * erfcf(-0.70710678118654752f * x); }); break;
     // x (1 + tanh u) / 2 = x / (1 + e^{-2u}), u = (2 / pi)^(1/2) (x + 0.044715 x^3)
-    case KDA_ACT_GELU_TANH: each([](float x) { return __fdividef(x, 1.f + expf(-1.5957691216057308f * (x + 0.044715f * x * x * x))); }); break;
+    case KDA_ACT_GELU_TANH: each([](float x) { return gated(x, 1.5957691216057308f * (x + 0.044715f * x * x * x)); }); break;
     }
 }
 

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_matmul_gpu import BF16, FP16, FP32, check, rows
+from tests.test_matmul_gpu import ACT, BF16, FP16, FP32, check, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,17 @@ def test_outputs_and_residuals_on_boundaries_of_their_own(kda, M, N, K, out, out
     res = None if res_at is None else rows(M, N, out, g, res_at[0], 1.0, res_at[1])
     kda.kda_matmul(a, w, residual=res, out=o)
     check(o, a, w, None, None, res)
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid", "gelu_tanh"])
+@pytest.mark.parametrize("M", [5, 600])
+def test_activations_far_below_zero(kda, act, M):
+    """Results down to fp32's smallest normal value, each by itself: act(bias) of an inner axis of zeros, exact. An exponent of up to 90 takes its roundings
+    90-fold (2^-24 each; gelu_tanh's has seven, constants and operations, the others' none), e^x and the quotient are off by two steps each, and e^-90 has lost digits: 15 half
+    steps more. 7 * 90 + 8 + 15 half steps of 2^-24 at most."""
+    x = torch.cat([torch.linspace(-12, 12, 500), torch.linspace(-90, 90, 1000), torch.tensor([-87.0, -87.4, -88.0, -88.6, -10.0, -10.05, 0.0])]).cuda()
+    y = ACT[act](x.double()) if act != "gelu_tanh" else x.double() * torch.sigmoid((8 / torch.pi) ** 0.5 * (x.double() + 0.044715 * x.double() ** 3))
+    x, y = x[y.abs() >= 2.0 ** -126], y[y.abs() >= 2.0 ** -126]
+    a, w = torch.zeros(M, 64, dtype=BF16, device="cuda"), torch.zeros(len(x), 64, dtype=BF16, device="cuda")
+    got = kda.kda_matmul(a, w, bias=x, activation=act, out_dtype=FP32).double()
+    assert ((got - y).abs() <= 653 * 2.0 ** -24 * y.abs()).all(), ((got - y).abs() / y.abs()).max()
