@@ -373,8 +373,12 @@ int kda_chunk_prefill_no_alloc(const uint16_t *mixed_qkv, int64_t ld_qkv, const 
  * mixed_qkv: bf16 [N, ld_qkv], row t = [ q (Hk*K) | k (Hk*K) | v (Hv*V) ]; raw_g and raw_beta: bf16 [N, ld], Hv used;
  * out: bf16 [N, ld_out], Hv*V written; the state pool holds [Hv][K][V] per slot. Alignment, slots, the null slot, error
  * bits and sizes are those of the calls above with H = Hv, and a row of mixed_qkv has fewer than 2^31 columns in use. out may not
- * overlap an input. All three calls can be captured in a CUDA graph. States are fp32 and advanced to about fp32's accuracy (a few 1e-6 of their norm in the products of
- * several tokens); squares, products and sums are fp32 too. A log-decay below -1000 is taken as -1000: alpha is 0 either way.
+ * overlap an input. All three calls can be captured in a CUDA graph.
+ * States are fp32, and squares and sums are held in fp32. Products of one token are fp32 too. Those of several take q, k and v
+ * as they are (bf16) and fp32 values as two tf32 terms (2^-20 of a value: blocks of a few rows) or as two bf16 terms (2^-17) and
+ * three (2^-25) on the way into a state (kda_gdn_chunk_prefill's chunks), which leaves states off by 5e-7 and about 1e-6 of their norm
+ * (up to 3e-6 with next to no decay, 3e-5 where all keys are alike and beta near 1); outputs of later parts of sequences that are cut into parts take two fp16 factors a term
+ * (2^-11, before they are rounded to bf16). A log-decay below -1000 is taken as -1000: alpha is 0 either way.
  * An infinity or NaN in a key, value or gate reaches its own token and the later ones of its sequence; in
  * kda_gdn_chunk_prefill's chunks of 64 rows (counted from the sequence's start) also the earlier ones of its chunk.
  */
@@ -406,11 +410,12 @@ int kda_gdn_spec_verify(const uint16_t *mixed_qkv, int64_t ld_qkv, const uint16_
  * kda_batch_maps'): lengths may differ from one graph replay to the next. A pair that is no range of the rows
  * (negative, decreasing, past num_rows) counts as an empty sequence and sets KDA_ERRFLAG_LENGTHS. Rows of no sequence
  * are left as they were; the slot of an empty sequence is left untouched (one >= num_slots is still flagged).
- * Ranges may not share rows. `workspace` (device, 256-byte aligned) must hold
- * kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, heads) bytes, about 21 KB per 64 rows and value head (where few long sequences
- * are cut into parts, with K = V, at most 50 sequences x value heads and 4096 rows a sequence or more, up to 4 (K + V) bytes per row and value head
- * and 65 KB per part and value head more); its contents are
- * scratch between calls, and calls that share one (two captured graphs, too) must not overlap on the device. It may be NULL
+ * Ranges may not share rows (where they do all the same, what passes the workspace's num_rows / 64 + num_seqs chunks counts as
+ * empty in the same way). `workspace` (device, 256-byte aligned) must hold
+ * kda_gdn_chunk_prefill_workspace_bytes(num_rows, num_seqs, heads) bytes, about 21 KB per 64 rows and value head. (Where few long
+ * sequences are cut into parts, with K = V, at most 50 sequences x value heads and 4096 rows a sequence or more on average, up to
+ * 4 (K + V) bytes per row and value head and 65 KB per part and value head more.) Its contents are scratch between calls, and calls
+ * that share one (two captured graphs, too) must not overlap on the device. It may be NULL
  * where that is 0 (K = 32). K of 64 and 128 with mixed_qkv 16-byte aligned and ld_qkv a multiple of 8 take the tensor cores
  * in chunks of 64 rows; other layouts, and K = 32, blocks of 16 rows that are several times slower.
  * A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT; what it was to give is not written or, where it was a chunk's factors or a
@@ -482,14 +487,17 @@ int kda_fp8_matmul(const uint8_t *a, int64_t ld_a, const float *a_scales, int64_
 /*
  * kda_matmul — a product of 16-bit operands with bias, activation and residual in its epilogue:
  *   out[m, n] = act(sum_k a[m, k] * w[n, k] + bias[n]) + residual[m, n]
- * a: [M, ld_a] and w: [N, ld_w] (row n holds output n's weights), both of element type dtype (KDA_BF16 or KDA_FP16), K columns used
- * of each; bias: [N] of bias_dtype (dtype or KDA_FP32), or NULL; act: KDA_ACT_*; residual: [M, ld_residual] of out_dtype, or NULL; out: [M, ld_out] of out_dtype
- * (KDA_BF16, KDA_FP16 or KDA_FP32). Sums, bias, activation and residual are held in fp32 and rounded once. residual may be out itself;
- * no other overlap is allowed. GELU is x (1 + erf(x / 2^(1/2))) / 2, GELU_TANH x (1 + tanh((2 / pi)^(1/2) (x + 0.044715 x^3))) / 2.
- * Any strides >= the columns and alignments of the element types are accepted; operands whose base and row pitch are multiples
- * of 16 bytes move by TMA, others by element loads, several times slower (pad rows, or ask kda_matmul_plan). M, N and K may be any
- * size >= 1 (K = 0: act(bias) + residual; M or N = 0: nothing to do), up to 2^30 each. A split of the inner axis is joined in a fixed order: results
- * repeat bit for bit. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT in *err_flags (may be NULL); what it was to give is not written.
+ * a: [M, ld_a] and w: [N, ld_w] (row n holds output n's weights), both of element type dtype (KDA_BF16 or KDA_FP16), K columns
+ * used of each; bias: [N] of bias_dtype (dtype or KDA_FP32), or NULL; act: KDA_ACT_*; residual: [M, ld_residual] of out_dtype, or
+ * NULL; out: [M, ld_out] of out_dtype (KDA_BF16, KDA_FP16 or KDA_FP32). Sums, bias, activation and residual are held in fp32 and
+ * rounded once. residual may be out itself; no other overlap is allowed. GELU is x (1 + erf(x / 2^(1/2))) / 2, GELU_TANH
+ * x (1 + tanh((2 / pi)^(1/2) (x + 0.044715 x^3))) / 2.
+ * Any strides >= the columns and alignments of the element types are accepted. Operands whose base and row pitch are multiples of
+ * 16 bytes move by TMA, others by element loads, several times slower (pad rows, or ask kda_matmul_plan); so do outputs and
+ * residuals of many rows. M, N and K may be any size >= 1 (K = 0: act(bias) + residual; M or N = 0: nothing to do), up to 2^30
+ * each; operands off 16-byte boundaries, and K = 0, up to 4,194,240 rows of a (KDA_ERR_UNSUPPORTED above: split the call). A split
+ * of the inner axis is joined in a fixed order: results repeat bit for bit. A wait that gives up (~2 s) sets KDA_ERRFLAG_TIMEOUT in
+ * *err_flags (may be NULL); what it was to give is not written.
  */
 #define KDA_ACT_NONE 0
 #define KDA_ACT_RELU 1

@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(1024) map_kernel(const __grid_constant__ Args 
 // T, W and the row factors of a chunk, for the value heads of a key head. Thread t has row t of K K^T (t < 64) or row
 // t - 64 of Q K^T, which one product of 128 x 64 gives. A warp's path through the inverse is bound by
 // its latencies: as many CTAs an SM as there is shared memory for at K = 128, and registers at 64 (257 sequences of 1 to 342 tokens x 8 heads:
-// the three launches 187 us, with six CTAs 189, with five 192).
+// the three launches 187 us, with six CTAs 189, with five 192; 191 since the increment has three terms).
 template <int NH>
 __global__ void __launch_bounds__(128, NH == 1 ? 8 : 6) prep_kernel(const __grid_constant__ CUtensorMap tm_qk, const __grid_constant__ Args a)
 {
@@ -1324,9 +1324,10 @@ constexpr int ends_bytes(int K) { return (K * 32 + 2 * K * K + 8 * 32) * 4; }
 // And of outputs_kernel.
 constexpr int outputs_bytes(int K) { return (K / 2 * (K + 4) + 128 * (K + 16)) * 4; }
 
-// The parts of long sequences: as many as give every chain a multiprocessor (152 of them), with two chains for each part behind the first.
+// The parts of long sequences: as many as give every chain a multiprocessor of a GB300's 152, with two chains for each part behind the first.
+// (Not by the current device's: the workspace's size goes by the parts, and may be asked for where another device is current, or none.)
 // Sequences that cannot have CUT_CHUNKS chunks on average stay whole: the joining costs 20 us and more. One sequence of K = V = 128, in parts and whole:
-// 2048 tokens x 32 heads 111 and 107 us, 4096 x 32 188 and 202, 16,384 x 32 620 and 757, 4096 x 8 112 and 180, 16,384 x 8 239 and 682.
+// 2048 tokens x 32 heads 111 and 107 us, 4096 x 32 188 and 202, 16,384 x 32 619 and 757, 4096 x 8 112 and 180, 16,384 x 8 239 and 682.
 int parts_of(int64_t rows, int64_t num_seqs, int Hv, int K, int V)
 {
     const int64_t chains = num_seqs * Hv;

@@ -631,7 +631,7 @@ def kda_matmul(a, w, *, bias=None, activation=None, residual=None, out=None, out
     a: bf16 or fp16 [M, K]; w: [N, K] of the same type; bias: [N] of that type or fp32; activation: None, "relu", "silu",
     "sigmoid", "gelu" (erf) or "gelu_tanh"; residual: [M, N] of out's type (it may be out itself); out: bf16, fp16 or fp32 [M, N],
     allocated as out_dtype (a's type by default) when not given. Operands with rows on 16-byte boundaries move by TMA, others
-    several times slower (kda_matmul_plan tells). Returns out."""
+    several times slower (kda_matmul_plan tells), and so do outputs and residuals of many rows. Returns out."""
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(map(repr, _ACTIVATIONS))} (got {activation!r})")
     if out is None:
@@ -741,7 +741,7 @@ def kda_gdn_chunk_prefill(mixed_qkv, raw_g, raw_beta, A_log, dt_bias, initial_st
                           scale=None, l2_eps=1e-6, null_slot=-1, out=None, workspace=None, err_flags=None, stream=None):
     """The same over packed sequences, in chunks: sequence s has rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the GPU,
     never read on the host: no synchronisation, and lengths may change between graph replays). A pair that is no range of
-    the rows counts as empty and sets KDA_ERRFLAG_LENGTHS in err_flags. workspace: a contiguous tensor of
+    the rows counts as empty and sets KDA_ERRFLAG_LENGTHS in err_flags. States come out within about 1e-6 of their norm. workspace: a contiguous tensor of
     kda_gdn_chunk_prefill_workspace_bytes, allocated where none or a smaller one is given. Returns (out, initial_state)."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens must be a contiguous 1-D int32 tensor")
